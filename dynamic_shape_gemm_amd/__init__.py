@@ -32,6 +32,8 @@ MKP_ACT_RELU = 1
 MKP_ACT_GELU = 2
 MKP_ACT_GELU_TANH = 3
 MKP_ACT_SILU = 4
+MKP_BF16 = 0
+MKP_F32 = 1
 ACTIVATIONS = {None: MKP_ACT_NONE, "none": MKP_ACT_NONE, "relu": MKP_ACT_RELU, "gelu": MKP_ACT_GELU,
                "gelu_tanh": MKP_ACT_GELU_TANH, "silu": MKP_ACT_SILU}
 
@@ -79,6 +81,20 @@ _lib.mkp_gemm_grouped.argtypes = _grp_args
 _lib.mkp_gemm_grouped.restype = _int
 _lib.mkp_gemm_grouped_bt.argtypes = _grp_args
 _lib.mkp_gemm_grouped_bt.restype = _int
+_f32 = ctypes.c_float
+_xent_args = [_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _f32, _f32, _f32, _f32]
+_lib.mkp_linear_xent.argtypes = _xent_args + [_p, _p, _p, _i64, _p]
+_lib.mkp_linear_xent.restype = _int
+_grad_args = [_p, _p, _p, _i64, _p, _i64, _p, _int, _p, _i64, _p]
+_lib.mkp_linear_xent_backward.argtypes = _xent_args + _grad_args
+_lib.mkp_linear_xent_backward.restype = _int
+_distill_args = [_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _f32, _f32, _f32]
+_lib.mkp_linear_distill.argtypes = _distill_args + [_p, _p, _p, _i64, _p]
+_lib.mkp_linear_distill.restype = _int
+_lib.mkp_linear_distill_backward.argtypes = _distill_args + _grad_args
+_lib.mkp_linear_distill_backward.restype = _int
+_lib.mkp_linear_loss_workspace.argtypes = [_i64, _i64, _i64, _i64, _p, _i64, _int, _p]
+_lib.mkp_linear_loss_workspace.restype = _int
 _lib.mkp_plan_describe_grouped.argtypes = [_i64, _i64, _i64, _p, _int, ctypes.c_char_p, ctypes.c_size_t]
 _lib.mkp_plan_describe_grouped.restype = _int
 _lib.mkp_plan_describe.argtypes = [_i64, _i64, _i64, _i64, _int, ctypes.c_char_p, ctypes.c_size_t]
@@ -117,7 +133,8 @@ _f_gemm_batched = _fast.gemm_batched if _fast else _lib.mkp_gemm_batched
 _f_gemm_batched_bt = _fast.gemm_batched_bt if _fast else _lib.mkp_gemm_batched_bt
 
 EXPORTED = ["mkp_gemm", "mkp_gemm_batched", "mkp_gemm_batched_noalloc", "mkp_noalloc_scratch_bytes", "mkp_gemm_bt", "mkp_gemm_batched_bt", "mkp_gemm_ex", "mkp_conv2d", "mkp_gemm_grouped",
-            "mkp_gemm_grouped_bt", "mkp_plan_describe", "mkp_plan_describe_grouped", "mkp_plan_with_table",
+            "mkp_gemm_grouped_bt", "mkp_linear_xent", "mkp_linear_xent_backward", "mkp_linear_distill",
+            "mkp_linear_distill_backward", "mkp_linear_loss_workspace", "mkp_plan_describe", "mkp_plan_describe_grouped", "mkp_plan_with_table",
             "mkp_load_calibration",
             "mkp_calibrate", "mkp_set_option", "mkp_kernel_count", "mkp_kernel_name", "mkp_cache_clear",
             "mkp_stats", "mkp_trace_dump", "mkp_last_error"]
@@ -272,6 +289,80 @@ def mkp_gemm_grouped_raw(M, K, A, lda, N, B, ldb, C, ldc, stream, bt=False) -> i
 def mkp_plan_describe_grouped(M, K, N, bt=False) -> dict:
     return json.loads(_text_call(_lib.mkp_plan_describe_grouped, len(N), M, K,
                                  ctypes.cast(_i64_array(N), _p), MKP_PLAN_B_NK if bt else 0))
+
+
+def mkp_linear_xent_raw(M, V, K, X, ldx, W, ldw, bias, labels, scale, softcap, smoothing, z_loss, loss, lse,
+                        workspace, workspace_bytes, stream) -> int:
+    return _lib.mkp_linear_xent(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), _addr(labels), scale, softcap,
+                                smoothing, z_loss, _addr(loss), _addr(lse), _addr(workspace), workspace_bytes,
+                                stream or 0)
+
+
+def mkp_linear_xent(M, V, K, X, ldx, W, ldw, bias, labels, scale, softcap, smoothing, z_loss, loss, lse,
+                    workspace, workspace_bytes, stream=None) -> int:
+    """loss[m], lse[m] := cross entropy of labels[m] (int64) with the logits
+    scale X . W^T + bias (X M x K, W V x K, bf16), which are not stored."""
+    return _check(mkp_linear_xent_raw(M, V, K, X, ldx, W, ldw, bias, labels, scale, softcap, smoothing, z_loss, loss,
+                                      lse, workspace, workspace_bytes, _stream(stream)))
+
+
+def mkp_linear_xent_backward_raw(M, V, K, X, ldx, W, ldw, bias, labels, scale, softcap, smoothing, z_loss, lse, dloss,
+                                 dX, lddx, dW, lddw, dbias, grad_type, workspace, workspace_bytes, stream) -> int:
+    return _lib.mkp_linear_xent_backward(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), _addr(labels), scale,
+                                         softcap, smoothing, z_loss, _addr(lse), _addr(dloss), _addr(dX), lddx,
+                                         _addr(dW), lddw, _addr(dbias), grad_type, _addr(workspace), workspace_bytes,
+                                         stream or 0)
+
+
+def mkp_linear_xent_backward(M, V, K, X, ldx, W, ldw, bias, labels, scale, softcap, smoothing, z_loss, lse, dloss,
+                             dX, lddx, dW, lddw, dbias, grad_type, workspace, workspace_bytes, stream=None) -> int:
+    """dX, dW, dbias (each may be None) := the gradients of
+    sum_m dloss[m] loss[m]; lse as mkp_linear_xent wrote it."""
+    return _check(mkp_linear_xent_backward_raw(M, V, K, X, ldx, W, ldw, bias, labels, scale, softcap, smoothing, z_loss,
+                                               lse, dloss, dX, lddx, dW, lddw, dbias, grad_type, workspace,
+                                               workspace_bytes, _stream(stream)))
+
+
+def mkp_linear_distill_raw(M, V, K, X, ldx, W, ldw, bias, k, ids, ldids, teacher, ldt, teacher_lse, temperature, scale,
+                           softcap, loss, lse, workspace, workspace_bytes, stream) -> int:
+    return _lib.mkp_linear_distill(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), k, _addr(ids), ldids,
+                                   _addr(teacher), ldt, _addr(teacher_lse), temperature, scale, softcap, _addr(loss),
+                                   _addr(lse), _addr(workspace), workspace_bytes, stream or 0)
+
+
+def mkp_linear_distill(M, V, K, X, ldx, W, ldw, bias, k, ids, ldids, teacher, ldt, teacher_lse, temperature, scale,
+                       softcap, loss, lse, workspace, workspace_bytes, stream=None) -> int:
+    """loss[m] := T^2 KL(teacher || softmax((scale X . W^T + bias) / T)), the
+    teacher known by k logits (fp32) at vocabulary entries ids (int64) a row."""
+    return _check(mkp_linear_distill_raw(M, V, K, X, ldx, W, ldw, bias, k, ids, ldids, teacher, ldt, teacher_lse,
+                                         temperature, scale, softcap, loss, lse, workspace, workspace_bytes,
+                                         _stream(stream)))
+
+
+def mkp_linear_distill_backward_raw(M, V, K, X, ldx, W, ldw, bias, k, ids, ldids, teacher, ldt, teacher_lse,
+                                    temperature, scale, softcap, lse, dloss, dX, lddx, dW, lddw, dbias, grad_type,
+                                    workspace, workspace_bytes, stream) -> int:
+    return _lib.mkp_linear_distill_backward(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), k, _addr(ids), ldids,
+                                            _addr(teacher), ldt, _addr(teacher_lse), temperature, scale, softcap,
+                                            _addr(lse), _addr(dloss), _addr(dX), lddx, _addr(dW), lddw, _addr(dbias),
+                                            grad_type, _addr(workspace), workspace_bytes, stream or 0)
+
+
+def mkp_linear_distill_backward(M, V, K, X, ldx, W, ldw, bias, k, ids, ldids, teacher, ldt, teacher_lse, temperature,
+                                scale, softcap, lse, dloss, dX, lddx, dW, lddw, dbias, grad_type, workspace,
+                                workspace_bytes, stream=None) -> int:
+    """The gradients of sum_m dloss[m] loss[m] of mkp_linear_distill."""
+    return _check(mkp_linear_distill_backward_raw(M, V, K, X, ldx, W, ldw, bias, k, ids, ldids, teacher, ldt,
+                                                  teacher_lse, temperature, scale, softcap, lse, dloss, dX, lddx, dW,
+                                                  lddw, dbias, grad_type, workspace, workspace_bytes,
+                                                  _stream(stream)))
+
+
+def mkp_linear_loss_workspace(M, V, K, k, W, ldw, backward) -> int:
+    """Bytes of workspace the vocabulary losses need (k = 0: cross entropy)."""
+    n = ctypes.c_int64(0)
+    _check(_lib.mkp_linear_loss_workspace(M, V, K, k, _addr(W), ldw, 1 if backward else 0, ctypes.byref(n)))
+    return n.value
 
 
 def _text_call(fn, *args, size=1 << 16):
@@ -441,3 +532,162 @@ def conv2d(x, w, bias=None, act=None, stride=1, padding=0, dilation=1, out=None,
         out = torch.empty((N, P, Q, K), dtype=torch.float32, device=x.device)
     mkp_conv2d(N, H, W, C, K, R, S, sh, sw, ph, pw, dh, dw, x, w, out, bias, act, stream)
     return out
+
+
+def _loss_inputs(x, w, bias, rows):
+    """Checks shared by the vocabulary losses; (M, V, K, ldx, ldw).  rows:
+    name -> (tensor or None, dtype, shape)."""
+    import torch
+    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+        raise TypeError("x and w must be bfloat16")
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError("x must be (M, K) and w (V, K)")
+    M, K = x.shape
+    V = w.shape[0]
+    if (x.stride(1) != 1 and K > 1) or (w.stride(1) != 1 and K > 1):
+        raise ValueError("rows must be contiguous (unit column stride)")
+    every = dict(rows, bias=(bias, torch.float32, (V,)), w=(w, w.dtype, tuple(w.shape)), x=(x, x.dtype, tuple(x.shape)))
+    every = {name: e for name, e in every.items() if e[0] is not None}
+    for name, (t, dtype, shape) in every.items():
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {str(dtype).split('.')[-1]}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must be contiguous along its last axis")
+    for name, (t, _, _) in every.items():
+        if t.device != x.device or t.device.type != "cuda":
+            raise ValueError(f"{name} must be on x's GPU")
+    return M, V, K, (x.stride(0) if M > 1 else K), (w.stride(0) if V > 1 else K)
+
+
+class _LossStream:
+    """The stream a vocabulary loss runs on, made current (with its device)
+    while the call's outputs and workspace are taken from torch's allocator,
+    so that they belong to it."""
+
+    def __init__(self, device, stream):
+        import torch
+        if stream is None:
+            self.stream = torch.cuda.current_stream(device)
+        elif isinstance(stream, int):
+            self.stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                           else torch.cuda.default_stream(device))
+        else:
+            self.stream = stream
+        if self.stream.device != device:
+            raise ValueError("the stream is on another device than x")
+        self.handle = self.stream.cuda_stream
+        here = torch.cuda.current_device() == device.index
+        self.ctx = None if stream is None and here else torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+
+def _loss_workspace(M, V, K, k, w, ldw, backward):
+    import torch
+    n = mkp_linear_loss_workspace(M, V, K, k, w, ldw, backward)
+    return torch.empty(n, dtype=torch.uint8, device=w.device), n
+
+
+def _loss_grads(x, w, bias, need_dx, need_dw, need_dbias, grad_dtype):
+    import torch
+    if grad_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("grad_dtype must be bfloat16 or float32")
+    if need_dbias is None:
+        need_dbias = bias is not None
+    dx = torch.empty(x.shape, dtype=grad_dtype, device=x.device) if need_dx else None
+    dw = torch.empty(w.shape, dtype=grad_dtype, device=x.device) if need_dw else None
+    dbias = torch.empty(w.shape[0], dtype=torch.float32, device=x.device) if need_dbias else None
+    return dx, dw, dbias, MKP_F32 if grad_dtype == torch.float32 else MKP_BF16
+
+
+def linear_xent(x, w, labels, bias=None, scale=1.0, softcap=0.0, smoothing=0.0, z_loss=0.0, stream=None):
+    """Cross entropy of each row's label with the logits of a linear layer,
+    which are not stored: x (M,K) bf16, w (V,K) bf16, labels (M,) int64, bias
+    (V,) fp32 or None.  Returns (loss, lse), fp32 (M,); rows whose label is not
+    in [0, V) get 0.  The mean over the others is loss.sum() / their number."""
+    import torch
+    M, V, K, ldx, ldw = _loss_inputs(x, w, bias, {"labels": (labels, torch.int64, (x.shape[0],))})
+    with _LossStream(x.device, stream) as st:
+        loss = torch.empty((2, M), dtype=torch.float32, device=x.device)
+        loss, lse = loss[0], loss[1]
+        ws, n = _loss_workspace(M, V, K, 0, w, ldw, False)
+        mkp_linear_xent(M, V, K, x, ldx, w, ldw, bias, labels, scale, softcap, smoothing, z_loss, loss, lse, ws, n, st)
+    return loss, lse
+
+
+def linear_xent_backward(x, w, labels, lse, dloss, bias=None, scale=1.0, softcap=0.0, smoothing=0.0, z_loss=0.0,
+                         need_dx=True, need_dw=True, need_dbias=None, grad_dtype=None, stream=None):
+    """Gradients of (dloss * loss).sum() for linear_xent's loss: (dx, dw,
+    dbias), dx and dw in grad_dtype (bfloat16, the default, or float32), dbias
+    fp32 (by default made when there is a bias); None for those not needed.
+    lse is linear_xent's; dloss (M,) fp32."""
+    import torch
+    M = x.shape[0]
+    M, V, K, ldx, ldw = _loss_inputs(x, w, bias, {"labels": (labels, torch.int64, (M,)),
+                                                  "lse": (lse, torch.float32, (M,))})
+    with _LossStream(x.device, stream) as st:
+        dloss = dloss.contiguous()   # a broadcast scalar has no stride
+        _loss_inputs(x, w, None, {"dloss": (dloss, torch.float32, (M,))})
+        dx, dw, dbias, gt = _loss_grads(x, w, bias, need_dx, need_dw, need_dbias, grad_dtype or torch.bfloat16)
+        ws, n = _loss_workspace(M, V, K, 0, w, ldw, True)
+        mkp_linear_xent_backward(M, V, K, x, ldx, w, ldw, bias, labels, scale, softcap, smoothing, z_loss, lse, dloss,
+                                 dx, K, dw, K, dbias, gt, ws, n, st)
+    return dx, dw, dbias
+
+
+def _distill_inputs(x, w, bias, ids, teacher, teacher_lse, **rows):
+    import torch
+    M = x.shape[0]
+    k = ids.shape[1] if ids.dim() == 2 else 0
+    rows = {name: (t, torch.float32, (M,)) for name, t in rows.items()}
+    rows.update(ids=(ids, torch.int64, (M, k)), teacher=(teacher, torch.float32, (M, k)),
+                teacher_lse=(teacher_lse, torch.float32, (M,)))
+    if k < 1:
+        raise ValueError("ids must be (M, k) with k >= 1")
+    sizes = _loss_inputs(x, w, bias, rows)
+    return sizes + (k, ids.stride(0) if M > 1 else k, teacher.stride(0) if M > 1 else k)
+
+
+def linear_distill(x, w, ids, teacher, bias=None, temperature=1.0, scale=1.0, softcap=0.0, teacher_lse=None,
+                   stream=None):
+    """T^2 times the Kullback-Leibler divergence of a linear layer's softmax
+    (at temperature T) from a teacher known by its k top logits: x (M,K) bf16,
+    w (V,K) bf16, ids (M,k) int64 (entries outside [0, V) are left out),
+    teacher (M,k) fp32, teacher_lse (M,) fp32 or None (then the teacher's
+    probabilities are normalised over the k).  Returns (loss, lse), fp32 (M,)."""
+    import torch
+    M, V, K, ldx, ldw, k, ldi, ldt = _distill_inputs(x, w, bias, ids, teacher, teacher_lse)
+    with _LossStream(x.device, stream) as st:
+        loss = torch.empty((2, M), dtype=torch.float32, device=x.device)
+        loss, lse = loss[0], loss[1]
+        ws, n = _loss_workspace(M, V, K, k, w, ldw, False)
+        mkp_linear_distill(M, V, K, x, ldx, w, ldw, bias, k, ids, ldi, teacher, ldt, teacher_lse, temperature, scale,
+                           softcap, loss, lse, ws, n, st)
+    return loss, lse
+
+
+def linear_distill_backward(x, w, ids, teacher, lse, dloss, bias=None, temperature=1.0, scale=1.0, softcap=0.0,
+                            teacher_lse=None, need_dx=True, need_dw=True, need_dbias=None, grad_dtype=None,
+                            stream=None):
+    """Gradients of (dloss * loss).sum() for linear_distill's loss, as
+    linear_xent_backward gives them."""
+    import torch
+    M, V, K, ldx, ldw, k, ldi, ldt = _distill_inputs(x, w, bias, ids, teacher, teacher_lse, lse=lse)
+    with _LossStream(x.device, stream) as st:
+        dloss = dloss.contiguous()   # a broadcast scalar has no stride
+        _loss_inputs(x, w, None, {"dloss": (dloss, torch.float32, (M,))})
+        dx, dw, dbias, gt = _loss_grads(x, w, bias, need_dx, need_dw, need_dbias, grad_dtype or torch.bfloat16)
+        ws, n = _loss_workspace(M, V, K, k, w, ldw, True)
+        mkp_linear_distill_backward(M, V, K, x, ldx, w, ldw, bias, k, ids, ldi, teacher, ldt, teacher_lse, temperature,
+                                    scale, softcap, lse, dloss, dx, K, dw, K, dbias, gt, ws, n, st)
+    return dx, dw, dbias

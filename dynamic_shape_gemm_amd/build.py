@@ -23,7 +23,9 @@ UNITS = [
     ("kernels.hip", "kernels_p2.o", ["-DMKP_PART=2"]),
     ("kernels.hip", "kernels_p3.o", ["-DMKP_PART=3"]),
     ("kernels.hip", "kernels_p4.o", ["-DMKP_PART=4"]),
+    ("loss.hip", "loss.o", []),
     ("planner.cpp", "planner.o", []),
+    ("loss_api.cpp", "loss_api.o", []),
     ("api.cpp", "api.o", []),
 ]
 SOURCES = sorted({u[0] for u in UNITS})

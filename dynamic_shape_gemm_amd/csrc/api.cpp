@@ -32,6 +32,7 @@
 #include <vector>
 
 #include "../../include/mkp.h"
+#include "internal.h"
 #include "kernels.h"
 #include "planner.h"
 
@@ -1062,6 +1063,23 @@ double time_launches(const std::function<hipError_t()>& fn, int warm, int reps, 
 }
 
 }  // namespace
+
+// ---- what the vocabulary losses share with the GEMM entry points -------------
+
+int report(int code, const std::string& msg) { return fail(code, msg); }
+
+void begin_call() {
+    t_call = lib().calls.fetch_add(1, std::memory_order_relaxed);
+}
+
+hipError_t traced_launch(hipStream_t st, int kernel, double flops, double bytes,
+                         const std::function<hipError_t()>& fn) {
+    Library& L = lib();
+    hipError_t e = traced(L, st, kernel, flops, bytes, fn);
+    if (e == hipSuccess) L.launches.fetch_add(1, std::memory_order_relaxed);
+    return e;
+}
+
 }  // namespace mkp
 
 using namespace mkp;
@@ -1432,6 +1450,7 @@ int mkp_trace_dump(char* buf, size_t len) {
                                  : k == -1   ? "splitk_reduce"
                                  : k == -2   ? "zero_fill"
                                  : k == -3   ? "pack_rows"
+                                 : k <= kTraceLoss ? loss_launch_name(kTraceLoss - k)
                                              : "transpose_b";
         if (i) o << ",";
         o << "{\"kernel\":\"" << name << "\",\"call\":" << recs[i].call << ",\"us\":" << 1000.0 * ms

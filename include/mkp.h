@@ -67,6 +67,12 @@ enum {
     MKP_ACT_SILU = 4          /* x * sigmoid(x) */
 };
 
+/* element types of the vocabulary losses' gradients */
+enum {
+    MKP_BF16 = 0,
+    MKP_F32 = 1
+};
+
 /* flags of mkp_plan_describe (align_flags) and mkp_plan_with_table (flags) */
 enum {
     MKP_PLAN_EXHAUSTIVE = 1,  /* mkp_plan_with_table: score every candidate */
@@ -231,6 +237,95 @@ int mkp_plan_describe_grouped(int64_t groups, int64_t M, int64_t K, const int64_
                               char *buf, size_t len);
 
 /*
+ * Vocabulary losses: what follows a model's last linear layer, computed from
+ * the layer's input X (M x K, bf16) and weight W (V x K, bf16, the layout of
+ * mkp_gemm_bt) without ever holding the M x V logits
+ *   s = scale * X . W^T + bias,   z = softcap * tanh(s / softcap)
+ * (z = s for softcap 0; bias: V fp32 values or NULL).  Products are
+ * accumulated, and every maximum, sum and loss is held, in binary32.
+ *
+ * mkp_linear_xent: softmax cross entropy with each row's label,
+ *   lse = log sum_v exp(z_v)
+ *   loss = lse - (1 - smoothing) z_label - smoothing mean_v(z_v) + z_loss lse^2
+ * (smoothing in [0, 1]).  A row whose label is not in [0, V) -- such as the
+ * customary -100 -- is left out: its loss and lse are 0, it has no gradient,
+ * costs nothing in the products, and whatever its X holds reaches no result.
+ * A label whose logit is -inf (a masked vocabulary entry: bias -inf) has loss
+ * +inf.  M fp32 values each are written to loss and lse.
+ *
+ * mkp_linear_xent_backward: from lse (as written by the forward call) and
+ * dloss (M fp32 values, the gradient by each row's loss; rows left out are
+ * not read), the gradients
+ *   dX (M x K) := scale D . W,  dW (V x K) := scale D^T . X,  dbias (V) := sum_m D
+ *   D = dloss [(1 + 2 z_loss lse) softmax(z) - (1 - smoothing) onehot(label)
+ *              - smoothing / V] * dz/ds
+ * Any of dX, dW and dbias may be NULL: it is not computed.  They are
+ * overwritten (rows of dX left out become 0); dX and dW hold grad_type
+ * elements (MKP_BF16 or MKP_F32), dbias fp32.  The logits are made again, a
+ * piece of the vocabulary at a time, and D passes through bf16 once (its
+ * entries relative to the largest |dloss|), being an operand of bf16
+ * products: with MKP_F32 too, dX and dW are as exact as that (relative 2^-8
+ * at most of each entry of D).
+ *
+ * mkp_linear_distill: the Kullback-Leibler divergence from a teacher that is
+ * known by its logits t at k (1 .. 1024) vocabulary entries ids per row,
+ *   p_j = exp(t_j / T - L),  log q_v = z_v / T - lse,  lse = log sum_v exp(z_v / T)
+ *   loss = T^2 sum_j p_j (log p_j - log q_{id_j})
+ * with temperature T and L the row's teacher_lse (the log-partition of t / T
+ * over the teacher's whole vocabulary; M fp32 values) or, with teacher_lse
+ * NULL, the one over the row's k entries.  An id outside [0, V), or a teacher
+ * logit of -inf, leaves its entry out; a row with no entry left is left out
+ * as above.  An id named twice counts twice.  mkp_linear_distill_backward:
+ * as mkp_linear_xent_backward with
+ *   D = dloss T [softmax(z / T) sum_j p_j - sum_j p_j onehot(id_j)] * dz/ds.
+ *
+ * X rows may have any alignment (ldx >= K); so may W (ldw >= K) and the
+ * outputs, but a W whose rows are not 16-byte aligned, or K not a multiple of
+ * 8, costs a padded copy of W per call.  labels and ids are int64 values,
+ * ldids and ldt >= k.  V and K are at least 1; M == 0 makes dW and dbias 0.
+ *
+ * workspace: device memory of at least mkp_linear_loss_workspace() bytes,
+ * 16-byte aligned, whose contents are of no meaning between calls.  The
+ * calls allocate nothing and never wait, so they can be captured into a HIP
+ * graph; calls that may run at the same time need a workspace each, and a
+ * graph's stays its own.  Every result is made in a fixed order: the same
+ * call gives the same bits.
+ */
+int mkp_linear_xent(int64_t M, int64_t V, int64_t K,
+                    const void *X, int64_t ldx, const void *W, int64_t ldw, const float *bias,
+                    const int64_t *labels, float scale, float softcap, float smoothing, float z_loss,
+                    float *loss, float *lse,
+                    void *workspace, int64_t workspace_bytes, void *stream);
+
+int mkp_linear_xent_backward(int64_t M, int64_t V, int64_t K,
+                             const void *X, int64_t ldx, const void *W, int64_t ldw, const float *bias,
+                             const int64_t *labels, float scale, float softcap, float smoothing, float z_loss,
+                             const float *lse, const float *dloss,
+                             void *dX, int64_t lddx, void *dW, int64_t lddw, float *dbias, int grad_type,
+                             void *workspace, int64_t workspace_bytes, void *stream);
+
+int mkp_linear_distill(int64_t M, int64_t V, int64_t K,
+                       const void *X, int64_t ldx, const void *W, int64_t ldw, const float *bias,
+                       int64_t k, const int64_t *ids, int64_t ldids, const float *teacher, int64_t ldt,
+                       const float *teacher_lse, float temperature, float scale, float softcap,
+                       float *loss, float *lse,
+                       void *workspace, int64_t workspace_bytes, void *stream);
+
+int mkp_linear_distill_backward(int64_t M, int64_t V, int64_t K,
+                                const void *X, int64_t ldx, const void *W, int64_t ldw, const float *bias,
+                                int64_t k, const int64_t *ids, int64_t ldids, const float *teacher, int64_t ldt,
+                                const float *teacher_lse, float temperature, float scale, float softcap,
+                                const float *lse, const float *dloss,
+                                void *dX, int64_t lddx, void *dW, int64_t lddw, float *dbias, int grad_type,
+                                void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that a vocabulary loss of these extents needs: k targets
+ * per row (0: cross entropy), W and ldw as in the call (only their alignment
+ * counts), backward 0 or 1.  Pure host code. */
+int mkp_linear_loss_workspace(int64_t M, int64_t V, int64_t K, int64_t k,
+                              const void *W, int64_t ldw, int backward, int64_t *bytes);
+
+/*
  * Describe the plan the polymerizer picks for a shape, without launching.
  * align_flags: bit0 = A rows 16-byte aligned, bit1 = B rows, bit2 = C rows
  * (pass 7 for aligned operands); MKP_PLAN_B_NK plans for mkp_gemm_bt.
@@ -356,7 +451,8 @@ int mkp_stats(char *buf, size_t len);
 
 /* Launch trace (option "trace" = 1): every kernel launch (micro-kernels,
  * "<a>+<b>" for both regions in one launch of a kernel pair,
- * "splitk_reduce", "zero_fill", "pack_rows", "transpose_b") is bracketed by
+ * "splitk_reduce", "zero_fill", "pack_rows", "transpose_b", the vocabulary
+ * losses' "loss_...") is bracketed by
  * HIP events on its stream.  Waits for the recorded launches, writes a JSON
  * list [{"kernel","call","us","flops","bytes"}...] ("call": sequence number
  * of the GEMM call that made the launch; algorithmic work per launch:

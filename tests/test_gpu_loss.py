@@ -1,0 +1,431 @@
+"""GPU parity of the vocabulary losses (linear_xent, linear_distill and their
+gradients) with the 64-bit oracle on the same bf16 inputs.  Tolerances are
+oracle.loss.bounds: errors followed through the formulas, element by element.
+"""
+import math
+
+import pytest
+import torch
+
+from oracle import loss as oracle
+
+pytestmark = pytest.mark.gpu
+
+BF, F64 = torch.bfloat16, torch.float64
+
+
+@pytest.fixture(scope="module")
+def mkp(gpu):
+    import dynamic_shape_gemm_amd as m
+    return m
+
+
+def inputs(seed, M, V, K, *, pad_x=0, pad_w=0, shift=0, std=0.2, sharp=4.0, bias=False, k=0, keep=1.0):
+    """bf16 x and w in rows of K + pad elements starting `shift` elements into
+    their buffers, and targets; some rows without any."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rows(n, pad, s):
+        buf = torch.full((n * (K + pad) + shift + 8,), float("nan"), device="cuda", dtype=BF)
+        v = buf[shift:shift + n * (K + pad)].view(n, K + pad)[:, :K]
+        v.copy_(torch.randn(n, K, generator=g, device="cuda") * s)
+        return v
+
+    t = {"x": rows(M, pad_x, 1.0), "w": rows(V, pad_w, std)}
+    on = torch.rand(M, generator=g, device="cuda") < keep
+    if keep < 1.0 and M > 1:
+        on[0], on[M - 1] = False, True
+    top = torch.randint(0, V, (M,), generator=g, device="cuda")
+    t["x"].add_((sharp * torch.rand(M, 1, generator=g, device="cuda") * torch.nn.functional.normalize(
+        t["w"][top].float(), dim=1)).to(BF))
+    if k:
+        ids = torch.randint(0, V, (M, k), generator=g, device="cuda")
+        ids[torch.rand(M, k, generator=g, device="cuda") < 0.1] = -1
+        ids[~on] = -1
+        t["ids"], t["teacher"] = ids, 2.0 * torch.randn(M, k, generator=g, device="cuda")
+    else:
+        t["labels"] = torch.where(on, top, torch.full_like(top, -100))
+    t["bias"] = torch.randn(V, generator=g, device="cuda") if bias else None
+    t["dloss"] = torch.rand(M, generator=g, device="cuda") * 2 - 0.5
+    return t
+
+
+def within(name, got, ref, tol, what):
+    got = got.to(F64)
+    assert got.shape == ref.shape, (what, name)
+    same = (got == ref) | (torch.isnan(got) & torch.isnan(ref))
+    err = torch.where(same, torch.zeros_like(ref), (got - ref).abs())
+    bad = ~(err <= tol)
+    if bad.any():
+        i = int(torch.nan_to_num(err / tol, nan=math.inf).argmax())
+        raise AssertionError(f"{what} {name}: {int(bad.sum())} of {bad.numel()} off; worst at {i}: "
+                             f"{got.reshape(-1)[i].item()} for {ref.reshape(-1)[i].item()}, "
+                             f"{err.reshape(-1)[i].item():.3e} > {torch.broadcast_to(tol, ref.shape).reshape(-1)[i].item():.3e}")
+
+
+def check(mkp, t, what, *, grad=True, f32=False, **opt):
+    """Forward and backward of one set of inputs against the oracle."""
+    print(f"[case] {what} x={tuple(t['x'].shape)} w={tuple(t['w'].shape)} {opt}", flush=True)
+    d = {n: (v.to(F64) if v is not None and v.is_floating_point() else v) for n, v in t.items()}
+    tl = opt.pop("teacher_lse", None)
+    dt = torch.float32 if f32 else BF
+    if "labels" in t:
+        loss, lse = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"], **opt)
+        if grad:
+            dx, dw, db = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"], t["bias"],
+                                                  need_dbias=True, grad_dtype=dt, **opt)
+        ref = oracle.xent(d["x"], d["w"], d["labels"], d["bias"], dloss=d["dloss"] if grad else None, **opt)
+        fin = ref["lse"][torch.isfinite(ref["lse"])]
+        most = float(fin.abs().max()) if fin.numel() else 0.0
+        more = {"weight": 1.0 + 2.0 * abs(opt.get("z_loss", 0.0)) * most,
+                "terms": abs(opt.get("z_loss", 0.0)) * most * most + 16.0 * most}
+        T = 1.0
+    else:
+        loss, lse = mkp.linear_distill(t["x"], t["w"], t["ids"], t["teacher"], t["bias"], teacher_lse=tl, **opt)
+        if grad:
+            dx, dw, db = mkp.linear_distill_backward(t["x"], t["w"], t["ids"], t["teacher"], lse, t["dloss"], t["bias"],
+                                                     teacher_lse=tl, need_dbias=True, grad_dtype=dt, **opt)
+        ref = oracle.distill(d["x"], d["w"], d["ids"], d["teacher"], d["bias"], dloss=d["dloss"] if grad else None,
+                             teacher_lse=None if tl is None else tl.to(F64), **opt)
+        more = {"weight": ref["weight"], "terms": ref["terms"] + ref["weight"] * 16.0}
+        T = opt.get("temperature", 1.0)
+    torch.cuda.synchronize()
+    tol = oracle.bounds(ref, d["x"], d["w"], d["bias"], opt.get("scale", 1.0), opt.get("softcap", 0.0), T, **more)
+    within("lse", lse, ref["lse"], tol["lse"], what)
+    within("loss", loss, ref["loss"], tol["loss"], what)
+    if grad:
+        s = "32" if f32 else ""
+        within("dbias", db, ref["dbias"], tol["dbias"], what)
+        within("dx", dx, ref["dx"], tol["dx" + s], what)
+        within("dw", dw, ref["dw"], tol["dw" + s], what)
+        return loss, lse, dx, dw, db
+    return loss, lse
+
+
+SIZES = [(1, 1, 1), (1, 2, 8), (2, 63, 64), (3, 65, 72), (17, 256, 65), (64, 257, 128), (65, 300, 192), (129, 1000, 200),
+         (256, 513, 64), (300, 129, 320), (513, 700, 264)]
+
+
+@pytest.mark.parametrize("M,V,K", SIZES)
+def test_xent(mkp, M, V, K):
+    check(mkp, inputs(M + V, M, V, K, keep=0.8), "xent")
+
+
+@pytest.mark.parametrize("M,V,K", SIZES)
+def test_distill(mkp, M, V, K):
+    check(mkp, inputs(M + V, M, V, K, keep=0.8, k=min(V, 5)), "distill", temperature=2.0)
+
+
+@pytest.mark.parametrize("opt", [dict(scale=0.5), dict(scale=-1.5), dict(softcap=5.0), dict(smoothing=0.1),
+                                 dict(smoothing=1.0), dict(z_loss=1e-2), dict(scale=1.3, softcap=2.0, smoothing=0.3,
+                                                                             z_loss=1e-3)], ids=str)
+@pytest.mark.parametrize("M", [50, 290])
+def test_xent_options(mkp, opt, M):
+    check(mkp, inputs(9, M, 333, 136, keep=0.7, bias=True), "xent options", **opt)
+
+
+@pytest.mark.parametrize("k", [1, 4, 33, 200, 1024])
+@pytest.mark.parametrize("own_lse", [False, True])
+def test_distill_targets(mkp, k, own_lse):
+    """From one target to the most, ids drawn with repetition (so named twice
+    or more), at a temperature, with a bias and a cap."""
+    for M in (40, 270):
+        t = inputs(k, M, 600, 72, keep=0.8, bias=True, k=k)
+        tl = None
+        if own_lse:
+            there = t["ids"] >= 0
+            tl = torch.where(there, t["teacher"] / 1.5, torch.full_like(t["teacher"], -1e30)).logsumexp(1) + 0.25
+        check(mkp, t, f"distill k={k}", temperature=1.5, softcap=6.0, scale=0.9, teacher_lse=tl)
+
+
+@pytest.mark.parametrize("pad_x,pad_w,shift", [(0, 8, 0), (5, 0, 0), (0, 3, 0), (8, 8, 1), (1, 1, 3)])
+@pytest.mark.parametrize("M", [1, 33, 280])
+def test_strides_and_alignment(mkp, pad_x, pad_w, shift, M):
+    check(mkp, inputs(3, M, 321, 120, pad_x=pad_x, pad_w=pad_w, shift=shift, keep=0.9), "strides")
+
+
+@pytest.mark.parametrize("M", [30, 300])
+def test_float32_gradients(mkp, M):
+    check(mkp, inputs(5, M, 260, 96, keep=0.9), "fp32 gradients", f32=True)
+    check(mkp, inputs(6, M, 260, 97, keep=0.9, k=3), "fp32 gradients", f32=True)
+
+
+def test_teacher_strides(mkp):
+    """ids and teacher as columns of wider arrays."""
+    t = inputs(8, 40, 200, 64, k=6)
+    wide = torch.full((40, 11), -7, device="cuda", dtype=torch.int64)
+    wide[:, 2:8] = t["ids"]
+    tw = torch.full((40, 9), float("nan"), device="cuda")
+    tw[:, 1:7] = t["teacher"]
+    a = check(mkp, t, "narrow")
+    t["ids"], t["teacher"] = wide[:, 2:8], tw[:, 1:7]
+    b = check(mkp, t, "wide")
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("M", [40, 300])
+def test_no_row_has_a_target(mkp, M):
+    t = inputs(11, M, 90, 64, bias=True)
+    t["labels"][:] = -100
+    t["labels"][0], t["labels"][1] = 90, 1 << 40   # beyond the vocabulary
+    t["x"][:] = float("nan")
+    loss, lse, dx, dw, db = check(mkp, t, "no labels")
+    for v in (loss, lse, dx, dw, db):
+        assert (v == 0).all()
+
+
+@pytest.mark.parametrize("M", [24, 301])
+def test_left_out_rows_may_hold_anything(mkp, M):
+    """NaN and infinity in rows without a target, in their dloss, lse and
+    teacher logits, reach nothing."""
+    t = inputs(12, M, 150, 80, keep=0.6)
+    dead = t["labels"] < 0
+    clean = check(mkp, t, "clean")
+    t["x"][dead] = float("nan")
+    t["x"][0] = float("inf")
+    t["dloss"][dead] = float("nan")
+    dirty = check(mkp, t, "dirty")
+    assert all(torch.equal(p, q) for p, q in zip(clean, dirty))
+    t = inputs(13, M, 150, 80, keep=0.6, k=4)
+    dead = (t["ids"] < 0).all(1)
+    t["teacher"] = torch.where(t["ids"] < 0, torch.full_like(t["teacher"], -math.inf), t["teacher"])
+    clean = check(mkp, t, "clean")
+    t["x"][dead] = float("nan")
+    t["dloss"][dead] = float("inf")
+    t["teacher"] = torch.where(t["ids"] < 0, torch.full_like(t["teacher"], float("nan")), t["teacher"])
+    dirty = check(mkp, t, "dirty")
+    assert all(torch.equal(p, q) for p, q in zip(clean, dirty))
+
+
+@pytest.mark.parametrize("M", [24, 301])
+def test_masked_vocabulary(mkp, M):
+    """A bias of -inf, and of the type's lowest value, takes entries out; a
+    label that is taken out has an infinite loss."""
+    for low in (-math.inf, torch.finfo(torch.float32).min):
+        t = inputs(14, M, 400, 64, bias=True)
+        t["bias"][50:390] = low
+        t["labels"] = torch.where(t["labels"] % 2 == 0, t["labels"] % 50, 390 + t["labels"] % 10)
+        check(mkp, t, "masked")
+        check(mkp, t, "masked", z_loss=1e-3, scale=0.7)
+    t["bias"][50:390] = -math.inf
+    t["labels"][3] = 100
+    loss, _ = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"])
+    assert math.isinf(loss[3].item()) and loss[3] > 0 and torch.isfinite(loss[:3]).all() and torch.isfinite(loss[4:]).all()
+    # every entry out: an infinite loss, no NaN in any gradient
+    t["bias"][:] = -math.inf
+    loss, lse = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"])
+    assert torch.isposinf(loss).all() and torch.isneginf(lse).all()
+    dx, dw, db = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"], t["bias"])
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all() and torch.isfinite(db).all()
+
+
+def test_a_nan_row_stays_its_own(mkp):
+    """A row with a target and NaN features: its loss, its dx row and dw are
+    NaN, no other row's."""
+    for M in (40, 300):
+        t = inputs(15, M, 100, 64)
+        t["x"][7] = float("nan")
+        loss, lse = mkp.linear_xent(t["x"], t["w"], t["labels"])
+        dx, _, _ = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"])
+        nan = torch.isnan(loss)
+        assert nan[7] and nan.sum() == 1
+        rows = torch.isnan(dx).any(1)
+        assert rows[7] and rows.sum() == 1
+
+
+@pytest.mark.parametrize("M", [0, 1, 40])
+def test_only_the_gradients_asked_for(mkp, M):
+    t = inputs(16, max(M, 1), 130, 72, bias=True)
+    t = {n: (v[:M] if n in ("x", "labels", "dloss") else v) for n, v in t.items()}
+    loss, lse = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"])
+    assert loss.shape == (M,) and lse.shape == (M,)
+    args = (t["x"], t["w"], t["labels"], lse, t["dloss"], t["bias"])
+    full = mkp.linear_xent_backward(*args)
+    if M == 0:
+        assert (full[1] == 0).all() and (full[2] == 0).all() and full[0].shape == (0, 72)
+    for need in range(8):
+        part = mkp.linear_xent_backward(*args, need_dx=bool(need & 1), need_dw=bool(need & 2),
+                                        need_dbias=bool(need & 4))
+        for i in range(3):
+            if need >> i & 1:
+                assert torch.equal(part[i], full[i])
+            else:
+                assert part[i] is None
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_several_pieces_of_the_vocabulary(mkp, op):
+    """Enough rows and a wide enough vocabulary that the gradient takes more
+    than one piece and dX more than one tile of rows."""
+    t = inputs(21, 4200, 40000, 64, bias=True, k=6 if op == "distill" else 0, keep=0.9)
+    ws1 = mkp.mkp_linear_loss_workspace(4200, 40000, 64, 0, t["w"], 64, True)
+    assert ws1 < 2 * 4200 * 40000   # less than the whole gradient by the logits
+    check(mkp, t, op + " pieces", **({"temperature": 2.0} if op == "distill" else {"smoothing": 0.05}))
+
+
+@pytest.mark.parametrize("grad_dtype", [BF, torch.float32])
+def test_writes_stay_inside(mkp, grad_dtype):
+    """Raw entry points with outputs inside larger buffers: what lies between
+    and behind the rows is left as it was."""
+    M, V, K = 70, 130, 72
+    t = inputs(31, M, V, K, keep=0.8, bias=True)
+    x, w = t["x"].contiguous(), t["w"].contiguous()
+    for lddx, lddw, off in ((K, K, 0), (K + 5, K + 3, 1), (K + 8, K + 16, 0)):
+        dxb = torch.full((M * lddx + off + 64,), float("nan"), device="cuda", dtype=grad_dtype)
+        dwb = torch.full((V * lddw + off + 64,), float("nan"), device="cuda", dtype=grad_dtype)
+        dbb = torch.full((V + 64,), float("nan"), device="cuda")
+        out = torch.full((2, M + 64), float("nan"), device="cuda")
+        nf, nb = (mkp.mkp_linear_loss_workspace(M, V, K, 0, w, K, b) for b in (0, 1))
+        ws = torch.full((max(nf, nb) + 256,), 255, device="cuda", dtype=torch.uint8)
+        es = dxb.element_size()
+        mkp.mkp_linear_xent(M, V, K, x, K, w, K, t["bias"], t["labels"], 1.0, 0.0, 0.0, 0.0, out[0], out[1], ws, nf)
+        mkp.mkp_linear_xent_backward(M, V, K, x, K, w, K, t["bias"], t["labels"], 1.0, 0.0, 0.0, 0.0, out[1], t["dloss"],
+                                     dxb.data_ptr() + es * off, lddx, dwb.data_ptr() + es * off, lddw, dbb,
+                                     mkp.MKP_F32 if grad_dtype == torch.float32 else mkp.MKP_BF16, ws, nb)
+        torch.cuda.synchronize()
+        ref = mkp.linear_xent_backward(x, w, t["labels"], out[1, :M].clone(), t["dloss"], t["bias"],
+                                       grad_dtype=grad_dtype)
+        for buf, ld, rows, want in ((dxb, lddx, M, ref[0]), (dwb, lddw, V, ref[1])):
+            body = buf[off:off + rows * ld].view(rows, ld)
+            assert torch.equal(body[:, :K], want)
+            assert torch.isnan(body[:, K:]).all() and torch.isnan(buf[:off]).all() and torch.isnan(buf[off + rows * ld:]).all()
+        assert torch.equal(dbb[:V], ref[2]) and torch.isnan(dbb[V:]).all()
+        assert torch.isfinite(out[:, :M]).all() and torch.isnan(out[:, M:]).all()
+        assert (ws[max(nf, nb):] == 255).all()
+
+
+@pytest.mark.parametrize("M", [3, 600])
+def test_same_call_same_bits(mkp, M):
+    t = inputs(41, M, 1500, 136, keep=0.8, bias=True)
+    run = lambda: (lambda f: f + mkp.linear_xent_backward(t["x"], t["w"], t["labels"], f[1], t["dloss"], t["bias"]))(  # noqa: E731
+        mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"]))
+    a, b = run(), run()
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_streams(mkp):
+    """Two streams with calls of different sizes in flight, from torch's
+    current stream and from the stream argument."""
+    ts = [inputs(50 + i, 40 + 260 * i, 900, 128, keep=0.8) for i in range(2)]
+    ref = [mkp.linear_xent(t["x"], t["w"], t["labels"]) for t in ts]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for rep in range(3):
+        got = []
+        for t, s in zip(ts, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            if rep == 0:
+                with torch.cuda.stream(s):
+                    f = mkp.linear_xent(t["x"], t["w"], t["labels"])
+                    got.append(f + mkp.linear_xent_backward(t["x"], t["w"], t["labels"], f[1], t["dloss"]))
+            else:
+                arg = s if rep == 1 else s.cuda_stream
+                f = mkp.linear_xent(t["x"], t["w"], t["labels"], stream=arg)
+                got.append(f + mkp.linear_xent_backward(t["x"], t["w"], t["labels"], f[1], t["dloss"], stream=arg))
+        torch.cuda.synchronize()
+        for g, r, t in zip(got, ref, ts):
+            assert torch.equal(g[0], r[0]) and torch.equal(g[1], r[1])
+            again = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], r[1], t["dloss"])
+            assert torch.equal(g[2], again[0]) and torch.equal(g[3], again[1])
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_captured_into_graphs(mkp, op):
+    """Two graphs of forward and backward, replayed by turns with new inputs
+    and with the program's own calls between, equal the eager results."""
+    k = 5 if op == "distill" else 0
+    sizes = [(30, 700, 136), (310, 700, 136)]
+    ts = [inputs(60 + i, M, V, K, keep=0.8, k=k, bias=True) for i, (M, V, K) in enumerate(sizes)]
+    tgt = (lambda t: (t["ids"], t["teacher"])) if k else (lambda t: (t["labels"],))
+    fwd = mkp.linear_distill if k else mkp.linear_xent
+    bwd = mkp.linear_distill_backward if k else mkp.linear_xent_backward
+
+    def step(t):
+        f = fwd(t["x"], t["w"], *tgt(t), t["bias"])
+        return f + bwd(t["x"], t["w"], *tgt(t), f[1], t["dloss"], t["bias"])
+
+    graphs, outs = [], []
+    for t in ts:
+        step(t)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(t))
+        graphs.append(g)
+    for rep in range(4):
+        for t in ts:
+            new = inputs(70 + rep, *t["x"].shape[:1], t["w"].shape[0], t["x"].shape[1], keep=0.3 + 0.2 * rep, k=k, bias=True)
+            for n in t:
+                t[n].copy_(new[n])
+        for g in graphs:
+            g.replay()
+        want = [step(t) for t in ts]
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert all(torch.equal(p, q) for p, q in zip(o, w))
+
+
+def test_a_training_step_with_both_losses(mkp):
+    """Labels and a teacher together, as a student is trained: the two losses'
+    gradients add up to the gradient of the weighted sum."""
+    t = inputs(80, 200, 500, 128, k=8)
+    y = inputs(80, 200, 500, 128, keep=0.9)["labels"]
+    a, b = 0.3, 0.7
+    l1, s1 = mkp.linear_xent(t["x"], t["w"], y)
+    l2, s2 = mkp.linear_distill(t["x"], t["w"], t["ids"], t["teacher"], temperature=2.0)
+    n = int((y >= 0).sum())
+    g1 = torch.full((200,), a / n, device="cuda")
+    g2 = torch.full((200,), b / 200, device="cuda")
+    f32 = torch.float32
+    dx1, dw1, _ = mkp.linear_xent_backward(t["x"], t["w"], y, s1, g1, grad_dtype=f32)
+    dx2, dw2, _ = mkp.linear_distill_backward(t["x"], t["w"], t["ids"], t["teacher"], s2, g2, temperature=2.0,
+                                              grad_dtype=f32)
+    d = {k: v.to(F64) if v is not None and v.is_floating_point() else v for k, v in t.items()}
+    r1 = oracle.xent(d["x"], d["w"], y, dloss=g1.to(F64))
+    r2 = oracle.distill(d["x"], d["w"], d["ids"], d["teacher"], temperature=2.0, dloss=g2.to(F64))
+    t1 = oracle.bounds(r1, d["x"], d["w"])
+    t2 = oracle.bounds(r2, d["x"], d["w"], T=2.0)
+    u = 2 * oracle.U
+    within("dx", dx1 + dx2, r1["dx"] + r2["dx"], t1["dx32"] + t2["dx32"] + u * (r1["dx"].abs() + r2["dx"].abs()), "both")
+    within("dw", dw1 + dw2, r1["dw"] + r2["dw"], t1["dw32"] + t2["dw32"] + u * (r1["dw"].abs() + r2["dw"].abs()), "both")
+    total = (g1 * l1).sum() + (g2 * l2).sum()
+    ref = (g1.to(F64) * r1["loss"]).sum() + (g2.to(F64) * r2["loss"]).sum()
+    assert abs(total.item() - ref.item()) <= 1e-5 * abs(ref.item()) + 1e-6
+
+
+def test_gradients_against_differences(mkp):
+    """The forward pass's own loss, moved along a direction of w by steps that
+    bf16 holds exactly."""
+    M, V, K = 60, 200, 64
+    t = inputs(90, M, V, K, keep=0.9)
+    w0 = (t["w"].float() * 64).round() / 64          # multiples of 1/64, below 4: bf16 keeps them and +- 1/64
+    w0 = w0.clamp(-1.5, 1.5)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dire = torch.randint(-1, 2, (V, K), generator=g, device="cuda").float() / 64
+    f = lambda w: (t["dloss"].to(F64) * mkp.linear_xent(t["x"], w.to(BF), t["labels"])[0].to(F64)).sum().item()  # noqa: E731
+    up, dn = f(w0 + dire), f(w0 - dire)
+    _, lse = mkp.linear_xent(t["x"], w0.to(BF), t["labels"])
+    _, dw, _ = mkp.linear_xent_backward(t["x"], w0.to(BF), t["labels"], lse, t["dloss"], grad_dtype=torch.float32)
+    slope = (dw.to(F64) * dire.to(F64)).sum().item()
+    # the oracle's own central difference differs from its slope by the third
+    # order; the library's may differ by that and the forward's and bf16's errors
+    d = {k: v.to(F64) if v is not None and v.is_floating_point() else v for k, v in t.items()}
+    fo = lambda w: (d["dloss"] * oracle.xent(d["x"], w, d["labels"])["loss"]).sum().item()  # noqa: E731
+    ro = oracle.xent(d["x"], w0.to(F64), d["labels"], dloss=d["dloss"])
+    third = abs((fo((w0 + dire).to(F64)) - fo((w0 - dire).to(F64))) / 2 - (ro["dw"] * dire.to(F64)).sum().item())
+    tol = oracle.bounds(ro, d["x"], w0.to(F64))
+    slack = third + (tol["dw32"] * dire.abs().to(F64)).sum().item() + (tol["loss"] * d["dloss"].abs()).sum().item()
+    assert abs((up - dn) / 2 - slope) <= slack
+
+
+def test_trace_names_the_launches(mkp):
+    t = inputs(95, 40, 300, 64, k=3, bias=True)
+    try:
+        mkp.mkp_set_option("trace", 1)
+        _, lse = mkp.linear_distill(t["x"], t["w"], t["ids"], t["teacher"], t["bias"])
+        mkp.linear_distill_backward(t["x"], t["w"], t["ids"], t["teacher"], lse, t["dloss"], t["bias"])
+        names = [r["kernel"] for r in mkp.mkp_trace_dump()]
+    finally:
+        mkp.mkp_set_option("trace", 0)
+    assert names == ["loss_flags", "loss_scan", "loss_gather", "loss_forward", "loss_finish", "loss_flags", "loss_scan",
+                     "loss_gather", "loss_grad", "loss_dx", "loss_dw", "loss_dbias", "loss_dx_finish"]
