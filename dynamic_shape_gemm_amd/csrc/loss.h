@@ -65,17 +65,17 @@ struct LossArgs {
     int* ids32;             // compact, n x kp: the targets (-1: none)
     float* wts;             // compact, n x kp: their weights in the gradient
     LossRow* rows;          // compact
-    float* part;            // forward: per (row, vocabulary tile) max and sum, base 2
+    float* part;            // forward: per (row, vocabulary tile) maximum and sum of exponentials
     float* sumz;            // forward with smoothing: per (row, vocabulary tile) sum of z
     float* zt;              // forward: the targets' z, compact n x kp
     uint16_t* G;            // backward: one piece's gradient by s, Mr x Vp
-    float* dxp;             // backward: dX partials, [splits][Mr][Kp]
+    float* dxp;             // backward: dX partials, [splits][rows of live tiles][Kp]
     float* dbp;             // backward: per row tile, sums of G's columns
     int Mr, Kp, Vp, kp;     // padded extents
     int ntiles;             // vocabulary tiles of the forward pass
     // the piece of the vocabulary a backward launch works on
     int v0, vn;
-    int splits, steps_per_split;
+    int slots;              // workgroups of a tile kernel that run at once
     bool first;             // dX partials are written, not added to
 };
 
@@ -91,7 +91,7 @@ hipError_t launch_loss_forward(const LossArgs& a, int tile, hipStream_t st);   /
 hipError_t launch_loss_finish(const LossArgs& a, bool compact, hipStream_t st);    // loss, lse
 hipError_t launch_loss_grad(const LossArgs& a, int tile, hipStream_t st);      // G (and dbp) of a piece
 hipError_t launch_loss_dx(const LossArgs& a, int tile, hipStream_t st);        // dxp of a piece
-hipError_t launch_loss_dx_finish(const LossArgs& a, hipStream_t st);           // dX
+hipError_t launch_loss_dx_finish(const LossArgs& a, int tile, hipStream_t st);  // dX
 hipError_t launch_loss_dw(const LossArgs& a, int tile, hipStream_t st);        // dW of a piece
 hipError_t launch_loss_dbias(const LossArgs& a, int row_tile, hipStream_t st); // dbias of a piece
 

@@ -25,6 +25,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace mkp {
 namespace {
@@ -136,11 +137,6 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t l
 }
 #pragma clang diagnostic pop
 
-template <int N>
-__device__ __forceinline__ void wait_and_barrier() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
 // One operand of a tile: where its halves' loads come from.
 //   rows (not TR): `lim` valid rows of the tile; a last step of fewer than 64
 //     columns (`tail` > 0 of them) repeats the step's first chunk in the
@@ -228,24 +224,51 @@ struct FragReader {
 template <class T>
 using Acc = f32x4[2][2][T::FM][T::FN];
 
-// acc := the tile's product over `steps` K steps.  Two LDS stages: a step's
-// loads are issued a step ahead.
+// Wait until at most N of this wave's direct loads are in flight and its LDS
+// reads are done, then meet the other waves; nothing is scheduled across.
+template <int N>
+__device__ __forceinline__ void phase_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void plain_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// acc := the tile's product over `steps` K steps, two LDS stages.
+//
+// A step is four phases, one quadrant of the wave's tile each:
+//     phase   reads into registers      loads issued     multiplies
+//       0     A0 of step s              B0 of step s+2   A0 x B0
+//       1     B1 of step s              A0 of step s+2   A0 x B1
+//       2     A1 of step s              B1 of step s+2   A1 x B0
+//       3     B0 of step s+1            A1 of step s+2   A1 x B1
+// Every half's LDS block is read in one phase only and refilled from the next
+// phase on, so loads have six phases (one and a half steps) to arrive with two
+// stages: at each phase's end six later halves may still be in flight.
+// Within a phase: the reads and loads, a barrier, the multiplications.  With
+// eight waves the second four run half a phase behind the first (one barrier
+// more at the start, one less at the end), so on every SIMD one wave
+// multiplies while the other reads.
 template <class T>
 __device__ __forceinline__ void main_loop(const Operand<T::HA, T::AT, T::IA, T::NW>& A,
                                           const Operand<T::HB, T::BT, T::IB, T::NW>& B, int steps, lds_t* smem,
                                           int wave, int lane, Acc<T>& acc) {
+    constexpr bool PP = T::NW == 8;
+    constexpr int I = T::IA;
+    static_assert(T::IA == T::IB, "halves are counted in loads");
     const int wm = wave % T::WGM, wn = wave / T::WGM;
     FragReader<T::HA, T::AT, T::FM> ra;
     FragReader<T::HB, T::BT, T::FN> rb;
     ra.init(wm, lane);
     rb.init(wn, lane);
-    const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
-    auto issue = [&](int s) {
-        const uint32_t st = __builtin_amdgcn_readfirstlane(lds0 + (s & 1) * T::STAGE);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) A.issue(h, s, st + h * T::HA_BYTES, wave, lane);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) B.issue(h, s, st + 2 * T::HA_BYTES + h * T::HB_BYTES, wave, lane);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
+    auto issue_a = [&](int h, int s) { A.issue(h, s, lds0 + (s & 1) * T::STAGE + h * T::HA_BYTES, wave, lane); };
+    auto issue_b = [&](int h, int s) {
+        B.issue(h, s, lds0 + (s & 1) * T::STAGE + 2 * T::HA_BYTES + h * T::HB_BYTES, wave, lane);
     };
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha)
@@ -255,33 +278,86 @@ __device__ __forceinline__ void main_loop(const Operand<T::HA, T::AT, T::IA, T::
             for (int i = 0; i < T::FM; ++i)
 #pragma unroll
                 for (int j = 0; j < T::FN; ++j) acc[ha][hb][i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (steps > 0) issue(0);
-    for (int s = 0; s < steps; ++s) {
-        wait_and_barrier<0>();
-        if (s + 1 < steps) issue(s + 1);
-        const lds_t* st = smem + (s & 1) * T::STAGE;
+    if (steps <= 0) {
+        __syncthreads();
+        return;
+    }
+    bf16x8 ya[2][T::FM], xb[2][2][T::FN];
+    auto read_a = [&](int h, int s) {
+        const lds_t* p = smem + (s & 1) * T::STAGE + h * T::HA_BYTES;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8 xb[2][T::FN], ya[2][T::FM];
+        for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int i = 0; i < T::FM; ++i) ya[ks][i] = ra.read(p, i, ks);
+    };
+    auto read_b = [&](int h, int s) {
+        const lds_t* p = smem + (s & 1) * T::STAGE + 2 * T::HA_BYTES + h * T::HB_BYTES;
 #pragma unroll
-                for (int j = 0; j < T::FN; ++j) xb[h][j] = rb.read(st + 2 * T::HA_BYTES + h * T::HB_BYTES, j, ks);
+        for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int i = 0; i < T::FM; ++i) ya[h][i] = ra.read(st + h * T::HA_BYTES, i, ks);
-            }
+            for (int j = 0; j < T::FN; ++j) xb[h][ks][j] = rb.read(p, j, ks);
+    };
+    auto multiply = [&](int ha, int hb) {
+        if constexpr (PP) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-            for (int ha = 0; ha < 2; ++ha)
+        for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int hb = 0; hb < 2; ++hb)
+            for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-                    for (int i = 0; i < T::FM; ++i)
+                for (int j = 0; j < T::FN; ++j)
+                    acc[ha][hb][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[hb][ks][j], ya[ks][i],
+                                                                               acc[ha][hb][i][j], 0, 0, 0);
+        if constexpr (PP) {
+            __builtin_amdgcn_s_setprio(0);
+            plain_barrier();
+        } else {
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // LEFT: steps after this one (2: two or more)
+    auto step = [&](auto left, int s) {
+        constexpr int LEFT = decltype(left)::value;
+        // loads that may still be in flight at each phase's end: six halves,
+        // fewer where nothing more is issued
+        constexpr int W0 = LEFT == 2 ? 6 : LEFT == 1 ? 5 : 1, W1 = LEFT == 2 ? 6 : LEFT == 1 ? 4 : 0;
+        constexpr int W2 = LEFT == 2 ? 6 : LEFT == 1 ? 3 : 0, W3 = LEFT == 2 ? 6 : LEFT == 1 ? 2 : 0;
+        read_a(0, s);
+        if constexpr (LEFT == 2) issue_b(0, s + 2);
+        phase_barrier<W0 * I>();
+        multiply(0, 0);
+        read_b(1, s);
+        if constexpr (LEFT == 2) issue_a(0, s + 2);
+        phase_barrier<W1 * I>();
+        multiply(0, 1);
+        read_a(1, s);
+        if constexpr (LEFT == 2) issue_b(1, s + 2);
+        phase_barrier<W2 * I>();
+        multiply(1, 0);
+        if constexpr (LEFT >= 1) read_b(0, s + 1);
+        if constexpr (LEFT == 2) issue_a(1, s + 2);
+        phase_barrier<W3 * I>();
+        multiply(1, 1);
+    };
+    // the first two steps' loads, in the order of their use
 #pragma unroll
-                        for (int j = 0; j < T::FN; ++j)
-                            acc[ha][hb][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[hb][j], ya[ha][i],
-                                                                                       acc[ha][hb][i][j], 0, 0, 0);
+    for (int s = 0; s < 2; ++s) {
+        if (s < steps) {
+            issue_b(0, s);
+            issue_a(0, s);
+            issue_b(1, s);
+            issue_a(1, s);
         }
     }
+    if (steps > 1) phase_barrier<6 * I>();
+    else phase_barrier<2 * I>();
+    read_b(0, 0);
+    phase_barrier<6 * I>();
+    if (PP && wave >= T::NW / 2) plain_barrier();
+    int s = 0;
+    for (; s + 2 < steps; ++s) step(std::integral_constant<int, 2>{}, s);
+    if (steps > 1) step(std::integral_constant<int, 1>{}, s++);
+    step(std::integral_constant<int, 0>{}, s);
+    if (PP && wave < T::NW / 2) plain_barrier();
     __syncthreads();   // the stages are free for the epilogue
 }
 
@@ -352,14 +428,16 @@ __device__ __forceinline__ void to_logits(Acc<T>& acc, const LossArgs& a, const 
 #pragma unroll
         for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
-            for (int hb = 0; hb < 2; ++hb)
+            for (int i = 0; i < T::FM; ++i) {
 #pragma unroll
-                for (int i = 0; i < T::FM; ++i)
+                for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
                     for (int j = 0; j < T::FN; ++j)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             acc[ha][hb][i][j][r] = a.cap * tanh_fast(acc[ha][hb][i][j][r] * inv);
+                __builtin_amdgcn_sched_barrier(0);   // (a row of fragments at a time, or the registers spill)
+            }
     }
 }
 
@@ -428,10 +506,43 @@ __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
         }
         __syncthreads();
     }
-    // per row: maximum, sum of 2^(z c - maximum), and sum of z where asked for
+    // per row: maximum, sum of 2^((z - maximum) c), and sum of z where asked for
     const float c2 = kLog2e / a.T;
     const bool smooth = a.sumz != nullptr;
     float __attribute__((address_space(3)))* red = (float __attribute__((address_space(3)))*)smem;
+    if (smooth) {
+#pragma unroll
+        for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) {
+                float sz = 0.0f;
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) sz += at.col(hb, j) + r < vr ? acc[ha][hb][i][j][r] : 0.0f;
+                sz += __shfl_xor(sz, 16);
+                sz += __shfl_xor(sz, 32);
+                if (at.g == 0) red[(2 * T::WGN + at.wn) * T::BM + at.row(ha, i)] = sz;
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
+    if (vr < T::BN) {
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+            for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool in = at.col(hb, j) + r < vr;
+#pragma unroll
+                    for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+                        for (int i = 0; i < T::FM; ++i)
+                            acc[ha][hb][i][j][r] = in ? acc[ha][hb][i][j][r] : -INFINITY;
+                }
+    }
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
@@ -451,20 +562,13 @@ __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
                         }
                     }
             }
-            float mx = -INFINITY, sz = 0.0f;
+            float mx = -INFINITY;
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
                 for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const bool in = at.col(hb, j) + r < vr;
-                        const float z = acc[ha][hb][i][j][r];
-                        if (smooth) sz += in ? z : 0.0f;
-                        const float y = in ? z * c2 : -INFINITY;
-                        acc[ha][hb][i][j][r] = y;
-                        mx = fmaxf(mx, y);
-                    }
+                    for (int r = 0; r < 4; ++r) mx = fmaxf(mx, acc[ha][hb][i][j][r]);
             mx = fmaxf(mx, __shfl_xor(mx, 16));
             mx = fmaxf(mx, __shfl_xor(mx, 32));
             const float base = mx == -INFINITY ? 0.0f : mx;   // a row of -inf only: a sum of zeros
@@ -474,18 +578,14 @@ __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
 #pragma unroll
                 for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) sm += exp2_fast(acc[ha][hb][i][j][r] - base);
+                    for (int r = 0; r < 4; ++r) sm += exp2_fast((acc[ha][hb][i][j][r] - base) * c2);
             sm += __shfl_xor(sm, 16);
             sm += __shfl_xor(sm, 32);
-            if (smooth) {
-                sz += __shfl_xor(sz, 16);
-                sz += __shfl_xor(sz, 32);
-            }
             if (at.g == 0) {
                 red[(0 * T::WGN + at.wn) * T::BM + row] = mx;
                 red[(1 * T::WGN + at.wn) * T::BM + row] = sm;
-                red[(2 * T::WGN + at.wn) * T::BM + row] = sz;
             }
+            __builtin_amdgcn_sched_barrier(0);   // one row of fragments at a time keeps the registers within bounds
         }
     __syncthreads();
     for (int row = tid; row < T::BM; row += T::NT) {
@@ -498,8 +598,8 @@ __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
 #pragma unroll
         for (int w = 0; w < T::WGN; ++w) {
             const float mw = red[w * T::BM + row];
-            sm += red[(T::WGN + w) * T::BM + row] * exp2_fast(mw - base);
-            sz += red[(2 * T::WGN + w) * T::BM + row];
+            sm += red[(T::WGN + w) * T::BM + row] * exp2_fast((mw - base) * c2);
+            if (smooth) sz += red[(2 * T::WGN + w) * T::BM + row];
         }
         *(float2*)(a.part + ((int64_t)m * a.ntiles + tn) * 2) = make_float2(mx, sm);
         if (smooth) a.sumz[(int64_t)m * a.ntiles + tn] = sz;
@@ -507,9 +607,12 @@ __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
 }
 
 // Join a row's tiles: one wave per row.
-//   lse = ln2 (max + log2 sum); a row without any finite logit has lse -inf
+//   lse = max / T + log sum; a row without any finite logit has lse -inf
 //   cross entropy: lse - (1 - e) z_y - e / V sum z + c lse^2
 //   distillation:  T^2 sum_j p_j (log p_j - (z_j / T - lse))
+// The differences from z are taken to the maximum first and the logarithm
+// added last: a label that is nearly certain has a small loss, and rounding
+// lse before the difference would leave it few digits.
 // Rows without a target get 0.  With COMPACT rows are looked up through the
 // map (every row's results were cleared by the gather kernel).
 template <bool COMPACT>
@@ -524,9 +627,10 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
     const float base = mx == -INFINITY ? 0.0f : mx;
+    const float c2 = kLog2e / a.T, it = 1.0f / a.T;
     float sm = 0.0f, sz = 0.0f;
     for (int t = lane; t < a.ntiles; t += 64) {
-        sm += part[2 * t + 1] * exp2_fast(part[2 * t] - base);
+        sm += part[2 * t + 1] * exp2_fast((part[2 * t] - base) * c2);
         if (a.sumz) sz += a.sumz[c * a.ntiles + t];
     }
 #pragma unroll
@@ -534,12 +638,13 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a) {
         sm += __shfl_xor(sm, o);
         sz += __shfl_xor(sz, o);
     }
-    const float lse = kLn2 * (base + __builtin_amdgcn_logf(sm));
+    const float ls = kLn2 * __builtin_amdgcn_logf(sm);
+    const float lse = fmaf(base, it, ls);
     if (a.labels != nullptr) {
         const int64_t y = a.labels[m];
         const bool live = y >= 0 && y < a.V;
         if (lane == 0) {
-            float v = (lse - a.zt[c]) + (a.smoothing > 0.0f ? a.smoothing * (a.zt[c] - sz / (float)a.V) : 0.0f) +
+            float v = (base - a.zt[c]) + ls + (a.smoothing > 0.0f ? a.smoothing * (a.zt[c] - sz / (float)a.V) : 0.0f) +
                       (a.z_loss != 0.0f ? a.z_loss * lse * lse : 0.0f);
             if (a.zt[c] == -INFINITY) v = INFINITY;   // the label is masked out, whatever else is
             a.loss[m] = live ? v : 0.0f;
@@ -548,7 +653,6 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a) {
         return;
     }
     // distillation (always compact): the teacher's log-partition over the row
-    const float it = 1.0f / a.T;
     const float* t = a.teacher + m * a.ldt;
     const int* ids = a.ids32 + c * a.kp;
     float tl;
@@ -572,7 +676,7 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a) {
         const float lp = t[j] * it - tl;
         const float p = exp2_fast(kLog2e * lp);
         const float z = a.zt[c * a.kp + j];
-        if (p != 0.0f) kl += z == -INFINITY ? INFINITY : p * (lp - (z * it - lse));
+        if (p != 0.0f) kl += z == -INFINITY ? INFINITY : p * (lp - ((z - base) * it - ls));
     }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) kl += __shfl_xor(kl, o);
@@ -698,7 +802,7 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
     }
     if (tid >= 64) return;
     if (m < 0) {
-        if (BWD && lane == 0) a.rows[c] = LossRow{0.0f, 0.0f, 0.0f, 0.0f};
+        if (BWD && lane == 0) a.rows[c] = LossRow{INFINITY, 0.0f, 0.0f, 0.0f};
         for (int j = lane; j < a.kp; j += 64) a.ids32[(int64_t)c * a.kp + j] = -1;
         return;
     }
@@ -825,31 +929,51 @@ __global__ __launch_bounds__(T::NT) void loss_grad_kernel(LossArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < T::FM; ++i) {
-            const int row = at.row(ha, i), m = m0 + row;
-            const bool live = m < n;
-            const LossRow c = live ? a.rows[m] : LossRow{0.0f, 0.0f, 0.0f, 0.0f};
-            int lab = -1;
-            if constexpr (!TG) lab = (live ? a.ids32[m] : -1) - v0;
+            const int row = at.row(ha, i);
+            const LossRow c = a.rows[m0 + row];   // (rows past the live ones: all entries come out 0)
+            int lab = 0;
+            if constexpr (!TG) lab = a.ids32[m0 + row] - v0;
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
                 for (int j = 0; j < T::FN; ++j) {
                     const int col = at.col(hb, j);
-                    f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if constexpr (TG)
-                        w = *(const f32x4 __attribute__((address_space(3)))*)(
-                            (float __attribute__((address_space(3)))*)smem + (row - ha * T::HA) * (T::BN + 4) + col);
+                    const f32x4 z = acc[ha][hb][i][j];
+                    f32x4 v;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float z = acc[ha][hb][i][j][r];
-                        float v = fmaf(exp2_fast(fmaf(z, c2, -c.lse2)), c.rq, -c.ru);
-                        if constexpr (TG) v -= w[r];
-                        else v -= lab == col + r ? c.rp : 0.0f;
-                        if (a.cap > 0.0f) v *= fmaf(-z * inv_cap, z * inv_cap, 1.0f);
-                        acc[ha][hb][i][j][r] = live && col + r < vr ? v : 0.0f;
+                    for (int r = 0; r < 4; ++r) v[r] = fmaf(exp2_fast(fmaf(z[r], c2, -c.lse2)), c.rq, -c.ru);
+                    if constexpr (TG) {
+                        v -= *(const f32x4 __attribute__((address_space(3)))*)(
+                            (float __attribute__((address_space(3)))*)smem + (row - ha * T::HA) * (T::BN + 4) + col);
+                    } else {
+                        const int d = lab - col;
+                        if ((unsigned)d < 4u) {   // (rarely taken by any lane)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) v[r] -= d == r ? c.rp : 0.0f;
+                        }
                     }
+                    if (a.cap > 0.0f) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[r] *= fmaf(-z[r] * inv_cap, z[r] * inv_cap, 1.0f);
+                    }
+                    acc[ha][hb][i][j] = v;
                 }
+            __builtin_amdgcn_sched_barrier(0);   // one row of fragments at a time keeps the registers within bounds
         }
+    }
+    if (vr < T::BN) {   // columns past the vocabulary
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+            for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool in = at.col(hb, j) + r < vr;
+#pragma unroll
+                    for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+                        for (int i = 0; i < T::FM; ++i) acc[ha][hb][i][j][r] = in ? acc[ha][hb][i][j][r] : 0.0f;
+                }
     }
     if constexpr (TG) __syncthreads();
     if (a.dbp != nullptr) {
@@ -905,6 +1029,32 @@ __global__ __launch_bounds__(T::NT) void loss_grad_kernel(LossArgs a) {
     }
 }
 
+// How dX's product over a piece is cut: its tiles are few where the live rows
+// or the features are, so the vocabulary steps are split over workgroups, each
+// split with a partial dX of its own.  Counted in steps of a workgroup, with
+// what a tile costs besides its steps (filling and draining the pipeline,
+// writing and summing the partial) taken as 8 of them: the cheapest of the
+// whole numbers of splits that give at most two rounds of workgroups.
+struct DxCut {
+    int tm, tk, splits;
+};
+__device__ __forceinline__ DxCut dx_cut(int n, int K, int Vp, int tile, int slots) {
+    DxCut c;
+    c.tm = (n + tile - 1) / tile;
+    c.tk = (K + tile - 1) / tile;
+    const int tiles = max(1, c.tm * c.tk), all = Vp >> 6;
+    c.splits = 1;
+    int best = ((tiles + slots - 1) / slots) * (all + 8);
+    for (int s = 2; s * tiles <= 2 * slots && s * 4 <= all; ++s) {
+        const int cost = ((tiles * s + slots - 1) / slots) * ((all + s - 1) / s + 8);
+        if (cost < best) {
+            best = cost;
+            c.splits = s;
+        }
+    }
+    return c;
+}
+
 // dX partials: [split] (+)= G(piece) . W(piece), a split's share of the
 // vocabulary steps.
 template <class T>
@@ -913,11 +1063,13 @@ __global__ __launch_bounds__(T::NT) void loss_dx_kernel(LossArgs a) {
     lds_t* smem = (lds_t*)raw;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = a.hdr->n;
+    const DxCut cut = dx_cut(n, a.K, a.Vp, T::BM, a.slots);
     int tm, tn, split;
-    if (!map_tile(blockIdx.x, (n + T::BM - 1) / T::BM, (a.K + T::BN - 1) / T::BN, tm, tn, split, a.splits)) return;
+    if (!map_tile(blockIdx.x, cut.tm, cut.tk, tm, tn, split, cut.splits)) return;
     const int m0 = tm * T::BM, k0 = tn * T::BN;
     const int all = (a.vn + 63) >> 6;
-    const int s0 = split * a.steps_per_split, steps = max(0, min(a.steps_per_split, all - s0));
+    const int per = (all + cut.splits - 1) / cut.splits;
+    const int s0 = min(split * per, all), steps = min(per, all - s0);
     Operand<T::HA, false, T::IA, T::NW> A;
     Operand<T::HB, true, T::IB, T::NW> B;
     A.init(a.G + (int64_t)m0 * a.Vp + s0 * 64, a.Vp, T::BM, steps, 0, wave, lane);
@@ -926,7 +1078,7 @@ __global__ __launch_bounds__(T::NT) void loss_dx_kernel(LossArgs a) {
     Acc<T> acc;
     main_loop<T>(A, B, steps, smem, wave, lane, acc);
     const Place<T> at(wave, lane);
-    float* P = a.dxp + ((int64_t)split * a.Mr + m0) * a.Kp + k0;
+    float* P = a.dxp + ((int64_t)split * cut.tm * T::BM + m0) * a.Kp + k0;
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
@@ -943,16 +1095,17 @@ __global__ __launch_bounds__(T::NT) void loss_dx_kernel(LossArgs a) {
 }
 
 // dX = gref unit scale (sum of the partials), in the rows' own places.
-__global__ __launch_bounds__(256) void loss_dx_finish_kernel(LossArgs a, float mul) {
-    const int c = blockIdx.x;
-    if (c >= a.hdr->n) return;
+__global__ __launch_bounds__(256) void loss_dx_finish_kernel(LossArgs a, float mul, int tile) {
+    const int c = blockIdx.x, n = a.hdr->n;
+    if (c >= n) return;
+    const DxCut cut = dx_cut(n, a.K, a.Vp, tile, a.slots);
     const int64_t m = a.map[c];
     const float f = mul * a.hdr->gref;
-    const int64_t sp = (int64_t)a.Mr * a.Kp;
+    const int64_t sp = (int64_t)cut.tm * tile * a.Kp;
     for (int k = threadIdx.x * 4; k < a.K; k += 1024) {
         const float* p = a.dxp + (int64_t)c * a.Kp + k;
         f32x4 v = *(const f32x4*)p;
-        for (int s = 1; s < a.splits; ++s) v += *(const f32x4*)(p + s * sp);
+        for (int s = 1; s < cut.splits; ++s) v += *(const f32x4*)(p + s * sp);
         v *= f;
         if (a.grad_f32) {
             float* d = (float*)a.dX + m * a.lddx + k;
@@ -1126,7 +1279,8 @@ hipError_t launch_loss_grad(const LossArgs& a, int tile, hipStream_t st) {
 
 hipError_t launch_loss_dx(const LossArgs& a, int tile, hipStream_t st) {
     const int b = loss_tile_rows(tile);
-    const dim3 grid((unsigned)(up(a.M, b) * up(a.K, b) * a.splits));
+    // (at most two rounds, or one workgroup a tile)
+    const dim3 grid((unsigned)std::max<int64_t>(up(a.M, b) * up(a.K, b), 2 * a.slots));
     if (tile == LT_256) {
         using T = L256<false, true>;
         return launch_kernel(loss_dx_kernel<T>, grid, dim3(T::NT), st, a);
@@ -1135,8 +1289,9 @@ hipError_t launch_loss_dx(const LossArgs& a, int tile, hipStream_t st) {
     return launch_kernel(loss_dx_kernel<T>, grid, dim3(T::NT), st, a);
 }
 
-hipError_t launch_loss_dx_finish(const LossArgs& a, hipStream_t st) {
-    return launch_kernel(loss_dx_finish_kernel, dim3((unsigned)a.M), dim3(256), st, a, unit_of(a) * a.scale);
+hipError_t launch_loss_dx_finish(const LossArgs& a, int tile, hipStream_t st) {
+    return launch_kernel(loss_dx_finish_kernel, dim3((unsigned)a.M), dim3(256), st, a, unit_of(a) * a.scale,
+                         loss_tile_rows(tile));
 }
 
 hipError_t launch_loss_dw(const LossArgs& a, int tile, hipStream_t st) {

@@ -38,7 +38,7 @@ constexpr int64_t kPieceBytes = int64_t(256) << 20;   // G of one piece
 struct Layout {
     int tile = LT_256, rows = 256;
     int64_t Mr = 0, Kp = 0, Vp = 0, kp = 1, ntiles = 0;
-    int pieces = 1, splits = 1;
+    int pieces = 1, slots = 256;
     bool pack_w = false;
     size_t hdr = 0, map = 0, live = 0, xc = 0, ids = 0, wts = 0, rws = 0, part = 0, sumz = 0, zt = 0, g = 0, dxp = 0, dbp = 0,
            w = 0, bytes = 0;
@@ -78,11 +78,12 @@ Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int6
         l.Vp = round_up(ceil_div(V, l.pieces), 256);
         l.pieces = (int)ceil_div(V, l.Vp);
         l.g = take(2 * l.Mr * l.Vp);
-        // dX: enough splits of a piece's vocabulary steps to fill the device
-        const int64_t tiles = std::max<int64_t>(1, ceil_div(M, l.rows) * ceil_div(K, l.rows));
-        const int64_t slots = l.tile == LT_256 ? 256 : 512;
-        l.splits = (int)std::max<int64_t>(1, std::min<int64_t>(slots / tiles, ceil_div(l.Vp, 64) / 4));
-        l.dxp = take(4 * l.splits * l.Mr * l.Kp);
+        // dX: one partial, or splits of at most two rounds of tiles and at
+        // least four vocabulary steps each
+        l.slots = l.tile == LT_256 ? 256 : 512;
+        const int64_t one = l.Mr * l.Kp, steps = l.Vp / 64;
+        const int64_t split = std::min<int64_t>(2 * l.slots * l.rows * l.rows, std::max<int64_t>(1, steps / 4) * one);
+        l.dxp = take(4 * std::max(one, split));
         l.dbp = take(4 * ceil_div(std::max<int64_t>(M, 1), l.rows) * l.Vp);
     }
     l.bytes = at;
@@ -263,7 +264,7 @@ int run(const Call& c) {
     if (c.M > 0)
         if ((rc = go(LL_GATHER, 0.0, 4.0 * m * k + target_bytes, [&] { return launch_loss_gather(a, true, st); })) != MKP_OK)
             return rc;
-    a.splits = l.splits;
+    a.slots = l.slots;
     for (int p = 0; p < l.pieces; ++p) {
         a.v0 = (int)(p * l.Vp);
         a.vn = (int)std::min<int64_t>(l.Vp, c.V - a.v0);
@@ -273,9 +274,8 @@ int run(const Call& c) {
                          [&] { return launch_loss_grad(a, l.tile, st); })) != MKP_OK)
                 return rc;
         if (c.dX && c.M > 0) {
-            a.steps_per_split = (int)ceil_div(ceil_div(a.vn, 64), l.splits);
             a.first = p == 0;
-            if ((rc = go(LL_DX, 2.0 * m * pv * k, elem * (pv * k + m * pv) + (p ? 8.0 : 4.0) * m * k * l.splits,
+            if ((rc = go(LL_DX, 2.0 * m * pv * k, elem * (pv * k + m * pv) + (p ? 8.0 : 4.0) * m * k,
                          [&] { return launch_loss_dx(a, l.tile, st); })) != MKP_OK)
                 return rc;
         }
@@ -289,7 +289,7 @@ int run(const Call& c) {
                 return rc;
     }
     if (c.dX && c.M > 0)
-        return go(LL_DX_FINISH, 0.0, (4.0 * l.splits + gb) * m * k, [&] { return launch_loss_dx_finish(a, st); });
+        return go(LL_DX_FINISH, 0.0, (4.0 + gb) * m * k, [&] { return launch_loss_dx_finish(a, l.tile, st); });
     return MKP_OK;
 }
 
