@@ -16,6 +16,7 @@ namespace mkp {
 struct LossHeader {
     int n;          // rows that carry a target ("live"), compacted to the front
     float gref;     // backward: the largest |dloss| of a live row (1 if that is 0 or not finite)
+    int splits;     // backward: partials of dX
 };
 
 // One live row's constants in the gradient (compact order):
@@ -36,6 +37,9 @@ struct LossArgs {
     int Kw;                 // W's columns: K (a multiple of 8), or Kp for the padded copy
     const float* bias;      // V values or null
     float scale, cap, T;
+    bool plain;             // z = scale x.w with scale > 0: the kernels keep x.w instead of z
+    float s2;               // from what they keep to the base-2 logit, log2(e) z / T
+    bool direct;            // forward on few aligned rows: X and targets as the caller has them
     // cross entropy
     const int64_t* labels;  // M, or null for distillation
     float smoothing, z_loss;
@@ -60,18 +64,20 @@ struct LossArgs {
     // workspace
     LossHeader* hdr;
     int* map;               // compact row -> row
+    int* pos;               // row -> compact row (calls of many rows)
     uint8_t* live;          // M (distillation)
     uint16_t* Xc;           // live rows of X, Mr x Kp, zero padded
     int* ids32;             // compact, n x kp: the targets (-1: none)
     float* wts;             // compact, n x kp: their weights in the gradient
     LossRow* rows;          // compact
     float* part;            // forward: per (row, vocabulary tile) maximum and sum of exponentials
-    float* sumz;            // forward with smoothing: per (row, vocabulary tile) sum of z
-    float* zt;              // forward: the targets' z, compact n x kp
+    float* sumz;            // forward with smoothing: per (row, vocabulary tile, wave column) sum of kept values
+    float* zt;              // forward: the targets' kept values, compact n x kp
     uint16_t* G;            // backward: one piece's gradient by s, Mr x Vp
     float* dxp;             // backward: dX partials, [splits][rows of live tiles][Kp]
     float* dbp;             // backward: per row tile, sums of G's columns
     int Mr, Kp, Vp, kp;     // padded extents
+    int tile;               // rows and columns of the tile kernels' tiles: 256 or 128
     int ntiles;             // vocabulary tiles of the forward pass
     // the piece of the vocabulary a backward launch works on
     int v0, vn;
@@ -79,20 +85,18 @@ struct LossArgs {
     bool first;             // dX partials are written, not added to
 };
 
-// Tile configuration of the large kernels.
-enum LossTile : int { LT_256 = 0, LT_128 = 1 };
-int loss_tile_rows(int tile);    // tile height = tile width
+// Partial sums of z per row and tile (LossArgs::sumz).
+int loss_sumz_parts(int tile);
 
 // Launches; each returns the launch's status.
-hipError_t launch_loss_flags(const LossArgs& a, hipStream_t st);               // distillation: live
-hipError_t launch_loss_scan(const LossArgs& a, hipStream_t st);                // hdr, map
-hipError_t launch_loss_gather(const LossArgs& a, bool backward, hipStream_t st);   // Xc, targets, rows
-hipError_t launch_loss_forward(const LossArgs& a, int tile, hipStream_t st);   // part, sumz, zt
-hipError_t launch_loss_finish(const LossArgs& a, bool compact, hipStream_t st);    // loss, lse
-hipError_t launch_loss_grad(const LossArgs& a, int tile, hipStream_t st);      // G (and dbp) of a piece
-hipError_t launch_loss_dx(const LossArgs& a, int tile, hipStream_t st);        // dxp of a piece
-hipError_t launch_loss_dx_finish(const LossArgs& a, int tile, hipStream_t st);  // dX
-hipError_t launch_loss_dw(const LossArgs& a, int tile, hipStream_t st);        // dW of a piece
-hipError_t launch_loss_dbias(const LossArgs& a, int row_tile, hipStream_t st); // dbias of a piece
+hipError_t launch_loss_flags(const LossArgs& a, hipStream_t st);       // distillation: live
+hipError_t launch_loss_scan(const LossArgs& a, hipStream_t st);        // hdr, pos (calls of many rows)
+hipError_t launch_loss_gather(const LossArgs& a, bool scanned, hipStream_t st);   // hdr, map, Xc, targets, rows
+hipError_t launch_loss_forward(const LossArgs& a, hipStream_t st);     // part, sumz, zt
+hipError_t launch_loss_finish(const LossArgs& a, hipStream_t st);      // loss, lse
+hipError_t launch_loss_grad(const LossArgs& a, hipStream_t st);        // G (and dbp) of a piece
+hipError_t launch_loss_products(const LossArgs& a, hipStream_t st);    // dxp and dW of a piece
+hipError_t launch_loss_dx_finish(const LossArgs& a, hipStream_t st);   // dX
+hipError_t launch_loss_dbias(const LossArgs& a, hipStream_t st);       // dbias of a piece
 
 }  // namespace mkp

@@ -31,6 +31,7 @@ namespace mkp {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -51,6 +52,20 @@ hipError_t launch_kernel(F kernel, dim3 grid, dim3 block, hipStream_t st, Args..
         hipLaunchKernelGGL(kernel, grid, block, 0, st, args...);
     }
     return hipGetLastError();
+}
+
+// A product rounded by itself, never part of a fused multiply-add.
+__device__ __forceinline__ float mul_rn(float a, float b) {
+#pragma clang fp contract(off)
+    return a * b;
+}
+
+// The base-2 value that the row's (lane's, tile's) exponentials are taken
+// relative to, from its largest u; 0 where even that is -inf in base 2, so
+// that every exponential there is 0 and none is NaN.
+__device__ __forceinline__ float stat_base(float umax, float s2) {
+    const float b = mul_rn(umax, s2);
+    return b == -INFINITY ? 0.0f : b;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -394,87 +409,104 @@ __device__ __forceinline__ bool map_tile(int bid, int tm_n, int tn_n, int& tm, i
 
 // ---- the logits of a tile ---------------------------------------------------
 
-// acc (x.w) -> z in place.
+// A lane's 16 bias values (0 without a bias).
 template <class T>
-__device__ __forceinline__ void to_logits(Acc<T>& acc, const LossArgs& a, const Place<T>& at, int v_tile) {
-    if (a.bias != nullptr) {
+struct BiasRegs {
+    f32x4 b[2][T::FN];
+    __device__ __forceinline__ BiasRegs(const LossArgs& a, const Place<T>& at, int v_tile) {
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-            for (int j = 0; j < T::FN; ++j) {
-                f32x4 b;
+            for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) b[r] = a.bias[min(v_tile + at.col(hb, j) + r, a.V - 1)];
-#pragma unroll
-                for (int ha = 0; ha < 2; ++ha)
-#pragma unroll
-                    for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            acc[ha][hb][i][j][r] = fmaf(a.scale, acc[ha][hb][i][j][r], b[r]);
-            }
-    } else if (a.scale != 1.0f) {
-#pragma unroll
-        for (int ha = 0; ha < 2; ++ha)
-#pragma unroll
-            for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-                for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-                    for (int j = 0; j < T::FN; ++j) acc[ha][hb][i][j] *= a.scale;
+                for (int r = 0; r < 4; ++r)
+                    b[hb][j][r] = a.bias != nullptr ? a.bias[min(v_tile + at.col(hb, j) + r, a.V - 1)] : 0.0f;
     }
+};
+
+// One row of fragments: acc (x.w) -> z in place.
+template <class T>
+__device__ __forceinline__ void row_logits(const LossArgs& a, const BiasRegs<T>& bias, float inv_cap, Acc<T>& acc, int ha,
+                                           int i) {
+#pragma unroll
+    for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                acc[ha][hb][i][j][r] = fmaf(a.scale, acc[ha][hb][i][j][r], bias.b[hb][j][r]);
     if (a.cap > 0.0f) {
-        const float inv = 1.0f / a.cap;
 #pragma unroll
-        for (int ha = 0; ha < 2; ++ha)
+        for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-            for (int i = 0; i < T::FM; ++i) {
+            for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-                for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-                    for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            acc[ha][hb][i][j][r] = a.cap * tanh_fast(acc[ha][hb][i][j][r] * inv);
-                __builtin_amdgcn_sched_barrier(0);   // (a row of fragments at a time, or the registers spill)
-            }
+                for (int r = 0; r < 4; ++r)
+                    acc[ha][hb][i][j][r] = a.cap * tanh_fast(acc[ha][hb][i][j][r] * inv_cap);
     }
 }
 
-// The tile's product X . W^T, as logits z.
+// The tile's product X . W^T, from the compacted rows or (direct: few rows,
+// nothing dropped) the caller's.
 template <class T>
-__device__ __forceinline__ void logits_tile(const LossArgs& a, int m0, int v_tile, lds_t* smem, int wave, int lane,
+__device__ __forceinline__ void logits_tile(const LossArgs& a, int m0, int v_tile, int n, lds_t* smem, int wave, int lane,
                                             Acc<T>& acc) {
     const int steps = (a.Kw + 63) >> 6;
+    const uint16_t* X = a.direct ? a.X : a.Xc;
+    const int64_t ldx = a.direct ? a.ldx : a.Kp;
     Operand<T::HA, false, T::IA, T::NW> A;
     Operand<T::HB, false, T::IB, T::NW> B;
-    A.init(a.Xc + (int64_t)m0 * a.Kp, a.Kp, T::BM, steps, 0, wave, lane);
+    A.init(X + (int64_t)m0 * ldx, ldx, n - m0, steps, 0, wave, lane);
     B.init(a.W + (int64_t)v_tile * a.ldw, a.ldw, a.V - v_tile, steps, a.Kw & 63, wave, lane);
     main_loop<T>(A, B, steps, smem, wave, lane, acc);
-    to_logits<T>(acc, a, Place<T>(wave, lane), v_tile);
+}
+
+// Compact row m's label (forward: the caller's where nothing is compacted).
+__device__ __forceinline__ int row_label(const LossArgs& a, int m, int n) {
+    if (m >= n) return -1;
+    if (!a.direct) return a.ids32[m];
+    const int64_t y = a.labels[m];
+    return y >= 0 && y < a.V ? (int)y : -1;
 }
 
 // ---- forward ----------------------------------------------------------------
 
-// Statistics of one logit tile.  TG: the targets' z are picked from the tile
-// staged in LDS, half its rows at a time (several targets a row); else each
-// lane compares its columns with the row's one label.
+// Statistics of one logit tile.  TG: the targets' values are picked from the
+// tile staged in LDS, half its rows at a time (several targets a row); else
+// each lane compares its columns with the row's one label.
+//
+// Kept are u = x.w with y = u s2 the logit in base 2, or, where a bias, a cap
+// or a scale below 0 asks for it, u = z (a.plain tells which): per row the
+// largest u and the sum of 2^(y - fl(umax s2)).  The subtraction is part of
+// the fused multiply, so an exponent keeps its digits, and what rounding umax
+// s2 loses is put back where the tiles are joined.  A lane reduces its own 16
+// values of a row; the 4 lanes and the waves that share the row meet in LDS.
 template <class T, bool TG>
 __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
     constexpr int TAB = TG ? T::HA * (T::BN + 4) * 4 : 0;
-    constexpr int RED = 3 * T::WGN * T::BM * 4;
+    constexpr int PARTS = 4 * T::WGN, LDP = 2 * PARTS + 2;   // floats per row
+    constexpr int RED = T::BM * LDP * 4;
     constexpr int NEED = TAB > RED ? TAB : RED;
     __shared__ __attribute__((aligned(1024))) unsigned char raw[T::LDS > NEED ? T::LDS : NEED];
     lds_t* smem = (lds_t*)raw;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n = a.hdr->n;
+    const int n = a.direct ? (int)a.M : a.hdr->n;
     int tm, tn, rest;
     if (!map_tile(blockIdx.x, (n + T::BM - 1) / T::BM, a.ntiles, tm, tn, rest, 1)) return;
     const int m0 = tm * T::BM, v0 = tn * T::BN;
     Acc<T> acc;
-    logits_tile<T>(a, m0, v0, smem, wave, lane, acc);
+    logits_tile<T>(a, m0, v0, n, smem, wave, lane, acc);
     const Place<T> at(wave, lane);
     const int vr = a.V - v0;   // valid columns
+    const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
+    const BiasRegs<T> bias(a, at, v0);
+    int labs[2][T::FM];
+    if constexpr (!TG) {
+#pragma unroll
+        for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) labs[ha][i] = row_label(a, m0 + at.row(ha, i), n) - v0 - at.wn * T::FN * 16;
+    }
     if constexpr (TG) {
         float __attribute__((address_space(3)))* tab = (float __attribute__((address_space(3)))*)smem;
         constexpr int LD = T::BN + 4;
@@ -482,39 +514,64 @@ __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
         for (int ha = 0; ha < 2; ++ha) {
             if (ha) __syncthreads();
 #pragma unroll
-            for (int hb = 0; hb < 2; ++hb)
+            for (int i = 0; i < T::FM; ++i) {
+                if (!a.plain) row_logits<T>(a, bias, inv_cap, acc, ha, i);
 #pragma unroll
-                for (int i = 0; i < T::FM; ++i)
+                for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
                     for (int j = 0; j < T::FN; ++j)
                         *(f32x4 __attribute__((address_space(3)))*)(tab + (at.row(ha, i) - ha * T::HA) * LD +
                                                                     at.col(hb, j)) = acc[ha][hb][i][j];
+                __builtin_amdgcn_sched_barrier(0);
+            }
             __syncthreads();
             constexpr int PER = T::NT / T::HA;   // threads per row
             const int r = tid / PER, m = m0 + ha * T::HA + r;
             if (m < n) {
-                const int* ids = a.ids32 + (int64_t)m * a.kp;
-                for (int q = (tid % PER) * 4; q < a.kp; q += PER * 4) {
-                    const int4 id = *(const int4*)(ids + q);
-                    const int c[4] = {id.x - v0, id.y - v0, id.z - v0, id.w - v0};
+                if (a.direct) {
+                    const int64_t* ids = a.ids + (int64_t)m * a.ldids;
+                    for (int q = tid % PER; q < a.k; q += PER) {
+                        const int64_t c = ids[q] - v0;
+                        if (c >= 0 && c < T::BN && c < vr) a.zt[(int64_t)m * a.kp + q] = tab[r * LD + (int)c];
+                    }
+                } else {
+                    const int* ids = a.ids32 + (int64_t)m * a.kp;
+                    for (int q = (tid % PER) * 4; q < a.kp; q += PER * 4) {
+                        const int4 id = *(const int4*)(ids + q);
+                        const int c[4] = {id.x - v0, id.y - v0, id.z - v0, id.w - v0};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if ((unsigned)c[e] < (unsigned)T::BN)
-                            a.zt[(int64_t)m * a.kp + q + e] = tab[r * LD + c[e]];
+                        for (int e = 0; e < 4; ++e)
+                            if ((unsigned)c[e] < (unsigned)T::BN)
+                                a.zt[(int64_t)m * a.kp + q + e] = tab[r * LD + c[e]];
+                    }
                 }
             }
         }
         __syncthreads();
     }
-    // per row: maximum, sum of 2^((z - maximum) c), and sum of z where asked for
-    const float c2 = kLog2e / a.T;
+    const float s2 = a.s2;
     const bool smooth = a.sumz != nullptr;
     float __attribute__((address_space(3)))* red = (float __attribute__((address_space(3)))*)smem;
-    if (smooth) {
 #pragma unroll
-        for (int ha = 0; ha < 2; ++ha)
+    for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
-            for (int i = 0; i < T::FM; ++i) {
+        for (int i = 0; i < T::FM; ++i) {
+            const int row = at.row(ha, i);
+            if constexpr (!TG) {
+                if (!a.plain) row_logits<T>(a, bias, inv_cap, acc, ha, i);
+                // (the wave's columns are two runs of FN * 16; rarely any lane's label is among them)
+                if ((unsigned)(labs[ha][i] % T::HB) < (unsigned)(T::FN * 16) && (unsigned)labs[ha][i] < (unsigned)T::BN) {
+#pragma unroll
+                    for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                        for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (labs[ha][i] == hb * T::HB + j * 16 + at.g * 4 + r)
+                                    a.zt[m0 + row] = acc[ha][hb][i][j][r];
+                }
+            }
+            if (smooth) {
                 float sz = 0.0f;
 #pragma unroll
                 for (int hb = 0; hb < 2; ++hb)
@@ -524,43 +581,18 @@ __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
                         for (int r = 0; r < 4; ++r) sz += at.col(hb, j) + r < vr ? acc[ha][hb][i][j][r] : 0.0f;
                 sz += __shfl_xor(sz, 16);
                 sz += __shfl_xor(sz, 32);
-                if (at.g == 0) red[(2 * T::WGN + at.wn) * T::BM + at.row(ha, i)] = sz;
-                __builtin_amdgcn_sched_barrier(0);
+                // (one value a row and wave, kept apart from the partials below)
+                if (at.g == 0 && m0 + row < n)
+                    a.sumz[((int64_t)(m0 + row) * a.ntiles + tn) * T::WGN + at.wn] = sz;
             }
-    }
-    if (vr < T::BN) {
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-            for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const bool in = at.col(hb, j) + r < vr;
-#pragma unroll
-                    for (int ha = 0; ha < 2; ++ha)
-#pragma unroll
-                        for (int i = 0; i < T::FM; ++i)
-                            acc[ha][hb][i][j][r] = in ? acc[ha][hb][i][j][r] : -INFINITY;
-                }
-    }
-#pragma unroll
-    for (int ha = 0; ha < 2; ++ha)
-#pragma unroll
-        for (int i = 0; i < T::FM; ++i) {
-            const int row = at.row(ha, i);
-            if constexpr (!TG) {
-                const int m = m0 + row;
-                const int lab = (m < n ? a.ids32[m] : -1) - v0;
+            if (vr < T::BN) {
 #pragma unroll
                 for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-                    for (int j = 0; j < T::FN; ++j) {
-                        const int d = lab - at.col(hb, j);
-                        if ((unsigned)d < 4u) {
-                            const f32x4 v = acc[ha][hb][i][j];
-                            a.zt[m] = d == 0 ? v[0] : d == 1 ? v[1] : d == 2 ? v[2] : v[3];
-                        }
-                    }
+                    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            acc[ha][hb][i][j][r] = at.col(hb, j) + r < vr ? acc[ha][hb][i][j][r] : -INFINITY;
             }
             float mx = -INFINITY;
 #pragma unroll
@@ -569,129 +601,138 @@ __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
                 for (int j = 0; j < T::FN; ++j)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) mx = fmaxf(mx, acc[ha][hb][i][j][r]);
-            mx = fmaxf(mx, __shfl_xor(mx, 16));
-            mx = fmaxf(mx, __shfl_xor(mx, 32));
-            const float base = mx == -INFINITY ? 0.0f : mx;   // a row of -inf only: a sum of zeros
+            const float base = stat_base(mx, s2);
             float sm = 0.0f;
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
                 for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) sm += exp2_fast((acc[ha][hb][i][j][r] - base) * c2);
-            sm += __shfl_xor(sm, 16);
-            sm += __shfl_xor(sm, 32);
-            if (at.g == 0) {
-                red[(0 * T::WGN + at.wn) * T::BM + row] = mx;
-                red[(1 * T::WGN + at.wn) * T::BM + row] = sm;
-            }
+                    for (int r = 0; r < 4; ++r) sm += exp2_fast(fmaf(acc[ha][hb][i][j][r], s2, -base));
+            *(f32x2 __attribute__((address_space(3)))*)(red + row * LDP + (at.wn * 4 + at.g) * 2) = f32x2{mx, sm};
             __builtin_amdgcn_sched_barrier(0);   // one row of fragments at a time keeps the registers within bounds
         }
     __syncthreads();
     for (int row = tid; row < T::BM; row += T::NT) {
         const int m = m0 + row;
         if (m >= n) continue;
-        float mx = -INFINITY, sm = 0.0f, sz = 0.0f;
+        f32x2 p[PARTS];
+        float mx = -INFINITY, sm = 0.0f;
 #pragma unroll
-        for (int w = 0; w < T::WGN; ++w) mx = fmaxf(mx, red[w * T::BM + row]);
-        const float base = mx == -INFINITY ? 0.0f : mx;
-#pragma unroll
-        for (int w = 0; w < T::WGN; ++w) {
-            const float mw = red[w * T::BM + row];
-            sm += red[(T::WGN + w) * T::BM + row] * exp2_fast((mw - base) * c2);
-            if (smooth) sz += red[(2 * T::WGN + w) * T::BM + row];
+        for (int w = 0; w < PARTS; ++w) {
+            p[w] = *(const f32x2 __attribute__((address_space(3)))*)(red + row * LDP + w * 2);
+            mx = fmaxf(mx, p[w].x);
         }
+        const float base = stat_base(mx, s2);
+#pragma unroll
+        for (int w = 0; w < PARTS; ++w) sm += p[w].y * exp2_fast(mul_rn(p[w].x, s2) - base);
         *(float2*)(a.part + ((int64_t)m * a.ntiles + tn) * 2) = make_float2(mx, sm);
-        if (smooth) a.sumz[(int64_t)m * a.ntiles + tn] = sz;
     }
 }
 
-// Join a row's tiles: one wave per row.
-//   lse = max / T + log sum; a row without any finite logit has lse -inf
+// Sum and maximum over the workgroup's 256 threads.
+__device__ __forceinline__ float block_sum(float v, float* buf) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (buf[0] + buf[1]) + (buf[2] + buf[3]);
+}
+__device__ __forceinline__ float block_max(float v, float* buf) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return fmaxf(fmaxf(buf[0], buf[1]), fmaxf(buf[2], buf[3]));
+}
+
+__device__ __forceinline__ bool target_ok(const LossArgs& a, int64_t m, int j) {
+    const int64_t id = a.ids[m * a.ldids + j];
+    return id >= 0 && id < a.V && a.teacher[m * a.ldt + j] * (1.0f / a.T) != -INFINITY;
+}
+
+// Join a row's tiles, one workgroup per row.  With s2 the factor to base 2:
+//   lse = ln2 (umax s2 + log2 sum); a row without any finite logit has -inf
 //   cross entropy: lse - (1 - e) z_y - e / V sum z + c lse^2
 //   distillation:  T^2 sum_j p_j (log p_j - (z_j / T - lse))
-// The differences from z are taken to the maximum first and the logarithm
+// The differences from the targets are taken to umax first and the logarithm
 // added last: a label that is nearly certain has a small loss, and rounding
 // lse before the difference would leave it few digits.
-// Rows without a target get 0.  With COMPACT rows are looked up through the
-// map (every row's results were cleared by the gather kernel).
-template <bool COMPACT>
-__global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t c = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (c >= (COMPACT ? (int64_t)a.hdr->n : a.M)) return;
-    const int64_t m = COMPACT ? (int64_t)a.map[c] : c;
+__global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a, int wgn) {
+    __shared__ float buf[4];
+    const int tid = threadIdx.x;
+    const int64_t c = blockIdx.x;
+    if (!a.direct && c >= (int64_t)a.hdr->n) return;   // (rows without a target were cleared by the gather kernel)
+    const int64_t m = a.direct ? c : (int64_t)a.map[c];
     const float* part = a.part + c * a.ntiles * 2;
+    const float s2 = a.s2;
     float mx = -INFINITY;
-    for (int t = lane; t < a.ntiles; t += 64) mx = fmaxf(mx, part[2 * t]);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    const float c2 = kLog2e / a.T, it = 1.0f / a.T;
+    for (int t = tid; t < a.ntiles; t += 256) mx = fmaxf(mx, part[2 * t]);
+    mx = block_max(mx, buf);
+    const float base = stat_base(mx, s2);
     float sm = 0.0f, sz = 0.0f;
-    for (int t = lane; t < a.ntiles; t += 64) {
-        sm += part[2 * t + 1] * exp2_fast((part[2 * t] - base) * c2);
-        if (a.sumz) sz += a.sumz[c * a.ntiles + t];
+    for (int t = tid; t < a.ntiles; t += 256) sm += part[2 * t + 1] * exp2_fast(mul_rn(part[2 * t], s2) - base);
+    if (a.sumz != nullptr) {
+        for (int t = tid; t < a.ntiles * wgn; t += 256) sz += a.sumz[c * a.ntiles * wgn + t];
+        sz = block_sum(sz, buf);
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        sm += __shfl_xor(sm, o);
-        sz += __shfl_xor(sz, o);
-    }
-    const float ls = kLn2 * __builtin_amdgcn_logf(sm);
-    const float lse = fmaf(base, it, ls);
+    sm = block_sum(sm, buf);
+    // log2 of the sum over 2^(umax s2): what rounding base lost, put back
+    const float top = mul_rn(mx, s2) == -INFINITY ? 0.0f : mx;
+    const float l2 = __builtin_amdgcn_logf(sm) + fmaf(-top, s2, base);
+    const float lse = kLn2 * fmaf(top, s2, l2);
+    const float uz = a.plain ? a.scale : 1.0f;   // u to z
     if (a.labels != nullptr) {
         const int64_t y = a.labels[m];
         const bool live = y >= 0 && y < a.V;
-        if (lane == 0) {
-            float v = (base - a.zt[c]) + ls + (a.smoothing > 0.0f ? a.smoothing * (a.zt[c] - sz / (float)a.V) : 0.0f) +
-                      (a.z_loss != 0.0f ? a.z_loss * lse * lse : 0.0f);
-            if (a.zt[c] == -INFINITY) v = INFINITY;   // the label is masked out, whatever else is
+        if (tid == 0) {
+            const float u = live ? a.zt[c] : 0.0f;
+            float v = kLn2 * fmaf(top - u, s2, l2);
+            if (a.smoothing > 0.0f) v += a.smoothing * uz * (u - sz / (float)a.V);
+            if (a.z_loss != 0.0f) v += a.z_loss * lse * lse;
+            if (u * s2 == -INFINITY) v = INFINITY;   // the label is masked out, whatever else is
             a.loss[m] = live ? v : 0.0f;
             a.lse[m] = live ? lse : 0.0f;
         }
         return;
     }
-    // distillation (always compact): the teacher's log-partition over the row
+    // the teacher's log-partition over the row
+    const float it = 1.0f / a.T;
     const float* t = a.teacher + m * a.ldt;
-    const int* ids = a.ids32 + c * a.kp;
+    float any = 0.0f, tm = -INFINITY, ts = 0.0f;
+    for (int j = tid; j < a.k; j += 256)
+        if (target_ok(a, m, j)) {
+            any = 1.0f;
+            tm = fmaxf(tm, t[j] * it);
+        }
+    any = block_max(any, buf);
     float tl;
     if (a.teacher_lse != nullptr) {
         tl = a.teacher_lse[m];
     } else {
-        float tm = -INFINITY, ts = 0.0f;
-        for (int j = lane; j < a.k; j += 64)
-            if (ids[j] >= 0) tm = fmaxf(tm, t[j] * it);
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) tm = fmaxf(tm, __shfl_xor(tm, o));
-        for (int j = lane; j < a.k; j += 64)
-            if (ids[j] >= 0) ts += exp2_fast(kLog2e * (t[j] * it - tm));
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) ts += __shfl_xor(ts, o);
-        tl = tm + kLn2 * __builtin_amdgcn_logf(ts);
+        tm = block_max(tm, buf);
+        for (int j = tid; j < a.k; j += 256)
+            if (target_ok(a, m, j)) ts += exp2_fast(kLog2e * (t[j] * it - tm));
+        tl = tm + kLn2 * __builtin_amdgcn_logf(block_sum(ts, buf));
     }
     float kl = 0.0f;
-    for (int j = lane; j < a.k; j += 64) {
-        if (ids[j] < 0) continue;
+    for (int j = tid; j < a.k; j += 256) {
+        if (!target_ok(a, m, j)) continue;
         const float lp = t[j] * it - tl;
         const float p = exp2_fast(kLog2e * lp);
-        const float z = a.zt[c * a.kp + j];
-        if (p != 0.0f) kl += z == -INFINITY ? INFINITY : p * (lp - ((z - base) * it - ls));
+        const float u = a.zt[c * a.kp + j];
+        if (p != 0.0f) kl += u * s2 == -INFINITY ? INFINITY : p * (lp + kLn2 * fmaf(top - u, s2, l2));
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) kl += __shfl_xor(kl, o);
-    if (lane == 0) {
-        a.loss[m] = a.T * a.T * kl;
-        a.lse[m] = lse;
+    kl = block_sum(kl, buf);
+    if (tid == 0) {
+        a.loss[m] = any != 0.0f ? a.T * a.T * kl : 0.0f;
+        a.lse[m] = any != 0.0f ? lse : 0.0f;
     }
 }
 
 // ---- rows with a target -----------------------------------------------------
-
-__device__ __forceinline__ bool target_ok(const LossArgs& a, int64_t m, int j) {
-    const int64_t id = a.ids[m * a.ldids + j];
-    return id >= 0 && id < a.V && a.teacher[m * a.ldt + j] != -INFINITY;
-}
 
 // Distillation: a row is live when it names a target of the vocabulary whose
 // teacher logit is not -inf.  One wave per row.
@@ -705,110 +746,98 @@ __global__ __launch_bounds__(256) void loss_flags_kernel(LossArgs a) {
     if (lane == 0) a.live[m] = any ? 1 : 0;
 }
 
-// Compact the live rows in order (map), count them, and (backward) find the
-// largest |dloss| among them.  One workgroup, so the order is the rows' own.
-__global__ __launch_bounds__(1024) void loss_scan_kernel(LossArgs a) {
-    __shared__ int wsum[16];
-    __shared__ float wmax[16];
+__device__ __forceinline__ bool row_live(const LossArgs& a, int64_t m) {
+    if (a.labels != nullptr) {
+        const int64_t y = a.labels[m];
+        return y >= 0 && y < a.V;
+    }
+    return a.live[m] != 0;
+}
+
+__device__ __forceinline__ float usable_gref(float g) { return (g > 0.0f && g < INFINITY) ? g : 1.0f; }
+
+// How dX's product over a piece is cut: its tiles are few where the live rows
+// or the features are, so the vocabulary steps are split over workgroups, each
+// split with a partial dX of its own.  In units of one K step of a workgroup,
+// with what a tile costs besides (filling and draining the pipeline, writing
+// and summing a partial) taken as 10: the whole number of splits, of at most
+// two rounds of workgroups and at least four steps each, for which the work
+// of dX's and dW's tiles (they run in one launch) over the workgroups that
+// run at once, and half the longest tile, come out least.  256 threads.
+__device__ __forceinline__ int dx_splits(const LossArgs& a, int n, float* buf) {
+    const int tile = a.tile, tk = (a.K + tile - 1) / tile;
+    const int tiles = max(1, (n + tile - 1) / tile * tk), all = a.Vp >> 6;
+    const float rest = a.dW != nullptr ? (float)((a.Vp + tile - 1) / tile * tk) * ((n + 63) / 64 + 10.0f) : 0.0f;
+    const float rest_one = a.dW != nullptr ? (n + 63) / 64 + 10.0f : 0.0f;
+    float best = -INFINITY;   // minus (cost, then splits), so that a maximum finds it
+    int mine = 1;
+    for (int s = 1 + threadIdx.x; s == 1 || (s * tiles <= 2 * a.slots && s * 4 <= all); s += 256) {
+        const float one = (float)((all + s - 1) / s) + 10.0f;
+        const float work = rest + (float)(tiles * s) * one;
+        const float cost = fmaxf(work / (float)a.slots, fmaxf(one, rest_one)) + 0.5f * fmaxf(one, rest_one);
+        if (-cost > best) {
+            best = -cost;
+            mine = s;
+        }
+    }
+    const float top = block_max(best, buf);
+    return (int)-block_max(best == top ? -(float)mine : -INFINITY, buf);
+}
+
+// For many rows: each row's place among the live ones (pos, -1 without a
+// target), their number, the largest |dloss| and dX's splits.  One workgroup.
+__global__ __launch_bounds__(256) void loss_scan_kernel(LossArgs a) {
+    __shared__ int wsum[4];
+    __shared__ float buf[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int base = 0;
     float g = 0.0f;
-    for (int64_t m0 = 0; m0 < a.M; m0 += 1024) {
+    for (int64_t m0 = 0; m0 < a.M; m0 += 256) {
         const int64_t m = m0 + tid;
-        bool on = false;
-        if (m < a.M) {
-            if (a.labels != nullptr) {
-                const int64_t y = a.labels[m];
-                on = y >= 0 && y < a.V;
-            } else {
-                on = a.live[m] != 0;
-            }
-        }
+        const bool on = m < a.M && row_live(a, m);
         const unsigned long long b = __ballot(on);
         if (lane == 0) wsum[wave] = __popcll(b);
         __syncthreads();
         int before = base, all = 0;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) {
+        for (int w = 0; w < 4; ++w) {
             before += w < wave ? wsum[w] : 0;
             all += wsum[w];
         }
-        if (on) {
-            a.map[before + __popcll(b & ((1ull << lane) - 1ull))] = (int)m;
-            if (a.dloss != nullptr) g = fmaxf(g, fabsf(a.dloss[m]));
-        }
+        if (m < a.M) a.pos[m] = on ? before + __popcll(b & ((1ull << lane) - 1ull)) : -1;
+        if (on && a.dloss != nullptr) g = fmaxf(g, fabsf(a.dloss[m]));
         base += all;
         __syncthreads();
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) g = fmaxf(g, __shfl_xor(g, o));
-    if (lane == 0) wmax[wave] = g;
-    __syncthreads();
-    if (tid == 0) {
-#pragma unroll
-        for (int w = 0; w < 16; ++w) g = fmaxf(g, wmax[w]);
-        a.hdr->n = base;
-        a.hdr->gref = (g > 0.0f && g < INFINITY) ? g : 1.0f;
-    }
+    g = block_max(g, buf);
+    const int splits = a.dloss != nullptr ? dx_splits(a, base, buf) : 1;
+    if (tid == 0) *a.hdr = LossHeader{base, usable_gref(g), splits};
 }
 
-// Workgroup b < M: if it is compact row c = b < n, copies X's row together
-// with its targets; rows n .. the next multiple of 256 are zeroed.  Then, for
-// row m = b of the call, clears what a row without a target gets.
-template <bool BWD>
-__global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int c = blockIdx.x;
-    const int n = a.hdr->n;
-    const int nr = min((n + 255) & ~255, a.Mr);
-    // clear the outputs of rows without a target
-    if (c < a.M) {
-        bool on;
-        if (a.labels != nullptr) {
-            const int64_t y = a.labels[c];
-            on = y >= 0 && y < a.V;
-        } else {
-            on = a.live[c] != 0;
-        }
-        if (!on) {
-            if constexpr (!BWD) {
-                if (tid == 0) a.loss[c] = a.lse[c] = 0.0f;
-            } else if (a.dX != nullptr) {
-                for (int k = tid; k < a.K; k += 256) {
-                    if (a.grad_f32) ((float*)a.dX)[(int64_t)c * a.lddx + k] = 0.0f;
-                    else ((uint16_t*)a.dX)[(int64_t)c * a.lddx + k] = 0;
-                }
-            }
-        }
-    }
-    if (c >= nr) return;
-    const int64_t m = c < n ? (int64_t)a.map[c] : -1;
-    // the row of X, zero padded to Kp columns
+// Copy one row of X to compact row c, zero padded to Kp columns (m < 0: zeros).
+__device__ __forceinline__ void copy_row(const LossArgs& a, int64_t m, int c, int t, int nt) {
     const uint16_t* src = a.X + m * a.ldx;
     uint16_t* dst = a.Xc + (int64_t)c * a.Kp;
-    const bool vec = ((uintptr_t)src & 15) == 0;
-    for (int k = tid * 8; k < a.Kp; k += 2048) {
+    const bool vec = m >= 0 && ((uintptr_t)src & 15) == 0;
+    for (int k = t * 8; k < a.Kp; k += nt * 8) {
         u32x4 v = {0u, 0u, 0u, 0u};
-        if (m >= 0) {
-            if (vec && k + 8 <= a.K) {
-                v = *(const u32x4*)(src + k);
-            } else {
+        if (vec && k + 8 <= a.K) {
+            v = *(const u32x4*)(src + k);
+        } else if (m >= 0) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (k + e < a.K) v[e >> 1] |= (uint32_t)src[k + e] << (16 * (e & 1));
-            }
+            for (int e = 0; e < 8; ++e)
+                if (k + e < a.K) v[e >> 1] |= (uint32_t)src[k + e] << (16 * (e & 1));
         }
         *(u32x4*)(dst + k) = v;
     }
-    if (tid >= 64) return;
-    if (m < 0) {
-        if (BWD && lane == 0) a.rows[c] = LossRow{INFINITY, 0.0f, 0.0f, 0.0f};
-        for (int j = lane; j < a.kp; j += 64) a.ids32[(int64_t)c * a.kp + j] = -1;
-        return;
-    }
+}
+
+// One wave: compact row c's targets and gradient constants, from row m.
+template <bool BWD>
+__device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c, float gref, int lane) {
     float rel = 1.0f, lse2 = 0.0f;
     if constexpr (BWD) {
-        rel = a.dloss[m] / a.hdr->gref;
+        rel = a.dloss[m] / gref;
         const float l = a.lse[m];
         // a row without any finite logit: every probability 0
         lse2 = l == -INFINITY ? INFINITY : l * kLog2e;
@@ -829,8 +858,9 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
     }
     int* ids = a.ids32 + (int64_t)c * a.kp;
     const float* t = a.teacher + m * a.ldt;
-    for (int j = lane; j < a.kp; j += 64) ids[j] = j < a.k && target_ok(a, m, j) ? (int)a.ids[m * a.ldids + j] : -1;
-    if constexpr (BWD) {
+    if constexpr (!BWD) {
+        for (int j = lane; j < a.kp; j += 64) ids[j] = j < a.k && target_ok(a, m, j) ? (int)a.ids[m * a.ldids + j] : -1;
+    } else {
         const float it = 1.0f / a.T;
         float tl;
         if (a.teacher_lse != nullptr) {
@@ -875,6 +905,84 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
     }
 }
 
+// Compacts the live rows of X with their targets, and clears what rows without
+// a target get.  A workgroup takes kGatherRows rows; unless SCANNED (many
+// rows: loss_scan_kernel has run) it counts the live rows before them and
+// altogether by itself, which is cheaper than a launch that does.  The rows
+// behind the last live one, up to a whole K step of dW's product, are zeroed.
+constexpr int kGatherRows = 16;
+template <bool BWD, bool SCANNED>
+__global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
+    __shared__ float buf[4];
+    __shared__ int cnt[2][4];
+    __shared__ int places[kGatherRows];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t r0 = (int64_t)blockIdx.x * kGatherRows;
+    int n, before = 0;
+    float gref = 1.0f;
+    if constexpr (SCANNED) {
+        n = a.hdr->n;
+        gref = a.hdr->gref;
+        if (tid < kGatherRows) places[tid] = r0 + tid < a.M ? a.pos[r0 + tid] : -2;
+    } else {
+        int b = 0, all = 0;
+        float g = 0.0f;
+        for (int64_t m = tid; m < a.M; m += 256) {
+            if (!row_live(a, m)) continue;
+            b += m < r0 ? 1 : 0;
+            all += 1;
+            if (BWD) g = fmaxf(g, fabsf(a.dloss[m]));
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            b += __shfl_xor(b, o);
+            all += __shfl_xor(all, o);
+        }
+        if (lane == 0) {
+            cnt[0][wave] = b;
+            cnt[1][wave] = all;
+        }
+        __syncthreads();
+        before = (cnt[0][0] + cnt[0][1]) + (cnt[0][2] + cnt[0][3]);
+        n = (cnt[1][0] + cnt[1][1]) + (cnt[1][2] + cnt[1][3]);
+        if constexpr (BWD) gref = usable_gref(block_max(g, buf));
+        if (blockIdx.x == 0) {
+            const int splits = BWD ? dx_splits(a, n, buf) : 1;
+            if (tid == 0) *a.hdr = LossHeader{n, gref, splits};
+        }
+        if (wave == 0) {
+            const int64_t m = r0 + lane;
+            const bool on = lane < kGatherRows && m < a.M && row_live(a, m);
+            const unsigned long long bits = __ballot(on);
+            if (lane < kGatherRows)
+                places[lane] = m >= a.M ? -2 : on ? before + __popcll(bits & ((1ull << lane) - 1ull)) : -1;
+        }
+    }
+    __syncthreads();
+    for (int r = wave; r < kGatherRows; r += 4) {
+        const int c = places[r];
+        const int64_t m = r0 + r;
+        if (c == -2) break;
+        if (c < 0) {
+            if constexpr (!BWD) {
+                if (lane == 0) a.loss[m] = a.lse[m] = 0.0f;
+            } else if (a.dX != nullptr) {
+                for (int k = lane; k < a.K; k += 64) {
+                    if (a.grad_f32) ((float*)a.dX)[m * a.lddx + k] = 0.0f;
+                    else ((uint16_t*)a.dX)[m * a.lddx + k] = 0;
+                }
+            }
+            continue;
+        }
+        if (lane == 0) a.map[c] = (int)m;
+        copy_row(a, m, c, lane, 64);
+        row_targets<BWD>(a, m, c, gref, lane);
+    }
+    // (at most 63 rows, over the workgroups' waves)
+    const int pad = ((n + 63) & ~63) - n;
+    for (int p = blockIdx.x * 4 + wave; p < pad; p += gridDim.x * 4) copy_row(a, -1, n + p, lane, 64);
+}
+
 // ---- backward ---------------------------------------------------------------
 
 // One tile of G, the gradient by s over gref (and over the call's unit: the
@@ -897,11 +1005,22 @@ __global__ __launch_bounds__(T::NT) void loss_grad_kernel(LossArgs a) {
     if (!map_tile(blockIdx.x, (n + T::BM - 1) / T::BM, (a.vn + T::BN - 1) / T::BN, tm, tn, rest, 1)) return;
     const int m0 = tm * T::BM, p0 = tn * T::BN, v0 = a.v0 + p0;
     Acc<T> acc;
-    logits_tile<T>(a, m0, v0, smem, wave, lane, acc);
+    logits_tile<T>(a, m0, v0, n, smem, wave, lane, acc);
     const Place<T> at(wave, lane);
     const int vr = a.V - v0;
-    const float c2 = kLog2e / a.T;
+    const float s2 = a.s2;
     const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
+    const BiasRegs<T> bias(a, at, v0);
+    LossRow rows[2][T::FM];
+    int labs[2][T::FM];
+#pragma unroll
+    for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            const int m = m0 + at.row(ha, i);
+            rows[ha][i] = a.rows[min(m, n - 1)];
+            if constexpr (!TG) labs[ha][i] = row_label(a, m, n) - v0 - at.wn * T::FN * 16;
+        }
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha) {
         if constexpr (TG) {
@@ -930,34 +1049,57 @@ __global__ __launch_bounds__(T::NT) void loss_grad_kernel(LossArgs a) {
 #pragma unroll
         for (int i = 0; i < T::FM; ++i) {
             const int row = at.row(ha, i);
-            const LossRow c = a.rows[m0 + row];   // (rows past the live ones: all entries come out 0)
-            int lab = 0;
-            if constexpr (!TG) lab = a.ids32[m0 + row] - v0;
+            const LossRow c = rows[ha][i];
+            if (!a.plain) row_logits<T>(a, bias, inv_cap, acc, ha, i);
+            f32x4 v[2][T::FN];
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
                 for (int j = 0; j < T::FN; ++j) {
-                    const int col = at.col(hb, j);
-                    const f32x4 z = acc[ha][hb][i][j];
-                    f32x4 v;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) v[r] = fmaf(exp2_fast(fmaf(z[r], c2, -c.lse2)), c.rq, -c.ru);
-                    if constexpr (TG) {
-                        v -= *(const f32x4 __attribute__((address_space(3)))*)(
-                            (float __attribute__((address_space(3)))*)smem + (row - ha * T::HA) * (T::BN + 4) + col);
-                    } else {
-                        const int d = lab - col;
-                        if ((unsigned)d < 4u) {   // (rarely taken by any lane)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) v[r] -= d == r ? c.rp : 0.0f;
-                        }
-                    }
-                    if (a.cap > 0.0f) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) v[r] *= fmaf(-z[r] * inv_cap, z[r] * inv_cap, 1.0f);
-                    }
-                    acc[ha][hb][i][j] = v;
+                    for (int r = 0; r < 4; ++r)
+                        v[hb][j][r] = fmaf(exp2_fast(fmaf(acc[ha][hb][i][j][r], s2, -c.lse2)), c.rq, -c.ru);
+                    if constexpr (TG)
+                        v[hb][j] -= *(const f32x4 __attribute__((address_space(3)))*)(
+                            (float __attribute__((address_space(3)))*)smem + (row - ha * T::HA) * (T::BN + 4) +
+                            at.col(hb, j));
                 }
+            if constexpr (!TG) {
+                // (the wave's columns are two runs of FN * 16; rarely any lane's label is among them)
+                if ((unsigned)(labs[ha][i] % T::HB) < (unsigned)(T::FN * 16) && (unsigned)labs[ha][i] < (unsigned)T::BN) {
+#pragma unroll
+                    for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                        for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                v[hb][j][r] -= labs[ha][i] == hb * T::HB + j * 16 + at.g * 4 + r ? c.rp : 0.0f;
+                }
+            }
+            if (a.cap > 0.0f) {   // (then acc holds z)
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float t = acc[ha][hb][i][j][r] * inv_cap;
+                            v[hb][j][r] *= fmaf(-t, t, 1.0f);
+                        }
+            }
+            if (m0 + T::BM > n) {   // rows past the live ones
+                const bool on = m0 + row < n;
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[hb][j][r] = on ? v[hb][j][r] : 0.0f;
+            }
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                for (int j = 0; j < T::FN; ++j) acc[ha][hb][i][j] = v[hb][j];
             __builtin_amdgcn_sched_barrier(0);   // one row of fragments at a time keeps the registers within bounds
         }
     }
@@ -1029,46 +1171,14 @@ __global__ __launch_bounds__(T::NT) void loss_grad_kernel(LossArgs a) {
     }
 }
 
-// How dX's product over a piece is cut: its tiles are few where the live rows
-// or the features are, so the vocabulary steps are split over workgroups, each
-// split with a partial dX of its own.  Counted in steps of a workgroup, with
-// what a tile costs besides its steps (filling and draining the pipeline,
-// writing and summing the partial) taken as 8 of them: the cheapest of the
-// whole numbers of splits that give at most two rounds of workgroups.
-struct DxCut {
-    int tm, tk, splits;
-};
-__device__ __forceinline__ DxCut dx_cut(int n, int K, int Vp, int tile, int slots) {
-    DxCut c;
-    c.tm = (n + tile - 1) / tile;
-    c.tk = (K + tile - 1) / tile;
-    const int tiles = max(1, c.tm * c.tk), all = Vp >> 6;
-    c.splits = 1;
-    int best = ((tiles + slots - 1) / slots) * (all + 8);
-    for (int s = 2; s * tiles <= 2 * slots && s * 4 <= all; ++s) {
-        const int cost = ((tiles * s + slots - 1) / slots) * ((all + s - 1) / s + 8);
-        if (cost < best) {
-            best = cost;
-            c.splits = s;
-        }
-    }
-    return c;
-}
-
-// dX partials: [split] (+)= G(piece) . W(piece), a split's share of the
-// vocabulary steps.
+// A workgroup's share of dX's partials: [split] (+)= G(piece) . W(piece) over
+// the split's vocabulary steps.
 template <class T>
-__global__ __launch_bounds__(T::NT) void loss_dx_kernel(LossArgs a) {
-    __shared__ __attribute__((aligned(1024))) unsigned char raw[T::LDS];
-    lds_t* smem = (lds_t*)raw;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n = a.hdr->n;
-    const DxCut cut = dx_cut(n, a.K, a.Vp, T::BM, a.slots);
-    int tm, tn, split;
-    if (!map_tile(blockIdx.x, cut.tm, cut.tk, tm, tn, split, cut.splits)) return;
+__device__ __forceinline__ void dx_tile(const LossArgs& a, int n, int tm, int tn, int split, int splits, lds_t* smem,
+                                        int wave, int lane) {
     const int m0 = tm * T::BM, k0 = tn * T::BN;
     const int all = (a.vn + 63) >> 6;
-    const int per = (all + cut.splits - 1) / cut.splits;
+    const int per = (all + splits - 1) / splits;
     const int s0 = min(split * per, all), steps = min(per, all - s0);
     Operand<T::HA, false, T::IA, T::NW> A;
     Operand<T::HB, true, T::IB, T::NW> B;
@@ -1078,7 +1188,7 @@ __global__ __launch_bounds__(T::NT) void loss_dx_kernel(LossArgs a) {
     Acc<T> acc;
     main_loop<T>(A, B, steps, smem, wave, lane, acc);
     const Place<T> at(wave, lane);
-    float* P = a.dxp + ((int64_t)split * cut.tm * T::BM + m0) * a.Kp + k0;
+    float* P = a.dxp + ((int64_t)split * ((n + T::BM - 1) / T::BM) * T::BM + m0) * a.Kp + k0;
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
@@ -1096,16 +1206,15 @@ __global__ __launch_bounds__(T::NT) void loss_dx_kernel(LossArgs a) {
 
 // dX = gref unit scale (sum of the partials), in the rows' own places.
 __global__ __launch_bounds__(256) void loss_dx_finish_kernel(LossArgs a, float mul, int tile) {
-    const int c = blockIdx.x, n = a.hdr->n;
+    const int c = blockIdx.x, n = a.hdr->n, splits = a.hdr->splits;
     if (c >= n) return;
-    const DxCut cut = dx_cut(n, a.K, a.Vp, tile, a.slots);
     const int64_t m = a.map[c];
     const float f = mul * a.hdr->gref;
-    const int64_t sp = (int64_t)cut.tm * tile * a.Kp;
+    const int64_t sp = (int64_t)((n + tile - 1) / tile) * tile * a.Kp;
     for (int k = threadIdx.x * 4; k < a.K; k += 1024) {
         const float* p = a.dxp + (int64_t)c * a.Kp + k;
         f32x4 v = *(const f32x4*)p;
-        for (int s = 1; s < cut.splits; ++s) v += *(const f32x4*)(p + s * sp);
+        for (int s = 1; s < splits; ++s) v += *(const f32x4*)(p + s * sp);
         v *= f;
         if (a.grad_f32) {
             float* d = (float*)a.dX + m * a.lddx + k;
@@ -1127,17 +1236,11 @@ __global__ __launch_bounds__(256) void loss_dx_finish_kernel(LossArgs a, float m
     }
 }
 
-// dW of a piece: gref unit scale G^T . X.
+// One tile of a piece's dW: gref unit scale G^T . X.
 template <class T>
-__global__ __launch_bounds__(T::NT) void loss_dw_kernel(LossArgs a, float mul) {
+__device__ __forceinline__ void dw_tile(const LossArgs& a, int n, int tm, int tn, float f, lds_t* smem, int wave, int lane) {
     constexpr int LDG = T::BN * 2 + 16;
-    constexpr int NEED = T::BM * LDG;
-    __shared__ __attribute__((aligned(1024))) unsigned char raw[T::LDS > NEED ? T::LDS : NEED];
-    lds_t* smem = (lds_t*)raw;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n = a.hdr->n;
-    int tm, tn, rest;
-    if (!map_tile(blockIdx.x, (a.vn + T::BM - 1) / T::BM, (a.K + T::BN - 1) / T::BN, tm, tn, rest, 1)) return;
+    const int tid = wave * 64 + lane;
     const int p0 = tm * T::BM, k0 = tn * T::BN;
     const int steps = (n + 63) >> 6;
     Operand<T::HA, true, T::IA, T::NW> A;
@@ -1147,7 +1250,6 @@ __global__ __launch_bounds__(T::NT) void loss_dw_kernel(LossArgs a, float mul) {
     Acc<T> acc;
     main_loop<T>(A, B, steps, smem, wave, lane, acc);
     const Place<T> at(wave, lane);
-    const float f = mul * a.hdr->gref;
     const int vr = a.vn - p0, kr = a.K - k0;
     if (a.grad_f32) {
         float* D = (float*)a.dW + (int64_t)(a.v0 + p0) * a.lddw + k0;
@@ -1202,6 +1304,28 @@ __global__ __launch_bounds__(T::NT) void loss_dw_kernel(LossArgs a, float mul) {
     }
 }
 
+// Both products of a piece in one launch, dX's workgroups first: they need
+// the same G, and together they fill the device better than one after the
+// other.
+template <class TX, class TW>
+__global__ __launch_bounds__(TX::NT) void loss_products_kernel(LossArgs a, float mul) {
+    constexpr int NEED = TW::BM * (TW::BN * 2 + 16);
+    __shared__ __attribute__((aligned(1024))) unsigned char raw[TX::LDS > NEED ? TX::LDS : NEED];
+    lds_t* smem = (lds_t*)raw;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = a.hdr->n, splits = a.hdr->splits;
+    const int tk = (a.K + TX::BN - 1) / TX::BN, tr = (n + TX::BM - 1) / TX::BM;
+    const int ndx = a.dX != nullptr ? tr * tk * splits : 0;
+    int tm, tn, split;
+    if ((int)blockIdx.x < ndx) {
+        map_tile(blockIdx.x, tr, tk, tm, tn, split, splits);
+        dx_tile<TX>(a, n, tm, tn, split, splits, smem, wave, lane);
+    } else if (a.dW != nullptr) {
+        if (!map_tile(blockIdx.x - ndx, (a.vn + TW::BM - 1) / TW::BM, tk, tm, tn, split, 1)) return;
+        dw_tile<TW>(a, n, tm, tn, mul * a.hdr->gref, smem, wave, lane);
+    }
+}
+
 // dbias of a piece: gref unit (sum over the row tiles, in order).
 __global__ __launch_bounds__(256) void loss_dbias_kernel(LossArgs a, float mul, int row_tile) {
     const int p = blockIdx.x * 256 + threadIdx.x;
@@ -1227,45 +1351,45 @@ float unit_of(const LossArgs& a) {
 
 }  // namespace
 
-int loss_tile_rows(int tile) { return tile == LT_256 ? 256 : 128; }
+int loss_sumz_parts(int tile) { return tile == 256 ? L256<false, false>::WGN : L128<false, false>::WGN; }
 
 hipError_t launch_loss_flags(const LossArgs& a, hipStream_t st) {
     return launch_kernel(loss_flags_kernel, dim3((unsigned)up(a.M, 4)), dim3(256), st, a);
 }
 
 hipError_t launch_loss_scan(const LossArgs& a, hipStream_t st) {
-    return launch_kernel(loss_scan_kernel, dim3(1), dim3(1024), st, a);
+    return launch_kernel(loss_scan_kernel, dim3(1), dim3(256), st, a);
 }
 
-hipError_t launch_loss_gather(const LossArgs& a, bool backward, hipStream_t st) {
-    const dim3 grid((unsigned)a.Mr);
-    return backward ? launch_kernel(loss_gather_kernel<true>, grid, dim3(256), st, a)
-                    : launch_kernel(loss_gather_kernel<false>, grid, dim3(256), st, a);
+hipError_t launch_loss_gather(const LossArgs& a, bool scanned, hipStream_t st) {
+    const dim3 grid((unsigned)std::max<int64_t>(1, up(a.M, kGatherRows)));
+    if (a.dloss != nullptr)
+        return scanned ? launch_kernel(loss_gather_kernel<true, true>, grid, dim3(256), st, a)
+                       : launch_kernel(loss_gather_kernel<true, false>, grid, dim3(256), st, a);
+    return scanned ? launch_kernel(loss_gather_kernel<false, true>, grid, dim3(256), st, a)
+                   : launch_kernel(loss_gather_kernel<false, false>, grid, dim3(256), st, a);
 }
 
-hipError_t launch_loss_forward(const LossArgs& a, int tile, hipStream_t st) {
+hipError_t launch_loss_forward(const LossArgs& a, hipStream_t st) {
     const bool tg = a.labels == nullptr;
-    if (tile == LT_256) {
+    const dim3 grid((unsigned)(up(a.M, a.tile) * a.ntiles));
+    if (a.tile == 256) {
         using T = L256<false, false>;
-        const dim3 grid((unsigned)(up(a.M, T::BM) * a.ntiles));
         return tg ? launch_kernel(loss_forward_kernel<T, true>, grid, dim3(T::NT), st, a)
                   : launch_kernel(loss_forward_kernel<T, false>, grid, dim3(T::NT), st, a);
     }
     using T = L128<false, false>;
-    const dim3 grid((unsigned)(up(a.M, T::BM) * a.ntiles));
     return tg ? launch_kernel(loss_forward_kernel<T, true>, grid, dim3(T::NT), st, a)
               : launch_kernel(loss_forward_kernel<T, false>, grid, dim3(T::NT), st, a);
 }
 
-hipError_t launch_loss_finish(const LossArgs& a, bool compact, hipStream_t st) {
-    const dim3 grid((unsigned)up(a.M, 4));
-    return compact ? launch_kernel(loss_finish_kernel<true>, grid, dim3(256), st, a)
-                   : launch_kernel(loss_finish_kernel<false>, grid, dim3(256), st, a);
+hipError_t launch_loss_finish(const LossArgs& a, hipStream_t st) {
+    return launch_kernel(loss_finish_kernel, dim3((unsigned)a.M), dim3(256), st, a, loss_sumz_parts(a.tile));
 }
 
-hipError_t launch_loss_grad(const LossArgs& a, int tile, hipStream_t st) {
+hipError_t launch_loss_grad(const LossArgs& a, hipStream_t st) {
     const bool tg = a.labels == nullptr;
-    if (tile == LT_256) {
+    if (a.tile == 256) {
         using T = L256<false, false>;
         const dim3 grid((unsigned)(up(a.M, T::BM) * up(a.vn, T::BN)));
         return tg ? launch_kernel(loss_grad_kernel<T, true>, grid, dim3(T::NT), st, a)
@@ -1277,37 +1401,24 @@ hipError_t launch_loss_grad(const LossArgs& a, int tile, hipStream_t st) {
               : launch_kernel(loss_grad_kernel<T, false>, grid, dim3(T::NT), st, a);
 }
 
-hipError_t launch_loss_dx(const LossArgs& a, int tile, hipStream_t st) {
-    const int b = loss_tile_rows(tile);
-    // (at most two rounds, or one workgroup a tile)
-    const dim3 grid((unsigned)std::max<int64_t>(up(a.M, b) * up(a.K, b), 2 * a.slots));
-    if (tile == LT_256) {
-        using T = L256<false, true>;
-        return launch_kernel(loss_dx_kernel<T>, grid, dim3(T::NT), st, a);
-    }
-    using T = L128<false, true>;
-    return launch_kernel(loss_dx_kernel<T>, grid, dim3(T::NT), st, a);
-}
-
-hipError_t launch_loss_dx_finish(const LossArgs& a, int tile, hipStream_t st) {
-    return launch_kernel(loss_dx_finish_kernel, dim3((unsigned)a.M), dim3(256), st, a, unit_of(a) * a.scale,
-                         loss_tile_rows(tile));
-}
-
-hipError_t launch_loss_dw(const LossArgs& a, int tile, hipStream_t st) {
-    const int b = loss_tile_rows(tile);
-    const dim3 grid((unsigned)(up(a.vn, b) * up(a.K, b)));
+hipError_t launch_loss_products(const LossArgs& a, hipStream_t st) {
+    const int b = a.tile;
+    // (dX: at most two rounds of workgroups, or one a tile)
+    const int64_t dx = a.dX != nullptr ? std::max<int64_t>(up(a.M, b) * up(a.K, b), 2 * a.slots) : 0;
+    const int64_t dw = a.dW != nullptr ? up(a.vn, b) * up(a.K, b) : 0;
+    const dim3 grid((unsigned)(dx + dw));
     const float mul = unit_of(a) * a.scale;
-    if (tile == LT_256) {
-        using T = L256<true, true>;
-        return launch_kernel(loss_dw_kernel<T>, grid, dim3(T::NT), st, a, mul);
-    }
-    using T = L128<true, true>;
-    return launch_kernel(loss_dw_kernel<T>, grid, dim3(T::NT), st, a, mul);
+    if (b == 256)
+        return launch_kernel(loss_products_kernel<L256<false, true>, L256<true, true>>, grid, dim3(512), st, a, mul);
+    return launch_kernel(loss_products_kernel<L128<false, true>, L128<true, true>>, grid, dim3(256), st, a, mul);
 }
 
-hipError_t launch_loss_dbias(const LossArgs& a, int row_tile, hipStream_t st) {
-    return launch_kernel(loss_dbias_kernel, dim3((unsigned)up(a.vn, 256)), dim3(256), st, a, unit_of(a), row_tile);
+hipError_t launch_loss_dx_finish(const LossArgs& a, hipStream_t st) {
+    return launch_kernel(loss_dx_finish_kernel, dim3((unsigned)a.M), dim3(256), st, a, unit_of(a) * a.scale, a.tile);
+}
+
+hipError_t launch_loss_dbias(const LossArgs& a, hipStream_t st) {
+    return launch_kernel(loss_dbias_kernel, dim3((unsigned)up(a.vn, 256)), dim3(256), st, a, unit_of(a), a.tile);
 }
 
 }  // namespace mkp

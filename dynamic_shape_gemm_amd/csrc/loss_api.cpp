@@ -18,8 +18,8 @@
 namespace mkp {
 
 const char* loss_launch_name(int i) {
-    static const char* const names[LL_COUNT] = {"loss_flags", "loss_scan", "loss_gather",    "loss_forward", "loss_finish",
-                                                "loss_grad",  "loss_dx",   "loss_dx_finish", "loss_dw",      "loss_dbias"};
+    static const char* const names[LL_COUNT] = {"loss_flags", "loss_scan",     "loss_gather",    "loss_forward", "loss_finish",
+                                                "loss_grad",  "loss_products", "loss_dx_finish", "loss_dbias"};
     return i >= 0 && i < LL_COUNT ? names[i] : "loss";
 }
 
@@ -32,26 +32,28 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 constexpr int kMaxTargets = 1024;
 // columns of X and W: a tile's 256 rows stay within 32-bit byte offsets
 constexpr int64_t kMaxK = int64_t(1) << 21;
+// above this many rows one workgroup counts the live ones; below, every
+// workgroup of the gather does so for itself
+constexpr int64_t kManyRows = 16384;
 constexpr int64_t kPieceBytes = int64_t(256) << 20;   // G of one piece
 
 // A call's extents and where its workspace's parts lie.
 struct Layout {
-    int tile = LT_256, rows = 256;
+    int tile = 256;
     int64_t Mr = 0, Kp = 0, Vp = 0, kp = 1, ntiles = 0;
     int pieces = 1, slots = 256;
     bool pack_w = false;
-    size_t hdr = 0, map = 0, live = 0, xc = 0, ids = 0, wts = 0, rws = 0, part = 0, sumz = 0, zt = 0, g = 0, dxp = 0, dbp = 0,
+    size_t hdr = 0, map = 0, pos = 0, live = 0, xc = 0, ids = 0, wts = 0, rws = 0, part = 0, sumz = 0, zt = 0, g = 0, dxp = 0, dbp = 0,
            w = 0, bytes = 0;
 };
 
 Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int64_t ldw, bool backward) {
     Layout l;
-    l.tile = M > 128 ? LT_256 : LT_128;
-    l.rows = loss_tile_rows(l.tile);
+    l.tile = M > 128 ? 256 : 128;
     l.Mr = round_up(M, 256);
     l.Kp = round_up(K, 64);
     l.kp = k > 0 ? round_up(k, 4) : 1;
-    l.ntiles = ceil_div(V, l.rows);
+    l.ntiles = ceil_div(V, l.tile);
     l.pack_w = !aligned16(W) || ldw % 8 != 0 || K % 8 != 0;
     size_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -61,13 +63,14 @@ Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int6
     };
     l.hdr = take(sizeof(LossHeader));
     l.map = take(4 * M);
+    l.pos = take(M > kManyRows ? 4 * M : 0);
     l.live = take(k > 0 ? M : 0);
     l.xc = take(2 * l.Mr * l.Kp);
     l.ids = take(4 * l.Mr * l.kp);
     if (l.pack_w) l.w = take(2 * V * l.Kp);
     if (!backward) {
         l.part = take(8 * M * l.ntiles);
-        l.sumz = take(4 * M * l.ntiles);
+        l.sumz = take(4 * M * l.ntiles * loss_sumz_parts(l.tile));
         l.zt = take(4 * l.Mr * l.kp);
     } else {
         l.wts = take(k > 0 ? 4 * l.Mr * l.kp : 0);
@@ -80,11 +83,11 @@ Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int6
         l.g = take(2 * l.Mr * l.Vp);
         // dX: one partial, or splits of at most two rounds of tiles and at
         // least four vocabulary steps each
-        l.slots = l.tile == LT_256 ? 256 : 512;
+        l.slots = l.tile == 256 ? 256 : 512;
         const int64_t one = l.Mr * l.Kp, steps = l.Vp / 64;
-        const int64_t split = std::min<int64_t>(2 * l.slots * l.rows * l.rows, std::max<int64_t>(1, steps / 4) * one);
+        const int64_t split = std::min<int64_t>(2 * l.slots * l.tile * l.tile, std::max<int64_t>(1, steps / 4) * one);
         l.dxp = take(4 * std::max(one, split));
-        l.dbp = take(4 * ceil_div(std::max<int64_t>(M, 1), l.rows) * l.Vp);
+        l.dbp = take(4 * ceil_div(std::max<int64_t>(M, 1), l.tile) * l.Vp);
     }
     l.bytes = at;
     return l;
@@ -173,7 +176,7 @@ int run(const Call& c) {
     if (!c.ws || c.ws_bytes < 0 || (size_t)c.ws_bytes < l.bytes || !aligned16(c.ws))
         return report(MKP_ERR_INVALID_ARG,
                       "workspace of " + std::to_string(l.bytes) + " bytes, 16-byte aligned, needed");
-    if (ceil_div(c.M, l.rows) * l.ntiles > INT_MAX || l.Mr > INT_MAX / 2)
+    if (ceil_div(c.M, l.tile) * l.ntiles > INT_MAX || l.Mr > INT_MAX / 2)
         return report(MKP_ERR_UNSUPPORTED, "grid too large");
     begin_call();
     hipStream_t st = (hipStream_t)c.stream;
@@ -191,6 +194,8 @@ int run(const Call& c) {
     a.scale = c.scale;
     a.cap = c.cap;
     a.T = c.distill ? c.T : 1.0f;
+    a.plain = !c.bias && c.cap == 0.0f && c.scale > 0.0f;
+    a.s2 = (float)(1.4426950408889634 * (a.plain ? (double)c.scale : 1.0) / (double)a.T);
     a.labels = c.distill ? nullptr : c.labels;
     a.smoothing = c.smoothing;
     a.z_loss = c.z_loss;
@@ -211,6 +216,7 @@ int run(const Call& c) {
     a.grad_f32 = c.grad_type == MKP_F32;
     a.hdr = (LossHeader*)(ws + l.hdr);
     a.map = (int*)(ws + l.map);
+    a.pos = (int*)(ws + l.pos);
     a.live = (uint8_t*)(ws + l.live);
     a.Xc = (uint16_t*)(ws + l.xc);
     a.ids32 = (int*)(ws + l.ids);
@@ -219,6 +225,8 @@ int run(const Call& c) {
     a.Vp = (int)l.Vp;
     a.kp = (int)l.kp;
     a.ntiles = (int)l.ntiles;
+    a.tile = l.tile;
+    a.slots = l.slots;
     const double elem = 2.0, m = (double)c.M, v = (double)c.V, k = (double)c.K;
     const double gb = a.grad_f32 ? 4.0 : 2.0;
 
@@ -240,20 +248,26 @@ int run(const Call& c) {
         a.Kw = (int)l.Kp;
     }
     const double target_bytes = c.distill ? 12.0 * m * (double)c.k : 8.0 * m;
-    if (c.distill && c.M > 0)
-        if ((rc = go(LL_FLAGS, 0.0, target_bytes, [&] { return launch_loss_flags(a, st); })) != MKP_OK) return rc;
-    if ((rc = go(LL_SCAN, 0.0, 8.0 * m, [&] { return launch_loss_scan(a, st); })) != MKP_OK) return rc;
+    const bool scanned = c.M > kManyRows;
+    auto compact = [&]() -> int {
+        if (c.distill && c.M > 0)
+            if ((rc = go(LL_FLAGS, 0.0, target_bytes, [&] { return launch_loss_flags(a, st); })) != MKP_OK) return rc;
+        if (scanned)
+            if ((rc = go(LL_SCAN, 0.0, 8.0 * m, [&] { return launch_loss_scan(a, st); })) != MKP_OK) return rc;
+        return go(LL_GATHER, 0.0, 4.0 * m * k + target_bytes, [&] { return launch_loss_gather(a, scanned, st); });
+    };
 
     if (!c.backward) {
         a.part = (float*)(ws + l.part);
         a.sumz = !c.distill && c.smoothing > 0.0f ? (float*)(ws + l.sumz) : nullptr;
         a.zt = (float*)(ws + l.zt);
-        if ((rc = go(LL_GATHER, 0.0, 4.0 * m * k + target_bytes, [&] { return launch_loss_gather(a, false, st); })) != MKP_OK)
+        // one tile of rows: the product costs the weight's bytes, not its
+        // rows, so none need dropping, and two launches fewer count for more
+        a.direct = c.M <= l.tile && !l.pack_w && aligned16(c.X) && c.ldx % 8 == 0 && c.K % 64 == 0;
+        if (!a.direct && (rc = compact()) != MKP_OK) return rc;
+        if ((rc = go(LL_FORWARD, 2.0 * m * v * k, elem * (m + v) * k, [&] { return launch_loss_forward(a, st); })) != MKP_OK)
             return rc;
-        if ((rc = go(LL_FORWARD, 2.0 * m * v * k, elem * (m + v) * k,
-                     [&] { return launch_loss_forward(a, l.tile, st); })) != MKP_OK)
-            return rc;
-        return go(LL_FINISH, 0.0, 8.0 * m * (double)l.ntiles, [&] { return launch_loss_finish(a, true, st); });
+        return go(LL_FINISH, 0.0, 8.0 * m * (double)l.ntiles, [&] { return launch_loss_finish(a, st); });
     }
 
     a.wts = (float*)(ws + l.wts);
@@ -261,35 +275,29 @@ int run(const Call& c) {
     a.G = (uint16_t*)(ws + l.g);
     a.dxp = (float*)(ws + l.dxp);
     a.dbp = c.dbias ? (float*)(ws + l.dbp) : nullptr;
-    if (c.M > 0)
-        if ((rc = go(LL_GATHER, 0.0, 4.0 * m * k + target_bytes, [&] { return launch_loss_gather(a, true, st); })) != MKP_OK)
-            return rc;
-    a.slots = l.slots;
+    if ((rc = compact()) != MKP_OK) return rc;
     for (int p = 0; p < l.pieces; ++p) {
         a.v0 = (int)(p * l.Vp);
         a.vn = (int)std::min<int64_t>(l.Vp, c.V - a.v0);
-        const double pv = a.vn;
+        a.first = p == 0;
+        const double pv = a.vn, both = (c.dX ? 1.0 : 0.0) + (c.dW ? 1.0 : 0.0);
         if (c.M > 0)
-            if ((rc = go(LL_GRAD, 2.0 * m * pv * k, elem * ((m + pv) * k + m * pv),
-                         [&] { return launch_loss_grad(a, l.tile, st); })) != MKP_OK)
+            if ((rc = go(LL_GRAD, 2.0 * m * pv * k, elem * ((m + pv) * k + m * pv), [&] { return launch_loss_grad(a, st); })) !=
+                MKP_OK)
                 return rc;
-        if (c.dX && c.M > 0) {
-            a.first = p == 0;
-            if ((rc = go(LL_DX, 2.0 * m * pv * k, elem * (pv * k + m * pv) + (p ? 8.0 : 4.0) * m * k,
-                         [&] { return launch_loss_dx(a, l.tile, st); })) != MKP_OK)
-                return rc;
-        }
-        if (c.dW)
-            if ((rc = go(LL_DW, 2.0 * m * pv * k, elem * (m * k + m * pv) + gb * pv * k,
-                         [&] { return launch_loss_dw(a, l.tile, st); })) != MKP_OK)
+        if (c.dX || c.dW)
+            if ((rc = go(LL_PRODUCTS, 2.0 * both * m * pv * k,
+                         both * elem * m * pv + (c.dX ? elem * pv * k + (p ? 8.0 : 4.0) * m * k : 0.0) +
+                             (c.dW ? elem * m * k + gb * pv * k : 0.0),
+                         [&] { return launch_loss_products(a, st); })) != MKP_OK)
                 return rc;
         if (c.dbias)
-            if ((rc = go(LL_DBIAS, 0.0, 4.0 * pv * (double)ceil_div(c.M, l.rows),
-                         [&] { return launch_loss_dbias(a, l.rows, st); })) != MKP_OK)
+            if ((rc = go(LL_DBIAS, 0.0, 4.0 * pv * (double)ceil_div(c.M, l.tile), [&] { return launch_loss_dbias(a, st); })) !=
+                MKP_OK)
                 return rc;
     }
     if (c.dX && c.M > 0)
-        return go(LL_DX_FINISH, 0.0, (4.0 + gb) * m * k, [&] { return launch_loss_dx_finish(a, l.tile, st); });
+        return go(LL_DX_FINISH, 0.0, (4.0 + gb) * m * k, [&] { return launch_loss_dx_finish(a, st); });
     return MKP_OK;
 }
 

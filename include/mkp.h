@@ -250,8 +250,10 @@ int mkp_plan_describe_grouped(int64_t groups, int64_t M, int64_t K, const int64_
  * (smoothing in [0, 1]).  A row whose label is not in [0, V) -- such as the
  * customary -100 -- is left out: its loss and lse are 0, it has no gradient,
  * costs nothing in the products, and whatever its X holds reaches no result.
- * A label whose logit is -inf (a masked vocabulary entry: bias -inf) has loss
- * +inf.  M fp32 values each are written to loss and lse.
+ * A logit z is -inf here when log2(e) z / T is in binary32 (so is the type's
+ * lowest value, T = 1): the entry is masked out.  A label that is has loss
+ * +inf; a row of which every entry is has lse -inf too, and probabilities 0
+ * in the gradient.  M fp32 values each are written to loss and lse.
  *
  * mkp_linear_xent_backward: from lse (as written by the forward call) and
  * dloss (M fp32 values, the gradient by each row's loss; rows left out are
@@ -274,7 +276,7 @@ int mkp_plan_describe_grouped(int64_t groups, int64_t M, int64_t K, const int64_
  * with temperature T and L the row's teacher_lse (the log-partition of t / T
  * over the teacher's whole vocabulary; M fp32 values) or, with teacher_lse
  * NULL, the one over the row's k entries.  An id outside [0, V), or a teacher
- * logit of -inf, leaves its entry out; a row with no entry left is left out
+ * logit t / T of -inf, leaves its entry out; a row with no entry left is left out
  * as above.  An id named twice counts twice.  mkp_linear_distill_backward:
  * as mkp_linear_xent_backward with
  *   D = dloss T [softmax(z / T) sum_j p_j - sum_j p_j onehot(id_j)] * dz/ds.

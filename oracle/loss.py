@@ -112,7 +112,7 @@ def bounds(out, x, w, bias=None, scale=1.0, softcap=0.0, T=1.0, weight=1.0, term
     ds = (K + 4) * U * (abs(scale) * (xf.abs() @ w.abs().t()) + (bias.abs() if bias is not None else 0.0))
     z, _ = _logits(xf, w, bias, scale, softcap)
     dz = ds + 2.0 ** -21 * z.abs() if softcap > 0 else ds
-    fin = torch.isfinite(z)
+    fin = torch.isfinite(z) & (z > -1e30)   # (lower ones are masked out: probability 0 either way)
     z, dz = torch.where(fin, z, torch.zeros_like(z)), torch.where(fin, dz, torch.zeros_like(dz))
     zmax, dzm = z.abs().max(1).values, dz.max(1).values
     lse = torch.where(torch.isfinite(out["lse"]), out["lse"].abs(), torch.zeros_like(out["lse"]))

@@ -200,23 +200,36 @@ def test_left_out_rows_may_hold_anything(mkp, M):
 @pytest.mark.parametrize("M", [24, 301])
 def test_masked_vocabulary(mkp, M):
     """A bias of -inf, and of the type's lowest value, takes entries out; a
-    label that is taken out has an infinite loss."""
+    label that is taken out has an infinite loss, and so has every label where
+    all entries are, with no NaN in any gradient."""
     for low in (-math.inf, torch.finfo(torch.float32).min):
         t = inputs(14, M, 400, 64, bias=True)
         t["bias"][50:390] = low
         t["labels"] = torch.where(t["labels"] % 2 == 0, t["labels"] % 50, 390 + t["labels"] % 10)
         check(mkp, t, "masked")
         check(mkp, t, "masked", z_loss=1e-3, scale=0.7)
-    t["bias"][50:390] = -math.inf
-    t["labels"][3] = 100
-    loss, _ = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"])
-    assert math.isinf(loss[3].item()) and loss[3] > 0 and torch.isfinite(loss[:3]).all() and torch.isfinite(loss[4:]).all()
-    # every entry out: an infinite loss, no NaN in any gradient
-    t["bias"][:] = -math.inf
-    loss, lse = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"])
-    assert torch.isposinf(loss).all() and torch.isneginf(lse).all()
-    dx, dw, db = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"], t["bias"])
-    assert torch.isfinite(dx).all() and torch.isfinite(dw).all() and torch.isfinite(db).all()
+        t["labels"][3] = 100
+        loss, _ = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"])
+        assert torch.isposinf(loss[3]) and torch.isfinite(loss[:3]).all() and torch.isfinite(loss[4:]).all()
+        t["bias"][:] = low
+        loss, lse = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"])
+        assert torch.isposinf(loss).all() and torch.isneginf(lse).all()
+        dx, dw, db = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"], t["bias"])
+        assert torch.isfinite(dx).all() and torch.isfinite(dw).all() and torch.isfinite(db).all()
+
+
+@pytest.mark.parametrize("M", [24, 301])
+def test_teacher_of_lowest_values(mkp, M):
+    """Teacher logits of the type's lowest value among others have no weight;
+    rows of nothing else (finite over T) are uniform."""
+    t = inputs(17, M, 120, 64, k=4)
+    t["ids"] = torch.arange(4, device="cuda").expand(M, 4) + 7 * (torch.arange(M, device="cuda")[:, None] % 5)
+    low = torch.finfo(torch.float32).min
+    t["teacher"][:, 2] = low
+    t["teacher"][5] = low
+    check(mkp, t, "lowest", temperature=2.0)
+    t["teacher"][5] = 0.0
+    check(mkp, t, "lowest over T is -inf", temperature=0.5)
 
 
 def test_a_nan_row_stays_its_own(mkp):
@@ -261,6 +274,12 @@ def test_several_pieces_of_the_vocabulary(mkp, op):
     ws1 = mkp.mkp_linear_loss_workspace(4200, 40000, 64, 0, t["w"], 64, True)
     assert ws1 < 2 * 4200 * 40000   # less than the whole gradient by the logits
     check(mkp, t, op + " pieces", **({"temperature": 2.0} if op == "distill" else {"smoothing": 0.05}))
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_many_rows(mkp, op):
+    """More rows than the gather counts by itself."""
+    check(mkp, inputs(22, 16600, 130, 64, bias=True, k=3 if op == "distill" else 0, keep=0.4), op + " many rows")
 
 
 @pytest.mark.parametrize("grad_dtype", [BF, torch.float32])
@@ -427,5 +446,5 @@ def test_trace_names_the_launches(mkp):
         names = [r["kernel"] for r in mkp.mkp_trace_dump()]
     finally:
         mkp.mkp_set_option("trace", 0)
-    assert names == ["loss_flags", "loss_scan", "loss_gather", "loss_forward", "loss_finish", "loss_flags", "loss_scan",
-                     "loss_gather", "loss_grad", "loss_dx", "loss_dw", "loss_dbias", "loss_dx_finish"]
+    assert names == ["loss_forward", "loss_finish", "loss_flags", "loss_gather", "loss_grad", "loss_products",
+                     "loss_dbias", "loss_dx_finish"]
