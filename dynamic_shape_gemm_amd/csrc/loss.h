@@ -11,6 +11,9 @@
 
 namespace mkp {
 
+constexpr int kMaxTargets = 1024;   // per row (distillation)
+constexpr int kDbiasRows = 128;
+
 // What a call keeps in its workspace besides the large arrays; written by
 // the row-scan kernel, read by every later one.
 struct LossHeader {
@@ -75,7 +78,7 @@ struct LossArgs {
     float* zt;              // forward: the targets' kept values, compact n x kp
     uint16_t* G;            // backward: one piece's gradient by s, Mr x Vp
     float* dxp;             // backward: dX partials, [splits][rows of live tiles][Kp]
-    float* dbp;             // backward: per row tile, sums of G's columns
+    float* dbp;             // backward: sums of G's columns over kDbiasRows rows each, [Mr / kDbiasRows][Vp]
     int Mr, Kp, Vp, kp;     // padded extents
     int tile;               // rows and columns of the tile kernels' tiles: 256 or 128
     int ntiles;             // vocabulary tiles of the forward pass

@@ -273,8 +273,7 @@ __device__ __forceinline__ void main_loop(const Operand<T::HA, T::AT, T::IA, T::
                                           const Operand<T::HB, T::BT, T::IB, T::NW>& B, int steps, lds_t* smem,
                                           int wave, int lane, Acc<T>& acc) {
     constexpr bool PP = T::NW == 8;
-    constexpr int I = T::IA;
-    static_assert(T::IA == T::IB, "halves are counted in loads");
+    constexpr int IA = T::IA, IB = T::IB;
     const int wm = wave % T::WGM, wn = wave / T::WGM;
     FragReader<T::HA, T::AT, T::FM> ra;
     FragReader<T::HB, T::BT, T::FN> rb;
@@ -332,25 +331,27 @@ __device__ __forceinline__ void main_loop(const Operand<T::HA, T::AT, T::IA, T::
     // LEFT: steps after this one (2: two or more)
     auto step = [&](auto left, int s) {
         constexpr int LEFT = decltype(left)::value;
-        // loads that may still be in flight at each phase's end: six halves,
-        // fewer where nothing more is issued
-        constexpr int W0 = LEFT == 2 ? 6 : LEFT == 1 ? 5 : 1, W1 = LEFT == 2 ? 6 : LEFT == 1 ? 4 : 0;
-        constexpr int W2 = LEFT == 2 ? 6 : LEFT == 1 ? 3 : 0, W3 = LEFT == 2 ? 6 : LEFT == 1 ? 2 : 0;
+        // loads that may still be in flight at each phase's end: six halves
+        // (three of each operand), fewer where nothing more is issued
+        constexpr int W0 = LEFT == 2 ? 3 * IA + 3 * IB : LEFT == 1 ? 3 * IA + 2 * IB : IA;
+        constexpr int W1 = LEFT == 2 ? 3 * IA + 3 * IB : LEFT == 1 ? 2 * IA + 2 * IB : 0;
+        constexpr int W2 = LEFT == 2 ? 3 * IA + 3 * IB : LEFT == 1 ? 2 * IA + IB : 0;
+        constexpr int W3 = LEFT == 2 ? 3 * IA + 3 * IB : LEFT == 1 ? IA + IB : 0;
         read_a(0, s);
         if constexpr (LEFT == 2) issue_b(0, s + 2);
-        phase_barrier<W0 * I>();
+        phase_barrier<W0>();
         multiply(0, 0);
         read_b(1, s);
         if constexpr (LEFT == 2) issue_a(0, s + 2);
-        phase_barrier<W1 * I>();
+        phase_barrier<W1>();
         multiply(0, 1);
         read_a(1, s);
         if constexpr (LEFT == 2) issue_b(1, s + 2);
-        phase_barrier<W2 * I>();
+        phase_barrier<W2>();
         multiply(1, 0);
         if constexpr (LEFT >= 1) read_b(0, s + 1);
         if constexpr (LEFT == 2) issue_a(1, s + 2);
-        phase_barrier<W3 * I>();
+        phase_barrier<W3>();
         multiply(1, 1);
     };
     // the first two steps' loads, in the order of their use
@@ -363,10 +364,10 @@ __device__ __forceinline__ void main_loop(const Operand<T::HA, T::AT, T::IA, T::
             issue_a(1, s);
         }
     }
-    if (steps > 1) phase_barrier<6 * I>();
-    else phase_barrier<2 * I>();
+    if (steps > 1) phase_barrier<3 * IA + 3 * IB>();
+    else phase_barrier<IA + IB>();
     read_b(0, 0);
-    phase_barrier<6 * I>();
+    phase_barrier<3 * IA + 3 * IB>();
     if (PP && wave >= T::NW / 2) plain_barrier();
     int s = 0;
     for (; s + 2 < steps; ++s) step(std::integral_constant<int, 2>{}, s);
@@ -392,18 +393,46 @@ struct Place {
 // tile rows per tile column (neighbours on one XCD share rows and columns in
 // its L2).  The run is cut from the live tiles, so that a batch with few live
 // rows still spreads over every XCD.
-__device__ __forceinline__ bool map_tile(int bid, int tm_n, int tn_n, int& tm, int& tn, int& rest, int parts) {
-    const int T = tm_n * tn_n, G = T * parts;
-    if (bid >= G) return false;
+__device__ __forceinline__ int xcd_run(int bid, int G) {
     const int q = G >> 3, r = G & 7, x = bid & 7;
-    const int L = x * q + min(x, r) + (bid >> 3);
-    rest = L / T;
-    const int tile = L - rest * T;
+    return x * q + min(x, r) + (bid >> 3);
+}
+__device__ __forceinline__ void tile_at(int tile, int tm_n, int tn_n, int& tm, int& tn) {
     constexpr int GROUP = 8;
     const int per = GROUP * tn_n, g = tile / per, first = g * GROUP;
     const int gsz = min(tm_n - first, GROUP), in = tile - g * per;
     tm = first + in % gsz;
     tn = in / gsz;
+}
+__device__ __forceinline__ bool map_tile(int bid, int tm_n, int tn_n, int& tm, int& tn, int& rest, int parts) {
+    const int T = tm_n * tn_n, G = T * parts;
+    if (bid >= G) return false;
+    const int L = xcd_run(bid, G);
+    rest = L / T;
+    tile_at(L - rest * T, tm_n, tn_n, tm, tn);
+    return true;
+}
+
+// The logit tiles of a launch.  Tiles of one size run in rounds of `slots`
+// workgroups; when the last round would be at most half full, its tiles are
+// halved (two workgroups of half the rows each), which takes about 0.6 of a
+// whole tile's round instead of one.  half: -1 a whole tile, else which half.
+__device__ __forceinline__ bool map_rounds(int bid, int tm_n, int tn_n, int slots, bool halves, int& tm, int& tn, int& half) {
+    const int T = tm_n * tn_n, full = T / slots * slots, r = T - full;
+    half = -1;
+    if (!halves || 2 * r > slots) {
+        if (bid >= T) return false;
+        tile_at(xcd_run(bid, T), tm_n, tn_n, tm, tn);
+        return true;
+    }
+    if (bid < full) {
+        tile_at(xcd_run(bid, full), tm_n, tn_n, tm, tn);
+        return true;
+    }
+    bid -= full;
+    if (bid >= 2 * r) return false;
+    half = bid >= r ? 1 : 0;
+    tile_at(full + bid - half * r, tm_n, tn_n, tm, tn);
     return true;
 }
 
@@ -482,18 +511,14 @@ __device__ __forceinline__ int row_label(const LossArgs& a, int m, int n) {
 // s2 loses is put back where the tiles are joined.  A lane reduces its own 16
 // values of a row; the 4 lanes and the waves that share the row meet in LDS.
 template <class T, bool TG>
-__global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
-    constexpr int TAB = TG ? T::HA * (T::BN + 4) * 4 : 0;
+constexpr int forward_lds() {
+    const int tab = TG ? T::HA * (T::BN + 4) * 4 : 0, red = T::BM * (8 * T::WGN + 2) * 4;
+    return std::max(T::LDS, std::max(tab, red));
+}
+template <class T, bool TG>
+__device__ __forceinline__ void forward_tile(const LossArgs& a, int n, int m0, int tn, lds_t* smem, int wave, int lane) {
     constexpr int PARTS = 4 * T::WGN, LDP = 2 * PARTS + 2;   // floats per row
-    constexpr int RED = T::BM * LDP * 4;
-    constexpr int NEED = TAB > RED ? TAB : RED;
-    __shared__ __attribute__((aligned(1024))) unsigned char raw[T::LDS > NEED ? T::LDS : NEED];
-    lds_t* smem = (lds_t*)raw;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n = a.direct ? (int)a.M : a.hdr->n;
-    int tm, tn, rest;
-    if (!map_tile(blockIdx.x, (n + T::BM - 1) / T::BM, a.ntiles, tm, tn, rest, 1)) return;
-    const int m0 = tm * T::BM, v0 = tn * T::BN;
+    const int tid = wave * 64 + lane, v0 = tn * T::BN;
     Acc<T> acc;
     logits_tile<T>(a, m0, v0, n, smem, wave, lane, acc);
     const Place<T> at(wave, lane);
@@ -630,6 +655,20 @@ __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
     }
 }
 
+template <class T, class H, bool TG>
+__global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char raw[std::max(forward_lds<T, TG>(), forward_lds<H, TG>())];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = a.direct ? (int)a.M : a.hdr->n;
+    int tm, tn, half;
+    if (!map_rounds(blockIdx.x, (n + T::BM - 1) / T::BM, a.ntiles, a.slots, T::BM > H::BM, tm, tn, half)) return;
+    if (half < 0) {
+        forward_tile<T, TG>(a, n, tm * T::BM, tn, (lds_t*)raw, wave, lane);
+    } else if (tm * T::BM + half * H::BM < n) {
+        forward_tile<H, TG>(a, n, tm * T::BM + half * H::BM, tn, (lds_t*)raw, wave, lane);
+    }
+}
+
 // Sum and maximum over the workgroup's 256 threads.
 __device__ __forceinline__ float block_sum(float v, float* buf) {
 #pragma unroll
@@ -762,79 +801,109 @@ __device__ __forceinline__ float usable_gref(float g) { return (g > 0.0f && g < 
 // with what a tile costs besides (filling and draining the pipeline, writing
 // and summing a partial) taken as 10: the whole number of splits, of at most
 // two rounds of workgroups and at least four steps each, for which the work
-// of dX's and dW's tiles (they run in one launch) over the workgroups that
-// run at once, and half the longest tile, come out least.  256 threads.
-__device__ __forceinline__ int dx_splits(const LossArgs& a, int n, float* buf) {
+// of dX's and dW's tiles (they run in one launch, dX's first) over the
+// workgroups that run at once, and half a tile of what runs last, come out
+// least.  One wave.
+__device__ __forceinline__ int dx_splits(const LossArgs& a, int n, int lane) {
     const int tile = a.tile, tk = (a.K + tile - 1) / tile;
     const int tiles = max(1, (n + tile - 1) / tile * tk), all = a.Vp >> 6;
     const float rest = a.dW != nullptr ? (float)((a.Vp + tile - 1) / tile * tk) * ((n + 63) / 64 + 10.0f) : 0.0f;
     const float rest_one = a.dW != nullptr ? (n + 63) / 64 + 10.0f : 0.0f;
-    float best = -INFINITY;   // minus (cost, then splits), so that a maximum finds it
+    float best = -INFINITY;   // minus the cost
     int mine = 1;
-    for (int s = 1 + threadIdx.x; s == 1 || (s * tiles <= 2 * a.slots && s * 4 <= all); s += 256) {
+    for (int s = 1 + lane; s == 1 || (s * tiles <= 2 * a.slots && s * 4 <= all); s += 64) {
         const float one = (float)((all + s - 1) / s) + 10.0f;
         const float work = rest + (float)(tiles * s) * one;
-        const float cost = fmaxf(work / (float)a.slots, fmaxf(one, rest_one)) + 0.5f * fmaxf(one, rest_one);
+        const float cost = fmaxf(work / (float)a.slots, one) + 0.5f * (rest > 0.0f ? rest_one : one);
         if (-cost > best) {
             best = -cost;
             mine = s;
         }
     }
-    const float top = block_max(best, buf);
-    return (int)-block_max(best == top ? -(float)mine : -INFINITY, buf);
+    float top = best;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    int least = best == top ? mine : 1 << 30;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) least = min(least, __shfl_xor(least, o));
+    return least;
 }
 
-// For many rows: each row's place among the live ones (pos, -1 without a
-// target), their number, the largest |dloss| and dX's splits.  One workgroup.
-__global__ __launch_bounds__(256) void loss_scan_kernel(LossArgs a) {
-    __shared__ int wsum[4];
-    __shared__ float buf[4];
+// For more than a few thousand rows: each row's place among the live ones
+// (pos, -1 without a target), their number, the largest |dloss| and dX's
+// splits.  One workgroup, eight consecutive rows a thread at a time.
+__global__ __launch_bounds__(1024) void loss_scan_kernel(LossArgs a) {
+    __shared__ int wsum[16];
+    __shared__ float buf[16];
+    constexpr int U = 8;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int base = 0;
     float g = 0.0f;
-    for (int64_t m0 = 0; m0 < a.M; m0 += 256) {
-        const int64_t m = m0 + tid;
-        const bool on = m < a.M && row_live(a, m);
-        const unsigned long long b = __ballot(on);
-        if (lane == 0) wsum[wave] = __popcll(b);
-        __syncthreads();
-        int before = base, all = 0;
+    for (int64_t m0 = 0; m0 < a.M; m0 += 1024 * U) {
+        const int64_t first = m0 + tid * U;
+        bool on[U];
+        float d[U];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            before += w < wave ? wsum[w] : 0;
+        for (int u = 0; u < U; ++u) {
+            const int64_t m = min(first + u, a.M - 1);
+            on[u] = row_live(a, m) && first + u < a.M;
+            d[u] = a.dloss != nullptr ? a.dloss[m] : 0.0f;
+        }
+        int mine = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mine += on[u] ? 1 : 0;
+            if (on[u]) g = fmaxf(g, fabsf(d[u]));
+        }
+        int upto = mine;   // of this wave's threads up to this one
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int t = __shfl_up(upto, o);
+            if (lane >= o) upto += t;
+        }
+        if (lane == 63) wsum[wave] = upto;
+        __syncthreads();
+        int at = base + upto - mine, all = 0;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            at += w < wave ? wsum[w] : 0;
             all += wsum[w];
         }
-        if (m < a.M) a.pos[m] = on ? before + __popcll(b & ((1ull << lane) - 1ull)) : -1;
-        if (on && a.dloss != nullptr) g = fmaxf(g, fabsf(a.dloss[m]));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (first + u < a.M) {
+                a.pos[first + u] = on[u] ? at : -1;
+                at += on[u] ? 1 : 0;
+            }
         base += all;
         __syncthreads();
     }
-    g = block_max(g, buf);
-    const int splits = a.dloss != nullptr ? dx_splits(a, base, buf) : 1;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) g = fmaxf(g, __shfl_xor(g, o));
+    if (lane == 0) buf[wave] = g;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 16; ++w) g = fmaxf(g, buf[w]);
+    if (wave > 0) return;
+    const int splits = a.dloss != nullptr ? dx_splits(a, base, lane) : 1;
     if (tid == 0) *a.hdr = LossHeader{base, usable_gref(g), splits};
 }
 
-// Copy one row of X to compact row c, zero padded to Kp columns (m < 0: zeros).
-__device__ __forceinline__ void copy_row(const LossArgs& a, int64_t m, int c, int t, int nt) {
-    const uint16_t* src = a.X + m * a.ldx;
-    uint16_t* dst = a.Xc + (int64_t)c * a.Kp;
-    const bool vec = m >= 0 && ((uintptr_t)src & 15) == 0;
-    for (int k = t * 8; k < a.Kp; k += nt * 8) {
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (vec && k + 8 <= a.K) {
-            v = *(const u32x4*)(src + k);
-        } else if (m >= 0) {
+// 8 values of row m of X from column k on, zeros past K (and for m < 0).
+__device__ __forceinline__ u32x4 row_chunk(const LossArgs& a, int64_t m, int k) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (m < 0) return v;
+    const uint16_t* src = a.X + m * a.ldx + k;
+    if (((uintptr_t)src & 15) == 0 && k + 8 <= a.K) return *(const u32x4*)src;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (k + e < a.K) v[e >> 1] |= (uint32_t)src[k + e] << (16 * (e & 1));
-        }
-        *(u32x4*)(dst + k) = v;
-    }
+    for (int e = 0; e < 8; ++e)
+        if (k + e < a.K) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+    return v;
 }
 
 // One wave: compact row c's targets and gradient constants, from row m.
 template <bool BWD>
-__device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c, float gref, int lane) {
+__device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c, float gref, int lane, int* sid, float* sp) {
     float rel = 1.0f, lse2 = 0.0f;
     if constexpr (BWD) {
         rel = a.dloss[m] / gref;
@@ -857,47 +926,47 @@ __device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c,
         return;
     }
     int* ids = a.ids32 + (int64_t)c * a.kp;
-    const float* t = a.teacher + m * a.ldt;
     if constexpr (!BWD) {
         for (int j = lane; j < a.kp; j += 64) ids[j] = j < a.k && target_ok(a, m, j) ? (int)a.ids[m * a.ldids + j] : -1;
     } else {
+        // the row's ids (-1: left out) and probabilities, staged in LDS
+        const float* t = a.teacher + m * a.ldt;
         const float it = 1.0f / a.T;
-        float tl;
+        float tl = 0.0f, tm = -INFINITY, ts = 0.0f, all = 0.0f;
+        for (int j = lane; j < a.k; j += 64) {
+            const bool ok = target_ok(a, m, j);
+            sid[j] = ok ? (int)a.ids[m * a.ldids + j] : -1;
+            if (ok) tm = fmaxf(tm, t[j] * it);
+        }
         if (a.teacher_lse != nullptr) {
             tl = a.teacher_lse[m];
         } else {
-            float tm = -INFINITY, ts = 0.0f;
-            for (int j = lane; j < a.k; j += 64)
-                if (target_ok(a, m, j)) tm = fmaxf(tm, t[j] * it);
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) tm = fmaxf(tm, __shfl_xor(tm, o));
             for (int j = lane; j < a.k; j += 64)
-                if (target_ok(a, m, j)) ts += exp2_fast(kLog2e * (t[j] * it - tm));
+                if (sid[j] >= 0) ts += exp2_fast(kLog2e * (t[j] * it - tm));
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) ts += __shfl_xor(ts, o);
             tl = tm + kLn2 * __builtin_amdgcn_logf(ts);
         }
+        for (int j = lane; j < a.k; j += 64) {
+            sp[j] = sid[j] >= 0 ? exp2_fast(kLog2e * (t[j] * it - tl)) : 0.0f;
+            all += sp[j];
+        }
+        __builtin_amdgcn_wave_barrier();   // (one wave's own LDS: its operations stay in order)
         // weights; a target named twice keeps its weight at its first place
-        float all = 0.0f;
         float* w = a.wts + (int64_t)c * a.kp;
         for (int j = lane; j < a.kp; j += 64) {
+            const int id = j < a.k ? sid[j] : -1;
+            bool first = id >= 0;
             float p = 0.0f;
-            int keep = -1;
-            if (j < a.k && target_ok(a, m, j)) {
-                const int64_t id = a.ids[m * a.ldids + j];
-                keep = (int)id;
-                all += exp2_fast(kLog2e * (t[j] * it - tl));
-                for (int u = 0; u < a.k; ++u) {
-                    if (a.ids[m * a.ldids + u] != id || !target_ok(a, m, u)) continue;
-                    if (u < j) {
-                        keep = -1;
-                        break;
-                    }
-                    p += exp2_fast(kLog2e * (t[u] * it - tl));
-                }
+            for (int u = 0; u < a.k; ++u) {
+                const bool same = sid[u] == id;
+                if (same && u < j) first = false;
+                if (same) p += sp[u];
             }
-            ids[j] = keep;
-            w[j] = keep >= 0 ? rel * p : 0.0f;
+            ids[j] = first ? id : -1;
+            w[j] = first ? rel * p : 0.0f;
         }
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) all += __shfl_xor(all, o);
@@ -906,16 +975,18 @@ __device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c,
 }
 
 // Compacts the live rows of X with their targets, and clears what rows without
-// a target get.  A workgroup takes kGatherRows rows; unless SCANNED (many
+// a target get.  A workgroup takes four rows, a wave each; unless SCANNED (many
 // rows: loss_scan_kernel has run) it counts the live rows before them and
 // altogether by itself, which is cheaper than a launch that does.  The rows
 // behind the last live one, up to a whole K step of dW's product, are zeroed.
-constexpr int kGatherRows = 16;
+constexpr int kGatherRows = 4;
 template <bool BWD, bool SCANNED>
 __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
     __shared__ float buf[4];
     __shared__ int cnt[2][4];
     __shared__ int places[kGatherRows];
+    __shared__ int sid[BWD ? 4 : 1][BWD ? kMaxTargets : 1];
+    __shared__ float sp[BWD ? 4 : 1][BWD ? kMaxTargets : 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t r0 = (int64_t)blockIdx.x * kGatherRows;
     int n, before = 0;
@@ -927,11 +998,23 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
     } else {
         int b = 0, all = 0;
         float g = 0.0f;
-        for (int64_t m = tid; m < a.M; m += 256) {
-            if (!row_live(a, m)) continue;
-            b += m < r0 ? 1 : 0;
-            all += 1;
-            if (BWD) g = fmaxf(g, fabsf(a.dloss[m]));
+        // (eight rows a thread at a time, so that their loads overlap)
+        constexpr int U = 8;
+        for (int64_t m0 = tid; m0 < a.M; m0 += 256 * U) {
+            bool on[U];
+            float d[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t m = m0 + 256 * u, at = min(m, a.M - 1);
+                on[u] = row_live(a, at) && m < a.M;
+                d[u] = BWD ? a.dloss[at] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                b += on[u] && m0 + 256 * u < r0 ? 1 : 0;
+                all += on[u] ? 1 : 0;
+                if (on[u]) g = fmaxf(g, fabsf(d[u]));
+            }
         }
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -946,9 +1029,9 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
         before = (cnt[0][0] + cnt[0][1]) + (cnt[0][2] + cnt[0][3]);
         n = (cnt[1][0] + cnt[1][1]) + (cnt[1][2] + cnt[1][3]);
         if constexpr (BWD) gref = usable_gref(block_max(g, buf));
-        if (blockIdx.x == 0) {
-            const int splits = BWD ? dx_splits(a, n, buf) : 1;
-            if (tid == 0) *a.hdr = LossHeader{n, gref, splits};
+        if (blockIdx.x == 0 && wave == 1) {
+            const int splits = BWD ? dx_splits(a, n, lane) : 1;
+            if (lane == 0) *a.hdr = LossHeader{n, gref, splits};
         }
         if (wave == 0) {
             const int64_t m = r0 + lane;
@@ -959,28 +1042,42 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
         }
     }
     __syncthreads();
-    for (int r = wave; r < kGatherRows; r += 4) {
-        const int c = places[r];
-        const int64_t m = r0 + r;
-        if (c == -2) break;
+    const int c = places[wave];
+    const int64_t m = r0 + wave;
+    if (c != -2) {
         if (c < 0) {
             if constexpr (!BWD) {
                 if (lane == 0) a.loss[m] = a.lse[m] = 0.0f;
             } else if (a.dX != nullptr) {
-                for (int k = lane; k < a.K; k += 64) {
-                    if (a.grad_f32) ((float*)a.dX)[m * a.lddx + k] = 0.0f;
-                    else ((uint16_t*)a.dX)[m * a.lddx + k] = 0;
-                }
+                // 16 bytes at a time from the row's first such boundary on
+                const int es = a.grad_f32 ? 4 : 2;
+                char* d = (char*)a.dX + m * a.lddx * es;
+                const int64_t bytes = (int64_t)a.K * es;
+                const int64_t head = min(bytes, (int64_t)((16 - ((uintptr_t)d & 15)) & 15));
+                const int64_t body = head + ((bytes - head) & ~int64_t(15));
+                for (int64_t b = head + lane * 16; b < body; b += 1024) *(u32x4*)(d + b) = u32x4{0u, 0u, 0u, 0u};
+                for (int64_t b = lane * 2; b < head; b += 128) *(uint16_t*)(d + b) = 0;
+                for (int64_t b = body + lane * 2; b < bytes; b += 128) *(uint16_t*)(d + b) = 0;
             }
-            continue;
+        } else {
+            if (lane == 0) a.map[c] = (int)m;
+            // the row itself, several loads a lane in flight, then its targets
+            constexpr int U = 8;
+            for (int k0 = lane * 8; k0 < a.Kp; k0 += 512 * U) {
+                u32x4 v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) v[u] = row_chunk(a, k0 + 512 * u < a.Kp ? m : -1, k0 + 512 * u);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (k0 + 512 * u < a.Kp) *(u32x4*)(a.Xc + (int64_t)c * a.Kp + k0 + 512 * u) = v[u];
+            }
+            row_targets<BWD>(a, m, c, gref, lane, sid[BWD ? wave : 0], sp[BWD ? wave : 0]);
         }
-        if (lane == 0) a.map[c] = (int)m;
-        copy_row(a, m, c, lane, 64);
-        row_targets<BWD>(a, m, c, gref, lane);
     }
     // (at most 63 rows, over the workgroups' waves)
     const int pad = ((n + 63) & ~63) - n;
-    for (int p = blockIdx.x * 4 + wave; p < pad; p += gridDim.x * 4) copy_row(a, -1, n + p, lane, 64);
+    for (int p = blockIdx.x * 4 + wave; p < pad; p += gridDim.x * 4)
+        for (int k = lane * 8; k < a.Kp; k += 512) *(u32x4*)(a.Xc + (int64_t)(n + p) * a.Kp + k) = row_chunk(a, -1, k);
 }
 
 // ---- backward ---------------------------------------------------------------
@@ -992,18 +1089,15 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
 // divided by.  G is rounded to bf16 (relative 2^-9 of each entry, to
 // nearest) because the products that follow run on bf16 MFMA.
 template <class T, bool TG>
-__global__ __launch_bounds__(T::NT) void loss_grad_kernel(LossArgs a) {
+constexpr int grad_lds() {
+    const int tab = TG ? T::HA * (T::BN + 4) * 4 : 0, stage = T::BM * (T::BN * 2 + 16);
+    return std::max(T::LDS, std::max(tab, stage));
+}
+template <class T, bool TG>
+__device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int tn, lds_t* smem, int wave, int lane) {
     constexpr int LDG = T::BN * 2 + 16;   // bytes of a staged row
-    constexpr int TAB = TG ? T::HA * (T::BN + 4) * 4 : 0;
-    constexpr int STG = T::BM * LDG;
-    constexpr int NEED = TAB > STG ? TAB : STG;
-    __shared__ __attribute__((aligned(1024))) unsigned char raw[T::LDS > NEED ? T::LDS : NEED];
-    lds_t* smem = (lds_t*)raw;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n = a.hdr->n;
-    int tm, tn, rest;
-    if (!map_tile(blockIdx.x, (n + T::BM - 1) / T::BM, (a.vn + T::BN - 1) / T::BN, tm, tn, rest, 1)) return;
-    const int m0 = tm * T::BM, p0 = tn * T::BN, v0 = a.v0 + p0;
+    const int tid = wave * 64 + lane;
+    const int p0 = tn * T::BN, v0 = a.v0 + p0;
     Acc<T> acc;
     logits_tile<T>(a, m0, v0, n, smem, wave, lane, acc);
     const Place<T> at(wave, lane);
@@ -1119,31 +1213,38 @@ __global__ __launch_bounds__(T::NT) void loss_grad_kernel(LossArgs a) {
     }
     if constexpr (TG) __syncthreads();
     if (a.dbp != nullptr) {
-        // column sums over the tile's rows: a lane's rows, the 16 lanes of a
-        // group, then (through LDS) the waves that share the columns
+        // column sums over 128 rows each (all of the tile's, or each half's):
+        // a lane's rows, the 16 lanes of a group, then (through LDS) the waves
+        // that share the columns
+        constexpr int PARTS = T::BM / kDbiasRows, PER = 2 / PARTS;
+        static_assert(T::BM == 128 || T::BM == 256, "column sums of 128 rows");
         float __attribute__((address_space(3)))* red = (float __attribute__((address_space(3)))*)smem;
 #pragma unroll
-        for (int hb = 0; hb < 2; ++hb)
+        for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-            for (int j = 0; j < T::FN; ++j) {
-                f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-                for (int ha = 0; ha < 2; ++ha)
+                for (int j = 0; j < T::FN; ++j) {
+                    f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < T::FM; ++i) t += acc[ha][hb][i][j];
+                    for (int h = 0; h < PER; ++h)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
+                        for (int i = 0; i < T::FM; ++i) t += acc[part * PER + h][hb][i][j];
 #pragma unroll
-                    for (int o = 1; o < 16; o <<= 1) t[r] += __shfl_xor(t[r], o);
-                    if (at.s == 0) red[at.wm * T::BN + at.col(hb, j) + r] = t[r];
+                    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+                        for (int o = 1; o < 16; o <<= 1) t[r] += __shfl_xor(t[r], o);
+                        if (at.s == 0) red[(part * T::WGM + at.wm) * T::BN + at.col(hb, j) + r] = t[r];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-            }
         __syncthreads();
-        for (int c = tid; c < T::BN; c += T::NT) {
+        for (int e = tid; e < PARTS * T::BN; e += T::NT) {
+            const int part = e / T::BN, c = e % T::BN;
             float t = 0.0f;
 #pragma unroll
-            for (int w = 0; w < T::WGM; ++w) t += red[w * T::BN + c];
-            a.dbp[(int64_t)tm * a.Vp + p0 + c] = t;
+            for (int w = 0; w < T::WGM; ++w) t += red[(part * T::WGM + w) * T::BN + c];
+            a.dbp[(int64_t)(m0 / kDbiasRows + part) * a.Vp + p0 + c] = t;
         }
         __syncthreads();
     }
@@ -1168,6 +1269,23 @@ __global__ __launch_bounds__(T::NT) void loss_grad_kernel(LossArgs a) {
         const int r = p / CPR, c = p % CPR;
         *(u32x4*)(G + (int64_t)r * a.Vp + c * 8) =
             *(const u32x4 __attribute__((address_space(3)))*)(smem + r * LDG + c * 16);
+    }
+}
+
+template <class T, class H, bool TG>
+__global__ __launch_bounds__(T::NT) void loss_grad_kernel(LossArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char raw[std::max(grad_lds<T, TG>(), grad_lds<H, TG>())];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = a.hdr->n;
+    int tm, tn, half;
+    if (!map_rounds(blockIdx.x, (n + T::BM - 1) / T::BM, (a.vn + T::BN - 1) / T::BN, a.slots, T::BM > H::BM, tm, tn, half))
+        return;
+    // (a half without a live row is not multiplied: an operand's rows are
+    // clamped to the live ones, of which it has none)
+    if (half < 0) {
+        grad_tile<T, TG>(a, n, tm * T::BM, tn, (lds_t*)raw, wave, lane);
+    } else if (tm * T::BM + half * H::BM < n) {
+        grad_tile<H, TG>(a, n, tm * T::BM + half * H::BM, tn, (lds_t*)raw, wave, lane);
     }
 }
 
@@ -1327,10 +1445,10 @@ __global__ __launch_bounds__(TX::NT) void loss_products_kernel(LossArgs a, float
 }
 
 // dbias of a piece: gref unit (sum over the row tiles, in order).
-__global__ __launch_bounds__(256) void loss_dbias_kernel(LossArgs a, float mul, int row_tile) {
+__global__ __launch_bounds__(256) void loss_dbias_kernel(LossArgs a, float mul) {
     const int p = blockIdx.x * 256 + threadIdx.x;
     if (p >= a.vn) return;
-    const int tiles = (a.hdr->n + row_tile - 1) / row_tile;
+    const int tiles = (a.hdr->n + kDbiasRows - 1) / kDbiasRows;
     float t = 0.0f;
     for (int i = 0; i < tiles; ++i) t += a.dbp[(int64_t)i * a.Vp + p];
     a.dbias[a.v0 + p] = t * (mul * a.hdr->gref);
@@ -1338,6 +1456,8 @@ __global__ __launch_bounds__(256) void loss_dbias_kernel(LossArgs a, float mul, 
 
 template <bool AT, bool BT>
 using L256 = LTile<2, 4, 4, 2, AT, BT>;
+template <bool AT, bool BT>
+using L256Half = LTile<2, 4, 2, 2, AT, BT>;   // half the rows of L256
 template <bool AT, bool BT>
 using L128 = LTile<2, 2, 2, 2, AT, BT>;
 
@@ -1358,7 +1478,7 @@ hipError_t launch_loss_flags(const LossArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_loss_scan(const LossArgs& a, hipStream_t st) {
-    return launch_kernel(loss_scan_kernel, dim3(1), dim3(256), st, a);
+    return launch_kernel(loss_scan_kernel, dim3(1), dim3(1024), st, a);
 }
 
 hipError_t launch_loss_gather(const LossArgs& a, bool scanned, hipStream_t st) {
@@ -1372,15 +1492,17 @@ hipError_t launch_loss_gather(const LossArgs& a, bool scanned, hipStream_t st) {
 
 hipError_t launch_loss_forward(const LossArgs& a, hipStream_t st) {
     const bool tg = a.labels == nullptr;
-    const dim3 grid((unsigned)(up(a.M, a.tile) * a.ntiles));
+    // (halved tiles of a last round: at most slots / 2 workgroups more)
+    const dim3 grid((unsigned)(up(a.M, a.tile) * a.ntiles + (a.tile == 256 ? a.slots / 2 : 0)));
     if (a.tile == 256) {
         using T = L256<false, false>;
-        return tg ? launch_kernel(loss_forward_kernel<T, true>, grid, dim3(T::NT), st, a)
-                  : launch_kernel(loss_forward_kernel<T, false>, grid, dim3(T::NT), st, a);
+        using H = L256Half<false, false>;
+        return tg ? launch_kernel(loss_forward_kernel<T, H, true>, grid, dim3(T::NT), st, a)
+                  : launch_kernel(loss_forward_kernel<T, H, false>, grid, dim3(T::NT), st, a);
     }
     using T = L128<false, false>;
-    return tg ? launch_kernel(loss_forward_kernel<T, true>, grid, dim3(T::NT), st, a)
-              : launch_kernel(loss_forward_kernel<T, false>, grid, dim3(T::NT), st, a);
+    return tg ? launch_kernel(loss_forward_kernel<T, T, true>, grid, dim3(T::NT), st, a)
+              : launch_kernel(loss_forward_kernel<T, T, false>, grid, dim3(T::NT), st, a);
 }
 
 hipError_t launch_loss_finish(const LossArgs& a, hipStream_t st) {
@@ -1389,16 +1511,17 @@ hipError_t launch_loss_finish(const LossArgs& a, hipStream_t st) {
 
 hipError_t launch_loss_grad(const LossArgs& a, hipStream_t st) {
     const bool tg = a.labels == nullptr;
+    // (halved tiles of a last round: at most slots / 2 workgroups more)
+    const dim3 grid((unsigned)(up(a.M, a.tile) * up(a.vn, a.tile) + (a.tile == 256 ? a.slots / 2 : 0)));
     if (a.tile == 256) {
         using T = L256<false, false>;
-        const dim3 grid((unsigned)(up(a.M, T::BM) * up(a.vn, T::BN)));
-        return tg ? launch_kernel(loss_grad_kernel<T, true>, grid, dim3(T::NT), st, a)
-                  : launch_kernel(loss_grad_kernel<T, false>, grid, dim3(T::NT), st, a);
+        using H = L256Half<false, false>;
+        return tg ? launch_kernel(loss_grad_kernel<T, H, true>, grid, dim3(T::NT), st, a)
+                  : launch_kernel(loss_grad_kernel<T, H, false>, grid, dim3(T::NT), st, a);
     }
     using T = L128<false, false>;
-    const dim3 grid((unsigned)(up(a.M, T::BM) * up(a.vn, T::BN)));
-    return tg ? launch_kernel(loss_grad_kernel<T, true>, grid, dim3(T::NT), st, a)
-              : launch_kernel(loss_grad_kernel<T, false>, grid, dim3(T::NT), st, a);
+    return tg ? launch_kernel(loss_grad_kernel<T, T, true>, grid, dim3(T::NT), st, a)
+              : launch_kernel(loss_grad_kernel<T, T, false>, grid, dim3(T::NT), st, a);
 }
 
 hipError_t launch_loss_products(const LossArgs& a, hipStream_t st) {
@@ -1418,7 +1541,7 @@ hipError_t launch_loss_dx_finish(const LossArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_loss_dbias(const LossArgs& a, hipStream_t st) {
-    return launch_kernel(loss_dbias_kernel, dim3((unsigned)up(a.vn, 256)), dim3(256), st, a, unit_of(a), a.tile);
+    return launch_kernel(loss_dbias_kernel, dim3((unsigned)up(a.vn, 256)), dim3(256), st, a, unit_of(a));
 }
 
 }  // namespace mkp

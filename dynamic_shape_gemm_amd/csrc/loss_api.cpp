@@ -29,13 +29,12 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-constexpr int kMaxTargets = 1024;
 // columns of X and W: a tile's 256 rows stay within 32-bit byte offsets
 constexpr int64_t kMaxK = int64_t(1) << 21;
 // above this many rows one workgroup counts the live ones; below, every
 // workgroup of the gather does so for itself
-constexpr int64_t kManyRows = 16384;
-constexpr int64_t kPieceBytes = int64_t(256) << 20;   // G of one piece
+constexpr int64_t kManyRows = 4096;
+constexpr int64_t kPieceBytes = int64_t(512) << 20;   // G of one piece
 
 // A call's extents and where its workspace's parts lie.
 struct Layout {
@@ -87,7 +86,7 @@ Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int6
         const int64_t one = l.Mr * l.Kp, steps = l.Vp / 64;
         const int64_t split = std::min<int64_t>(2 * l.slots * l.tile * l.tile, std::max<int64_t>(1, steps / 4) * one);
         l.dxp = take(4 * std::max(one, split));
-        l.dbp = take(4 * ceil_div(std::max<int64_t>(M, 1), l.tile) * l.Vp);
+        l.dbp = take(4 * std::max<int64_t>(1, l.Mr / kDbiasRows) * l.Vp);
     }
     l.bytes = at;
     return l;
@@ -176,7 +175,7 @@ int run(const Call& c) {
     if (!c.ws || c.ws_bytes < 0 || (size_t)c.ws_bytes < l.bytes || !aligned16(c.ws))
         return report(MKP_ERR_INVALID_ARG,
                       "workspace of " + std::to_string(l.bytes) + " bytes, 16-byte aligned, needed");
-    if (ceil_div(c.M, l.tile) * l.ntiles > INT_MAX || l.Mr > INT_MAX / 2)
+    if (ceil_div(c.M, l.tile) * l.ntiles > INT_MAX / 2 || l.Mr > INT_MAX / 2)
         return report(MKP_ERR_UNSUPPORTED, "grid too large");
     begin_call();
     hipStream_t st = (hipStream_t)c.stream;
@@ -292,7 +291,7 @@ int run(const Call& c) {
                          [&] { return launch_loss_products(a, st); })) != MKP_OK)
                 return rc;
         if (c.dbias)
-            if ((rc = go(LL_DBIAS, 0.0, 4.0 * pv * (double)ceil_div(c.M, l.tile), [&] { return launch_loss_dbias(a, st); })) !=
+            if ((rc = go(LL_DBIAS, 0.0, 4.0 * pv * (double)ceil_div(c.M, kDbiasRows), [&] { return launch_loss_dbias(a, st); })) !=
                 MKP_OK)
                 return rc;
     }

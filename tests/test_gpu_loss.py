@@ -270,9 +270,9 @@ def test_only_the_gradients_asked_for(mkp, M):
 def test_several_pieces_of_the_vocabulary(mkp, op):
     """Enough rows and a wide enough vocabulary that the gradient takes more
     than one piece and dX more than one tile of rows."""
-    t = inputs(21, 4200, 40000, 64, bias=True, k=6 if op == "distill" else 0, keep=0.9)
-    ws1 = mkp.mkp_linear_loss_workspace(4200, 40000, 64, 0, t["w"], 64, True)
-    assert ws1 < 2 * 4200 * 40000   # less than the whole gradient by the logits
+    t = inputs(21, 4200, 70000, 64, bias=True, k=6 if op == "distill" else 0, keep=0.9)
+    ws1 = mkp.mkp_linear_loss_workspace(4200, 70000, 64, 0, t["w"], 64, True)
+    assert ws1 < 2 * 4200 * 70000   # less than the whole gradient by the logits
     check(mkp, t, op + " pieces", **({"temperature": 2.0} if op == "distill" else {"smoothing": 0.05}))
 
 
