@@ -1322,17 +1322,45 @@ __device__ __forceinline__ void dx_tile(const LossArgs& a, int n, int tm, int tn
                 }
 }
 
-// dX = gref unit scale (sum of the partials), in the rows' own places.
+// dX = gref unit scale (sum of the partials), in the rows' own places.  One
+// workgroup per row; where a row has fewer than 128 runs of four features,
+// several threads share each run's splits and join through LDS, in order.
 __global__ __launch_bounds__(256) void loss_dx_finish_kernel(LossArgs a, float mul, int tile) {
+    __shared__ f32x4 buf[256];
     const int c = blockIdx.x, n = a.hdr->n, splits = a.hdr->splits;
     if (c >= n) return;
     const int64_t m = a.map[c];
     const float f = mul * a.hdr->gref;
     const int64_t sp = (int64_t)((n + tile - 1) / tile) * tile * a.Kp;
-    for (int k = threadIdx.x * 4; k < a.K; k += 1024) {
-        const float* p = a.dxp + (int64_t)c * a.Kp + k;
-        f32x4 v = *(const f32x4*)p;
-        for (int s = 1; s < splits; ++s) v += *(const f32x4*)(p + s * sp);
+    const int runs = (a.K + 3) >> 2;
+    int width = 256;   // threads along the row
+    while (width > runs && width > 16) width >>= 1;
+    const int groups = 256 / width, grp = threadIdx.x / width;
+    for (int k0 = 0; k0 < a.K; k0 += width * 4) {
+        const int k = k0 + (threadIdx.x % width) * 4;
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (k < a.K) {
+            const float* p = a.dxp + (int64_t)c * a.Kp + k;
+            constexpr int U = 8;
+            for (int s0 = grp; s0 < splits; s0 += groups * U) {
+                f32x4 t[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int s = s0 + u * groups;
+                    t[u] = s < splits ? *(const f32x4*)(p + s * sp) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) v += t[u];
+            }
+        }
+        if (groups > 1) {
+            __syncthreads();
+            buf[threadIdx.x] = v;
+            __syncthreads();
+            if (grp > 0) continue;
+            for (int g = 1; g < groups; ++g) v += buf[g * width + threadIdx.x];
+        }
+        if (k >= a.K) continue;
         v *= f;
         if (a.grad_f32) {
             float* d = (float*)a.dX + m * a.lddx + k;
