@@ -13,6 +13,8 @@ namespace mkp {
 
 constexpr int kMaxTargets = 1024;   // per row (distillation)
 constexpr int kDbiasRows = 128;
+constexpr int kStreamRows = 64;
+constexpr int kStreamGroups = 256;   // workgroups of the kernel for few rows: one per CU
 
 // What a call keeps in its workspace besides the large arrays; written by
 // the row-scan kernel, read by every later one.
@@ -42,6 +44,7 @@ struct LossArgs {
     float scale, cap, T;
     bool plain;             // z = scale x.w with scale > 0: the kernels keep x.w instead of z
     float s2;               // from what they keep to the base-2 logit, log2(e) z / T
+    bool stream;            // forward: the kernel for few rows (then direct too)
     bool direct;            // forward on few aligned rows: X and targets as the caller has them
     // cross entropy
     const int64_t* labels;  // M, or null for distillation
@@ -96,6 +99,7 @@ hipError_t launch_loss_flags(const LossArgs& a, hipStream_t st);       // distil
 hipError_t launch_loss_scan(const LossArgs& a, hipStream_t st);        // hdr, pos (calls of many rows)
 hipError_t launch_loss_gather(const LossArgs& a, bool scanned, hipStream_t st);   // hdr, map, Xc, targets, rows
 hipError_t launch_loss_forward(const LossArgs& a, hipStream_t st);     // part, sumz, zt
+hipError_t launch_loss_stream(const LossArgs& a, hipStream_t st);      // the same for at most kStreamRows rows
 hipError_t launch_loss_finish(const LossArgs& a, hipStream_t st);      // loss, lse
 hipError_t launch_loss_grad(const LossArgs& a, hipStream_t st);        // G (and dbp) of a piece
 hipError_t launch_loss_products(const LossArgs& a, hipStream_t st);    // dxp and dW of a piece

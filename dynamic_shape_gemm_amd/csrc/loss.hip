@@ -669,6 +669,223 @@ __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
     }
 }
 
+// Forward for few rows: the weight streams past them, so what counts is how
+// many of its bytes are on their way.  One workgroup per CU takes a run of
+// the vocabulary, in blocks of at most 64 rows of W, and walks (block, K step)
+// as one sequence through a ring of S stages of BK columns, so the loads of a
+// block's first steps are under way while the block before is finished.  Each
+// wave multiplies 16 rows of W with the FM * 16 rows of X and keeps every
+// row's running maximum and sum over the blocks; a workgroup leaves one
+// partial per row.  Long K steps: 512 (256) contiguous bytes of a row of W at
+// a time.
+template <int FM_, int BK_, int S_>
+struct Stream {
+    static constexpr int FM = FM_, BK = BK_, S = S_;
+    static constexpr int NW = 4, NT = 256, BN = 64;
+    static constexpr int CPR = BK / 8;                       // chunks per LDS row
+    static constexpr int W_BYTES = BN * BK * 2, X_BYTES = FM * 16 * BK * 2, STAGE = W_BYTES + X_BYTES;
+    static constexpr int IW = W_BYTES / 1024 / NW, IX = X_BYTES / 1024 / NW;
+    static constexpr int LD = BN + 4;                        // staged logits
+    static constexpr int LDS = S * STAGE;
+    static_assert(X_BYTES % (1024 * NW) == 0 && LDS <= 160 * 1024 && (S - 1) * (IW + IX) <= 63, "stages");
+};
+
+template <class T, bool TG>
+__global__ __launch_bounds__(T::NT) void loss_stream_kernel(LossArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char raw[T::LDS];
+    __shared__ float tab[TG ? T::FM * 16 * T::LD : 1];
+    __shared__ float red[T::NW][3][T::FM * 16];
+    const lds_t* smem = (const lds_t*)raw;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, s16 = lane & 15, M = (int)a.M;
+    // this workgroup's run of the vocabulary, in equal blocks
+    const int vb = (int)((int64_t)a.V * blockIdx.x / gridDim.x), ve = (int)((int64_t)a.V * (blockIdx.x + 1) / gridDim.x);
+    const int blocks = (ve - vb + T::BN - 1) / T::BN, rows = blocks > 0 ? (ve - vb + blocks - 1) / blocks : 0;
+    const int ksteps = (a.K + T::BK - 1) / T::BK, steps = blocks * ksteps;
+
+    int ib = 0, ik = 0, is = 0;   // the next loads' block, K step and stage
+    auto issue = [&]() {
+        const int v0 = vb + ib * rows, k0 = ik * T::BK;
+        const int vl = min(rows, ve - v0) - 1, kl = min(T::BK, a.K - k0);
+        const char* wb = (const char*)(a.W + (int64_t)v0 * a.ldw + k0);
+        const char* xb = (const char*)(a.X + k0);
+        const uint32_t st = lds0 + is * T::STAGE;
+#pragma unroll
+        for (int i = 0; i < T::IW + T::IX; ++i) {
+            const bool w = i < T::IW;
+            const int grp = (w ? i : i - T::IW) * T::NW + wave, p = grp * 64 + lane;
+            const int r = p / T::CPR;
+            int c = ((p % T::CPR) ^ (r & 15)) * 8;
+            if (c >= kl) c = 0;   // past K: not multiplied
+            if (w) dma16(wb, (uint32_t)((min(r, vl) * a.ldw + c) * 2), st + grp * 1024);
+            else dma16(xb, (uint32_t)((min(r, M - 1) * a.ldx + c) * 2), st + T::W_BYTES + grp * 1024);
+        }
+        is = is + 1 == T::S ? 0 : is + 1;
+        if (++ik == ksteps) {
+            ik = 0;
+            ++ib;
+        }
+    };
+    // The targets, read before the ring starts: a load of the compiler's among
+    // the ring's would be waited for together with all of them.  Several a
+    // row: up to NID per thread, of all rows in a line; more are read again
+    // for every block.
+    constexpr int NID = TG ? 8 : 1;
+    const bool few = TG && M * a.k <= NID * 256;
+    int labs[T::FM], ids[NID];
+    if constexpr (TG) {
+        if (few) {
+#pragma unroll
+            for (int e = 0; e < NID; ++e) {
+                const int at = tid + 256 * e;
+                const int64_t id = at < M * a.k ? a.ids[(int64_t)(at / a.k) * a.ldids + at % a.k] : -1;
+                ids[e] = id >= 0 && id < a.V ? (int)id : -1;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) labs[i] = row_label(a, i * 16 + s16, M);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // (vmcnt 0)
+    const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f, s2 = a.s2;
+    const bool smooth = a.sumz != nullptr;
+    float mx[T::FM], sm[T::FM], sz[T::FM];
+    f32x4 acc[T::FM];
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) {
+        mx[i] = -INFINITY;
+        sm[i] = sz[i] = 0.0f;
+        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int s = 0; s < T::S - 1; ++s)
+        if (s < steps) issue();
+    int blk = 0, ks = 0, st = 0;
+    for (int s = 0; s < steps; ++s) {
+        // the step's loads have landed (S - 2 later steps may be in flight,
+        // none counted on near the end), in every wave, and every wave is done
+        // with the stage that is filled next
+        if (s + T::S - 1 <= steps) phase_barrier<(T::S - 2) * (T::IW + T::IX)>();
+        else phase_barrier<0>();
+        if (s + T::S - 1 < steps) issue();
+        const lds_t* ws = smem + st * T::STAGE;
+        const int wrow = (wave * 16 + s16) * T::BK * 2, xrow = T::W_BYTES + s16 * T::BK * 2;
+        const int kn = min(T::BK, a.K - ks * T::BK) / 32;
+        auto part = [&](int q) {
+            const int off = ((q * 4 + g) ^ s16) << 4;
+            const bf16x8 wv = __builtin_bit_cast(bf16x8, *(const u32x4 __attribute__((address_space(3)))*)(ws + wrow + off));
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) {
+                const bf16x8 xv = __builtin_bit_cast(
+                    bf16x8, *(const u32x4 __attribute__((address_space(3)))*)(ws + xrow + i * 16 * T::BK * 2 + off));
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xv, acc[i], 0, 0, 0);
+            }
+        };
+        if (kn == T::BK / 32) {
+#pragma unroll
+            for (int q = 0; q < T::BK / 32; ++q) part(q);
+        } else {
+            for (int q = 0; q < kn; ++q) part(q);
+        }
+        st = st + 1 == T::S ? 0 : st + 1;
+        if (++ks < ksteps) continue;
+        // a block is done: lane 16 g + s holds X row 16 i + s, columns 4 g + 0..3 of the wave's 16
+        const int v0 = vb + blk * rows, v = v0 + wave * 16 + g * 4, left = min(ve, v0 + rows) - v;   // valid from v on
+        ks = 0;
+        ++blk;
+        if (!a.plain) {
+            f32x4 b = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (a.bias != nullptr) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) b[r] = a.bias[min(v + r, a.V - 1)];
+            }
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float z = fmaf(a.scale, acc[i][r], b[r]);
+                    acc[i][r] = a.cap > 0.0f ? a.cap * tanh_fast(z * inv_cap) : z;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            f32x4 u = acc[i];
+            acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (TG) {
+                *(f32x4*)(tab + (i * 16 + s16) * T::LD + wave * 16 + g * 4) = u;
+            } else {
+                const int d = labs[i] - v;
+                if ((unsigned)d < 4u && d < left) a.zt[i * 16 + s16] = d == 0 ? u[0] : d == 1 ? u[1] : d == 2 ? u[2] : u[3];
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (smooth) sz[i] += r < left ? u[r] : 0.0f;
+                u[r] = r < left ? u[r] : -INFINITY;
+            }
+            const float top = fmaxf(fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])), mx[i]);
+            const float base = stat_base(top, s2);
+            float t = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t += exp2_fast(fmaf(u[r], s2, -base));
+            sm[i] = fmaf(sm[i], exp2_fast(mul_rn(mx[i], s2) - base), t);
+            mx[i] = top;
+        }
+        if constexpr (TG) {
+            // the targets among the block's columns: its logits are in LDS
+            // (the direct loads in flight write elsewhere)
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            const int vn = min(ve, v0 + rows);
+            if (few) {
+#pragma unroll
+                for (int e = 0; e < NID; ++e)
+                    if (ids[e] >= v0 && ids[e] < vn)
+                        a.zt[(tid + 256 * e) / a.k * a.kp + (tid + 256 * e) % a.k] =
+                            tab[(tid + 256 * e) / a.k * T::LD + ids[e] - v0];
+            } else {
+                for (int m = tid >> 3; m < M; m += 32)
+                    for (int q = tid & 7; q < a.k; q += 8) {
+                        const int64_t id = a.ids[(int64_t)m * a.ldids + q];
+                        if (id >= v0 && id < vn) a.zt[(int64_t)m * a.kp + q] = tab[m * T::LD + (int)(id - v0)];
+                    }
+            }
+        }
+    }
+    // join the four lanes, then the waves, that share a row
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) {
+        float top = fmaxf(mx[i], __shfl_xor(mx[i], 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        float t = sm[i] * exp2_fast(mul_rn(mx[i], s2) - stat_base(top, s2));
+        t += __shfl_xor(t, 16);
+        t += __shfl_xor(t, 32);
+        float z = sz[i];
+        z += __shfl_xor(z, 16);
+        z += __shfl_xor(z, 32);
+        if (g == 0) {
+            red[wave][0][i * 16 + s16] = top;
+            red[wave][1][i * 16 + s16] = t;
+            red[wave][2][i * 16 + s16] = z;
+        }
+    }
+    __syncthreads();
+    if (tid < M) {
+        float top = -INFINITY, t = 0.0f, z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < T::NW; ++w) top = fmaxf(top, red[w][0][tid]);
+        const float base = stat_base(top, s2);
+#pragma unroll
+        for (int w = 0; w < T::NW; ++w) {
+            t += red[w][1][tid] * exp2_fast(mul_rn(red[w][0][tid], s2) - base);
+            z += red[w][2][tid];
+        }
+        *(float2*)(a.part + ((int64_t)tid * a.ntiles + blockIdx.x) * 2) = make_float2(top, t);
+        if (smooth) a.sumz[(int64_t)tid * a.ntiles + blockIdx.x] = z;
+    }
+}
+
 // Sum and maximum over the workgroup's 256 threads.
 __device__ __forceinline__ float block_sum(float v, float* buf) {
 #pragma unroll
@@ -1533,8 +1750,20 @@ hipError_t launch_loss_forward(const LossArgs& a, hipStream_t st) {
               : launch_kernel(loss_forward_kernel<T, T, false>, grid, dim3(T::NT), st, a);
 }
 
+hipError_t launch_loss_stream(const LossArgs& a, hipStream_t st) {
+    const bool tg = a.labels == nullptr;
+    const dim3 grid((unsigned)a.ntiles);
+    auto go = [&](auto tag) {
+        using T = decltype(tag);
+        return tg ? launch_kernel(loss_stream_kernel<T, true>, grid, dim3(T::NT), st, a)
+                  : launch_kernel(loss_stream_kernel<T, false>, grid, dim3(T::NT), st, a);
+    };
+    return a.M <= 16 ? go(Stream<1, 256, 3>{}) : a.M <= 32 ? go(Stream<2, 256, 3>{}) : go(Stream<4, 128, 4>{});
+}
+
 hipError_t launch_loss_finish(const LossArgs& a, hipStream_t st) {
-    return launch_kernel(loss_finish_kernel, dim3((unsigned)a.M), dim3(256), st, a, loss_sumz_parts(a.tile));
+    return launch_kernel(loss_finish_kernel, dim3((unsigned)a.M), dim3(256), st, a,
+                         a.stream ? 1 : loss_sumz_parts(a.tile));
 }
 
 hipError_t launch_loss_grad(const LossArgs& a, hipStream_t st) {

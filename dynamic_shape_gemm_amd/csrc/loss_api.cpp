@@ -41,7 +41,7 @@ struct Layout {
     int tile = 256;
     int64_t Mr = 0, Kp = 0, Vp = 0, kp = 1, ntiles = 0;
     int pieces = 1, slots = 256;
-    bool pack_w = false;
+    bool pack_w = false, stream = false;
     size_t hdr = 0, map = 0, pos = 0, live = 0, xc = 0, ids = 0, wts = 0, rws = 0, part = 0, sumz = 0, zt = 0, g = 0, dxp = 0, dbp = 0,
            w = 0, bytes = 0;
 };
@@ -68,6 +68,8 @@ Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int6
     l.ids = take(4 * l.Mr * l.kp);
     if (l.pack_w) l.w = take(2 * V * l.Kp);
     if (!backward) {
+        l.stream = M <= kStreamRows && !l.pack_w && K % 64 == 0;
+        if (l.stream) l.ntiles = std::max<int64_t>(l.ntiles, kStreamGroups);
         l.part = take(8 * M * l.ntiles);
         l.sumz = take(4 * M * l.ntiles * loss_sumz_parts(l.tile));
         l.zt = take(4 * l.Mr * l.kp);
@@ -223,7 +225,7 @@ int run(const Call& c) {
     a.Kp = (int)l.Kp;
     a.Vp = (int)l.Vp;
     a.kp = (int)l.kp;
-    a.ntiles = (int)l.ntiles;
+    a.ntiles = (int)ceil_div(c.V, l.tile);
     a.tile = l.tile;
     a.slots = l.slots;
     const double elem = 2.0, m = (double)c.M, v = (double)c.V, k = (double)c.K;
@@ -262,9 +264,12 @@ int run(const Call& c) {
         a.zt = (float*)(ws + l.zt);
         // one tile of rows: the product costs the weight's bytes, not its
         // rows, so none need dropping, and two launches fewer count for more
-        a.direct = c.M <= l.tile && !l.pack_w && aligned16(c.X) && c.ldx % 8 == 0 && c.K % 64 == 0;
+        a.direct = c.M <= l.tile && !l.pack_w && aligned16(c.X) && c.ldx % 8 == 0 && c.ldx <= 2 * kMaxK &&
+                   c.K % 64 == 0;
+        a.stream = l.stream && a.direct;
+        if (a.stream) a.ntiles = kStreamGroups;
         if (!a.direct && (rc = compact()) != MKP_OK) return rc;
-        if ((rc = go(LL_FORWARD, 2.0 * m * v * k, elem * (m + v) * k, [&] { return launch_loss_forward(a, st); })) != MKP_OK)
+        if ((rc = go(LL_FORWARD, 2.0 * m * v * k, elem * (m + v) * k, [&] { return a.stream ? launch_loss_stream(a, st) : launch_loss_forward(a, st); })) != MKP_OK)
             return rc;
         return go(LL_FINISH, 0.0, 8.0 * m * (double)l.ntiles, [&] { return launch_loss_finish(a, st); });
     }

@@ -116,6 +116,17 @@ def test_distill(mkp, M, V, K):
     check(mkp, inputs(M + V, M, V, K, keep=0.8, k=min(V, 5)), "distill", temperature=2.0)
 
 
+@pytest.mark.parametrize("M", [1, 16, 17, 32, 33, 64, 65])
+@pytest.mark.parametrize("V,K", [(3, 64), (255, 256), (1000, 320), (20000, 192), (33000, 512)])
+def test_few_rows(mkp, M, V, K):
+    """The forms for few rows: blocks of the vocabulary that end inside a
+    workgroup's run, K steps that end inside a stage, workgroups without any."""
+    check(mkp, inputs(M + V, M, V, K, keep=0.8), "few", grad=False)
+    check(mkp, inputs(M + V, M, V, K, bias=True), "few", grad=False, smoothing=0.1, softcap=4.0, scale=0.8)
+    for k in (2, 70):
+        check(mkp, inputs(M + V, M, V, K, keep=0.8, k=k), "few", grad=False, temperature=2.0)
+
+
 @pytest.mark.parametrize("opt", [dict(scale=0.5), dict(scale=-1.5), dict(softcap=5.0), dict(smoothing=0.1),
                                  dict(smoothing=1.0), dict(z_loss=1e-2), dict(scale=1.3, softcap=2.0, smoothing=0.3,
                                                                              z_loss=1e-3)], ids=str)
