@@ -19,8 +19,7 @@ hipError_t traced_launch(hipStream_t st, int kernel, double flops, double bytes,
 
 // Trace codes kTraceLoss - i: the i-th launch of the vocabulary losses.
 constexpr int kTraceLoss = -20;
-enum LossLaunch : int { LL_FLAGS, LL_SCAN, LL_GATHER, LL_FORWARD, LL_FINISH, LL_GRAD, LL_PRODUCTS, LL_DX_FINISH, LL_DBIAS,
-                        LL_COUNT };
+enum LossLaunch : int { LL_FLAGS, LL_SCAN, LL_GATHER, LL_FORWARD, LL_FINISH, LL_GRAD, LL_PRODUCTS, LL_OUTPUTS, LL_COUNT };
 const char* loss_launch_name(int i);
 
 }  // namespace mkp

@@ -81,7 +81,8 @@ struct LossArgs {
     float* zt;              // forward: the targets' kept values, compact n x kp
     uint16_t* G;            // backward: one piece's gradient by s, Mr x Vp
     float* dxp;             // backward: dX partials, [splits][rows of live tiles][Kp]
-    float* dbp;             // backward: sums of G's columns over kDbiasRows rows each, [Mr / kDbiasRows][Vp]
+    float* dbp;             // backward: sums of G's columns over kDbiasRows rows each, [Mr / kDbiasRows][ldb]
+    int ldb;
     int Mr, Kp, Vp, kp;     // padded extents
     int tile;               // rows and columns of the tile kernels' tiles: 256 or 128
     int ntiles;             // vocabulary tiles of the forward pass
@@ -103,7 +104,6 @@ hipError_t launch_loss_stream(const LossArgs& a, hipStream_t st);      // the sa
 hipError_t launch_loss_finish(const LossArgs& a, hipStream_t st);      // loss, lse
 hipError_t launch_loss_grad(const LossArgs& a, hipStream_t st);        // G (and dbp) of a piece
 hipError_t launch_loss_products(const LossArgs& a, hipStream_t st);    // dxp and dW of a piece
-hipError_t launch_loss_dx_finish(const LossArgs& a, hipStream_t st);   // dX
-hipError_t launch_loss_dbias(const LossArgs& a, hipStream_t st);       // dbias of a piece
+hipError_t launch_loss_outputs(const LossArgs& a, hipStream_t st);     // dX and dbias from their partials
 
 }  // namespace mkp

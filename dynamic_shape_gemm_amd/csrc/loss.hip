@@ -442,7 +442,7 @@ __device__ __forceinline__ bool map_rounds(int bid, int tm_n, int tn_n, int slot
 template <class T>
 struct BiasRegs {
     f32x4 b[2][T::FN];
-    __device__ __forceinline__ BiasRegs(const LossArgs& a, const Place<T>& at, int v_tile) {
+    __device__ __forceinline__ void read(const LossArgs& a, const Place<T>& at, int v_tile) {
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
@@ -519,19 +519,20 @@ template <class T, bool TG>
 __device__ __forceinline__ void forward_tile(const LossArgs& a, int n, int m0, int tn, lds_t* smem, int wave, int lane) {
     constexpr int PARTS = 4 * T::WGN, LDP = 2 * PARTS + 2;   // floats per row
     const int tid = wave * 64 + lane, v0 = tn * T::BN;
-    Acc<T> acc;
-    logits_tile<T>(a, m0, v0, n, smem, wave, lane, acc);
     const Place<T> at(wave, lane);
-    const int vr = a.V - v0;   // valid columns
-    const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
-    const BiasRegs<T> bias(a, at, v0);
     int labs[2][T::FM];
-    if constexpr (!TG) {
+    if constexpr (!TG) {   // (read ahead of the product, whose loop hides it)
 #pragma unroll
         for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
             for (int i = 0; i < T::FM; ++i) labs[ha][i] = row_label(a, m0 + at.row(ha, i), n) - v0 - at.wn * T::FN * 16;
     }
+    Acc<T> acc;
+    logits_tile<T>(a, m0, v0, n, smem, wave, lane, acc);
+    const int vr = a.V - v0;   // valid columns
+    const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
+    BiasRegs<T> bias;
+    if (!a.plain) bias.read(a, at, v0);
     if constexpr (TG) {
         float __attribute__((address_space(3)))* tab = (float __attribute__((address_space(3)))*)smem;
         constexpr int LD = T::BN + 4;
@@ -1321,7 +1322,8 @@ __device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int 
     const int vr = a.V - v0;
     const float s2 = a.s2;
     const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
-    const BiasRegs<T> bias(a, at, v0);
+    BiasRegs<T> bias;
+    if (!a.plain) bias.read(a, at, v0);
     LossRow rows[2][T::FM];
     int labs[2][T::FM];
 #pragma unroll
@@ -1461,7 +1463,7 @@ __device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int 
             float t = 0.0f;
 #pragma unroll
             for (int w = 0; w < T::WGM; ++w) t += red[(part * T::WGM + w) * T::BN + c];
-            a.dbp[(int64_t)(m0 / kDbiasRows + part) * a.Vp + p0 + c] = t;
+            a.dbp[(int64_t)(m0 / kDbiasRows + part) * a.ldb + v0 + c] = t;
         }
         __syncthreads();
     }
@@ -1539,13 +1541,32 @@ __device__ __forceinline__ void dx_tile(const LossArgs& a, int n, int tm, int tn
                 }
 }
 
-// dX = gref unit scale (sum of the partials), in the rows' own places.  One
-// workgroup per row; where a row has fewer than 128 runs of four features,
-// several threads share each run's splits and join through LDS, in order.
-__global__ __launch_bounds__(256) void loss_dx_finish_kernel(LossArgs a, float mul, int tile) {
+// The results that are made from partials.  Workgroups from `dx_groups` on:
+// dbias = gref unit (the sum over the row blocks, in order).  Before them, one
+// per row: dX = gref unit scale (the sum of its partials), in the row's own
+// place; where a row has fewer than 128 runs of four features, several threads
+// share each run's splits and join through LDS, in order.
+__global__ __launch_bounds__(256) void loss_outputs_kernel(LossArgs a, float unit, int dx_groups) {
     __shared__ f32x4 buf[256];
-    const int c = blockIdx.x, n = a.hdr->n, splits = a.hdr->splits;
+    const int c = blockIdx.x, n = a.hdr->n, splits = a.hdr->splits, tile = a.tile;
+    if (c >= dx_groups) {
+        const int v = (c - dx_groups) * 256 + threadIdx.x;
+        if (v >= a.V) return;
+        const int parts = (n + kDbiasRows - 1) / kDbiasRows;
+        constexpr int U = 8;
+        float t = 0.0f;
+        for (int i0 = 0; i0 < parts; i0 += U) {
+            float x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = i0 + u < parts ? a.dbp[(int64_t)(i0 + u) * a.ldb + v] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) t += x[u];
+        }
+        a.dbias[v] = t * (unit * a.hdr->gref);
+        return;
+    }
     if (c >= n) return;
+    const float mul = unit * a.scale;
     const int64_t m = a.map[c];
     const float f = mul * a.hdr->gref;
     const int64_t sp = (int64_t)((n + tile - 1) / tile) * tile * a.Kp;
@@ -1689,16 +1710,6 @@ __global__ __launch_bounds__(TX::NT) void loss_products_kernel(LossArgs a, float
     }
 }
 
-// dbias of a piece: gref unit (sum over the row tiles, in order).
-__global__ __launch_bounds__(256) void loss_dbias_kernel(LossArgs a, float mul) {
-    const int p = blockIdx.x * 256 + threadIdx.x;
-    if (p >= a.vn) return;
-    const int tiles = (a.hdr->n + kDbiasRows - 1) / kDbiasRows;
-    float t = 0.0f;
-    for (int i = 0; i < tiles; ++i) t += a.dbp[(int64_t)i * a.Vp + p];
-    a.dbias[a.v0 + p] = t * (mul * a.hdr->gref);
-}
-
 template <bool AT, bool BT>
 using L256 = LTile<2, 4, 4, 2, AT, BT>;
 template <bool AT, bool BT>
@@ -1793,12 +1804,9 @@ hipError_t launch_loss_products(const LossArgs& a, hipStream_t st) {
     return launch_kernel(loss_products_kernel<L128<false, true>, L128<true, true>>, grid, dim3(256), st, a, mul);
 }
 
-hipError_t launch_loss_dx_finish(const LossArgs& a, hipStream_t st) {
-    return launch_kernel(loss_dx_finish_kernel, dim3((unsigned)a.M), dim3(256), st, a, unit_of(a) * a.scale, a.tile);
-}
-
-hipError_t launch_loss_dbias(const LossArgs& a, hipStream_t st) {
-    return launch_kernel(loss_dbias_kernel, dim3((unsigned)up(a.vn, 256)), dim3(256), st, a, unit_of(a));
+hipError_t launch_loss_outputs(const LossArgs& a, hipStream_t st) {
+    const int64_t dx = a.dX != nullptr ? a.M : 0, db = a.dbias != nullptr ? up(a.V, 256) : 0;
+    return launch_kernel(loss_outputs_kernel, dim3((unsigned)(dx + db)), dim3(256), st, a, unit_of(a), (int)dx);
 }
 
 }  // namespace mkp

@@ -19,7 +19,7 @@ namespace mkp {
 
 const char* loss_launch_name(int i) {
     static const char* const names[LL_COUNT] = {"loss_flags", "loss_scan",     "loss_gather",    "loss_forward", "loss_finish",
-                                                "loss_grad",  "loss_products", "loss_dx_finish", "loss_dbias"};
+                                                "loss_grad",  "loss_products", "loss_outputs"};
     return i >= 0 && i < LL_COUNT ? names[i] : "loss";
 }
 
@@ -88,7 +88,7 @@ Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int6
         const int64_t one = l.Mr * l.Kp, steps = l.Vp / 64;
         const int64_t split = std::min<int64_t>(2 * l.slots * l.tile * l.tile, std::max<int64_t>(1, steps / 4) * one);
         l.dxp = take(4 * std::max(one, split));
-        l.dbp = take(4 * std::max<int64_t>(1, l.Mr / kDbiasRows) * l.Vp);
+        l.dbp = take(4 * std::max<int64_t>(1, l.Mr / kDbiasRows) * l.Vp * l.pieces);
     }
     l.bytes = at;
     return l;
@@ -279,6 +279,7 @@ int run(const Call& c) {
     a.G = (uint16_t*)(ws + l.g);
     a.dxp = (float*)(ws + l.dxp);
     a.dbp = c.dbias ? (float*)(ws + l.dbp) : nullptr;
+    a.ldb = (int)(l.Vp * l.pieces);
     if ((rc = compact()) != MKP_OK) return rc;
     for (int p = 0; p < l.pieces; ++p) {
         a.v0 = (int)(p * l.Vp);
@@ -295,14 +296,11 @@ int run(const Call& c) {
                              (c.dW ? elem * m * k + gb * pv * k : 0.0),
                          [&] { return launch_loss_products(a, st); })) != MKP_OK)
                 return rc;
-        if (c.dbias)
-            if ((rc = go(LL_DBIAS, 0.0, 4.0 * pv * (double)ceil_div(c.M, kDbiasRows), [&] { return launch_loss_dbias(a, st); })) !=
-                MKP_OK)
-                return rc;
     }
-    if (c.dX && c.M > 0)
-        return go(LL_DX_FINISH, 0.0, (4.0 + gb) * m * k, [&] { return launch_loss_dx_finish(a, st); });
-    return MKP_OK;
+    if (!(c.dX && c.M > 0) && !c.dbias) return MKP_OK;
+    return go(LL_OUTPUTS, 0.0,
+              (c.dX ? (4.0 + gb) * m * k : 0.0) + (c.dbias ? 4.0 * v * (double)ceil_div(c.M, kDbiasRows) : 0.0),
+              [&] { return launch_loss_outputs(a, st); });
 }
 
 // No exception leaves the C entry points.

@@ -458,4 +458,4 @@ def test_trace_names_the_launches(mkp):
     finally:
         mkp.mkp_set_option("trace", 0)
     assert names == ["loss_forward", "loss_finish", "loss_flags", "loss_gather", "loss_grad", "loss_products",
-                     "loss_dbias", "loss_dx_finish"]
+                     "loss_outputs"]
