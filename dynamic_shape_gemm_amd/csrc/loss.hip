@@ -84,6 +84,10 @@ __device__ __forceinline__ float tanh_fast(float x) {
     return fabsf(x) < 0.25f ? p : f;
 }
 
+// At the head of a branch that few calls or lanes take: keeps the compiler
+// from computing the branch's work ahead of it, for everyone.
+__device__ __forceinline__ void rarely() { asm volatile("; rarely taken"); }
+
 // ---- tiles -----------------------------------------------------------------
 //
 // One workgroup multiplies a BM x BN tile over K steps of 64 on 16x16x32
@@ -465,6 +469,7 @@ __device__ __forceinline__ void row_logits(const LossArgs& a, const BiasRegs<T>&
             for (int r = 0; r < 4; ++r)
                 acc[ha][hb][i][j][r] = fmaf(a.scale, acc[ha][hb][i][j][r], bias.b[hb][j][r]);
     if (a.cap > 0.0f) {
+        rarely();
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
@@ -585,19 +590,27 @@ __device__ __forceinline__ void forward_tile(const LossArgs& a, int n, int m0, i
             const int row = at.row(ha, i);
             if constexpr (!TG) {
                 if (!a.plain) row_logits<T>(a, bias, inv_cap, acc, ha, i);
-                // (the wave's columns are two runs of FN * 16; rarely any lane's label is among them)
-                if ((unsigned)(labs[ha][i] % T::HB) < (unsigned)(T::FN * 16) && (unsigned)labs[ha][i] < (unsigned)T::BN) {
+                // (the wave's columns are two runs of FN * 16)
+                const unsigned lab = (unsigned)labs[ha][i];
+                if (lab < (unsigned)T::BN && (lab & (T::HB - 1)) < (unsigned)(T::FN * 16)) {
+                    rarely();
+                    float u = 0.0f;
+                    bool mine = false;
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
                         for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (labs[ha][i] == hb * T::HB + j * 16 + at.g * 4 + r)
-                                    a.zt[m0 + row] = acc[ha][hb][i][j][r];
+                            for (int r = 0; r < 4; ++r) {
+                                const bool is = lab == (unsigned)(hb * T::HB + j * 16 + at.g * 4 + r);
+                                u = is ? acc[ha][hb][i][j][r] : u;
+                                mine |= is;
+                            }
+                    if (mine) a.zt[m0 + row] = u;
                 }
             }
             if (smooth) {
+                rarely();
                 float sz = 0.0f;
 #pragma unroll
                 for (int hb = 0; hb < 2; ++hb)
@@ -612,6 +625,7 @@ __device__ __forceinline__ void forward_tile(const LossArgs& a, int n, int m0, i
                     a.sumz[((int64_t)(m0 + row) * a.ntiles + tn) * T::WGN + at.wn] = sz;
             }
             if (vr < T::BN) {
+                rarely();
 #pragma unroll
                 for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
@@ -628,13 +642,14 @@ __device__ __forceinline__ void forward_tile(const LossArgs& a, int n, int m0, i
 #pragma unroll
                     for (int r = 0; r < 4; ++r) mx = fmaxf(mx, acc[ha][hb][i][j][r]);
             const float base = stat_base(mx, s2);
-            float sm = 0.0f;
+            f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
                 for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) sm += exp2_fast(fmaf(acc[ha][hb][i][j][r], s2, -base));
+                    for (int r = 0; r < 4; ++r) part[r] += exp2_fast(fmaf(acc[ha][hb][i][j][r], s2, -base));
+            const float sm = (part[0] + part[1]) + (part[2] + part[3]);
             *(f32x2 __attribute__((address_space(3)))*)(red + row * LDP + (at.wn * 4 + at.g) * 2) = f32x2{mx, sm};
             __builtin_amdgcn_sched_barrier(0);   // one row of fragments at a time keeps the registers within bounds
         }
@@ -1378,18 +1393,21 @@ __device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int 
                             at.col(hb, j));
                 }
             if constexpr (!TG) {
-                // (the wave's columns are two runs of FN * 16; rarely any lane's label is among them)
-                if ((unsigned)(labs[ha][i] % T::HB) < (unsigned)(T::FN * 16) && (unsigned)labs[ha][i] < (unsigned)T::BN) {
+                // (the wave's columns are two runs of FN * 16)
+                const unsigned lab = (unsigned)labs[ha][i];
+                if (lab < (unsigned)T::BN && (lab & (T::HB - 1)) < (unsigned)(T::FN * 16)) {
+                    rarely();
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
                         for (int j = 0; j < T::FN; ++j)
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
-                                v[hb][j][r] -= labs[ha][i] == hb * T::HB + j * 16 + at.g * 4 + r ? c.rp : 0.0f;
+                                v[hb][j][r] -= lab == (unsigned)(hb * T::HB + j * 16 + at.g * 4 + r) ? c.rp : 0.0f;
                 }
             }
             if (a.cap > 0.0f) {   // (then acc holds z)
+                rarely();
 #pragma unroll
                 for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
@@ -1401,6 +1419,7 @@ __device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int 
                         }
             }
             if (m0 + T::BM > n) {   // rows past the live ones
+                rarely();
                 const bool on = m0 + row < n;
 #pragma unroll
                 for (int hb = 0; hb < 2; ++hb)
@@ -1417,6 +1436,7 @@ __device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int 
         }
     }
     if (vr < T::BN) {   // columns past the vocabulary
+        rarely();
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
