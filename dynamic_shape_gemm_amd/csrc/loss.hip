@@ -116,9 +116,13 @@ struct LTile {
     static_assert(LDS <= 160 * 1024, "LDS budget");
 };
 
-// Chunk swizzle of a 128-byte row (eight 16-byte chunks): the 16 rows of a
-// fragment read meet 16 distinct bank windows.
-__device__ __forceinline__ int swz_row(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+// Chunk swizzle of a 128-byte row (eight 16-byte chunks).  A 128-bit read of
+// 64 lanes goes in four passes of 16 lanes, lanes 0-3, 12-15 and 20-27 of each
+// 32 in one and the others in the next; with lane 16 g + s on row s, chunk c +
+// g, the rows' low three bits spread each pass over all 16 bank windows
+// (measured: no conflict cycles; with the third bit folded in as well, half of
+// all LDS cycles were).
+__device__ __forceinline__ int swz_row(int row) { return row & 7; }
 
 // Segment swizzle of a transposed row (32-byte segments): the eight rows a
 // 32-lane pass of the transpose read touches (8g .. 8g+3 for two g) meet
