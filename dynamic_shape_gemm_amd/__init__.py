@@ -564,12 +564,15 @@ def _loss_inputs(x, w, bias, rows):
 class _LossStream:
     """The stream a vocabulary loss runs on, made current (with its device)
     while the call's outputs and workspace are taken from torch's allocator,
-    so that they belong to it."""
+    so that they belong to it.  On another stream than the current one the
+    inputs are marked as used there: their memory is not handed out again
+    before the call is done with it."""
 
-    def __init__(self, device, stream):
+    def __init__(self, device, stream, *inputs):
         import torch
+        current = torch.cuda.current_stream(device)
         if stream is None:
-            self.stream = torch.cuda.current_stream(device)
+            self.stream = current
         elif isinstance(stream, int):
             self.stream = (torch.cuda.ExternalStream(stream, device=device) if stream
                            else torch.cuda.default_stream(device))
@@ -578,6 +581,10 @@ class _LossStream:
         if self.stream.device != device:
             raise ValueError("the stream is on another device than x")
         self.handle = self.stream.cuda_stream
+        if self.handle != current.cuda_stream:
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(self.stream)
         here = torch.cuda.current_device() == device.index
         self.ctx = None if stream is None and here else torch.cuda.stream(self.stream)
 
@@ -617,7 +624,7 @@ def linear_xent(x, w, labels, bias=None, scale=1.0, softcap=0.0, smoothing=0.0, 
     in [0, V) get 0.  The mean over the others is loss.sum() / their number."""
     import torch
     M, V, K, ldx, ldw = _loss_inputs(x, w, bias, {"labels": (labels, torch.int64, (x.shape[0],))})
-    with _LossStream(x.device, stream) as st:
+    with _LossStream(x.device, stream, x, w, labels, bias) as st:
         loss = torch.empty((2, M), dtype=torch.float32, device=x.device)
         loss, lse = loss[0], loss[1]
         ws, n = _loss_workspace(M, V, K, 0, w, ldw, False)
@@ -635,7 +642,7 @@ def linear_xent_backward(x, w, labels, lse, dloss, bias=None, scale=1.0, softcap
     M = x.shape[0]
     M, V, K, ldx, ldw = _loss_inputs(x, w, bias, {"labels": (labels, torch.int64, (M,)),
                                                   "lse": (lse, torch.float32, (M,))})
-    with _LossStream(x.device, stream) as st:
+    with _LossStream(x.device, stream, x, w, labels, bias, lse, dloss) as st:
         dloss = dloss.contiguous()   # a broadcast scalar has no stride
         _loss_inputs(x, w, None, {"dloss": (dloss, torch.float32, (M,))})
         dx, dw, dbias, gt = _loss_grads(x, w, bias, need_dx, need_dw, need_dbias, grad_dtype or torch.bfloat16)
@@ -667,7 +674,7 @@ def linear_distill(x, w, ids, teacher, bias=None, temperature=1.0, scale=1.0, so
     probabilities are normalised over the k).  Returns (loss, lse), fp32 (M,)."""
     import torch
     M, V, K, ldx, ldw, k, ldi, ldt = _distill_inputs(x, w, bias, ids, teacher, teacher_lse)
-    with _LossStream(x.device, stream) as st:
+    with _LossStream(x.device, stream, x, w, ids, teacher, bias, teacher_lse) as st:
         loss = torch.empty((2, M), dtype=torch.float32, device=x.device)
         loss, lse = loss[0], loss[1]
         ws, n = _loss_workspace(M, V, K, k, w, ldw, False)
@@ -683,7 +690,7 @@ def linear_distill_backward(x, w, ids, teacher, lse, dloss, bias=None, temperatu
     linear_xent_backward gives them."""
     import torch
     M, V, K, ldx, ldw, k, ldi, ldt = _distill_inputs(x, w, bias, ids, teacher, teacher_lse, lse=lse)
-    with _LossStream(x.device, stream) as st:
+    with _LossStream(x.device, stream, x, w, ids, teacher, bias, teacher_lse, lse, dloss) as st:
         dloss = dloss.contiguous()   # a broadcast scalar has no stride
         _loss_inputs(x, w, None, {"dloss": (dloss, torch.float32, (M,))})
         dx, dw, dbias, gt = _loss_grads(x, w, bias, need_dx, need_dw, need_dbias, grad_dtype or torch.bfloat16)

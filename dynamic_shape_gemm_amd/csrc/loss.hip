@@ -1155,7 +1155,8 @@ __device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c,
                 // everything over (1 - smoothing), so that a label's own
                 // weight is exactly the row's share of gref
                 const float unit = a.smoothing < 1.0f ? 1.0f - a.smoothing : 1.0f;
-                const float cq = a.z_loss != 0.0f ? 1.0f + 2.0f * a.z_loss * a.lse[m] : 1.0f;
+                // (no probability: nothing for the penalty to weigh either)
+                const float cq = a.z_loss != 0.0f && lse2 != INFINITY ? 1.0f + 2.0f * a.z_loss * a.lse[m] : 1.0f;
                 a.rows[c] = LossRow{lse2, rel * cq / unit, rel * a.smoothing / ((float)a.V * unit),
                                     a.smoothing < 1.0f ? rel : 0.0f};
             }

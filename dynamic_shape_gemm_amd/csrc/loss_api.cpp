@@ -177,7 +177,9 @@ int run(const Call& c) {
     if (!c.ws || c.ws_bytes < 0 || (size_t)c.ws_bytes < l.bytes || !aligned16(c.ws))
         return report(MKP_ERR_INVALID_ARG,
                       "workspace of " + std::to_string(l.bytes) + " bytes, 16-byte aligned, needed");
-    if (ceil_div(c.M, l.tile) * l.ntiles > INT_MAX / 2 || l.Mr > INT_MAX / 2)
+    const int64_t row_tiles = ceil_div(c.M, l.tile), col_tiles = ceil_div(c.K, l.tile);
+    if (row_tiles * ceil_div(c.V, l.tile) > INT_MAX / 2 ||
+        (c.backward && (row_tiles + ceil_div(l.Vp, l.tile)) * col_tiles > INT_MAX / 2))
         return report(MKP_ERR_UNSUPPORTED, "grid too large");
     begin_call();
     hipStream_t st = (hipStream_t)c.stream;

@@ -227,6 +227,9 @@ def test_masked_vocabulary(mkp, M):
         assert torch.isposinf(loss).all() and torch.isneginf(lse).all()
         dx, dw, db = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"], t["bias"])
         assert torch.isfinite(dx).all() and torch.isfinite(dw).all() and torch.isfinite(db).all()
+        _, lse = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"], z_loss=1e-3)
+        again = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"], t["bias"], z_loss=1e-3)
+        assert all(torch.equal(p, q) for p, q in zip(again, (dx, dw, db)))
 
 
 @pytest.mark.parametrize("M", [24, 301])
@@ -357,6 +360,25 @@ def test_streams(mkp):
             assert torch.equal(g[0], r[0]) and torch.equal(g[1], r[1])
             again = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], r[1], t["dloss"])
             assert torch.equal(g[2], again[0]) and torch.equal(g[3], again[1])
+
+
+def test_inputs_freed_while_their_stream_runs(mkp):
+    """With the stream argument the inputs may be dropped as soon as the call
+    returns: their memory is not handed out again before the call is done."""
+    side = torch.cuda.Stream()
+    t = inputs(55, 700, 20000, 256, keep=0.9)
+    ref = mkp.linear_xent(t["x"], t["w"], t["labels"])[0].clone()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        x, w, y = t["x"].clone(), t["w"].clone(), t["labels"].clone()
+        side.wait_stream(torch.cuda.current_stream())
+        loss, _ = mkp.linear_xent(x, w, y, stream=side)
+        shapes = (x.shape, w.shape)
+        del x, w, y
+        junk = [torch.full(s, float("nan"), device="cuda", dtype=BF) for s in shapes for _ in range(2)]
+        torch.cuda.synchronize()
+        assert torch.equal(loss, ref)
+        del junk
 
 
 @pytest.mark.parametrize("op", ["xent", "distill"])

@@ -75,6 +75,16 @@ def test_workspace_is_checked(mkp, fn, k, back):
             mkp.mkp_linear_loss_workspace(*bad, A, 8, back)
 
 
+def test_too_large_for_a_launch(mkp):
+    """Extents whose tiles a launch cannot count, with a workspace to match."""
+    M = V = 1 << 29
+    need = mkp.mkp_linear_loss_workspace(M, V, 64, 0, A, 64, 0)
+    assert xent(mkp, M=M, V=V, K=64, ldx=64, ldw=64, workspace_bytes=need) == mkp.MKP_ERR_UNSUPPORTED
+    M, K = (1 << 30) - 1, 1 << 21
+    need = mkp.mkp_linear_loss_workspace(M, 10, K, 0, A, K, 1)
+    assert xent_bwd(mkp, M=M, K=K, ldx=K, ldw=K, lddx=K, lddw=K, workspace_bytes=need) == mkp.MKP_ERR_UNSUPPORTED
+
+
 def test_nothing_to_do(mkp):
     assert xent(mkp, M=0, X=0, labels=0, loss=0, lse=0, workspace=0) == mkp.MKP_OK
     assert distill(mkp, M=0, X=0, ids=0, teacher=0, loss=0, lse=0, workspace=0) == mkp.MKP_OK
