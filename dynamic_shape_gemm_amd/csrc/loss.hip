@@ -1030,6 +1030,25 @@ __device__ __forceinline__ bool row_live(const LossArgs& a, int64_t m) {
     return a.live[m] != 0;
 }
 
+// The same for U rows from m on, `by` apart (false past the last), their loads
+// issued together.
+template <int U>
+__device__ __forceinline__ void rows_live(const LossArgs& a, int64_t m, int by, bool (&on)[U]) {
+    if (a.labels != nullptr) {
+        int64_t y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) y[u] = a.labels[min(m + by * u, a.M - 1)];
+#pragma unroll
+        for (int u = 0; u < U; ++u) on[u] = y[u] >= 0 && y[u] < a.V && m + by * u < a.M;
+    } else {
+        uint8_t y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) y[u] = a.live[min(m + by * u, a.M - 1)];
+#pragma unroll
+        for (int u = 0; u < U; ++u) on[u] = y[u] != 0 && m + by * u < a.M;
+    }
+}
+
 __device__ __forceinline__ float usable_gref(float g) { return (g > 0.0f && g < INFINITY) ? g : 1.0f; }
 
 // How dX's product over a piece is cut: its tiles are few where the live rows
@@ -1068,60 +1087,62 @@ __device__ __forceinline__ int dx_splits(const LossArgs& a, int n, int lane) {
 
 // For more than a few thousand rows: each row's place among the live ones
 // (pos, -1 without a target), their number, the largest |dloss| and dX's
-// splits.  One workgroup, eight consecutive rows a thread at a time.
+// splits.  One workgroup, 8192 rows at a time: eight runs of 1024, a row of
+// each per thread, whose live rows the waves count with a ballot per run.
 __global__ __launch_bounds__(1024) void loss_scan_kernel(LossArgs a) {
-    __shared__ int wsum[16];
-    __shared__ float buf[16];
-    constexpr int U = 8;
+    constexpr int U = 8, NW = 16;
+    __shared__ int cnt[U * NW];
+    __shared__ float buf[NW];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int base = 0;
     float g = 0.0f;
     for (int64_t m0 = 0; m0 < a.M; m0 += 1024 * U) {
-        const int64_t first = m0 + tid * U;
         bool on[U];
-        float d[U];
+        float d[U] = {};
+        rows_live<U>(a, m0 + tid, 1024, on);
+        if (a.dloss != nullptr) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t m = min(first + u, a.M - 1);
-            on[u] = row_live(a, m) && first + u < a.M;
-            d[u] = a.dloss != nullptr ? a.dloss[m] : 0.0f;
+            for (int u = 0; u < U; ++u) d[u] = a.dloss[min(m0 + tid + 1024 * u, a.M - 1)];
         }
-        int mine = 0;
+        unsigned long long bits[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            mine += on[u] ? 1 : 0;
+            bits[u] = __ballot(on[u]);
+            if (lane == 0) cnt[u * NW + wave] = __popcll(bits[u]);
             if (on[u]) g = fmaxf(g, fabsf(d[u]));
         }
-        int upto = mine;   // of this wave's threads up to this one
+        __syncthreads();
+        // live rows up to and with each (run, wave), over the 128 of them
+        static_assert(U * NW == 128, "two counts a lane");
+        int lo = cnt[lane], hi = cnt[64 + lane];
+        const int lo1 = lo, hi1 = hi;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
-            const int t = __shfl_up(upto, o);
-            if (lane >= o) upto += t;
-        }
-        if (lane == 63) wsum[wave] = upto;
-        __syncthreads();
-        int at = base + upto - mine, all = 0;
-#pragma unroll
-        for (int w = 0; w < 16; ++w) {
-            at += w < wave ? wsum[w] : 0;
-            all += wsum[w];
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (first + u < a.M) {
-                a.pos[first + u] = on[u] ? at : -1;
-                at += on[u] ? 1 : 0;
+            const int p = __shfl_up(lo, o), q = __shfl_up(hi, o);
+            if (lane >= o) {
+                lo += p;
+                hi += q;
             }
-        base += all;
+        }
+        const int half = __shfl(lo, 63);
+        hi += half;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = u * NW + wave;
+            const int before = at < 64 ? __shfl(lo - lo1, at) : __shfl(hi - hi1, at - 64);
+            const int64_t m = m0 + tid + 1024 * u;
+            if (m < a.M) a.pos[m] = on[u] ? base + before + __popcll(bits[u] & ((1ull << lane) - 1ull)) : -1;
+        }
+        base += __shfl(hi, 63);
         __syncthreads();
     }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) g = fmaxf(g, __shfl_xor(g, o));
     if (lane == 0) buf[wave] = g;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 16; ++w) g = fmaxf(g, buf[w]);
     if (wave > 0) return;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) g = fmaxf(g, buf[w]);
     const int splits = a.dloss != nullptr ? dx_splits(a, base, lane) : 1;
     if (tid == 0) *a.hdr = LossHeader{base, usable_gref(g), splits};
 }
@@ -1129,7 +1150,7 @@ __global__ __launch_bounds__(1024) void loss_scan_kernel(LossArgs a) {
 // 8 values of row m of X from column k on, zeros past K (and for m < 0).
 __device__ __forceinline__ u32x4 row_chunk(const LossArgs& a, int64_t m, int k) {
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (m < 0) return v;
+    if (m < 0 || k >= a.K) return v;
     const uint16_t* src = a.X + m * a.ldx + k;
     if (((uintptr_t)src & 15) == 0 && k + 8 <= a.K) return *(const u32x4*)src;
 #pragma unroll
@@ -1227,6 +1248,13 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
     __shared__ float sp[BWD ? 4 : 1][BWD ? kMaxTargets : 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t r0 = (int64_t)blockIdx.x * kGatherRows;
+    // the wave's row, its first loads (all of them up to 4096 features) under
+    // way while the live rows are counted
+    const int64_t m = r0 + wave;
+    constexpr int U = 8;
+    u32x4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = row_chunk(a, m < a.M ? m : -1, lane * 8 + 512 * u);
     int n, before = 0;
     float gref = 1.0f;
     if constexpr (SCANNED) {
@@ -1237,15 +1265,13 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
         int b = 0, all = 0;
         float g = 0.0f;
         // (eight rows a thread at a time, so that their loads overlap)
-        constexpr int U = 8;
         for (int64_t m0 = tid; m0 < a.M; m0 += 256 * U) {
             bool on[U];
-            float d[U];
+            float d[U] = {};
+            rows_live<U>(a, m0, 256, on);
+            if constexpr (BWD) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t m = m0 + 256 * u, at = min(m, a.M - 1);
-                on[u] = row_live(a, at) && m < a.M;
-                d[u] = BWD ? a.dloss[at] : 0.0f;
+                for (int u = 0; u < U; ++u) d[u] = a.dloss[min(m0 + 256 * u, a.M - 1)];
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -1272,16 +1298,15 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
             if (lane == 0) *a.hdr = LossHeader{n, gref, splits};
         }
         if (wave == 0) {
-            const int64_t m = r0 + lane;
-            const bool on = lane < kGatherRows && m < a.M && row_live(a, m);
+            const int64_t r = r0 + lane;
+            const bool on = lane < kGatherRows && r < a.M && row_live(a, r);
             const unsigned long long bits = __ballot(on);
             if (lane < kGatherRows)
-                places[lane] = m >= a.M ? -2 : on ? before + __popcll(bits & ((1ull << lane) - 1ull)) : -1;
+                places[lane] = r >= a.M ? -2 : on ? before + __popcll(bits & ((1ull << lane) - 1ull)) : -1;
         }
     }
     __syncthreads();
     const int c = places[wave];
-    const int64_t m = r0 + wave;
     if (c != -2) {
         if (c < 0) {
             if constexpr (!BWD) {
@@ -1299,12 +1324,12 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
             }
         } else {
             if (lane == 0) a.map[c] = (int)m;
-            // the row itself, several loads a lane in flight, then its targets
-            constexpr int U = 8;
+            // the row itself, then its targets
             for (int k0 = lane * 8; k0 < a.Kp; k0 += 512 * U) {
-                u32x4 v[U];
+                if (k0 >= 512 * U) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) v[u] = row_chunk(a, k0 + 512 * u < a.Kp ? m : -1, k0 + 512 * u);
+                    for (int u = 0; u < U; ++u) v[u] = row_chunk(a, m, k0 + 512 * u);
+                }
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (k0 + 512 * u < a.Kp) *(u32x4*)(a.Xc + (int64_t)c * a.Kp + k0 + 512 * u) = v[u];
