@@ -1558,10 +1558,78 @@ __global__ __launch_bounds__(T::NT) void loss_grad_kernel(LossArgs a) {
     }
 }
 
-// A workgroup's share of dX's partials: [split] (+)= G(piece) . W(piece) over
-// the split's vocabulary steps.
+// A finished tile times f as rows of a gradient matrix D (bf16 or binary32),
+// columns k0 on: row r of the tile is row where(r) of D; rows of them and cols
+// columns exist.  bf16 goes through LDS, so that the stores write whole row
+// segments.
+template <class T, class Where>
+__device__ __forceinline__ void store_tile(const Acc<T>& acc, float f, void* Dv, bool f32, int64_t ld, int k0, int rows,
+                                           int cols, lds_t* smem, int wave, int lane, Where where) {
+    constexpr int LDG = T::BN * 2 + 16;
+    const Place<T> at(wave, lane);
+    if (f32) {
+        float* D = (float*)Dv + k0;
+        const bool vec = ((uintptr_t)D & 15) == 0 && ld % 4 == 0;
+#pragma unroll
+        for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) {
+                const int row = at.row(ha, i);
+                if (row >= rows) continue;
+                float* d = D + where(row) * ld;
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                    for (int j = 0; j < T::FN; ++j) {
+                        const int col = at.col(hb, j);
+                        const f32x4 v = acc[ha][hb][i][j] * f;
+                        if (vec && col + 4 <= cols) *(f32x4*)(d + col) = v;
+                        else
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (col + r < cols) d[col + r] = v[r];
+                    }
+            }
+        return;
+    }
+#pragma unroll
+    for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+                for (int j = 0; j < T::FN; ++j) {
+                    const f32x4 v = acc[ha][hb][i][j] * f;
+                    const u32x2 w = {(uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16),
+                                     (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16)};
+                    *(u32x2 __attribute__((address_space(3)))*)(smem + at.row(ha, i) * LDG + at.col(hb, j) * 2) = w;
+                }
+    __syncthreads();
+    uint16_t* D = (uint16_t*)Dv + k0;
+    const bool vec = ((uintptr_t)D & 15) == 0 && ld % 8 == 0;
+    constexpr int CPR = T::BN / 8;
+    for (int p = wave * 64 + lane; p < T::BM * CPR; p += T::NT) {
+        const int r = p / CPR, c = (p % CPR) * 8;
+        if (r >= rows || c >= cols) continue;
+        const u32x4 w = *(const u32x4 __attribute__((address_space(3)))*)(smem + r * LDG + c * 2);
+        uint16_t* d = D + where(r) * ld + c;
+        if (vec && c + 8 <= cols) *(u32x4*)d = w;
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < cols) d[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+}
+
+// Whether dX's tiles are its final values: one split of one piece.
+__device__ __forceinline__ bool dx_at_once(const LossArgs& a, int splits) { return splits == 1 && a.vn == a.V; }
+
+// A workgroup's share of dX: G(piece) . W(piece) over the split's vocabulary
+// steps, as the result's own rows where that is all of it, else as a partial
+// ([split] (+)=, live rows only).
 template <class T>
-__device__ __forceinline__ void dx_tile(const LossArgs& a, int n, int tm, int tn, int split, int splits, lds_t* smem,
+__device__ __forceinline__ void dx_tile(const LossArgs& a, int n, int tm, int tn, int split, int splits, float f, lds_t* smem,
                                         int wave, int lane) {
     const int m0 = tm * T::BM, k0 = tn * T::BN;
     const int all = (a.vn + 63) >> 6;
@@ -1575,6 +1643,11 @@ __device__ __forceinline__ void dx_tile(const LossArgs& a, int n, int tm, int tn
     Acc<T> acc;
     main_loop<T>(A, B, steps, smem, wave, lane, acc);
     const Place<T> at(wave, lane);
+    if (dx_at_once(a, splits)) {
+        store_tile<T>(acc, f, a.dX, a.grad_f32, a.lddx, k0, n - m0, a.K - k0, smem, wave, lane,
+                      [&](int r) { return (int64_t)a.map[m0 + r]; });
+        return;
+    }
     float* P = a.dxp + ((int64_t)split * ((n + T::BM - 1) / T::BM) * T::BM + m0) * a.Kp + k0;
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha)
@@ -1585,7 +1658,7 @@ __device__ __forceinline__ void dx_tile(const LossArgs& a, int n, int tm, int tn
 #pragma unroll
                 for (int j = 0; j < T::FN; ++j) {
                     const int col = at.col(hb, j);
-                    if (k0 + col >= a.Kp) continue;
+                    if (k0 + col >= a.Kp || m0 + at.row(ha, i) >= n) continue;
                     f32x4* p = (f32x4*)(P + (int64_t)at.row(ha, i) * a.Kp + col);
                     *p = a.first ? acc[ha][hb][i][j] : *p + acc[ha][hb][i][j];
                 }
@@ -1593,7 +1666,7 @@ __device__ __forceinline__ void dx_tile(const LossArgs& a, int n, int tm, int tn
 
 // The results that are made from partials.  Workgroups from `dx_groups` on:
 // dbias = gref unit (the sum over the row blocks, in order).  Before them, one
-// per row: dX = gref unit scale (the sum of its partials), in the row's own
+// per row, unless the products wrote dX themselves: dX = gref unit scale (the sum of its partials), in the row's own
 // place; where a row has fewer than 128 runs of four features, several threads
 // share each run's splits and join through LDS, in order.
 __global__ __launch_bounds__(256) void loss_outputs_kernel(LossArgs a, float unit, int dx_groups) {
@@ -1615,7 +1688,7 @@ __global__ __launch_bounds__(256) void loss_outputs_kernel(LossArgs a, float uni
         a.dbias[v] = t * (unit * a.hdr->gref);
         return;
     }
-    if (c >= n) return;
+    if (c >= n || dx_at_once(a, splits)) return;
     const float mul = unit * a.scale;
     const int64_t m = a.map[c];
     const float f = mul * a.hdr->gref;
@@ -1673,8 +1746,6 @@ __global__ __launch_bounds__(256) void loss_outputs_kernel(LossArgs a, float uni
 // One tile of a piece's dW: gref unit scale G^T . X.
 template <class T>
 __device__ __forceinline__ void dw_tile(const LossArgs& a, int n, int tm, int tn, float f, lds_t* smem, int wave, int lane) {
-    constexpr int LDG = T::BN * 2 + 16;
-    const int tid = wave * 64 + lane;
     const int p0 = tm * T::BM, k0 = tn * T::BN;
     const int steps = (n + 63) >> 6;
     Operand<T::HA, true, T::IA, T::NW> A;
@@ -1683,59 +1754,8 @@ __device__ __forceinline__ void dw_tile(const LossArgs& a, int n, int tm, int tn
     B.init(a.Xc + k0, a.Kp, a.Kp - k0, steps, 0, wave, lane);
     Acc<T> acc;
     main_loop<T>(A, B, steps, smem, wave, lane, acc);
-    const Place<T> at(wave, lane);
-    const int vr = a.vn - p0, kr = a.K - k0;
-    if (a.grad_f32) {
-        float* D = (float*)a.dW + (int64_t)(a.v0 + p0) * a.lddw + k0;
-        const bool vec = ((uintptr_t)D & 15) == 0 && a.lddw % 4 == 0;
-#pragma unroll
-        for (int ha = 0; ha < 2; ++ha)
-#pragma unroll
-            for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-                for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-                    for (int j = 0; j < T::FN; ++j) {
-                        const int row = at.row(ha, i), col = at.col(hb, j);
-                        if (row >= vr) continue;
-                        const f32x4 v = acc[ha][hb][i][j] * f;
-                        float* p = D + (int64_t)row * a.lddw + col;
-                        if (vec && col + 4 <= kr) *(f32x4*)p = v;
-                        else
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (col + r < kr) p[r] = v[r];
-                    }
-        return;
-    }
-#pragma unroll
-    for (int ha = 0; ha < 2; ++ha)
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-            for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-                for (int j = 0; j < T::FN; ++j) {
-                    const f32x4 v = acc[ha][hb][i][j] * f;
-                    const u32x2 w = {(uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16),
-                                     (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16)};
-                    *(u32x2 __attribute__((address_space(3)))*)(smem + at.row(ha, i) * LDG + at.col(hb, j) * 2) = w;
-                }
-    __syncthreads();
-    uint16_t* D = (uint16_t*)a.dW + (int64_t)(a.v0 + p0) * a.lddw + k0;
-    const bool vec = ((uintptr_t)D & 15) == 0 && a.lddw % 8 == 0;
-    constexpr int CPR = T::BN / 8;
-    for (int p = tid; p < T::BM * CPR; p += T::NT) {
-        const int r = p / CPR, c = (p % CPR) * 8;
-        if (r >= vr || c >= kr) continue;
-        const u32x4 w = *(const u32x4 __attribute__((address_space(3)))*)(smem + r * LDG + c * 2);
-        uint16_t* d = D + (int64_t)r * a.lddw + c;
-        if (vec && c + 8 <= kr) *(u32x4*)d = w;
-        else
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < kr) d[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-    }
+    store_tile<T>(acc, f, a.dW, a.grad_f32, a.lddw, k0, a.vn - p0, a.K - k0, smem, wave, lane,
+                  [&](int r) { return (int64_t)(a.v0 + p0 + r); });
 }
 
 // Both products of a piece in one launch, dX's workgroups first: they need
@@ -1753,7 +1773,7 @@ __global__ __launch_bounds__(TX::NT) void loss_products_kernel(LossArgs a, float
     int tm, tn, split;
     if ((int)blockIdx.x < ndx) {
         map_tile(blockIdx.x, tr, tk, tm, tn, split, splits);
-        dx_tile<TX>(a, n, tm, tn, split, splits, smem, wave, lane);
+        dx_tile<TX>(a, n, tm, tn, split, splits, mul * a.hdr->gref, smem, wave, lane);
     } else if (a.dW != nullptr) {
         if (!map_tile(blockIdx.x - ndx, (a.vn + TW::BM - 1) / TW::BM, tk, tm, tn, split, 1)) return;
         dw_tile<TW>(a, n, tm, tn, mul * a.hdr->gref, smem, wave, lane);

@@ -290,6 +290,16 @@ def test_several_pieces_of_the_vocabulary(mkp, op):
     check(mkp, t, op + " pieces", **({"temperature": 2.0} if op == "distill" else {"smoothing": 0.05}))
 
 
+@pytest.mark.parametrize("f32", [False, True])
+def test_gradients_written_at_once(mkp, f32):
+    """Enough rows and features that dX is one split, written by the product
+    itself: rows left out between live ones, features that end inside a tile."""
+    t = inputs(23, 3000, 300, 4424, keep=0.7, std=0.02)
+    check(mkp, t, "dX at once", f32=f32)
+    t = inputs(24, 2900, 270, 4101, keep=0.7, std=0.02, k=3)
+    check(mkp, t, "dX at once", f32=f32)
+
+
 @pytest.mark.parametrize("op", ["xent", "distill"])
 def test_many_rows(mkp, op):
     """More rows than the gather counts by itself."""
