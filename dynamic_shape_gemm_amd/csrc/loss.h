@@ -73,8 +73,8 @@ struct LossArgs {
     int* pos;               // row -> compact row (calls of many rows)
     uint8_t* live;          // M (distillation)
     uint16_t* Xc;           // live rows of X, Mr x Kp, zero padded
-    int* ids32;             // compact, n x kp: the targets (-1: none)
-    float* wts;             // compact, n x kp: their weights in the gradient
+    int* ids32;             // compact, n x kp: the targets (-1: none; distillation: forward)
+    int2* targets;          // backward, distillation: compact, n x kp: the targets and the bits of their weights
     LossRow* rows;          // compact
     float* part;            // forward: per (row, vocabulary tile) maximum and sum of exponentials
     float* sumz;            // forward with smoothing: per (row, vocabulary tile, wave column) sum of kept values

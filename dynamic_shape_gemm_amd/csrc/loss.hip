@@ -88,6 +88,19 @@ __device__ __forceinline__ float tanh_fast(float x) {
 // from computing the branch's work ahead of it, for everyone.
 __device__ __forceinline__ void rarely() { asm volatile("; rarely taken"); }
 
+// Sum over the 16 lanes of a row (lanes 16 r .. 16 r + 15), by rotations
+// within it.
+template <int N>
+__device__ __forceinline__ float row_rotate(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x120 + N, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row_sum(float v) {
+    v += row_rotate<8>(v);
+    v += row_rotate<4>(v);
+    v += row_rotate<2>(v);
+    return v + row_rotate<1>(v);
+}
+
 // ---- tiles -----------------------------------------------------------------
 //
 // One workgroup multiplies a BM x BN tile over K steps of 64 on 16x16x32
@@ -1184,8 +1197,8 @@ __device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c,
         }
         return;
     }
-    int* ids = a.ids32 + (int64_t)c * a.kp;
     if constexpr (!BWD) {
+        int* ids = a.ids32 + (int64_t)c * a.kp;
         for (int j = lane; j < a.kp; j += 64) ids[j] = j < a.k && target_ok(a, m, j) ? (int)a.ids[m * a.ldids + j] : -1;
     } else {
         // the row's ids (-1: left out) and probabilities, staged in LDS
@@ -1214,7 +1227,7 @@ __device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c,
         }
         __builtin_amdgcn_wave_barrier();   // (one wave's own LDS: its operations stay in order)
         // weights; a target named twice keeps its weight at its first place
-        float* w = a.wts + (int64_t)c * a.kp;
+        int2* out = a.targets + (int64_t)c * a.kp;
         for (int j = lane; j < a.kp; j += 64) {
             const int id = j < a.k ? sid[j] : -1;
             bool first = id >= 0;
@@ -1224,8 +1237,7 @@ __device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c,
                 if (same && u < j) first = false;
                 if (same) p += sp[u];
             }
-            ids[j] = first ? id : -1;
-            w[j] = first ? rel * p : 0.0f;
+            out[j] = make_int2(first ? id : -1, __builtin_bit_cast(int, first ? rel * p : 0.0f));
         }
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) all += __shfl_xor(all, o);
@@ -1367,6 +1379,19 @@ __device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int 
     const int vr = a.V - v0;
     const float s2 = a.s2;
     const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
+    // several targets a row: the first AHEAD pairs of them per thread of a
+    // row's PER, read a half of the rows ahead (-1 past the last)
+    constexpr int PER = T::NT / T::HA, AHEAD = TG ? 32 / PER : 1;
+    int4 tg[AHEAD];
+    [[maybe_unused]] auto targets_ahead = [&](int ha) {
+        const int m = m0 + ha * T::HA + tid / PER;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int q = (tid % PER + PER * i) * 2;
+            tg[i] = m < n && q < a.kp ? *(const int4*)(a.targets + (int64_t)m * a.kp + q) : int4{-1, 0, -1, 0};
+        }
+    };
+    if constexpr (TG) targets_ahead(0);
     BiasRegs<T> bias;
     if (!a.plain) bias.read(a, at, v0);
     LossRow rows[2][T::FM];
@@ -1382,27 +1407,32 @@ __device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int 
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha) {
         if constexpr (TG) {
-            // the weights of the targets in these rows, as a table
+            // the weights of the targets in these rows, as a table; the
+            // targets themselves were read a half ahead
             float __attribute__((address_space(3)))* tab = (float __attribute__((address_space(3)))*)smem;
             constexpr int LD = T::BN + 4;
             if (ha) __syncthreads();
             for (int e = tid * 4; e < T::HA * LD; e += T::NT * 4)
                 *(f32x4 __attribute__((address_space(3)))*)(tab + e) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             __syncthreads();
-            constexpr int PER = T::NT / T::HA;
             const int r = tid / PER, m = m0 + ha * T::HA + r;
+            auto put = [&](int id, int w) {
+                if ((unsigned)(id - v0) < (unsigned)T::BN) tab[r * LD + id - v0] = __builtin_bit_cast(float, w);
+            };
             if (m < n) {
-                const int* ids = a.ids32 + (int64_t)m * a.kp;
-                const float* w = a.wts + (int64_t)m * a.kp;
-                for (int q = (tid % PER) * 4; q < a.kp; q += PER * 4) {
-                    const int4 id = *(const int4*)(ids + q);
-                    const int v[4] = {id.x, id.y, id.z, id.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (v[e] >= 0 && (unsigned)(v[e] - v0) < (unsigned)T::BN) tab[r * LD + v[e] - v0] = w[q + e];
+                for (int i = 0; i < AHEAD; ++i) {
+                    put(tg[i].x, tg[i].y);
+                    put(tg[i].z, tg[i].w);
+                }
+                for (int q = (tid % PER + PER * AHEAD) * 2; q < a.kp; q += PER * 2) {
+                    const int4 p = *(const int4*)(a.targets + (int64_t)m * a.kp + q);
+                    put(p.x, p.y);
+                    put(p.z, p.w);
                 }
             }
             __syncthreads();
+            if (ha == 0) targets_ahead(1);
         }
 #pragma unroll
         for (int i = 0; i < T::FM; ++i) {
@@ -1501,8 +1531,7 @@ __device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int 
                         for (int i = 0; i < T::FM; ++i) t += acc[part * PER + h][hb][i][j];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-#pragma unroll
-                        for (int o = 1; o < 16; o <<= 1) t[r] += __shfl_xor(t[r], o);
+                        t[r] = row_sum(t[r]);
                         if (at.s == 0) red[(part * T::WGM + at.wm) * T::BN + at.col(hb, j) + r] = t[r];
                     }
                     __builtin_amdgcn_sched_barrier(0);

@@ -42,7 +42,7 @@ struct Layout {
     int64_t Mr = 0, Kp = 0, Vp = 0, kp = 1, ntiles = 0;
     int pieces = 1, slots = 256;
     bool pack_w = false, stream = false;
-    size_t hdr = 0, map = 0, pos = 0, live = 0, xc = 0, ids = 0, wts = 0, rws = 0, part = 0, sumz = 0, zt = 0, g = 0, dxp = 0, dbp = 0,
+    size_t hdr = 0, map = 0, pos = 0, live = 0, xc = 0, ids = 0, targets = 0, rws = 0, part = 0, sumz = 0, zt = 0, g = 0, dxp = 0, dbp = 0,
            w = 0, bytes = 0;
 };
 
@@ -65,7 +65,7 @@ Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int6
     l.pos = take(M > kManyRows ? 4 * M : 0);
     l.live = take(k > 0 ? M : 0);
     l.xc = take(2 * l.Mr * l.Kp);
-    l.ids = take(4 * l.Mr * l.kp);
+    l.ids = take(k > 0 && backward ? 0 : 4 * l.Mr * l.kp);
     if (l.pack_w) l.w = take(2 * V * l.Kp);
     if (!backward) {
         l.stream = M <= kStreamRows && !l.pack_w && K % 64 == 0;
@@ -74,7 +74,7 @@ Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int6
         l.sumz = take(4 * M * l.ntiles * loss_sumz_parts(l.tile));
         l.zt = take(4 * l.Mr * l.kp);
     } else {
-        l.wts = take(k > 0 ? 4 * l.Mr * l.kp : 0);
+        l.targets = take(k > 0 ? 8 * l.Mr * l.kp : 0);
         l.rws = take((int64_t)sizeof(LossRow) * l.Mr);
         // pieces of the vocabulary, about equal, whose G fits kPieceBytes
         const int64_t most = std::max<int64_t>(256, kPieceBytes / (2 * std::max<int64_t>(l.Mr, 1)) / 256 * 256);
@@ -276,7 +276,7 @@ int run(const Call& c) {
         return go(LL_FINISH, 0.0, 8.0 * m * (double)l.ntiles, [&] { return launch_loss_finish(a, st); });
     }
 
-    a.wts = (float*)(ws + l.wts);
+    a.targets = (int2*)(ws + l.targets);
     a.rows = (LossRow*)(ws + l.rws);
     a.G = (uint16_t*)(ws + l.g);
     a.dxp = (float*)(ws + l.dxp);
