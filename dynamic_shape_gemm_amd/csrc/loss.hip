@@ -558,8 +558,20 @@ __device__ __forceinline__ void forward_tile(const LossArgs& a, int n, int m0, i
     if constexpr (TG) {
         float __attribute__((address_space(3)))* tab = (float __attribute__((address_space(3)))*)smem;
         constexpr int LD = T::BN + 4;
+        // a row's first targets, AHEAD fours for each of its PER threads, are
+        // read while the half is staged (-1 past the last)
+        constexpr int PER = T::NT / T::HA, AHEAD = 16 / PER;
+        int4 tg[AHEAD];
 #pragma unroll
         for (int ha = 0; ha < 2; ++ha) {
+            const int r = tid / PER, m = m0 + ha * T::HA + r;
+            if (!a.direct) {
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int q = (tid % PER + PER * i) * 4;
+                    tg[i] = m < n && q < a.kp ? *(const int4*)(a.ids32 + (int64_t)m * a.kp + q) : int4{-1, -1, -1, -1};
+                }
+            }
             if (ha) __syncthreads();
 #pragma unroll
             for (int i = 0; i < T::FM; ++i) {
@@ -573,25 +585,28 @@ __device__ __forceinline__ void forward_tile(const LossArgs& a, int n, int m0, i
                 __builtin_amdgcn_sched_barrier(0);
             }
             __syncthreads();
-            constexpr int PER = T::NT / T::HA;   // threads per row
-            const int r = tid / PER, m = m0 + ha * T::HA + r;
-            if (m < n) {
-                if (a.direct) {
-                    const int64_t* ids = a.ids + (int64_t)m * a.ldids;
-                    for (int q = tid % PER; q < a.k; q += PER) {
-                        const int64_t c = ids[q] - v0;
-                        if (c >= 0 && c < T::BN && c < vr) a.zt[(int64_t)m * a.kp + q] = tab[r * LD + (int)c];
-                    }
-                } else {
-                    const int* ids = a.ids32 + (int64_t)m * a.kp;
-                    for (int q = (tid % PER) * 4; q < a.kp; q += PER * 4) {
-                        const int4 id = *(const int4*)(ids + q);
-                        const int c[4] = {id.x - v0, id.y - v0, id.z - v0, id.w - v0};
+            auto pick = [&](int q, int id) {
+                if ((unsigned)(id - v0) < (unsigned)T::BN) a.zt[(int64_t)m * a.kp + q] = tab[r * LD + id - v0];
+            };
+            if (m < n && a.direct) {
+                const int64_t* ids = a.ids + (int64_t)m * a.ldids;
+                for (int q = tid % PER; q < a.k; q += PER)
+                    if (ids[q] >= 0 && ids[q] < a.V) pick(q, (int)ids[q]);
+            } else if (m < n) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if ((unsigned)c[e] < (unsigned)T::BN)
-                                a.zt[(int64_t)m * a.kp + q + e] = tab[r * LD + c[e]];
-                    }
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int q = (tid % PER + PER * i) * 4;
+                    pick(q, tg[i].x);
+                    pick(q + 1, tg[i].y);
+                    pick(q + 2, tg[i].z);
+                    pick(q + 3, tg[i].w);
+                }
+                for (int q = (tid % PER + PER * AHEAD) * 4; q < a.kp; q += PER * 4) {
+                    const int4 id = *(const int4*)(a.ids32 + (int64_t)m * a.kp + q);
+                    pick(q, id.x);
+                    pick(q + 1, id.y);
+                    pick(q + 2, id.z);
+                    pick(q + 3, id.w);
                 }
             }
         }
