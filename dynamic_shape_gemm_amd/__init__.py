@@ -11,6 +11,7 @@ stream) and mkp_gemm_batched(...).
 from __future__ import annotations
 
 import ctypes
+import functools
 import json
 import os
 
@@ -131,6 +132,10 @@ _f_gemm = _fast.gemm if _fast else _lib.mkp_gemm
 _f_gemm_bt = _fast.gemm_bt if _fast else _lib.mkp_gemm_bt
 _f_gemm_batched = _fast.gemm_batched if _fast else _lib.mkp_gemm_batched
 _f_gemm_batched_bt = _fast.gemm_batched_bt if _fast else _lib.mkp_gemm_batched_bt
+_f_linear_xent = _fast.linear_xent if _fast else _lib.mkp_linear_xent
+_f_linear_xent_backward = _fast.linear_xent_backward if _fast else _lib.mkp_linear_xent_backward
+_f_linear_distill = _fast.linear_distill if _fast else _lib.mkp_linear_distill
+_f_linear_distill_backward = _fast.linear_distill_backward if _fast else _lib.mkp_linear_distill_backward
 
 EXPORTED = ["mkp_gemm", "mkp_gemm_batched", "mkp_gemm_batched_noalloc", "mkp_noalloc_scratch_bytes", "mkp_gemm_bt", "mkp_gemm_batched_bt", "mkp_gemm_ex", "mkp_conv2d", "mkp_gemm_grouped",
             "mkp_gemm_grouped_bt", "mkp_linear_xent", "mkp_linear_xent_backward", "mkp_linear_distill",
@@ -293,9 +298,9 @@ def mkp_plan_describe_grouped(M, K, N, bt=False) -> dict:
 
 def mkp_linear_xent_raw(M, V, K, X, ldx, W, ldw, bias, labels, scale, softcap, smoothing, z_loss, loss, lse,
                         workspace, workspace_bytes, stream) -> int:
-    return _lib.mkp_linear_xent(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), _addr(labels), scale, softcap,
-                                smoothing, z_loss, _addr(loss), _addr(lse), _addr(workspace), workspace_bytes,
-                                stream or 0)
+    return _f_linear_xent(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), _addr(labels), scale, softcap,
+                          smoothing, z_loss, _addr(loss), _addr(lse), _addr(workspace), workspace_bytes,
+                          stream or 0)
 
 
 def mkp_linear_xent(M, V, K, X, ldx, W, ldw, bias, labels, scale, softcap, smoothing, z_loss, loss, lse,
@@ -308,10 +313,10 @@ def mkp_linear_xent(M, V, K, X, ldx, W, ldw, bias, labels, scale, softcap, smoot
 
 def mkp_linear_xent_backward_raw(M, V, K, X, ldx, W, ldw, bias, labels, scale, softcap, smoothing, z_loss, lse, dloss,
                                  dX, lddx, dW, lddw, dbias, grad_type, workspace, workspace_bytes, stream) -> int:
-    return _lib.mkp_linear_xent_backward(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), _addr(labels), scale,
-                                         softcap, smoothing, z_loss, _addr(lse), _addr(dloss), _addr(dX), lddx,
-                                         _addr(dW), lddw, _addr(dbias), grad_type, _addr(workspace), workspace_bytes,
-                                         stream or 0)
+    return _f_linear_xent_backward(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), _addr(labels), scale,
+                                   softcap, smoothing, z_loss, _addr(lse), _addr(dloss), _addr(dX), lddx,
+                                   _addr(dW), lddw, _addr(dbias), grad_type, _addr(workspace), workspace_bytes,
+                                   stream or 0)
 
 
 def mkp_linear_xent_backward(M, V, K, X, ldx, W, ldw, bias, labels, scale, softcap, smoothing, z_loss, lse, dloss,
@@ -325,9 +330,9 @@ def mkp_linear_xent_backward(M, V, K, X, ldx, W, ldw, bias, labels, scale, softc
 
 def mkp_linear_distill_raw(M, V, K, X, ldx, W, ldw, bias, k, ids, ldids, teacher, ldt, teacher_lse, temperature, scale,
                            softcap, loss, lse, workspace, workspace_bytes, stream) -> int:
-    return _lib.mkp_linear_distill(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), k, _addr(ids), ldids,
-                                   _addr(teacher), ldt, _addr(teacher_lse), temperature, scale, softcap, _addr(loss),
-                                   _addr(lse), _addr(workspace), workspace_bytes, stream or 0)
+    return _f_linear_distill(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), k, _addr(ids), ldids,
+                             _addr(teacher), ldt, _addr(teacher_lse), temperature, scale, softcap, _addr(loss),
+                             _addr(lse), _addr(workspace), workspace_bytes, stream or 0)
 
 
 def mkp_linear_distill(M, V, K, X, ldx, W, ldw, bias, k, ids, ldids, teacher, ldt, teacher_lse, temperature, scale,
@@ -342,10 +347,10 @@ def mkp_linear_distill(M, V, K, X, ldx, W, ldw, bias, k, ids, ldids, teacher, ld
 def mkp_linear_distill_backward_raw(M, V, K, X, ldx, W, ldw, bias, k, ids, ldids, teacher, ldt, teacher_lse,
                                     temperature, scale, softcap, lse, dloss, dX, lddx, dW, lddw, dbias, grad_type,
                                     workspace, workspace_bytes, stream) -> int:
-    return _lib.mkp_linear_distill_backward(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), k, _addr(ids), ldids,
-                                            _addr(teacher), ldt, _addr(teacher_lse), temperature, scale, softcap,
-                                            _addr(lse), _addr(dloss), _addr(dX), lddx, _addr(dW), lddw, _addr(dbias),
-                                            grad_type, _addr(workspace), workspace_bytes, stream or 0)
+    return _f_linear_distill_backward(M, V, K, _addr(X), ldx, _addr(W), ldw, _addr(bias), k, _addr(ids), ldids,
+                                      _addr(teacher), ldt, _addr(teacher_lse), temperature, scale, softcap,
+                                      _addr(lse), _addr(dloss), _addr(dX), lddx, _addr(dW), lddw, _addr(dbias),
+                                      grad_type, _addr(workspace), workspace_bytes, stream or 0)
 
 
 def mkp_linear_distill_backward(M, V, K, X, ldx, W, ldw, bias, k, ids, ldids, teacher, ldt, teacher_lse, temperature,
@@ -599,9 +604,13 @@ class _LossStream:
         return False
 
 
+# (the size goes by the extents and the weight's alignment alone)
+_loss_workspace_bytes = functools.lru_cache(maxsize=1024)(mkp_linear_loss_workspace)
+
+
 def _loss_workspace(M, V, K, k, w, ldw, backward):
     import torch
-    n = mkp_linear_loss_workspace(M, V, K, k, w, ldw, backward)
+    n = _loss_workspace_bytes(M, V, K, k, w.data_ptr() & 15, ldw, backward)
     return torch.empty(n, dtype=torch.uint8, device=w.device), n
 
 

@@ -104,12 +104,13 @@ def build_library(verbose: bool = False) -> str:
             u = usage[k]
             f.write(f"{k} vgpr={u.get('vgpr')} agpr={u.get('agpr')} scratch={u.get('scratch')} "
                     f"lds={u.get('lds')} occupancy={u.get('occupancy')}\n")
-    # a GEMM micro-kernel that spills to scratch has lost its register
-    # tiling; refuse to ship it
-    spills = [k for k, u in usage.items()
-              if ("gemm_tile_kernel" in k or "gemm_dual_kernel" in k) and u.get("scratch", 0) > 0]
+    # a GEMM micro-kernel or a loss kernel's tile that spills to scratch has
+    # lost its register tiling; refuse to ship it
+    tiles = ("gemm_tile_kernel", "gemm_dual_kernel", "loss_forward_kernel", "loss_grad_kernel",
+             "loss_products_kernel", "loss_stream_kernel")
+    spills = [k for k, u in usage.items() if any(t in k for t in tiles) and u.get("scratch", 0) > 0]
     if spills:
-        raise RuntimeError("GEMM micro-kernels use scratch memory: " + ", ".join(spills))
+        raise RuntimeError("tile kernels use scratch memory: " + ", ".join(spills))
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs, "-ldl"]
     if verbose:
