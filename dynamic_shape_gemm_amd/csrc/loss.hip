@@ -289,6 +289,11 @@ __device__ __forceinline__ void plain_barrier() {
 // eight waves the second four run half a phase behind the first (one barrier
 // more at the start, one less at the end), so on every SIMD one wave
 // multiplies while the other reads.
+// Measured (256 x 256 tile, one per CU): 1.43 us a step, 1500 TFLOP/s over the
+// device, whichever way the operands are read; the waves' MFMAs fill 76-78 %
+// of the cycles at the 1.6-1.8 GHz that the card's power leaves.  Two phases
+// of 32 MFMAs ran out of registers (5-25 % slower), one stage a step ahead
+// with all waves in step took 1.7 us.
 template <class T>
 __device__ __forceinline__ void main_loop(const Operand<T::HA, T::AT, T::IA, T::NW>& A,
                                           const Operand<T::HB, T::BT, T::IB, T::NW>& B, int steps, lds_t* smem,
@@ -437,8 +442,10 @@ __device__ __forceinline__ bool map_tile(int bid, int tm_n, int tn_n, int& tm, i
 // The logit tiles of a launch.  Tiles of one size run in rounds of `slots`
 // workgroups; when the last round would be at most half full, its tiles are
 // halved (two workgroups of half the rows each), which takes about 0.6 of a
-// whole tile's round instead of one.  half: -1 a whole tile, else which half.
-__device__ __forceinline__ bool map_rounds(int bid, int tm_n, int tn_n, int slots, bool halves, int& tm, int& tn, int& half) {
+// whole tile's round instead of one (256 workgroups at 768 features: 19.8 us
+// of halves, 33.6 of whole tiles).  half: -1 a whole tile, else which half.
+__device__ __forceinline__ bool map_rounds(int bid, int tm_n, int tn_n, int slots, bool halves, int& tm, int& tn,
+                                           int& half) {
     const int T = tm_n * tn_n, full = T / slots * slots, r = T - full;
     half = -1;
     if (!halves || 2 * r > slots) {
@@ -532,6 +539,9 @@ __device__ __forceinline__ int row_label(const LossArgs& a, int m, int n) {
 // the fused multiply, so an exponent keeps its digits, and what rounding umax
 // s2 loses is put back where the tiles are joined.  A lane reduces its own 16
 // values of a row; the 4 lanes and the waves that share the row meet in LDS.
+// Bound by the product at many K steps (4096 x 32000 x 4096: 769 us, 1400
+// TFLOP/s), at few by this epilogue too, about 6 us a tile, most of it the
+// 65536 exponentials (1024 x 16384 x 768, one tile a CU: 29.6 us).
 template <class T, bool TG>
 constexpr int forward_lds() {
     const int tab = TG ? T::HA * (T::BN + 4) * 4 : 0, red = T::BM * (8 * T::WGN + 2) * 4;
@@ -724,8 +734,12 @@ __global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
 // block's first steps are under way while the block before is finished.  Each
 // wave multiplies 16 rows of W with the FM * 16 rows of X and keeps every
 // row's running maximum and sum over the blocks; a workgroup leaves one
-// partial per row.  Long K steps: 512 (256) contiguous bytes of a row of W at
-// a time.
+// partial per row.  Long K steps: 512 contiguous bytes of a row of W at a time.
+// Measured, with cold weights (and on 128 x 128 tiles, a quarter of the bytes
+// in flight): 8 x 32000 x 4096 in 49 us (60), 32 rows 50 (60), 8 x 30522 x 768
+// 10.2 (12.6), 32 rows 11.6 (13.7); a form for 33 to 64 rows, its ring of 128
+// columns, took 67 (61), 17 (14) at 33 rows and was dropped.  24 x 128256 x
+// 4096: 175 us, 6.0 TB/s.
 template <int FM_, int BK_, int S_>
 struct Stream {
     static constexpr int FM = FM_, BK = BK_, S = S_;
@@ -1116,7 +1130,8 @@ __device__ __forceinline__ int dx_splits(const LossArgs& a, int n, int lane) {
 // For more than a few thousand rows: each row's place among the live ones
 // (pos, -1 without a target), their number, the largest |dloss| and dX's
 // splits.  One workgroup, 8192 rows at a time: eight runs of 1024, a row of
-// each per thread, whose live rows the waves count with a ballot per run.
+// each per thread, whose live rows the waves count with a ballot per run
+// (5.7 us for 8192 rows).
 __global__ __launch_bounds__(1024) void loss_scan_kernel(LossArgs a) {
     constexpr int U = 8, NW = 16;
     __shared__ int cnt[U * NW];
@@ -1265,6 +1280,7 @@ __device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c,
 // rows: loss_scan_kernel has run) it counts the live rows before them and
 // altogether by itself, which is cheaper than a launch that does.  The rows
 // behind the last live one, up to a whole K step of dW's product, are zeroed.
+// Bound by latencies: 333 x 768 in 5.7 us, 4096 x 4096 in 16 (67 MB).
 constexpr int kGatherRows = 4;
 template <bool BWD, bool SCANNED>
 __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
@@ -1374,9 +1390,10 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
 
 // One tile of G, the gradient by s over gref (and over the call's unit: the
 // label's weight, or T): what multiplies it is put back, in 32 bits, where
-// dX, dW and dbias are made.  So the entry of a label that is far from
-// learnt is near -1 and survives bf16 nearly exactly, whatever the loss is
-// divided by.  G is rounded to bf16 (relative 2^-9 of each entry, to
+// dX, dW and dbias are made.  So the entry of a label that is far from learnt
+// is near -1 and survives bf16 nearly exactly, whatever the loss is divided
+// by.  Bound as the forward tile is, with 128 KB of G a tile to write: 4096 x
+// 32000 x 4096 in 780 us.  G is rounded to bf16 (relative 2^-9 of each entry, to
 // nearest) because the products that follow run on bf16 MFMA.
 template <class T, bool TG>
 constexpr int grad_lds() {
@@ -1673,8 +1690,8 @@ __device__ __forceinline__ bool dx_at_once(const LossArgs& a, int splits) { retu
 // steps, as the result's own rows where that is all of it, else as a partial
 // ([split] (+)=, live rows only).
 template <class T>
-__device__ __forceinline__ void dx_tile(const LossArgs& a, int n, int tm, int tn, int split, int splits, float f, lds_t* smem,
-                                        int wave, int lane) {
+__device__ __forceinline__ void dx_tile(const LossArgs& a, int n, int tm, int tn, int split, int splits, float f,
+                                        lds_t* smem, int wave, int lane) {
     const int m0 = tm * T::BM, k0 = tn * T::BN;
     const int all = (a.vn + 63) >> 6;
     const int per = (all + splits - 1) / splits;
@@ -1708,11 +1725,13 @@ __device__ __forceinline__ void dx_tile(const LossArgs& a, int n, int tm, int tn
                 }
 }
 
-// The results that are made from partials.  Workgroups from `dx_groups` on:
+// The results that are made from partials (bound by their bytes: 7373 x 4096
+// from one partial in 33 us, 5.5 TB/s).  Workgroups from `dx_groups` on:
 // dbias = gref unit (the sum over the row blocks, in order).  Before them, one
-// per row, unless the products wrote dX themselves: dX = gref unit scale (the sum of its partials), in the row's own
-// place; where a row has fewer than 128 runs of four features, several threads
-// share each run's splits and join through LDS, in order.
+// per row, unless the products wrote dX themselves: dX = gref unit scale (the
+// sum of its partials), in the row's own place; where a row has fewer than 128
+// runs of four features, several threads share each run's splits and join
+// through LDS, in order.
 __global__ __launch_bounds__(256) void loss_outputs_kernel(LossArgs a, float unit, int dx_groups) {
     __shared__ f32x4 buf[256];
     const int c = blockIdx.x, n = a.hdr->n, splits = a.hdr->splits, tile = a.tile;
@@ -1804,7 +1823,9 @@ __device__ __forceinline__ void dw_tile(const LossArgs& a, int n, int tm, int tn
 
 // Both products of a piece in one launch, dX's workgroups first: they need
 // the same G, and together they fill the device better than one after the
-// other.
+// other (950 x 50257 x 768: 140 us against 80 and 82; 4096 x 32000 x 4096:
+// 1480 us, 1450 TFLOP/s, bound by the matrix pipe; 333 x 30522 x 768: 49 us,
+// bound by the partials of dX and by dW's 47 MB).
 template <class TX, class TW>
 __global__ __launch_bounds__(TX::NT) void loss_products_kernel(LossArgs a, float mul) {
     constexpr int NEED = TW::BM * (TW::BN * 2 + 16);
@@ -1883,7 +1904,8 @@ hipError_t launch_loss_stream(const LossArgs& a, hipStream_t st) {
         return tg ? launch_kernel(loss_stream_kernel<T, true>, grid, dim3(T::NT), st, a)
                   : launch_kernel(loss_stream_kernel<T, false>, grid, dim3(T::NT), st, a);
     };
-    return a.M <= 16 ? go(Stream<1, 256, 3>{}) : a.M <= 32 ? go(Stream<2, 256, 3>{}) : go(Stream<4, 128, 4>{});
+    static_assert(kStreamRows == 32, "rows of the larger form");
+    return a.M <= 16 ? go(Stream<1, 256, 3>{}) : go(Stream<2, 256, 3>{});
 }
 
 hipError_t launch_loss_finish(const LossArgs& a, hipStream_t st) {

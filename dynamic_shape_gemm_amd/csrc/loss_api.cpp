@@ -18,8 +18,8 @@
 namespace mkp {
 
 const char* loss_launch_name(int i) {
-    static const char* const names[LL_COUNT] = {"loss_flags", "loss_scan",     "loss_gather",    "loss_forward", "loss_finish",
-                                                "loss_grad",  "loss_products", "loss_outputs"};
+    static const char* const names[LL_COUNT] = {"loss_flags",  "loss_scan", "loss_gather",   "loss_forward",
+                                                "loss_finish", "loss_grad", "loss_products", "loss_outputs"};
     return i >= 0 && i < LL_COUNT ? names[i] : "loss";
 }
 
@@ -33,8 +33,14 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 constexpr int64_t kMaxK = int64_t(1) << 21;
 // above this many rows one workgroup counts the live ones; below, every
 // workgroup of the gather does so for itself
+// (rows x features, scan and gather apart / in one: 4096 x 768 11.0 / 9.1 us,
+// 8192 x 768 14.2 / 21.8)
 constexpr int64_t kManyRows = 4096;
-constexpr int64_t kPieceBytes = int64_t(512) << 20;   // G of one piece
+constexpr int64_t kDirectRows = 256;
+// G of one piece: 8192 rows of which 15 % are live, 30522 x 768, took 372 us a
+// step in pieces of 256 MB (two), 325 of 512 and 335 of 1024 (one); 8192 x
+// 128256 x 4096 the same within 0.5 % in 2, 4 or 8 pieces
+constexpr int64_t kPieceBytes = int64_t(512) << 20;
 
 // A call's extents and where its workspace's parts lie.
 struct Layout {
@@ -42,13 +48,17 @@ struct Layout {
     int64_t Mr = 0, Kp = 0, Vp = 0, kp = 1, ntiles = 0;
     int pieces = 1, slots = 256;
     bool pack_w = false, stream = false;
-    size_t hdr = 0, map = 0, pos = 0, live = 0, xc = 0, ids = 0, targets = 0, rws = 0, part = 0, sumz = 0, zt = 0, g = 0, dxp = 0, dbp = 0,
-           w = 0, bytes = 0;
+    size_t hdr = 0, map = 0, pos = 0, live = 0, xc = 0, ids = 0, targets = 0, rws = 0, part = 0, sumz = 0, zt = 0, g = 0,
+           dxp = 0, dbp = 0, w = 0, bytes = 0;
 };
 
 Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int64_t ldw, bool backward) {
     Layout l;
-    l.tile = M > 128 ? 256 : 128;
+    // 256 x 256 tiles, one workgroup per CU, or 128 x 128, two: at 160 rows the
+    // latter made the step over 32000 x 4096 in 372 us (the former 377) and the
+    // one over 30522 x 768 in 66 (75), at 256 in 394 (389) and 72 (80), at 384
+    // in 489 (470) and 99 (102)
+    l.tile = M > 256 ? 256 : 128;
     l.Mr = round_up(M, 256);
     l.Kp = round_up(K, 64);
     l.kp = k > 0 ? round_up(k, 4) : 1;
@@ -264,14 +274,16 @@ int run(const Call& c) {
         a.part = (float*)(ws + l.part);
         a.sumz = !c.distill && c.smoothing > 0.0f ? (float*)(ws + l.sumz) : nullptr;
         a.zt = (float*)(ws + l.zt);
-        // one tile of rows: the product costs the weight's bytes, not its
-        // rows, so none need dropping, and two launches fewer count for more
-        a.direct = c.M <= l.tile && !l.pack_w && aligned16(c.X) && c.ldx % 8 == 0 && c.ldx <= 2 * kMaxK &&
+        // few rows: the product costs the weight's bytes, not its rows, so none
+        // need dropping, and a launch (two) fewer count for more
+        a.direct = c.M <= kDirectRows && !l.pack_w && aligned16(c.X) && c.ldx % 8 == 0 && c.ldx <= 2 * kMaxK &&
                    c.K % 64 == 0;
         a.stream = l.stream && a.direct;
         if (a.stream) a.ntiles = kStreamGroups;
         if (!a.direct && (rc = compact()) != MKP_OK) return rc;
-        if ((rc = go(LL_FORWARD, 2.0 * m * v * k, elem * (m + v) * k, [&] { return a.stream ? launch_loss_stream(a, st) : launch_loss_forward(a, st); })) != MKP_OK)
+        if ((rc = go(LL_FORWARD, 2.0 * m * v * k, elem * (m + v) * k, [&] {
+                 return a.stream ? launch_loss_stream(a, st) : launch_loss_forward(a, st);
+             })) != MKP_OK)
             return rc;
         return go(LL_FINISH, 0.0, 8.0 * m * (double)l.ntiles, [&] { return launch_loss_finish(a, st); });
     }
@@ -289,8 +301,8 @@ int run(const Call& c) {
         a.first = p == 0;
         const double pv = a.vn, both = (c.dX ? 1.0 : 0.0) + (c.dW ? 1.0 : 0.0);
         if (c.M > 0)
-            if ((rc = go(LL_GRAD, 2.0 * m * pv * k, elem * ((m + pv) * k + m * pv), [&] { return launch_loss_grad(a, st); })) !=
-                MKP_OK)
+            if ((rc = go(LL_GRAD, 2.0 * m * pv * k, elem * ((m + pv) * k + m * pv),
+                         [&] { return launch_loss_grad(a, st); })) != MKP_OK)
                 return rc;
         if (c.dX || c.dW)
             if ((rc = go(LL_PRODUCTS, 2.0 * both * m * pv * k,

@@ -127,6 +127,14 @@ def test_few_rows(mkp, M, V, K):
         check(mkp, inputs(M + V, M, V, K, keep=0.8, k=k), "few", grad=False, temperature=2.0)
 
 
+@pytest.mark.parametrize("M", [127, 128, 129, 200, 255, 256, 257])
+@pytest.mark.parametrize("V,K", [(700, 192), (20000, 128)])
+def test_where_the_tiles_change(mkp, M, V, K):
+    """Either side of the rows where the tile and the forward's gather change."""
+    check(mkp, inputs(M + V, M, V, K, keep=0.8, bias=True), "tiles", smoothing=0.1)
+    check(mkp, inputs(M + V, M, V, K, keep=0.8, k=9), "tiles", temperature=1.5)
+
+
 @pytest.mark.parametrize("opt", [dict(scale=0.5), dict(scale=-1.5), dict(softcap=5.0), dict(smoothing=0.1),
                                  dict(smoothing=1.0), dict(z_loss=1e-2), dict(scale=1.3, softcap=2.0, smoothing=0.3,
                                                                              z_loss=1e-3)], ids=str)
