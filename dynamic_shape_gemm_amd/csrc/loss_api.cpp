@@ -154,7 +154,9 @@ int check(const Call& c) {
     if (!c.W) return report(MKP_ERR_INVALID_ARG, "W is NULL");
     if (c.M > 0 && !c.X) return report(MKP_ERR_INVALID_ARG, "X is NULL");
     if (!std::isfinite(c.scale)) return report(MKP_ERR_INVALID_ARG, "scale is not finite");
-    if (!(c.cap >= 0.0f) || !std::isfinite(c.cap)) return report(MKP_ERR_INVALID_ARG, "softcap must be >= 0");
+    // (1 / softcap and log2(e) / T are factors in the kernels)
+    if (!(c.cap >= 0.0f) || !std::isfinite(c.cap) || (c.cap > 0.0f && !std::isfinite(1.0f / c.cap)))
+        return report(MKP_ERR_INVALID_ARG, "softcap must be 0 or more, its reciprocal finite");
     if (!c.distill) {
         if (c.M > 0 && !c.labels) return report(MKP_ERR_INVALID_ARG, "labels is NULL");
         if (!(c.smoothing >= 0.0f && c.smoothing <= 1.0f))
@@ -164,7 +166,8 @@ int check(const Call& c) {
         if (c.k < 1) return report(MKP_ERR_INVALID_ARG, "targets per row must be 1.." + std::to_string(kMaxTargets));
         if (c.M > 0 && (!c.ids || !c.teacher)) return report(MKP_ERR_INVALID_ARG, "ids or teacher is NULL");
         if (c.ldids < c.k || c.ldt < c.k) return report(MKP_ERR_INVALID_ARG, "ldids < k or ldt < k");
-        if (!(c.T > 0.0f) || !std::isfinite(c.T)) return report(MKP_ERR_INVALID_ARG, "temperature must be > 0");
+        if (!(c.T > 0.0f) || !std::isfinite(c.T) || !std::isfinite(1.4427f / c.T))
+            return report(MKP_ERR_INVALID_ARG, "temperature must be more than 0, its reciprocal finite");
     }
     if (c.M > 0 && !c.lse) return report(MKP_ERR_INVALID_ARG, "lse is NULL");
     if (!c.backward) {
@@ -187,9 +190,14 @@ int run(const Call& c) {
     if (!c.ws || c.ws_bytes < 0 || (size_t)c.ws_bytes < l.bytes || !aligned16(c.ws))
         return report(MKP_ERR_INVALID_ARG,
                       "workspace of " + std::to_string(l.bytes) + " bytes, 16-byte aligned, needed");
+    // a launch counts its threads in 32 bits: the tile kernels' (and the halves
+    // and splits that they may add), a workgroup per row, a packed row's chunks
     const int64_t row_tiles = ceil_div(c.M, l.tile), col_tiles = ceil_div(c.K, l.tile);
-    if (row_tiles * ceil_div(c.V, l.tile) > INT_MAX / 2 ||
-        (c.backward && (row_tiles + ceil_div(l.Vp, l.tile)) * col_tiles > INT_MAX / 2))
+    const int64_t logit_tiles = row_tiles * ceil_div(c.V, l.tile) + l.slots;
+    const int64_t grad_tiles = c.backward ? (row_tiles + ceil_div(l.Vp, l.tile)) * col_tiles + 2 * l.slots : 0;
+    const int64_t most = UINT32_MAX;
+    if (std::max(logit_tiles, grad_tiles) > most / (l.tile == 256 ? 512 : 256) ||
+        c.M + ceil_div(c.V, 256) > most / 256 || (l.pack_w && c.V * (l.Kp / 8) > most - 255))
         return report(MKP_ERR_UNSUPPORTED, "grid too large");
     begin_call();
     hipStream_t st = (hipStream_t)c.stream;
@@ -207,7 +215,7 @@ int run(const Call& c) {
     a.scale = c.scale;
     a.cap = c.cap;
     a.T = c.distill ? c.T : 1.0f;
-    a.plain = !c.bias && c.cap == 0.0f && c.scale > 0.0f;
+    a.plain = !c.bias && c.cap == 0.0f && c.scale > 0.0f && std::isfinite(1.4427f * c.scale / a.T);
     a.s2 = (float)(1.4426950408889634 * (a.plain ? (double)c.scale : 1.0) / (double)a.T);
     a.labels = c.distill ? nullptr : c.labels;
     a.smoothing = c.smoothing;

@@ -1,5 +1,6 @@
-/* Argument marshalling for the GEMM and vocabulary-loss entry points of libmkp.so, as a CPython
- * extension: integers in, the C ABI's status code out.  It exists because a
+/* Argument marshalling for the GEMM and vocabulary-loss entry points of
+ * libmkp.so, as a CPython extension: integers in (and floats, for the losses),
+ * the C ABI's status code out.  It exists because a
  * ctypes call converts each of its 10-14 arguments through Python objects,
  * which for the smallest GEMMs costs as much host time as the launch itself.
  * Every argument is a Python int (device addresses included); the stream is

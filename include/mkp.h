@@ -285,6 +285,8 @@ int mkp_plan_describe_grouped(int64_t groups, int64_t M, int64_t K, const int64_
  * outputs, but a W whose rows are not 16-byte aligned, or K not a multiple of
  * 8, costs a padded copy of W per call.  labels and ids are int64 values,
  * ldids and ldt >= k.  V and K are at least 1; M == 0 makes dW and dbias 0.
+ * softcap (unless 0) and temperature have a finite reciprocal.  Extents that
+ * a launch cannot count (2^24 rows, for one) are MKP_ERR_UNSUPPORTED.
  *
  * workspace: device memory of at least mkp_linear_loss_workspace() bytes,
  * 16-byte aligned, whose contents are of no meaning between calls.  The

@@ -254,6 +254,19 @@ def test_teacher_of_lowest_values(mkp, M):
     check(mkp, t, "lowest over T is -inf", temperature=0.5)
 
 
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_largest_scale_over_a_temperature(mkp, M):
+    """scale / T past the largest binary32: logits of 0 stay 0."""
+    t = inputs(14, M, 100, 64, k=2)
+    x = torch.zeros_like(t["x"])
+    loss, lse = mkp.linear_distill(x, t["w"], t["ids"], t["teacher"], scale=3e38, temperature=0.5)
+    # a sum of 100 exponentials of 0, its logarithm to 1 ulp of log2(100) = 6.6 and of ln 2 times that;
+    # a row whose ids are both -1 is left out, its lse 0
+    want = torch.where((t["ids"] >= 0).any(1), math.log(100), 0.0)
+    assert (lse - want).abs().max() <= 4 * 2.0 ** -21
+    assert torch.isfinite(loss).all()
+
+
 def test_a_nan_row_stays_its_own(mkp):
     """A row with a target and NaN features: its loss, its dx row and dw are
     NaN, no other row's."""

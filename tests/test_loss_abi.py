@@ -43,10 +43,11 @@ def distill_bwd(mkp, **over):
 
 COMMON = [dict(M=-1), dict(V=0), dict(K=0), dict(V=-3), dict(K=1 << 22, ldx=1 << 22, ldw=1 << 22), dict(M=1 << 31),
           dict(V=1 << 31), dict(ldx=7), dict(ldw=7), dict(X=0), dict(W=0), dict(lse=0), dict(scale=float("nan")),
-          dict(scale=float("inf")), dict(softcap=-1.0), dict(softcap=float("nan"))]
+          dict(scale=float("inf")), dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=1e-39)]
 BWD = [dict(dloss=0), dict(grad_type=2), dict(lddx=7), dict(lddw=7)]
 DISTILL = [dict(k=0), dict(k=-1), dict(k=1025, ldids=1025, ldt=1025), dict(ids=0), dict(teacher=0), dict(ldids=2),
-           dict(ldt=2), dict(temperature=0.0), dict(temperature=-1.0), dict(temperature=float("inf"))]
+           dict(ldt=2), dict(temperature=0.0), dict(temperature=-1.0), dict(temperature=float("inf")),
+           dict(temperature=1e-39)]
 XENT = [dict(labels=0), dict(smoothing=-0.1), dict(smoothing=1.1), dict(smoothing=float("nan")),
         dict(z_loss=float("inf"))]
 
@@ -83,6 +84,13 @@ def test_too_large_for_a_launch(mkp):
     M, K = (1 << 30) - 1, 1 << 21
     need = mkp.mkp_linear_loss_workspace(M, 10, K, 0, A, K, 1)
     assert xent_bwd(mkp, M=M, K=K, ldx=K, ldw=K, lddx=K, lddw=K, workspace_bytes=need) == mkp.MKP_ERR_UNSUPPORTED
+    # a workgroup per row, tiles of 512 threads, chunks of a padded weight: 2^32 threads each
+    for fn, back, W, ext in ((xent, 0, A, dict(M=1 << 24)), (xent_bwd, 1, A, dict(M=1 << 24)),
+                             (xent, 0, A, dict(M=1 << 20, V=1 << 19)),
+                             (xent, 0, A + 2, dict(V=1 << 29, K=64, ldx=64, ldw=64))):
+        a = dict(dict(M=4, V=10, K=8, ldw=8), **ext)
+        need = mkp.mkp_linear_loss_workspace(a["M"], a["V"], a["K"], 0, W, a["ldw"], back)
+        assert fn(mkp, W=W, workspace_bytes=need, **ext) == mkp.MKP_ERR_UNSUPPORTED, ext
 
 
 def test_nothing_to_do(mkp):
