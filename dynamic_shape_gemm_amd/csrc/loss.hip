@@ -539,7 +539,7 @@ __device__ __forceinline__ int row_label(const LossArgs& a, int m, int n) {
 // the fused multiply, so an exponent keeps its digits, and what rounding umax
 // s2 loses is put back where the tiles are joined.  A lane reduces its own 16
 // values of a row; the 4 lanes and the waves that share the row meet in LDS.
-// Bound by the product at many K steps (4096 x 32000 x 4096: 769 us, 1400
+// Bound by the product at many K steps (4096 x 32000 x 4096: 760 us, 1410
 // TFLOP/s), at few by this epilogue too, about 6 us a tile, most of it the
 // 65536 exponentials (1024 x 16384 x 768, one tile a CU: 29.6 us).
 template <class T, bool TG>

@@ -327,6 +327,52 @@ def test_many_rows(mkp, op):
     check(mkp, inputs(22, 16600, 130, 64, bias=True, k=3 if op == "distill" else 0, keep=0.4), op + " many rows")
 
 
+def past_32_bits(mkp, what, t, rows, cols):
+    """A call on the whole of t against the oracle on those of its rows and
+    vocabulary entries that count (the others have dloss 0, bias -inf)."""
+    print(f"[case] {what} x={tuple(t['x'].shape)} w={tuple(t['w'].shape)}", flush=True)
+    loss, lse = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"])
+    dx, dw, db = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"], t["bias"])
+    x, w, bias, dloss = (v.to(F64) for v in (t["x"][rows], t["w"][cols], t["bias"][cols], t["dloss"][rows]))
+    place = torch.full((len(t["bias"]),), -1, device="cuda")
+    place[cols] = torch.arange(len(cols), device="cuda")
+    ref = oracle.xent(x, w, place[t["labels"][rows]], bias, dloss=dloss)
+    tol = oracle.bounds(ref, x, w, bias, terms=16.0 * float(ref["lse"].abs().max()))
+    for name, got in (("lse", lse[rows]), ("loss", loss[rows]), ("dx", dx[rows]), ("dw", dw[cols]), ("dbias", db[cols])):
+        within(name, got, ref[name], tol[name], what)
+    # the rest is 0: as many entries that are not as among those
+    assert torch.count_nonzero(dx) == torch.count_nonzero(dx[rows])
+    assert torch.count_nonzero(dw) == torch.count_nonzero(dw[cols])
+    assert torch.count_nonzero(db) == torch.count_nonzero(db[cols])
+
+
+@pytest.mark.parametrize("M", [20, 300])
+def test_a_weight_of_more_than_4_gib(mkp, M):
+    V, K, n = (1 << 20) + 5, 2112, 300
+    t = inputs(26, M, n, K, bias=True)
+    few = t["w"]
+    t["w"] = torch.randn(V, K, device="cuda", dtype=BF)
+    cols = torch.cat([torch.arange(100, device="cuda"), torch.arange(V - n + 100, V, device="cuda")])
+    t["w"][cols] = few
+    bias = torch.full((V,), -math.inf, device="cuda")
+    bias[cols] = t["bias"]
+    t["bias"], t["labels"] = bias, cols[t["labels"]]
+    past_32_bits(mkp, "long weight", t, torch.arange(M, device="cuda"), cols)
+
+
+def test_rows_of_more_than_4_gib(mkp):
+    M, V, K, n = (1 << 20) + 5, 300, 2112, 200
+    t = inputs(27, n, V, K, bias=True)
+    few = {name: t[name] for name in ("x", "labels", "dloss")}
+    rows = torch.cat([torch.arange(70, device="cuda"), torch.arange(M - n + 70, M, device="cuda")])
+    t["x"] = torch.randn(M, K, device="cuda", dtype=BF)
+    t["labels"] = torch.randint(0, V, (M,), device="cuda")
+    t["dloss"] = torch.zeros(M, device="cuda")
+    for name, v in few.items():
+        t[name][rows] = v
+    past_32_bits(mkp, "many long rows", t, rows, torch.arange(V, device="cuda"))
+
+
 @pytest.mark.parametrize("grad_dtype", [BF, torch.float32])
 def test_writes_stay_inside(mkp, grad_dtype):
     """Raw entry points with outputs inside larger buffers: what lies between
