@@ -968,7 +968,8 @@ __device__ __forceinline__ float block_max(float v, float* buf) {
 
 __device__ __forceinline__ bool target_ok(const LossArgs& a, int64_t m, int j) {
     const int64_t id = a.ids[m * a.ldids + j];
-    return id >= 0 && id < a.V && a.teacher[m * a.ldt + j] * (1.0f / a.T) != -INFINITY;
+    const float t = a.teacher[m * a.ldt + j];   // (read with the id, not after it)
+    return (id >= 0) & (id < a.V) & (t * (1.0f / a.T) != -INFINITY);
 }
 
 // Join a row's tiles, one workgroup per row.  With s2 the factor to base 2:
@@ -978,22 +979,49 @@ __device__ __forceinline__ bool target_ok(const LossArgs& a, int64_t m, int j) {
 // The differences from the targets are taken to umax first and the logarithm
 // added last: a label that is nearly certain has a small loss, and rounding
 // lse before the difference would leave it few digits.
+// Bound by latencies: what a thread needs first is read ahead of the
+// reductions, all at once.
 __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a, int wgn) {
     __shared__ float buf[4];
     const int tid = threadIdx.x;
     const int64_t c = blockIdx.x;
-    if (!a.direct && c >= (int64_t)a.hdr->n) return;   // (rows without a target were cleared by the gather kernel)
+    const int n = a.direct ? (int)a.M : a.hdr->n;
+    if (c >= n) return;   // (rows without a target were cleared by the gather kernel)
     const int64_t m = a.direct ? c : (int64_t)a.map[c];
     const float* part = a.part + c * a.ntiles * 2;
+    constexpr int U = 2;
+    float2 p[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        p[u] = tid + 256 * u < a.ntiles ? *(const float2*)(part + 2 * (tid + 256 * u)) : make_float2(-INFINITY, 0.0f);
+    const bool xent = a.labels != nullptr;
+    const int64_t y = xent ? a.labels[m] : 0;
+    // the label's kept value, or the thread's first target's, with that target
+    const float* zt = a.zt + c * a.kp;
+    const float* t = xent ? nullptr : a.teacher + m * a.ldt;
+    const float it = 1.0f / a.T;
+    bool ok = false;
+    float u0 = 0.0f, t0 = 0.0f;
+    if (xent) {
+        u0 = zt[0];
+    } else if (tid < a.k) {
+        ok = target_ok(a, m, tid);
+        t0 = t[tid] * it;
+        u0 = zt[tid];
+    }
     const float s2 = a.s2;
     float mx = -INFINITY;
-    for (int t = tid; t < a.ntiles; t += 256) mx = fmaxf(mx, part[2 * t]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) mx = fmaxf(mx, p[u].x);
+    for (int i = tid + 256 * U; i < a.ntiles; i += 256) mx = fmaxf(mx, part[2 * i]);
     mx = block_max(mx, buf);
     const float base = stat_base(mx, s2);
     float sm = 0.0f, sz = 0.0f;
-    for (int t = tid; t < a.ntiles; t += 256) sm += part[2 * t + 1] * exp2_fast(mul_rn(part[2 * t], s2) - base);
+#pragma unroll
+    for (int u = 0; u < U; ++u) sm += p[u].y * exp2_fast(mul_rn(p[u].x, s2) - base);
+    for (int i = tid + 256 * U; i < a.ntiles; i += 256) sm += part[2 * i + 1] * exp2_fast(mul_rn(part[2 * i], s2) - base);
     if (a.sumz != nullptr) {
-        for (int t = tid; t < a.ntiles * wgn; t += 256) sz += a.sumz[c * a.ntiles * wgn + t];
+        for (int i = tid; i < a.ntiles * wgn; i += 256) sz += a.sumz[c * a.ntiles * wgn + i];
         sz = block_sum(sz, buf);
     }
     sm = block_sum(sm, buf);
@@ -1002,11 +1030,10 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a, int wgn) {
     const float l2 = __builtin_amdgcn_logf(sm) + fmaf(-top, s2, base);
     const float lse = kLn2 * fmaf(top, s2, l2);
     const float uz = a.plain ? a.scale : 1.0f;   // u to z
-    if (a.labels != nullptr) {
-        const int64_t y = a.labels[m];
+    if (xent) {
         const bool live = y >= 0 && y < a.V;
         if (tid == 0) {
-            const float u = live ? a.zt[c] : 0.0f;
+            const float u = live ? u0 : 0.0f;
             float v = kLn2 * fmaf(top - u, s2, l2);
             if (a.smoothing > 0.0f) v += a.smoothing * uz * (u - sz / (float)a.V);
             if (a.z_loss != 0.0f) v += a.z_loss * lse * lse;
@@ -1017,10 +1044,8 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a, int wgn) {
         return;
     }
     // the teacher's log-partition over the row
-    const float it = 1.0f / a.T;
-    const float* t = a.teacher + m * a.ldt;
-    float any = 0.0f, tm = -INFINITY, ts = 0.0f;
-    for (int j = tid; j < a.k; j += 256)
+    float any = ok ? 1.0f : 0.0f, tm = ok ? t0 : -INFINITY;
+    for (int j = tid + 256; j < a.k; j += 256)
         if (target_ok(a, m, j)) {
             any = 1.0f;
             tm = fmaxf(tm, t[j] * it);
@@ -1031,18 +1056,20 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a, int wgn) {
         tl = a.teacher_lse[m];
     } else {
         tm = block_max(tm, buf);
-        for (int j = tid; j < a.k; j += 256)
+        float ts = ok ? exp2_fast(kLog2e * (t0 - tm)) : 0.0f;
+        for (int j = tid + 256; j < a.k; j += 256)
             if (target_ok(a, m, j)) ts += exp2_fast(kLog2e * (t[j] * it - tm));
         tl = tm + kLn2 * __builtin_amdgcn_logf(block_sum(ts, buf));
     }
     float kl = 0.0f;
-    for (int j = tid; j < a.k; j += 256) {
-        if (!target_ok(a, m, j)) continue;
-        const float lp = t[j] * it - tl;
-        const float p = exp2_fast(kLog2e * lp);
-        const float u = a.zt[c * a.kp + j];
-        if (p != 0.0f) kl += u * s2 == -INFINITY ? INFINITY : p * (lp + kLn2 * fmaf(top - u, s2, l2));
-    }
+    auto add = [&](float tj, float u) {
+        const float lp = tj - tl;
+        const float q = exp2_fast(kLog2e * lp);
+        if (q != 0.0f) kl += u * s2 == -INFINITY ? INFINITY : q * (lp + kLn2 * fmaf(top - u, s2, l2));
+    };
+    if (ok) add(t0, u0);
+    for (int j = tid + 256; j < a.k; j += 256)
+        if (target_ok(a, m, j)) add(t[j] * it, zt[j]);
     kl = block_sum(kl, buf);
     if (tid == 0) {
         a.loss[m] = any != 0.0f ? a.T * a.T * kl : 0.0f;
@@ -1064,16 +1091,8 @@ __global__ __launch_bounds__(256) void loss_flags_kernel(LossArgs a) {
     if (lane == 0) a.live[m] = any ? 1 : 0;
 }
 
-__device__ __forceinline__ bool row_live(const LossArgs& a, int64_t m) {
-    if (a.labels != nullptr) {
-        const int64_t y = a.labels[m];
-        return y >= 0 && y < a.V;
-    }
-    return a.live[m] != 0;
-}
-
-// The same for U rows from m on, `by` apart (false past the last), their loads
-// issued together.
+// Which of U rows from m on, `by` apart, are live (false past the last), their
+// loads issued together.
 template <int U>
 __device__ __forceinline__ void rows_live(const LossArgs& a, int64_t m, int by, bool (&on)[U]) {
     if (a.labels != nullptr) {
@@ -1202,57 +1221,85 @@ __device__ __forceinline__ u32x4 row_chunk(const LossArgs& a, int64_t m, int k) 
     return v;
 }
 
+// What a wave reads of its row before it knows the row's place: the label, or
+// lane j's first target, and the row's gradient.
+struct RowInput {
+    int64_t id = -1;
+    float t = 0.0f, tl = 0.0f, dloss = 0.0f, lse = 0.0f;
+};
+template <bool BWD>
+__device__ __forceinline__ RowInput row_input(const LossArgs& a, int64_t m, int lane) {
+    RowInput in;
+    if (a.labels != nullptr) {
+        in.id = a.labels[m];
+    } else if (lane < a.k) {
+        in.id = a.ids[m * a.ldids + lane];
+        in.t = a.teacher[m * a.ldt + lane];
+    }
+    if constexpr (BWD) {
+        in.dloss = a.dloss[m];
+        in.lse = a.lse[m];
+        if (a.labels == nullptr && a.teacher_lse != nullptr) in.tl = a.teacher_lse[m];
+    }
+    return in;
+}
+
 // One wave: compact row c's targets and gradient constants, from row m.
 template <bool BWD>
-__device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c, float gref, int lane, int* sid, float* sp) {
+__device__ __forceinline__ void row_targets(const LossArgs& a, int64_t m, int c, const RowInput& in, float gref, int lane,
+                                            int* sid, float* sp) {
     float rel = 1.0f, lse2 = 0.0f;
     if constexpr (BWD) {
-        rel = a.dloss[m] / gref;
-        const float l = a.lse[m];
+        rel = in.dloss / gref;
         // a row without any finite logit: every probability 0
-        lse2 = l == -INFINITY ? INFINITY : l * kLog2e;
+        lse2 = in.lse == -INFINITY ? INFINITY : in.lse * kLog2e;
     }
     if (a.labels != nullptr) {
         if (lane == 0) {
-            a.ids32[(int64_t)c * a.kp] = (int)a.labels[m];
+            a.ids32[(int64_t)c * a.kp] = (int)in.id;
             if constexpr (BWD) {
                 // everything over (1 - smoothing), so that a label's own
                 // weight is exactly the row's share of gref
                 const float unit = a.smoothing < 1.0f ? 1.0f - a.smoothing : 1.0f;
                 // (no probability: nothing for the penalty to weigh either)
-                const float cq = a.z_loss != 0.0f && lse2 != INFINITY ? 1.0f + 2.0f * a.z_loss * a.lse[m] : 1.0f;
+                const float cq = a.z_loss != 0.0f && lse2 != INFINITY ? 1.0f + 2.0f * a.z_loss * in.lse : 1.0f;
                 a.rows[c] = LossRow{lse2, rel * cq / unit, rel * a.smoothing / ((float)a.V * unit),
                                     a.smoothing < 1.0f ? rel : 0.0f};
             }
         }
         return;
     }
+    const float it = 1.0f / a.T;
+    // lane j's first target, then those 64 on: the id (-1: left out) and t / T
+    auto target = [&](int j, float& t) {
+        const int64_t id = j < 64 ? in.id : a.ids[m * a.ldids + j];
+        t = (j < 64 ? in.t : a.teacher[m * a.ldt + j]) * it;
+        return id >= 0 && id < a.V && t != -INFINITY ? (int)id : -1;
+    };
     if constexpr (!BWD) {
         int* ids = a.ids32 + (int64_t)c * a.kp;
-        for (int j = lane; j < a.kp; j += 64) ids[j] = j < a.k && target_ok(a, m, j) ? (int)a.ids[m * a.ldids + j] : -1;
+        float t;
+        for (int j = lane; j < a.kp; j += 64) ids[j] = j < a.k ? target(j, t) : -1;
     } else {
-        // the row's ids (-1: left out) and probabilities, staged in LDS
-        const float* t = a.teacher + m * a.ldt;
-        const float it = 1.0f / a.T;
-        float tl = 0.0f, tm = -INFINITY, ts = 0.0f, all = 0.0f;
+        // the row's ids and t / T, then its probabilities, staged in LDS
+        float tl = in.tl, tm = -INFINITY, ts = 0.0f, all = 0.0f;
         for (int j = lane; j < a.k; j += 64) {
-            const bool ok = target_ok(a, m, j);
-            sid[j] = ok ? (int)a.ids[m * a.ldids + j] : -1;
-            if (ok) tm = fmaxf(tm, t[j] * it);
+            float t;
+            sid[j] = target(j, t);
+            sp[j] = t;
+            if (sid[j] >= 0) tm = fmaxf(tm, t);
         }
-        if (a.teacher_lse != nullptr) {
-            tl = a.teacher_lse[m];
-        } else {
+        if (a.teacher_lse == nullptr) {
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) tm = fmaxf(tm, __shfl_xor(tm, o));
             for (int j = lane; j < a.k; j += 64)
-                if (sid[j] >= 0) ts += exp2_fast(kLog2e * (t[j] * it - tm));
+                if (sid[j] >= 0) ts += exp2_fast(kLog2e * (sp[j] - tm));
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) ts += __shfl_xor(ts, o);
             tl = tm + kLn2 * __builtin_amdgcn_logf(ts);
         }
         for (int j = lane; j < a.k; j += 64) {
-            sp[j] = sid[j] >= 0 ? exp2_fast(kLog2e * (t[j] * it - tl)) : 0.0f;
+            sp[j] = sid[j] >= 0 ? exp2_fast(kLog2e * (sp[j] - tl)) : 0.0f;
             all += sp[j];
         }
         __builtin_amdgcn_wave_barrier();   // (one wave's own LDS: its operations stay in order)
@@ -1291,13 +1338,18 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
     __shared__ float sp[BWD ? 4 : 1][BWD ? kMaxTargets : 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t r0 = (int64_t)blockIdx.x * kGatherRows;
-    // the wave's row, its first loads (all of them up to 4096 features) under
-    // way while the live rows are counted
+    // the wave's row, its first loads (all of them up to 4096 features) and
+    // what its place hangs on under way while the live rows are counted
     const int64_t m = r0 + wave;
     constexpr int U = 8;
     u32x4 v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = row_chunk(a, m < a.M ? m : -1, lane * 8 + 512 * u);
+    RowInput in;
+    if (m < a.M) in = row_input<BWD>(a, m, lane);
+    int64_t own = -1;
+    if (!SCANNED && lane < kGatherRows && r0 + lane < a.M)
+        own = a.labels != nullptr ? a.labels[r0 + lane] : a.live[r0 + lane] != 0 ? 0 : -1;
     int n, before = 0;
     float gref = 1.0f;
     if constexpr (SCANNED) {
@@ -1341,11 +1393,10 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
             if (lane == 0) *a.hdr = LossHeader{n, gref, splits};
         }
         if (wave == 0) {
-            const int64_t r = r0 + lane;
-            const bool on = lane < kGatherRows && r < a.M && row_live(a, r);
+            const bool on = own >= 0 && own < a.V;
             const unsigned long long bits = __ballot(on);
             if (lane < kGatherRows)
-                places[lane] = r >= a.M ? -2 : on ? before + __popcll(bits & ((1ull << lane) - 1ull)) : -1;
+                places[lane] = r0 + lane >= a.M ? -2 : on ? before + __popcll(bits & ((1ull << lane) - 1ull)) : -1;
         }
     }
     __syncthreads();
@@ -1377,7 +1428,7 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
                 for (int u = 0; u < U; ++u)
                     if (k0 + 512 * u < a.Kp) *(u32x4*)(a.Xc + (int64_t)c * a.Kp + k0 + 512 * u) = v[u];
             }
-            row_targets<BWD>(a, m, c, gref, lane, sid[BWD ? wave : 0], sp[BWD ? wave : 0]);
+            row_targets<BWD>(a, m, c, in, gref, lane, sid[BWD ? wave : 0], sp[BWD ? wave : 0]);
         }
     }
     // (at most 63 rows, over the workgroups' waves)

@@ -215,7 +215,8 @@ int run(const Call& c) {
     a.scale = c.scale;
     a.cap = c.cap;
     a.T = c.distill ? c.T : 1.0f;
-    a.plain = !c.bias && c.cap == 0.0f && c.scale > 0.0f && std::isfinite(1.4427f * c.scale / a.T);
+    // (x.w times a factor that is 0, or more than there is, would lose what z has)
+    a.plain = !c.bias && c.cap == 0.0f && c.scale > 0.0f && std::isnormal(1.4427f * c.scale / a.T);
     a.s2 = (float)(1.4426950408889634 * (a.plain ? (double)c.scale : 1.0) / (double)a.T);
     a.labels = c.distill ? nullptr : c.labels;
     a.smoothing = c.smoothing;
