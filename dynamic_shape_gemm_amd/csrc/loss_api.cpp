@@ -54,11 +54,16 @@ struct Layout {
 
 Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int64_t ldw, bool backward) {
     Layout l;
-    // 256 x 256 tiles, one workgroup per CU, or 128 x 128, two: at 160 rows the
-    // latter made the step over 32000 x 4096 in 372 us (the former 377) and the
-    // one over 30522 x 768 in 66 (75), at 256 in 394 (389) and 72 (80), at 384
-    // in 489 (470) and 99 (102)
-    l.tile = M > 256 ? 256 : 128;
+    // 256 x 256 tiles, one workgroup per CU, or 128 x 128, two, which few
+    // rows fill better and which reuse half as much of what they load.  Steps, 128 (256): 160 rows x 32000 x 4096 372 us
+    // (377), x 30522 x 768 66 (75); 256 rows 394 (389) and 72 (80).  Where the
+    // last row of large tiles would be at most half full, and few K steps leave
+    // much of a tile's time to its ends: 384 rows x 30522 x 768 117 (125), x
+    // 50257 x 768 191 (206), x 50257 x 256 99 (110), 640 rows 166 (177), 250
+    // (265), 124 (143); but x 32000 x 1024 155 (148) and 217 (213), and 509 rows
+    // x 30522 x 768 137 (130).
+    const bool half_full = (M - 1) % 256 < 128;
+    l.tile = M <= 256 || (M <= 640 && K <= 768 && half_full) ? 128 : 256;
     l.Mr = round_up(M, 256);
     l.Kp = round_up(K, 64);
     l.kp = k > 0 ? round_up(k, 4) : 1;

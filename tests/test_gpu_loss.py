@@ -127,8 +127,8 @@ def test_few_rows(mkp, M, V, K):
         check(mkp, inputs(M + V, M, V, K, keep=0.8, k=k), "few", grad=False, temperature=2.0)
 
 
-@pytest.mark.parametrize("M", [127, 128, 129, 200, 255, 256, 257])
-@pytest.mark.parametrize("V,K", [(700, 192), (20000, 128)])
+@pytest.mark.parametrize("M", [127, 128, 129, 200, 255, 256, 257, 384, 385, 513, 640, 641])
+@pytest.mark.parametrize("V,K", [(700, 192), (20000, 128), (300, 776)])
 def test_where_the_tiles_change(mkp, M, V, K):
     """Either side of the rows where the tile and the forward's gather change."""
     check(mkp, inputs(M + V, M, V, K, keep=0.8, bias=True), "tiles", smoothing=0.1)
