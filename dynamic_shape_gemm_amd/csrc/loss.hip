@@ -20,6 +20,7 @@
 #include "loss.h"
 
 #include "kernels.h"
+#include "load8.h"
 
 #include <hip/hip_ext.h>
 
@@ -33,7 +34,6 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) unsigned char lds_t;
@@ -1211,14 +1211,10 @@ __global__ __launch_bounds__(1024) void loss_scan_kernel(LossArgs a) {
 
 // 8 values of row m of X from column k on, zeros past K (and for m < 0).
 __device__ __forceinline__ u32x4 row_chunk(const LossArgs& a, int64_t m, int k) {
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (m < 0 || k >= a.K) return v;
+    if (m < 0 || k >= a.K) return u32x4{0u, 0u, 0u, 0u};
     const uint16_t* src = a.X + m * a.ldx + k;
     if (((uintptr_t)src & 15) == 0 && k + 8 <= a.K) return *(const u32x4*)src;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (k + e < a.K) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
-    return v;
+    return load8_any(src, a.K - k);
 }
 
 // What a wave reads of its row before it knows the row's place: the label, or
