@@ -12,8 +12,8 @@
 namespace mkp {
 
 constexpr int kMaxTargets = 1024;   // per row (distillation)
-constexpr int kDbiasRows = 128;
-constexpr int kStreamRows = 32;
+constexpr int kDbiasRows = 128;     // rows of one partial sum of dbias
+constexpr int kStreamRows = 32;     // most rows of the kernel for few rows
 constexpr int kStreamGroups = 256;   // workgroups of the kernel for few rows: one per CU
 
 // What a call keeps in its workspace besides the large arrays; written by

@@ -36,6 +36,9 @@ constexpr int64_t kMaxK = int64_t(1) << 21;
 // (rows x features, scan and gather apart / in one: 4096 x 768 11.0 / 9.1 us,
 // 8192 x 768 14.2 / 21.8)
 constexpr int64_t kManyRows = 4096;
+// up to here the forward pass takes rows as they come: a gather costs 6 us,
+// 256 rows instead of 128 cost 5 (32000 x 4096: 87 against 83) or 2.5 (30522 x
+// 768: 17 against 14)
 constexpr int64_t kDirectRows = 256;
 // G of one piece: 8192 rows of which 15 % are live, 30522 x 768, took 372 us a
 // step in pieces of 256 MB (two), 325 of 512 and 335 of 1024 (one); 8192 x
