@@ -73,15 +73,17 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // Round to nearest even, NaN kept a NaN: the conversion instruction.
 __device__ __forceinline__ uint16_t f32_to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// tanh: an odd polynomial (its Taylor series, next term below 1e-8 relative)
-// where 1 - 2/(1 + e^2x) would cancel, that form elsewhere.
+// tanh: x (1 + x^2 p(x^2)), p fitted to the least largest relative error (0.25 of
+// U = 2^-24) below 1/2, where 1 - 2/(1 + e^2|x|) would cancel; that form elsewhere.
+// Relative error at most 2.2 U below 1/2 and 6.5 U above (1.7 and 3.4 found over
+// 400000 points); a longer p instead costs 7 % of 4096 x 30522 x 768 forward.
 __device__ __forceinline__ float tanh_fast(float x) {
     const float x2 = x * x;
-    const float p = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f),
-                                      -1.0f / 3.0f), 1.0f);
-    const float e = exp2_fast(2.0f * kLog2e * x);
-    const float f = fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + e), 1.0f);
-    return fabsf(x) < 0.25f ? p : f;
+    const float p = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 0.017241468653082848f, -0.05304548516869545f),
+                                               0.13325878977775574f), -0.333331435918808f), 1.0f);
+    const float e = exp2_fast(2.0f * kLog2e * fabsf(x));
+    const float f = copysignf(fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + e), 1.0f), x);
+    return fabsf(x) < 0.5f ? p : f;
 }
 
 // At the head of a branch that few calls or lanes take: keeps the compiler

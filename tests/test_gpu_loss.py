@@ -558,3 +558,27 @@ def test_trace_names_the_launches(mkp):
         mkp.mkp_set_option("trace", 0)
     assert names == ["loss_forward", "loss_finish", "loss_flags", "loss_gather", "loss_grad", "loss_products",
                      "loss_outputs"]
+
+
+@pytest.mark.parametrize("M", [32, 200, 4096])
+def test_capped_logits_keep_their_digits(mkp, M):
+    """With one vocabulary entry lse is the logit itself, cap tanh(s / cap).
+    s and s / 4 are exact (x0 + x1 / 256 of bf16 values, cap 4).  In units of
+    U = 2^-24: lse = fl(ln2 fl(log2e z)) adds 1 + 1 and the constants' 0.3.
+    Below |s / 4| = 1/2 tanh is a polynomial: its own 0.25, the last addition's
+    0.6, what is rounded before it times s^2 / 48 < 0.1 (0.3), the product's 1.
+    From 1/2 on it is 1 - 2 / (1 + e), e = e^(2 |s / 4|) good to 2.5 |s / 4| + 2:
+    with the sum's and the reciprocal's 3 at most 6.5."""
+    U = 2.0 ** -24
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.zeros(M, 64, device="cuda", dtype=BF)
+    x[:, 0] = (torch.randint(1, 129, (M,), generator=g, device="cuda") / 16).to(BF)     # 1/16 .. 8
+    x[:, 1] = (torch.randint(0, 256, (M,), generator=g, device="cuda") / 16).to(BF)     # over 256: below 1/16
+    x *= torch.where(torch.rand(M, 1, generator=g, device="cuda") < 0.5, -1.0, 1.0).to(BF)
+    w = torch.zeros(1, 64, device="cuda", dtype=BF)
+    w[0, 0], w[0, 1] = 1.0, 2.0 ** -8
+    y = torch.zeros(M, dtype=torch.int64, device="cuda")
+    _, lse = mkp.linear_xent(x, w, y, softcap=4.0)
+    s = x[:, 0].to(F64) + x[:, 1].to(F64) / 256
+    ref = 4.0 * torch.tanh(s / 4)
+    within("lse", lse, ref, torch.where(s.abs() < 2.0, 4.5, 9.0) * U * ref.abs(), "capped")
