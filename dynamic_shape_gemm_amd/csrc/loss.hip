@@ -77,13 +77,21 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float v) { return __builtin_bit_
 // U = 2^-24) below 1/2, where 1 - 2/(1 + e^2|x|) would cancel; that form elsewhere.
 // Relative error at most 2.2 U below 1/2 and 6.5 U above (1.7 and 3.4 found over
 // 400000 points); a longer p instead costs 7 % of 4096 x 30522 x 768 forward.
-__device__ __forceinline__ float tanh_fast(float x) {
+// slope: 1 - tanh^2 = 4 r (1 - r), r = 1/(1 + e^2|x|) <= 1/2, without a difference
+// of nearly equal values however close to 1 the tanh is.
+__device__ __forceinline__ float tanh_fast(float x, float& slope) {
     const float x2 = x * x;
     const float p = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 0.017241468653082848f, -0.05304548516869545f),
                                                0.13325878977775574f), -0.333331435918808f), 1.0f);
     const float e = exp2_fast(2.0f * kLog2e * fabsf(x));
-    const float f = copysignf(fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + e), 1.0f), x);
+    const float r = __builtin_amdgcn_rcpf(1.0f + e);
+    const float f = copysignf(fmaf(-2.0f, r, 1.0f), x);
+    slope = 4.0f * fmaf(-r, r, r);
     return fabsf(x) < 0.5f ? p : f;
+}
+__device__ __forceinline__ float tanh_fast(float x) {
+    float slope;
+    return tanh_fast(x, slope);
 }
 
 // At the head of a branch that few calls or lanes take: keeps the compiler
@@ -483,10 +491,9 @@ struct BiasRegs {
     }
 };
 
-// One row of fragments: acc (x.w) -> z in place.
+// One row of fragments: acc (x.w) -> s in place.
 template <class T>
-__device__ __forceinline__ void row_logits(const LossArgs& a, const BiasRegs<T>& bias, float inv_cap, Acc<T>& acc, int ha,
-                                           int i) {
+__device__ __forceinline__ void row_affine(const LossArgs& a, const BiasRegs<T>& bias, Acc<T>& acc, int ha, int i) {
 #pragma unroll
     for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
@@ -494,6 +501,13 @@ __device__ __forceinline__ void row_logits(const LossArgs& a, const BiasRegs<T>&
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 acc[ha][hb][i][j][r] = fmaf(a.scale, acc[ha][hb][i][j][r], bias.b[hb][j][r]);
+}
+
+// One row of fragments: acc (x.w) -> z in place.
+template <class T>
+__device__ __forceinline__ void row_logits(const LossArgs& a, const BiasRegs<T>& bias, float inv_cap, Acc<T>& acc, int ha,
+                                           int i) {
+    row_affine<T>(a, bias, acc, ha, i);
     if (a.cap > 0.0f) {
         rarely();
 #pragma unroll
@@ -1519,20 +1533,39 @@ __device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int 
         for (int i = 0; i < T::FM; ++i) {
             const int row = at.row(ha, i);
             const LossRow c = rows[ha][i];
-            if (!a.plain) row_logits<T>(a, bias, inv_cap, acc, ha, i);
+            if (!a.plain) row_affine<T>(a, bias, acc, ha, i);
             f32x4 v[2][T::FN];
+            if (a.cap > 0.0f) {   // acc becomes dz/ds
+                rarely();
 #pragma unroll
-            for (int hb = 0; hb < 2; ++hb)
+                for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-                for (int j = 0; j < T::FN; ++j) {
+                    for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[hb][j][r] = fmaf(exp2_fast(fmaf(acc[ha][hb][i][j][r], s2, -c.lse2)), c.rq, -c.ru);
-                    if constexpr (TG)
+                        for (int r = 0; r < 4; ++r) {
+                            float slope;
+                            const float z = a.cap * tanh_fast(acc[ha][hb][i][j][r] * inv_cap, slope);
+                            v[hb][j][r] = fmaf(exp2_fast(fmaf(z, s2, -c.lse2)), c.rq, -c.ru);
+                            acc[ha][hb][i][j][r] = slope;
+                        }
+            } else {
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            v[hb][j][r] = fmaf(exp2_fast(fmaf(acc[ha][hb][i][j][r], s2, -c.lse2)), c.rq, -c.ru);
+            }
+            if constexpr (TG) {
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                    for (int j = 0; j < T::FN; ++j)
                         v[hb][j] -= *(const f32x4 __attribute__((address_space(3)))*)(
                             (float __attribute__((address_space(3)))*)smem + (row - ha * T::HA) * (T::BN + 4) +
                             at.col(hb, j));
-                }
+            }
             if constexpr (!TG) {
                 // (the wave's columns are two runs of FN * 16)
                 const unsigned lab = (unsigned)labs[ha][i];
@@ -1547,17 +1580,12 @@ __device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int 
                                 v[hb][j][r] -= lab == (unsigned)(hb * T::HB + j * 16 + at.g * 4 + r) ? c.rp : 0.0f;
                 }
             }
-            if (a.cap > 0.0f) {   // (then acc holds z)
+            if (a.cap > 0.0f) {
                 rarely();
 #pragma unroll
                 for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-                    for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float t = acc[ha][hb][i][j][r] * inv_cap;
-                            v[hb][j][r] *= fmaf(-t, t, 1.0f);
-                        }
+                    for (int j = 0; j < T::FN; ++j) v[hb][j] *= acc[ha][hb][i][j];
             }
             if (m0 + T::BM > n) {   // rows past the live ones
                 rarely();

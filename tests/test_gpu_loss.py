@@ -582,3 +582,38 @@ def test_capped_logits_keep_their_digits(mkp, M):
     s = x[:, 0].to(F64) + x[:, 1].to(F64) / 256
     ref = 4.0 * torch.tanh(s / 4)
     within("lse", lse, ref, torch.where(s.abs() < 2.0, 4.5, 9.0) * U * ref.abs(), "capped")
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_slope_of_saturated_logits(mkp, op, M):
+    """dbias of one row is its D.  With x = 0 the logits are cap tanh(b / cap)
+    of known b, up to 15 caps: their slope (1 - tanh^2, down to 4e-13) keeps
+    its digits.  Relative errors: the slope's exponential (6 |b / cap| + 16) U;
+    a probability's (|z|, lse < 10, cap tanh good to 2^-21) 2^-18."""
+    cap, V = 2.0, 97
+    t = inputs(33, M, V, 64, k=3 if op == "distill" else 0)
+    t["x"][:] = 0
+    t["bias"] = torch.linspace(-15.0 * cap, 15.0 * cap, V, device="cuda")
+    t["dloss"][:] = 0
+    t["dloss"][0] = 0.75
+    if op == "xent":
+        t["labels"][0] = V - 3
+        _, lse = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"], softcap=cap)
+        _, _, db = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"], t["bias"], softcap=cap)
+    else:
+        t["ids"][0] = torch.tensor([1, V // 2, V - 3])
+        _, lse = mkp.linear_distill(t["x"], t["w"], t["ids"], t["teacher"], t["bias"], softcap=cap)
+        _, _, db = mkp.linear_distill_backward(t["x"], t["w"], t["ids"], t["teacher"], lse, t["dloss"], t["bias"],
+                                               softcap=cap)
+    b = t["bias"].to(F64)
+    slope = 1.0 / torch.cosh(b / cap) ** 2
+    q = torch.softmax(cap * torch.tanh(b / cap), 0)
+    p = torch.zeros(V, device="cuda", dtype=F64)
+    if op == "xent":
+        p[V - 3] = 1.0
+    else:
+        p[t["ids"][0]] = torch.softmax(t["teacher"][0].to(F64), 0)
+    f = 0.75 * slope
+    tol = f * ((q + p) * 2.0 ** -18 + (q - p).abs() * (6.0 * b.abs() / cap + 16.0) * 2.0 ** -24)
+    within("dbias", db, (q - p) * f, tol, "saturated")
