@@ -181,14 +181,20 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t l
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
                  : "memory", "m0");
 }
+// The same from an address of each lane's own.
+__device__ __forceinline__ void dma16_at(const void* p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds)
+                 : "memory", "m0");
+}
 #pragma clang diagnostic pop
 
 // One operand of a tile: where its halves' loads come from.
 //   rows (not TR): `lim` valid rows of the tile; a last step of fewer than 64
-//     columns (`tail` > 0 of them) repeats the step's first chunk in the
-//     missing ones, where the other operand holds zeros
+//     columns (`tail` > 0 of them) takes the missing ones from `zeros`, 16 bytes
+//     of them, as does the other operand: an infinity times 0 would be NaN
 //   columns (TR): `lim` valid columns of the tile; a last step of fewer than
-//     64 rows repeats its last row likewise
+//     64 rows repeats its last row, where the other operand holds zeros (that
+//     row's own product takes part already, so an infinity in it changes nothing)
 // Both need `lim` and `tail` to be multiples of 8 columns.
 template <int H, bool TR, int I, int NW>
 struct Operand {
@@ -197,12 +203,13 @@ struct Operand {
     int64_t ld;
     uint32_t off[2][I];
     int lim, steps, tail;
+    const uint16_t* zeros;
 
+    // (most: TR, the rows there are)
     __device__ __forceinline__ uint32_t offset(int h, int i, int wave, int lane, int most) const {
         int r, c;
         half_slot<H, TR>((i * NW + wave) * 64 + lane, r, c);
         if constexpr (!TR) {
-            if (c >= most) c = 0;
             r = min(h * H + r, lim - 1);
         } else {
             r = min(r, most - 1);
@@ -211,8 +218,9 @@ struct Operand {
         return (uint32_t)((r * ld + c) * 2);
     }
     __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_, int lim_, int steps_, int tail_, int wave,
-                                         int lane) {
+                                         int lane, const uint16_t* zeros_ = nullptr) {
         base = (const char*)p;
+        zeros = zeros_;
         ld = ld_;
         lim = lim_;
         steps = steps_;
@@ -227,7 +235,15 @@ struct Operand {
         const char* b = base + step * step_bytes;
         if (tail > 0 && step == steps - 1) {
 #pragma unroll
-            for (int i = 0; i < I; ++i) dma16(b, offset(h, i, wave, lane, tail), lds + (i * NW + wave) * 1024);
+            for (int i = 0; i < I; ++i) {
+                if constexpr (TR) {
+                    dma16(b, offset(h, i, wave, lane, tail), lds + (i * NW + wave) * 1024);
+                } else {
+                    int r, c;
+                    half_slot<H, TR>((i * NW + wave) * 64 + lane, r, c);
+                    dma16_at(c < tail ? b + off[h][i] : (const char*)zeros, lds + (i * NW + wave) * 1024);
+                }
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < I; ++i) dma16(b, off[h][i], lds + (i * NW + wave) * 1024);
@@ -531,7 +547,8 @@ __device__ __forceinline__ void logits_tile(const LossArgs& a, int m0, int v_til
     Operand<T::HA, false, T::IA, T::NW> A;
     Operand<T::HB, false, T::IB, T::NW> B;
     A.init(X + (int64_t)m0 * ldx, ldx, n - m0, steps, 0, wave, lane);
-    B.init(a.W + (int64_t)v_tile * a.ldw, a.ldw, a.V - v_tile, steps, a.Kw & 63, wave, lane);
+    // (K not a multiple of 64: the compacted rows end in zeros, at least eight)
+    B.init(a.W + (int64_t)v_tile * a.ldw, a.ldw, a.V - v_tile, steps, a.Kw & 63, wave, lane, a.Xc + a.Kp - 8);
     main_loop<T>(A, B, steps, smem, wave, lane, acc);
 }
 

@@ -617,3 +617,16 @@ def test_slope_of_saturated_logits(mkp, op, M):
     f = 0.75 * slope
     tol = f * ((q + p) * 2.0 ** -18 + (q - p).abs() * (6.0 * b.abs() / cap + 16.0) * 2.0 ** -24)
     within("dbias", db, (q - p) * f, tol, "saturated")
+
+
+@pytest.mark.parametrize("M", [20, 300])
+@pytest.mark.parametrize("K", [8, 72, 200, 76])
+def test_weight_rows_of_minus_infinity(mkp, M, K):
+    """Rows of W that hold -inf under features above 0: their logits are -inf,
+    so they are out of the sum, also where the last K step is not full."""
+    t = inputs(34, M, 150, K)
+    t["x"].abs_().clamp_(min=0.01)
+    t["w"][::7] = -math.inf
+    t["labels"] = t["labels"] // 7 * 7 + 1
+    loss, lse = check(mkp, t, "-inf in w", grad=False)
+    assert torch.isfinite(loss).all() and torch.isfinite(lse).all()
