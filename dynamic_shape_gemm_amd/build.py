@@ -72,6 +72,14 @@ def parse_resource_usage(remarks: str) -> dict:
     return out
 
 
+def too_few_waves(usage: dict) -> list:
+    """The vocabulary losses' tile kernels whose registers leave a SIMD fewer
+    than two waves: their launches count two workgroups of the 128 x 128 tile
+    (or the eight waves of a 256 x 256 one) on a CU."""
+    tiles = ("loss_forward_kernel", "loss_grad_kernel", "loss_products_kernel")
+    return sorted(k for k, u in usage.items() if any(t in k for t in tiles) and u.get("occupancy", 0) < 2)
+
+
 def build_library(verbose: bool = False) -> str:
     obj_dir = os.path.join(HERE, "_build")
     os.makedirs(obj_dir, exist_ok=True)
@@ -111,6 +119,9 @@ def build_library(verbose: bool = False) -> str:
     spills = [k for k, u in usage.items() if any(t in k for t in tiles) and u.get("scratch", 0) > 0]
     if spills:
         raise RuntimeError("tile kernels use scratch memory: " + ", ".join(spills))
+    alone = too_few_waves(usage)
+    if alone:
+        raise RuntimeError("loss tiles counted as two workgroups per CU fit one: " + ", ".join(alone))
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs, "-ldl"]
     if verbose:

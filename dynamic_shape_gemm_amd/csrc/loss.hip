@@ -746,8 +746,11 @@ __device__ __forceinline__ void forward_tile(const LossArgs& a, int n, int m0, i
     }
 }
 
+// (At least two waves a SIMD: LossArgs::slots counts two workgroups of a 128 x
+// 128 tile on a CU.  Without that bound the distillation gradient took 269
+// registers and ran one: 99 us a step of 160 x 30522 x 768, 91 with it.)
 template <class T, class H, bool TG>
-__global__ __launch_bounds__(T::NT) void loss_forward_kernel(LossArgs a) {
+__global__ __launch_bounds__(T::NT, 2) void loss_forward_kernel(LossArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char raw[std::max(forward_lds<T, TG>(), forward_lds<H, TG>())];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = a.direct ? (int)a.M : a.hdr->n;
@@ -1697,7 +1700,7 @@ __device__ __forceinline__ void grad_tile(const LossArgs& a, int n, int m0, int 
 }
 
 template <class T, class H, bool TG>
-__global__ __launch_bounds__(T::NT) void loss_grad_kernel(LossArgs a) {
+__global__ __launch_bounds__(T::NT, 2) void loss_grad_kernel(LossArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char raw[std::max(grad_lds<T, TG>(), grad_lds<H, TG>())];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = a.hdr->n;
@@ -1921,7 +1924,7 @@ __device__ __forceinline__ void dw_tile(const LossArgs& a, int n, int tm, int tn
 // 1480 us, 1450 TFLOP/s, bound by the matrix pipe; 333 x 30522 x 768: 49 us,
 // bound by the partials of dX and by dW's 47 MB).
 template <class TX, class TW>
-__global__ __launch_bounds__(TX::NT) void loss_products_kernel(LossArgs a, float mul) {
+__global__ __launch_bounds__(TX::NT, 2) void loss_products_kernel(LossArgs a, float mul) {
     constexpr int NEED = TW::BM * (TW::BN * 2 + 16);
     __shared__ __attribute__((aligned(1024))) unsigned char raw[TX::LDS > NEED ? TX::LDS : NEED];
     lds_t* smem = (lds_t*)raw;

@@ -129,3 +129,26 @@ def test_helpers_refuse(mkp):
         mkp.linear_distill(x, w, ids, t[:, :1])
     with pytest.raises(TypeError):
         mkp.linear_distill(x, w, ids, t.double())
+
+
+def test_build_refuses_tiles_that_fill_a_cu_alone():
+    """A loss tile of 269 registers (one wave a SIMD) is named, one of 239 not."""
+    import importlib.util
+    import os
+
+    import dynamic_shape_gemm_amd as m
+    path = os.path.join(os.path.dirname(m.__file__), "build.py")
+    spec = importlib.util.spec_from_file_location("mkp_build", path)
+    build = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(build)
+    remark = ("x.hip:1:0: remark: Function Name: {} [-R]\nx.hip:1:0: remark:     VGPRs: {} [-R]\n"
+              "x.hip:1:0: remark:     Occupancy [waves/SIMD]: {} [-R]\n")
+    usage = build.parse_resource_usage(remark.format("a_loss_grad_kernel", 173, 1) +
+                                       remark.format("b_loss_grad_kernel", 143, 2) +
+                                       remark.format("loss_stream_kernel", 62, 1))
+    assert build.too_few_waves(usage) == ["a_loss_grad_kernel"]
+    if os.path.exists(build.RESOURCE_REPORT):   # what was built
+        with open(build.RESOURCE_REPORT) as f:
+            built = {line.split()[0]: dict(p.split("=") for p in line.split()[1:]) for line in f}
+        tiles = [u for k, u in built.items() if "loss_grad_kernel" in k or "loss_forward_kernel" in k]
+        assert tiles and all(int(u["occupancy"]) >= 2 for u in tiles)
