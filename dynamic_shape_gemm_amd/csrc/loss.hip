@@ -1013,8 +1013,10 @@ __device__ __forceinline__ bool target_ok(const LossArgs& a, int64_t m, int j) {
 //   cross entropy: lse - (1 - e) z_y - e / V sum z + c lse^2
 //   distillation:  T^2 sum_j p_j (log p_j - (z_j / T - lse))
 // The differences from the targets are taken to umax first and the logarithm
-// added last: a label that is nearly certain has a small loss, and rounding
-// lse before the difference would leave it few digits.
+// added last, so a loss is good to some 40 x 2^-24 (17 found, of losses below 1)
+// however large lse is; rounding lse before the difference would cost that of
+// lse (1300 at 980).  Not less than that: a label that is the row's largest adds
+// its own exponential, 1, to the others', so a loss of 1e-5 has one digit or two.
 // Bound by latencies: what a thread needs first is read ahead of the
 // reductions, all at once.
 __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a, int wgn) {

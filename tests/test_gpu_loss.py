@@ -630,3 +630,40 @@ def test_weight_rows_of_minus_infinity(mkp, M, K):
     t["labels"] = t["labels"] // 7 * 7 + 1
     loss, lse = check(mkp, t, "-inf in w", grad=False)
     assert torch.isfinite(loss).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("V", [500, 70000])
+@pytest.mark.parametrize("M", [20, 200, 1000])
+def test_small_losses_at_a_large_log_partition(mkp, M, V, bias):
+    """Labels ahead of the rest by margins that leave losses from ln V down to
+    1e-5, every logit near 960 and exact (small multiples of 1/8).  In units of
+    U = 2^-24: the label's exponential, 1, takes part in about 30 additions,
+    with its own error, the logarithm's and the last products' at most 40; the
+    other terms' sum is good to 80 of itself (their exponents' rounding, 30
+    additions), the result to 4.  Rounding lse before the label's logit is
+    taken off would cost 700."""
+    U = 2.0 ** -24
+    g = torch.Generator(device="cuda").manual_seed(M + V)
+    y = 7
+    w = torch.zeros(V, 64, device="cuda", dtype=BF)
+    n = torch.randint(-24, 25, (V,), generator=g, device="cuda") / 8
+    n[y] = 0
+    w[:, 1] = n.to(BF)
+    w[y, 2] = 1.0
+    x = torch.zeros(M, 64, device="cuda", dtype=BF)
+    x[:, 1] = 1.0
+    margin = torch.linspace(0, math.log(V) + 14, M, device="cuda").mul(4).round().div(4)
+    x[:, 2] = margin.to(BF)
+    b = None
+    if bias:
+        b = torch.full((V,), 960.0, device="cuda")
+    else:
+        x[:, 0], w[:, 0] = 30.0, 32.0
+    labels = torch.full((M,), y, device="cuda")
+    loss, lse = mkp.linear_xent(x, w, labels, b)
+    rest = torch.cat([n[:y], n[y + 1:]]).to(F64)
+    ref = torch.log1p(torch.exp(torch.logsumexp(rest, 0) - x[:, 2].to(F64)))
+    within("loss", loss, ref, U * (40 + 80 * -torch.expm1(-ref) + 4 * ref), "small losses")
+    want = 960 + x[:, 2].to(F64) + ref
+    within("lse", lse, want, U * (120 + 8 * want), "small losses")
