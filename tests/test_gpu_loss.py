@@ -667,3 +667,61 @@ def test_small_losses_at_a_large_log_partition(mkp, M, V, bias):
     within("loss", loss, ref, U * (40 + 80 * -torch.expm1(-ref) + 4 * ref), "small losses")
     want = 960 + x[:, 2].to(F64) + ref
     within("lse", lse, want, U * (120 + 8 * want), "small losses")
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("M,V,K", [(1, 9000, 64), (40, 20000, 128), (300, 20000, 128), (1000, 50257, 64), (700, 33000, 264)])
+def test_dx_alone(mkp, M, V, K, op, f32):
+    """dX without dW is cut into more splits of the vocabulary, up to what its
+    workspace is sized for, on both tiles."""
+    print(f"[case] dx alone {op} {M} {V} {K}", flush=True)
+    t = inputs(36, M, V, K, keep=0.9, k=5 if op == "distill" else 0, std=0.1)
+    d = {n: (v.to(F64) if v is not None and v.is_floating_point() else v) for n, v in t.items()}
+    more = dict(need_dw=False, need_dbias=False, grad_dtype=torch.float32 if f32 else BF)
+    if op == "xent":
+        _, lse = mkp.linear_xent(t["x"], t["w"], t["labels"])
+        dx, dw, db = mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"], **more)
+        ref = oracle.xent(d["x"], d["w"], d["labels"], dloss=d["dloss"])
+    else:
+        _, lse = mkp.linear_distill(t["x"], t["w"], t["ids"], t["teacher"])
+        dx, dw, db = mkp.linear_distill_backward(t["x"], t["w"], t["ids"], t["teacher"], lse, t["dloss"], **more)
+        ref = oracle.distill(d["x"], d["w"], d["ids"], d["teacher"], dloss=d["dloss"])
+    assert dw is None and db is None
+    within("dx", dx, ref["dx"], oracle.bounds(ref, d["x"], d["w"])["dx32" if f32 else "dx"], "dx alone")
+
+
+@pytest.mark.parametrize("need", [(True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("M,V,K,pad_w,k", [(20, 5000, 128, 0, 0), (20, 5000, 128, 0, 200), (40, 20000, 128, 0, 0),
+                                           (300, 20000, 128, 0, 5), (1000, 50257, 64, 0, 0), (600, 3000, 100, 0, 3),
+                                           (70, 1300, 72, 3, 7), (5000, 1300, 72, 3, 0), (4200, 70000, 64, 0, 6),
+                                           (9000, 40000, 64, 0, 0)])
+def test_calls_stay_inside_their_workspace(mkp, M, V, K, pad_w, k, need):
+    """A workspace of exactly the bytes reported, between guards: splits of dX,
+    several pieces of the vocabulary, both losses, a copied weight.  What it
+    holds before (bytes of 0xA5, or of 0xFF: NaN) does not matter."""
+    print(f"[case] workspace {M} {V} {K} pad {pad_w} k {k} {need}", flush=True)
+    t = inputs(37, M, V, K, pad_w=pad_w, keep=0.9, k=k)
+    ldw = t["w"].stride(0)
+    loss, lse = torch.empty(2, M, device="cuda")
+    dx, dw, db = torch.empty(M, K, device="cuda"), torch.empty(V, K, device="cuda"), torch.empty(V, device="cuda")
+    out = (dx if need[0] else None, K, dw if need[1] else None, K, db, mkp.MKP_F32)
+    got = []
+    for fill in (0xA5, 0xFF):
+        for back in (False, True):
+            n = mkp.mkp_linear_loss_workspace(M, V, K, k, t["w"], ldw, back)
+            buf = torch.full((n + 2048,), fill, device="cuda", dtype=torch.uint8)
+            ws = buf.data_ptr() + 1024
+            tgt = (t["labels"], 1.0, 0.0, 0.1, 0.0) if not k else (k, t["ids"], k, t["teacher"], k, 0, 1.0, 1.0, 0.0)
+            fwd = mkp.mkp_linear_distill if k else mkp.mkp_linear_xent
+            bwd = mkp.mkp_linear_distill_backward if k else mkp.mkp_linear_xent_backward
+            args = (M, V, K, t["x"], K, t["w"], ldw, None) + tgt
+            if back:
+                bwd(*args, lse, t["dloss"], *out, ws, n)
+            else:
+                fwd(*args, loss, lse, ws, n)
+            torch.cuda.synchronize()
+            assert (buf[:1024] == fill).all() and (buf[1024 + n:] == fill).all(), back
+        got.append([v.clone() for v in (loss, lse, db) + (dx,) * need[0] + (dw,) * need[1]])
+        assert all(torch.isfinite(v).all() for v in got[-1])
+    assert all(torch.equal(p, q) for p, q in zip(*got))
