@@ -55,18 +55,45 @@ struct Layout {
            dxp = 0, dbp = 0, w = 0, bytes = 0;
 };
 
+// What a call costs on tiles of one size, in K steps of all CUs on 256 x 256
+// tiles (1.37 us).  Of those one workgroup runs per CU, of 128 x 128 tiles two,
+// which reuse half as much of what they load (a step of theirs, a quarter of
+// the work in each, 0.7) but have smaller ends.  The logits take rounds of as
+// many tiles as run at once, a last one that is at most half full little more
+// than half the time (halved tiles, or one workgroup a CU); a tile's ends (its
+// exponentials, the pipeline's filling) come on top of its steps.  Backward,
+// dX's and dW's tiles share a launch without rounds; dW's have a step per 64
+// rows, and ends again.
+double tile_cost(int64_t M, int64_t V, int64_t K, bool backward, int tile) {
+    const bool big = tile == 256;
+    const double step = big ? 1.0 : 0.7, end = big ? 4.0 : 1.75;
+    const int64_t slots = big ? 256 : 512, tiles = ceil_div(M, tile) * ceil_div(V, tile), last = tiles % slots;
+    const double rounds = (double)(tiles / slots) + (last == 0 ? 0.0 : 2 * last <= slots ? 0.55 : 1.0);
+    double cost = rounds * (step * (double)ceil_div(K, 64) + end);
+    if (backward) {
+        const double one = (double)ceil_div(M, 64) + (big ? 10.0 : 5.5), cols = (double)ceil_div(K, tile);
+        const double all = cols * ((double)ceil_div(V, tile) * one + (double)ceil_div(M, tile) * (double)ceil_div(V, 64));
+        cost += step * (all / (double)slots + 0.5 * one);
+    }
+    return cost;
+}
+
+// The tile that costs less.  Over 528 extents of 48 to 8000 rows x 1000 to
+// 128256 x 64 to 5120 it is within 0.5 % in the mean of the faster of the two,
+// forward and backward (always 256: 5 and 10 %; 128 up to 256 rows only: 4 and
+// 8).  Forward, 128 / 256: 256 rows x 50257 x 4096 153 us / 108, 384 x 8000 x
+// 4096 52 / 72, 320 x 50257 x 768 51 / 56; backward, 320 x 50257 x 768 131 /
+// 149, 512 x 50257 x 4096 732 / 623, 8000 x 1000 x 640 104 / 187.
+int tile_for(int64_t M, int64_t V, int64_t K, bool backward) {
+    // (small tiles only where a launch can count them, with room to spare)
+    const int64_t rows = ceil_div(M, 128), cols = ceil_div(V, 128), most = int64_t(1) << 22;
+    if (rows > most || cols > most || rows * cols > most || (rows + cols) * ceil_div(K, 128) > most) return 256;
+    return tile_cost(M, V, K, backward, 128) < tile_cost(M, V, K, backward, 256) ? 128 : 256;
+}
+
 Layout layout_of(int64_t M, int64_t V, int64_t K, int64_t k, const void* W, int64_t ldw, bool backward) {
     Layout l;
-    // 256 x 256 tiles, one workgroup per CU, or 128 x 128, two, which few
-    // rows fill better and which reuse half as much of what they load.  Steps, 128 (256): 160 rows x 32000 x 4096 372 us
-    // (377), x 30522 x 768 66 (75); 256 rows 394 (389) and 72 (80).  Where the
-    // last row of large tiles would be at most half full, and few K steps leave
-    // much of a tile's time to its ends: 384 rows x 30522 x 768 117 (125), x
-    // 50257 x 768 191 (206), x 50257 x 256 99 (110), 640 rows 166 (177), 250
-    // (265), 124 (143); but x 32000 x 1024 155 (148) and 217 (213), and 509 rows
-    // x 30522 x 768 137 (130).
-    const bool half_full = (M - 1) % 256 < 128;
-    l.tile = M <= 256 || (M <= 640 && K <= 768 && half_full) ? 128 : 256;
+    l.tile = tile_for(M, V, K, backward);
     l.Mr = round_up(M, 256);
     l.Kp = round_up(K, 64);
     l.kp = k > 0 ? round_up(k, 4) : 1;

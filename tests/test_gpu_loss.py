@@ -725,3 +725,62 @@ def test_calls_stay_inside_their_workspace(mkp, M, V, K, pad_w, k, need):
         got.append([v.clone() for v in (loss, lse, db) + (dx,) * need[0] + (dw,) * need[1]])
         assert all(torch.isfinite(v).all() for v in got[-1])
     assert all(torch.equal(p, q) for p, q in zip(*got))
+
+
+LARGE = [(513, 20000, 512), (400, 16000, 1024), (400, 16000, 1000), (700, 8000, 1021)]
+
+
+@pytest.mark.parametrize("opt", [dict(), dict(smoothing=0.1, z_loss=1e-3), dict(scale=0.8, softcap=4.0)], ids=str)
+@pytest.mark.parametrize("M,V,K", LARGE)
+def test_xent_on_large_tiles(mkp, M, V, K, opt):
+    """Extents for which 256 x 256 tiles cost less, forward and backward: whole
+    and halved last rounds, halves without a live row, K steps not full."""
+    check(mkp, inputs(M + K, M, V, K, keep=0.8, std=0.05, bias=bool(opt)), "large", f32=not opt, **dict(opt))
+
+
+@pytest.mark.parametrize("k", [1, 9, 300])
+@pytest.mark.parametrize("M,V,K", LARGE)
+def test_distill_on_large_tiles(mkp, M, V, K, k):
+    check(mkp, inputs(M + K + k, M, V, K, keep=0.8, std=0.05, bias=k == 9, k=k), "large", temperature=1.5,
+          **({"softcap": 5.0} if k == 9 else {}))
+
+
+@pytest.mark.parametrize("M,V,K", [(200, 20000, 200), (256, 33000, 1024), (129, 65000, 192)])
+def test_few_rows_on_large_tiles(mkp, M, V, K):
+    """Rows as they come, on 256 x 256 tiles."""
+    check(mkp, inputs(M, M, V, K, keep=0.8, std=0.05), "large", grad=False)
+    check(mkp, inputs(M, M, V, K, keep=0.8, std=0.05, bias=True, k=9), "large", grad=False, temperature=2.0, softcap=4.0)
+    x = torch.randn(M, (K + 63) // 64 * 64, device="cuda", dtype=BF)   # K a multiple of 64: nothing is gathered
+    w = torch.randn(V, x.shape[1], device="cuda", dtype=BF) * 0.05
+    y = torch.randint(-20, V, (M,), device="cuda")
+    check(mkp, {"x": x, "w": w, "labels": y, "bias": None}, "direct", grad=False, smoothing=0.1)
+    ids = torch.randint(-2000, V, (M, 7), device="cuda")
+    check(mkp, {"x": x, "w": w, "ids": ids, "teacher": torch.randn(M, 7, device="cuda"), "bias": None}, "direct", grad=False)
+
+
+def test_left_out_and_masked_on_large_tiles(mkp):
+    M, V, K = 400, 16000, 1024
+    t = inputs(44, M, V, K, keep=0.6, std=0.05, bias=True)
+    dead = t["labels"] < 0
+    clean = check(mkp, t, "clean")
+    t["x"][dead] = float("nan")
+    t["dloss"][dead] = float("nan")
+    assert all(torch.equal(p, q) for p, q in zip(clean, check(mkp, t, "dirty")))
+    t["bias"][50:15000] = -math.inf
+    t["labels"] = torch.where(dead, t["labels"], t["labels"] % 50)
+    check(mkp, t, "masked", z_loss=1e-3)
+    t["bias"][:] = torch.finfo(torch.float32).min
+    loss, lse = mkp.linear_xent(t["x"], t["w"], t["labels"], t["bias"])
+    assert torch.isposinf(loss[~dead]).all() and torch.isneginf(lse[~dead]).all() and (loss[dead] == 0).all()
+    for v in mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"], t["bias"]):
+        assert torch.isfinite(v).all()
+    t["labels"][:] = -1
+    for v in mkp.linear_xent_backward(t["x"], t["w"], t["labels"], lse, t["dloss"], t["bias"]):
+        assert (v == 0).all()
+
+
+@pytest.mark.parametrize("M", [5000, 8200])
+def test_many_rows_on_small_tiles(mkp, M):
+    """A narrow vocabulary, for which 128 x 128 tiles cost less at any M."""
+    check(mkp, inputs(45, M, 700, 136, keep=0.7, bias=True), "small", smoothing=0.05)
+    check(mkp, inputs(46, M, 700, 136, keep=0.7, k=20), "small", temperature=2.0, softcap=6.0)
