@@ -121,7 +121,7 @@ _lib.mkp_trace_dump.restype = _int
 _lib.mkp_last_error.argtypes = []
 _lib.mkp_last_error.restype = ctypes.c_char_p
 
-# The GEMM entry points through the CPython marshalling module built beside
+# The GEMM and loss entry points through the CPython marshalling module built beside
 # the library (a ctypes call spends ~1.5 us converting 10-14 arguments, as
 # long as the smallest GEMMs take on the GPU); ctypes where it is absent.
 try:
@@ -630,7 +630,8 @@ def linear_xent(x, w, labels, bias=None, scale=1.0, softcap=0.0, smoothing=0.0, 
     """Cross entropy of each row's label with the logits of a linear layer,
     which are not stored: x (M,K) bf16, w (V,K) bf16, labels (M,) int64, bias
     (V,) fp32 or None.  Returns (loss, lse), fp32 (M,); rows whose label is not
-    in [0, V) get 0.  The mean over the others is loss.sum() / their number."""
+    in [0, V) get 0.  The mean over the others is loss.sum() / their number.
+    Neither has a grad_fn: gradients come from linear_xent_backward."""
     import torch
     M, V, K, ldx, ldw = _loss_inputs(x, w, bias, {"labels": (labels, torch.int64, (x.shape[0],))})
     with _LossStream(x.device, stream, x, w, labels, bias) as st:
@@ -680,7 +681,8 @@ def linear_distill(x, w, ids, teacher, bias=None, temperature=1.0, scale=1.0, so
     (at temperature T) from a teacher known by its k top logits: x (M,K) bf16,
     w (V,K) bf16, ids (M,k) int64 (entries outside [0, V) are left out),
     teacher (M,k) fp32, teacher_lse (M,) fp32 or None (then the teacher's
-    probabilities are normalised over the k).  Returns (loss, lse), fp32 (M,)."""
+    probabilities are normalised over the k).  Returns (loss, lse), fp32 (M,),
+    without a grad_fn: gradients come from linear_distill_backward."""
     import torch
     M, V, K, ldx, ldw, k, ldi, ldt = _distill_inputs(x, w, bias, ids, teacher, teacher_lse)
     with _LossStream(x.device, stream, x, w, ids, teacher, bias, teacher_lse) as st:

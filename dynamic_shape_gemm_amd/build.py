@@ -136,7 +136,7 @@ FAST = os.path.join(HERE, "_mkpfast" + (sysconfig.get_config_var("EXT_SUFFIX") o
 
 
 def build_fast_binding(verbose: bool = False) -> str:
-    """The CPython marshalling module for the GEMM entry points (host C,
+    """The CPython marshalling module for the GEMM and loss entry points (host C,
     linked against libmkp.so next to it)."""
     tmp = FAST + ".tmp"
     cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-Wall", "-I", sysconfig.get_paths()["include"],

@@ -1478,7 +1478,7 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
 // dX, dW and dbias are made.  So the entry of a label that is far from learnt
 // is near -1 and survives bf16 nearly exactly, whatever the loss is divided
 // by.  Bound as the forward tile is, with 128 KB of G a tile to write: 4096 x
-// 32000 x 4096 in 780 us.  G is rounded to bf16 (relative 2^-9 of each entry, to
+// 32000 x 4096 in 780 us.  G is rounded to bf16 (at most 2^-8 of each entry, to
 // nearest) because the products that follow run on bf16 MFMA.
 template <class T, bool TG>
 constexpr int grad_lds() {

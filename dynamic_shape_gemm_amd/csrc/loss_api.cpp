@@ -36,9 +36,12 @@ constexpr int64_t kMaxK = int64_t(1) << 21;
 // (rows x features, scan and gather apart / in one: 4096 x 768 11.0 / 9.1 us,
 // 8192 x 768 14.2 / 21.8)
 constexpr int64_t kManyRows = 4096;
-// up to here the forward pass takes rows as they come: a gather costs 6 us,
-// 256 rows instead of 128 cost 5 (32000 x 4096: 87 against 83) or 2.5 (30522 x
-// 768: 17 against 14)
+// up to here the forward pass takes rows as they come, which saves a launch or
+// two.  As they come / gathered, us: 32000 x 4096 at 64 rows 63 / 68, at 256 89 /
+// 95; 30522 x 768 at 64 21 / 23, at 256 21 / 25, whatever part of the rows is
+// labelled.  It loses only where dropping rows spares a row of tiles of a
+// product that is not bound by W: 256 x 32000 x 4096 with 50 % labelled 90 / 84,
+// 15 % 90 / 76.
 constexpr int64_t kDirectRows = 256;
 // G of one piece: 8192 rows of which 15 % are live, 30522 x 768, took 372 us a
 // step in pieces of 256 MB (two), 325 of 512 and 335 of 1024 (one); 8192 x
@@ -318,8 +321,6 @@ int run(const Call& c) {
         a.part = (float*)(ws + l.part);
         a.sumz = !c.distill && c.smoothing > 0.0f ? (float*)(ws + l.sumz) : nullptr;
         a.zt = (float*)(ws + l.zt);
-        // few rows: the product costs the weight's bytes, not its rows, so none
-        // need dropping, and a launch (two) fewer count for more
         a.direct = c.M <= kDirectRows && !l.pack_w && aligned16(c.X) && c.ldx % 8 == 0 && c.ldx <= 2 * kMaxK &&
                    c.K % 64 == 0;
         a.stream = l.stream && a.direct;

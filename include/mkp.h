@@ -249,15 +249,16 @@ int mkp_plan_describe_grouped(int64_t groups, int64_t M, int64_t K, const int64_
  *   loss = lse - (1 - smoothing) z_label - smoothing mean_v(z_v) + z_loss lse^2
  * (smoothing in [0, 1]).  A row whose label is not in [0, V) -- such as the
  * customary -100 -- is left out: its loss and lse are 0, it has no gradient,
- * costs nothing in the products, and whatever its X holds reaches no result.
+ * and whatever its X holds reaches no result.  It costs nothing in the products
+ * (but in a forward call of up to 256 rows, which takes them as they come).
  * A logit z is -inf here when log2(e) z / T is in binary32 (so is the type's
  * lowest value, T = 1): the entry is masked out.  A label that is has loss
  * +inf; a row of which every entry is has lse -inf too, and probabilities 0
  * in the gradient.  M fp32 values each are written to loss and lse.
  *
  * mkp_linear_xent_backward: from lse (as written by the forward call) and
- * dloss (M fp32 values, the gradient by each row's loss; rows left out are
- * not read), the gradients
+ * dloss (M fp32 values, the gradient by each row's loss; both are read for
+ * every row, and what they hold for rows left out has no effect), the gradients
  *   dX (M x K) := scale D . W,  dW (V x K) := scale D^T . X,  dbias (V) := sum_m D
  *   D = dloss [(1 + 2 z_loss lse) softmax(z) - (1 - smoothing) onehot(label)
  *              - smoothing / V] * dz/ds
