@@ -204,8 +204,9 @@ int check(const Call& c) {
         if (c.k < 1) return report(MKP_ERR_INVALID_ARG, "targets per row must be 1.." + std::to_string(kMaxTargets));
         if (c.M > 0 && (!c.ids || !c.teacher)) return report(MKP_ERR_INVALID_ARG, "ids or teacher is NULL");
         if (c.ldids < c.k || c.ldt < c.k) return report(MKP_ERR_INVALID_ARG, "ldids < k or ldt < k");
-        if (!(c.T > 0.0f) || !std::isfinite(c.T) || !std::isfinite(1.4427f / c.T))
-            return report(MKP_ERR_INVALID_ARG, "temperature must be more than 0, its reciprocal finite");
+        // (T^2 is a factor of the loss: infinite, or 0 times an infinite divergence, it would be NaN)
+        if (!(c.T > 0.0f) || !std::isfinite(c.T) || !std::isnormal(c.T * c.T))
+            return report(MKP_ERR_INVALID_ARG, "temperature must be more than 0, its square finite and normal");
     }
     if (c.M > 0 && !c.lse) return report(MKP_ERR_INVALID_ARG, "lse is NULL");
     if (!c.backward) {

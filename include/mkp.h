@@ -268,7 +268,9 @@ int mkp_plan_describe_grouped(int64_t groups, int64_t M, int64_t K, const int64_
  * piece of the vocabulary at a time, and D passes through bf16 once (its
  * entries relative to the largest |dloss|), being an operand of bf16
  * products: with MKP_F32 too, dX and dW are as exact as that (relative 2^-8
- * at most of each entry of D).
+ * at most of each entry of D).  softmax(z) is exp(z - lse) with lse as given,
+ * in binary32, so it is off by about 2^-23 |lse| of itself: rows of which every
+ * logit is far below -1e5 but not masked out have no usable gradient.
  *
  * mkp_linear_distill: the Kullback-Leibler divergence from a teacher that is
  * known by its logits t at k (1 .. 1024) vocabulary entries ids per row,
@@ -286,7 +288,8 @@ int mkp_plan_describe_grouped(int64_t groups, int64_t M, int64_t K, const int64_
  * outputs, but a W whose rows are not 16-byte aligned, or K not a multiple of
  * 8, costs a padded copy of W per call.  labels and ids are int64 values,
  * ldids and ldt >= k.  V and K are at least 1; M == 0 makes dW and dbias 0.
- * softcap (unless 0) and temperature have a finite reciprocal.  Extents that
+ * softcap (unless 0) has a finite reciprocal, temperature a finite and normal
+ * square (about 2^-63 to 2^63).  Extents that
  * a launch cannot count (2^24 rows, for one) are MKP_ERR_UNSUPPORTED.
  *
  * workspace: device memory of at least mkp_linear_loss_workspace() bytes,

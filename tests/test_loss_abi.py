@@ -152,3 +152,13 @@ def test_build_refuses_tiles_that_fill_a_cu_alone():
             built = {line.split()[0]: dict(p.split("=") for p in line.split()[1:]) for line in f}
         tiles = [u for k, u in built.items() if "loss_grad_kernel" in k or "loss_forward_kernel" in k]
         assert tiles and all(int(u["occupancy"]) >= 2 for u in tiles)
+
+
+@pytest.mark.parametrize("fn", [distill, distill_bwd])
+def test_temperatures_whose_square_is_no_number(mkp, fn):
+    """T^2 times the divergence is the loss: infinite or 0 it would be NaN."""
+    for T in (1e20, 2e19, 1e-20, 1e-30):
+        assert fn(mkp, temperature=T) == mkp.MKP_ERR_INVALID_ARG, T
+        assert "temperature" in mkp.last_error(), T
+    for T in (1e18, 1e-18):   # what is missing now is the workspace
+        assert fn(mkp, temperature=T) == mkp.MKP_ERR_INVALID_ARG and "workspace" in mkp.last_error(), T
