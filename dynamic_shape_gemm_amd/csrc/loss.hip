@@ -317,7 +317,7 @@ __device__ __forceinline__ void plain_barrier() {
 // multiplies while the other reads.
 // Measured (256 x 256 tile, one per CU): 1.43 us a step, 1500 TFLOP/s over the
 // device, whichever way the operands are read; the waves' MFMAs fill 76-78 %
-// of the cycles at the 1.6-1.8 GHz that the card's power leaves.  Two phases
+// of the cycles at the 1.6-1.9 GHz that the card's power leaves.  Two phases
 // of 32 MFMAs ran out of registers (5-25 % slower), one stage a step ahead
 // with all waves in step took 1.7 us.
 template <class T>
@@ -572,7 +572,7 @@ __device__ __forceinline__ int row_label(const LossArgs& a, int m, int n) {
 // the fused multiply, so an exponent keeps its digits, and what rounding umax
 // s2 loses is put back where the tiles are joined.  A lane reduces its own 16
 // values of a row; the 4 lanes and the waves that share the row meet in LDS.
-// Bound by the product at many K steps (4096 x 32000 x 4096: 760 us, 1410
+// Bound by the product at many K steps (4096 x 32000 x 4096: 750 us, 1430
 // TFLOP/s), at few by this epilogue too, about 6 us a tile, most of it the
 // 65536 exponentials (1024 x 16384 x 768, one tile a CU: 29.6 us).
 template <class T, bool TG>
@@ -1923,8 +1923,9 @@ __device__ __forceinline__ void dw_tile(const LossArgs& a, int n, int tm, int tn
 // Both products of a piece in one launch, dX's workgroups first: they need
 // the same G, and together they fill the device better than one after the
 // other (950 x 50257 x 768: 140 us against 80 and 82; 4096 x 32000 x 4096:
-// 1480 us, 1450 TFLOP/s, bound by the matrix pipe; 333 x 30522 x 768: 49 us,
-// bound by the partials of dX and by dW's 47 MB).
+// 1440 us, 1490 TFLOP/s, bound by the matrix pipe; 333 x 30522 x 768: 47 us, of
+// which the bytes of dX's partials (9 MB) and of dW (47 MB) are a quarter, the
+// ends of dW's tiles of six K steps most of the rest).
 template <class TX, class TW>
 __global__ __launch_bounds__(TX::NT, 2) void loss_products_kernel(LossArgs a, float mul) {
     constexpr int NEED = TW::BM * (TW::BN * 2 + 16);
