@@ -193,8 +193,8 @@ __device__ __forceinline__ void dma16_at(const void* p, uint32_t lds) {
 //     columns (`tail` > 0 of them) takes the missing ones from `zeros`, 16 bytes
 //     of them, as does the other operand: an infinity times 0 would be NaN
 //   columns (TR): `lim` valid columns of the tile; a last step of fewer than
-//     64 rows repeats its last row, where the other operand holds zeros (that
-//     row's own product takes part already, so an infinity in it changes nothing)
+//     64 rows repeats its last row, where the other operand holds zeros (an
+//     infinity in that row leaves no finite dX in any case)
 // Both need `lim` and `tail` to be multiples of 8 columns.
 template <int H, bool TR, int I, int NW>
 struct Operand {
