@@ -19,8 +19,8 @@ def _logits(x, w, bias, scale, softcap):
     if bias is not None:
         s = s + bias
     if softcap > 0:
-        t = torch.tanh(s / softcap)
-        return softcap * t, 1.0 - t * t
+        # (1 - tanh^2 as it stays exact where the tanh rounds to 1)
+        return softcap * torch.tanh(s / softcap), 1.0 / torch.cosh(s / softcap) ** 2
     return s, torch.ones_like(s)
 
 
