@@ -2,8 +2,11 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <exception>
 #include <functional>
 #include <string>
+
+#include "../../include/mkp.h"
 
 namespace mkp {
 
@@ -21,5 +24,25 @@ hipError_t traced_launch(hipStream_t st, int kernel, double flops, double bytes,
 constexpr int kTraceLoss = -20;
 enum LossLaunch : int { LL_FLAGS, LL_SCAN, LL_GATHER, LL_FORWARD, LL_FINISH, LL_GRAD, LL_PRODUCTS, LL_OUTPUTS, LL_COUNT };
 const char* loss_launch_name(int i);
+
+// Trace codes kTraceQ8 - i: the i-th launch of the 8-bit matrices.
+constexpr int kTraceQ8 = -40;
+enum Q8Launch : int { QL_QUANTIZE, QL_DEQUANTIZE, QL_PACK, QL_I8_PRODUCT, QL_I8_FINISH, QL_SLOPES, QL_Q8_PRODUCT, QL_Q8_FINISH, QL_COUNT };
+const char* q8_launch_name(int i);
+
+// No exception leaves the C entry points.
+template <class F>
+int guarded(F&& fn) {
+    try {
+        return fn();
+    } catch (const std::exception& e) {
+        try {
+            return report(MKP_ERR_HIP, e.what());
+        } catch (...) {
+        }
+    } catch (...) {
+    }
+    return MKP_ERR_HIP;
+}
 
 }  // namespace mkp

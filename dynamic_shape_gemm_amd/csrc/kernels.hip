@@ -28,6 +28,7 @@
 //     when K is not a multiple of uK, operands whose rows are not 16-byte
 //     aligned, and the last tile column when N is not a multiple of 8.
 #include "kernels.h"
+#include "act.h"
 #include "load8.h"
 
 #include <hip/hip_runtime.h>
@@ -56,52 +57,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) unsigned char lds_t;
 
 // ---- fused epilogue -------------------------------------------------------
-
-// Activations, branch-free on the native 2^x and reciprocal instructions.
-//   sigmoid(z) = 1 / (1 + e^-z)
-//   silu(x) = x sigmoid(x); the tanh form of GELU, x/2 (1 + tanh u), equals
-//   x sigmoid(2u) since (1 + tanh u) / 2 = sigmoid(2u)
-//   GELU, x Phi(x) = x/2 (1 + erf(x / sqrt 2)), with erf from Abramowitz &
-//   Stegun, Handbook of Mathematical Functions, formula 7.1.26 (absolute
-//   error <= 1.5e-7): for a >= 0, 1 - erf(a) = q(a) = P(t) e^{-a^2},
-//   t = 1 / (1 + p a), P a degree-5 polynomial without constant term; so
-//   1 + erf(x / sqrt 2) is q(|x| / sqrt 2) for x < 0 (no cancellation in the
-//   negative tail) and 2 - q for x >= 0.
-__device__ __forceinline__ float sigmoid_fast(float z) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
-}
-
-__device__ __forceinline__ float gelu_erf_fast(float x) {
-    const float a = fabsf(x) * 0.70710678118654752f;
-    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * a);
-    float poly = 1.061405429f;
-    poly = fmaf(poly, t, -1.453152027f);
-    poly = fmaf(poly, t, 1.421413741f);
-    poly = fmaf(poly, t, -0.284496736f);
-    poly = fmaf(poly, t, 0.254829592f);
-    const float q = poly * t * __builtin_amdgcn_exp2f(-1.4426950408889634f * a * a);
-    return 0.5f * x * (x < 0.0f ? q : 2.0f - q);
-}
-
-template <int ACT>
-__device__ __forceinline__ float act_t(float v) {
-    if constexpr (ACT == ACT_RELU) return v > 0.0f ? v : 0.0f;
-    if constexpr (ACT == ACT_GELU) return gelu_erf_fast(v);
-    if constexpr (ACT == ACT_GELU_TANH)
-        return v * sigmoid_fast(2.0f * 0.79788456080286536f * (v + 0.044715f * v * v * v));
-    if constexpr (ACT == ACT_SILU) return v * sigmoid_fast(v);
-    return v;
-}
-
-__device__ __forceinline__ float act_apply(int act, float v) {
-    switch (act) {
-        case ACT_RELU: return act_t<ACT_RELU>(v);
-        case ACT_GELU: return act_t<ACT_GELU>(v);
-        case ACT_GELU_TANH: return act_t<ACT_GELU_TANH>(v);
-        case ACT_SILU: return act_t<ACT_SILU>(v);
-        default: return v;
-    }
-}
 
 // bias[n..n+3] (zeros past nvalid, or without a bias)
 __device__ __forceinline__ f32x4 load_bias4(const KEpi& e, int n, int nvalid) {

@@ -7,7 +7,6 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <exception>
 #include <string>
 
 #include "../../include/mkp.h"
@@ -361,21 +360,6 @@ int run(const Call& c) {
     return go(LL_OUTPUTS, 0.0,
               (c.dX ? (4.0 + gb) * m * k : 0.0) + (c.dbias ? 4.0 * v * (double)ceil_div(c.M, kDbiasRows) : 0.0),
               [&] { return launch_loss_outputs(a, st); });
-}
-
-// No exception leaves the C entry points.
-template <class F>
-int guarded(F&& fn) {
-    try {
-        return fn();
-    } catch (const std::exception& e) {
-        try {
-            return report(MKP_ERR_HIP, e.what());
-        } catch (...) {
-        }
-    } catch (...) {
-    }
-    return MKP_ERR_HIP;
 }
 
 }  // namespace
