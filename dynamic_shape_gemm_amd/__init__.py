@@ -35,6 +35,7 @@ MKP_ACT_GELU_TANH = 3
 MKP_ACT_SILU = 4
 MKP_BF16 = 0
 MKP_F32 = 1
+MKP_I8 = 2
 ACTIVATIONS = {None: MKP_ACT_NONE, "none": MKP_ACT_NONE, "relu": MKP_ACT_RELU, "gelu": MKP_ACT_GELU,
                "gelu_tanh": MKP_ACT_GELU_TANH, "silu": MKP_ACT_SILU}
 
@@ -96,6 +97,19 @@ _lib.mkp_linear_distill_backward.argtypes = _distill_args + _grad_args
 _lib.mkp_linear_distill_backward.restype = _int
 _lib.mkp_linear_loss_workspace.argtypes = [_i64, _i64, _i64, _i64, _p, _i64, _int, _p]
 _lib.mkp_linear_loss_workspace.restype = _int
+_lib.mkp_quantize_rows.argtypes = [_i64, _i64, _p, _i64, _int, _i64, _p, _i64, _p, _i64, _p]
+_lib.mkp_quantize_rows.restype = _int
+_lib.mkp_dequantize_rows.argtypes = [_i64, _i64, _p, _i64, _p, _i64, _i64, _p, _i64, _int, _p]
+_lib.mkp_dequantize_rows.restype = _int
+_lib.mkp_linear_i8.argtypes = [_i64, _i64, _i64, _p, _i64, _int, _p, _p, _i64, _p, _p, _int, _p, _i64, _int, _p, _i64, _p]
+_lib.mkp_linear_i8.restype = _int
+_lib.mkp_linear_i8_workspace.argtypes = [_i64, _i64, _i64, _p, _i64, _int, _p, _i64, _p]
+_lib.mkp_linear_i8_workspace.restype = _int
+_lib.mkp_linear_q8_backward.argtypes = [_i64, _i64, _i64, _p, _i64, _int, _p, _i64, _p, _p, _i64, _p, _i64, _i64, _int,
+                                        _p, _i64, _p, _i64, _int, _p, _p, _i64, _p]
+_lib.mkp_linear_q8_backward.restype = _int
+_lib.mkp_linear_q8_backward_workspace.argtypes = [_i64, _i64, _i64, _int, _int, _p]
+_lib.mkp_linear_q8_backward_workspace.restype = _int
 _lib.mkp_plan_describe_grouped.argtypes = [_i64, _i64, _i64, _p, _int, ctypes.c_char_p, ctypes.c_size_t]
 _lib.mkp_plan_describe_grouped.restype = _int
 _lib.mkp_plan_describe.argtypes = [_i64, _i64, _i64, _i64, _int, ctypes.c_char_p, ctypes.c_size_t]
@@ -121,7 +135,7 @@ _lib.mkp_trace_dump.restype = _int
 _lib.mkp_last_error.argtypes = []
 _lib.mkp_last_error.restype = ctypes.c_char_p
 
-# The GEMM and loss entry points through the CPython marshalling module built beside
+# The GEMM, loss and 8-bit entry points through the CPython marshalling module built beside
 # the library (a ctypes call spends ~1.5 us converting 10-14 arguments, as
 # long as the smallest GEMMs take on the GPU); ctypes where it is absent.
 try:
@@ -136,10 +150,15 @@ _f_linear_xent = _fast.linear_xent if _fast else _lib.mkp_linear_xent
 _f_linear_xent_backward = _fast.linear_xent_backward if _fast else _lib.mkp_linear_xent_backward
 _f_linear_distill = _fast.linear_distill if _fast else _lib.mkp_linear_distill
 _f_linear_distill_backward = _fast.linear_distill_backward if _fast else _lib.mkp_linear_distill_backward
+_f_quantize_rows = _fast.quantize_rows if _fast else _lib.mkp_quantize_rows
+_f_dequantize_rows = _fast.dequantize_rows if _fast else _lib.mkp_dequantize_rows
+_f_linear_i8 = _fast.linear_i8 if _fast else _lib.mkp_linear_i8
+_f_linear_q8_backward = _fast.linear_q8_backward if _fast else _lib.mkp_linear_q8_backward
 
 EXPORTED = ["mkp_gemm", "mkp_gemm_batched", "mkp_gemm_batched_noalloc", "mkp_noalloc_scratch_bytes", "mkp_gemm_bt", "mkp_gemm_batched_bt", "mkp_gemm_ex", "mkp_conv2d", "mkp_gemm_grouped",
             "mkp_gemm_grouped_bt", "mkp_linear_xent", "mkp_linear_xent_backward", "mkp_linear_distill",
-            "mkp_linear_distill_backward", "mkp_linear_loss_workspace", "mkp_plan_describe", "mkp_plan_describe_grouped", "mkp_plan_with_table",
+            "mkp_linear_distill_backward", "mkp_linear_loss_workspace", "mkp_quantize_rows", "mkp_dequantize_rows",
+            "mkp_linear_i8", "mkp_linear_i8_workspace", "mkp_linear_q8_backward", "mkp_linear_q8_backward_workspace", "mkp_plan_describe", "mkp_plan_describe_grouped", "mkp_plan_with_table",
             "mkp_load_calibration",
             "mkp_calibrate", "mkp_set_option", "mkp_kernel_count", "mkp_kernel_name", "mkp_cache_clear",
             "mkp_stats", "mkp_trace_dump", "mkp_last_error"]
@@ -370,6 +389,73 @@ def mkp_linear_loss_workspace(M, V, K, k, W, ldw, backward) -> int:
     return n.value
 
 
+def mkp_quantize_rows_raw(M, K, X, ldx, x_type, group, Q, ldq, S, lds, stream) -> int:
+    return _f_quantize_rows(M, K, _addr(X), ldx, x_type, group, _addr(Q), ldq, _addr(S), lds, stream or 0)
+
+
+def mkp_quantize_rows(M, K, X, ldx, x_type, group, Q, ldq, S, lds, stream=None) -> int:
+    """Q (int8), S (fp32) := X's rows as integers of -127..127 times scales, one
+    for each row (group 0) or for each group of columns."""
+    return _check(mkp_quantize_rows_raw(M, K, X, ldx, x_type, group, Q, ldq, S, lds, _stream(stream)))
+
+
+def mkp_dequantize_rows_raw(M, K, Q, ldq, S, lds, group, Y, ldy, y_type, stream) -> int:
+    return _f_dequantize_rows(M, K, _addr(Q), ldq, _addr(S), lds, group, _addr(Y), ldy, y_type, stream or 0)
+
+
+def mkp_dequantize_rows(M, K, Q, ldq, S, lds, group, Y, ldy, y_type, stream=None) -> int:
+    """Y := the values that Q and S of mkp_quantize_rows stand for."""
+    return _check(mkp_dequantize_rows_raw(M, K, Q, ldq, S, lds, group, Y, ldy, y_type, _stream(stream)))
+
+
+def mkp_linear_i8_raw(M, N, K, X, ldx, x_type, x_scale, W, ldw, w_scale, bias, act, Y, ldy, y_type, workspace,
+                      workspace_bytes, stream) -> int:
+    if not isinstance(act, int):
+        act = ACTIVATIONS[act]
+    return _f_linear_i8(M, N, K, _addr(X), ldx, x_type, _addr(x_scale), _addr(W), ldw, _addr(w_scale), _addr(bias), act,
+                        _addr(Y), ldy, y_type, _addr(workspace), workspace_bytes, stream or 0)
+
+
+def mkp_linear_i8(M, N, K, X, ldx, x_type, x_scale, W, ldw, w_scale, bias, act, Y, ldy, y_type, workspace,
+                  workspace_bytes, stream=None) -> int:
+    """Y := act(x_scale w_scale (X . W^T) + bias) with W (and X of MKP_I8) in
+    8-bit integers; X of another type is quantised row by row within the call."""
+    return _check(mkp_linear_i8_raw(M, N, K, X, ldx, x_type, x_scale, W, ldw, w_scale, bias, act, Y, ldy, y_type,
+                                    workspace, workspace_bytes, _stream(stream)))
+
+
+def mkp_linear_i8_workspace(M, N, K, X, ldx, x_type, W, ldw) -> int:
+    """Bytes of workspace mkp_linear_i8 needs."""
+    n = ctypes.c_int64(0)
+    _check(_lib.mkp_linear_i8_workspace(M, N, K, _addr(X), ldx, x_type, _addr(W), ldw, ctypes.byref(n)))
+    return n.value
+
+
+def mkp_linear_q8_backward_raw(M, N, K, dY, lddy, dy_type, X, ldx, x_scale, Z, ldz, z_scale, ldzs, z_group, act, dZ, lddz,
+                               dW, lddw, dw_type, dbias, workspace, workspace_bytes, stream) -> int:
+    if not isinstance(act, int):
+        act = ACTIVATIONS[act]
+    return _f_linear_q8_backward(M, N, K, _addr(dY), lddy, dy_type, _addr(X), ldx, _addr(x_scale), _addr(Z), ldz,
+                                 _addr(z_scale), ldzs, z_group, act, _addr(dZ), lddz, _addr(dW), lddw, dw_type,
+                                 _addr(dbias), _addr(workspace), workspace_bytes, stream or 0)
+
+
+def mkp_linear_q8_backward(M, N, K, dY, lddy, dy_type, X, ldx, x_scale, Z, ldz, z_scale, ldzs, z_group, act, dZ, lddz,
+                           dW, lddw, dw_type, dbias, workspace, workspace_bytes, stream=None) -> int:
+    """dZ := dY act'(z), dW := dZ^T . x, dbias := the sum of dZ's rows (each may be
+    None), from a linear layer's input x and pre-activation z kept in 8 bits."""
+    return _check(mkp_linear_q8_backward_raw(M, N, K, dY, lddy, dy_type, X, ldx, x_scale, Z, ldz, z_scale, ldzs, z_group,
+                                             act, dZ, lddz, dW, lddw, dw_type, dbias, workspace, workspace_bytes,
+                                             _stream(stream)))
+
+
+def mkp_linear_q8_backward_workspace(M, N, K, need_dw, need_dbias) -> int:
+    """Bytes of workspace mkp_linear_q8_backward needs."""
+    n = ctypes.c_int64(0)
+    _check(_lib.mkp_linear_q8_backward_workspace(M, N, K, 1 if need_dw else 0, 1 if need_dbias else 0, ctypes.byref(n)))
+    return n.value
+
+
 def _text_call(fn, *args, size=1 << 16):
     buf = ctypes.create_string_buffer(size)
     _check(fn(*args, buf, size))
@@ -567,7 +653,7 @@ def _loss_inputs(x, w, bias, rows):
 
 
 class _LossStream:
-    """The stream a vocabulary loss runs on, made current (with its device)
+    """The stream a vocabulary loss or an 8-bit call runs on, made current (with its device)
     while the call's outputs and workspace are taken from torch's allocator,
     so that they belong to it.  On another stream than the current one the
     inputs are marked as used there: their memory is not handed out again
@@ -709,3 +795,164 @@ def linear_distill_backward(x, w, ids, teacher, lse, dloss, bias=None, temperatu
         mkp_linear_distill_backward(M, V, K, x, ldx, w, ldw, bias, k, ids, ldi, teacher, ldt, teacher_lse, temperature,
                                     scale, softcap, lse, dloss, dx, K, dw, K, dbias, gt, ws, n, st)
     return dx, dw, dbias
+
+
+def _q8_tensor(name, t, device, dtypes, shape):
+    """One operand of an 8-bit call: (address, leading dimension)."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d).split('.')[-1] for d in dtypes)}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on the same GPU as the other operands")
+    cols = shape[-1]
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    return t.data_ptr(), t.stride(0) if len(shape) == 2 and shape[0] > 1 else cols
+
+
+def _q8_groups(K, group):
+    if group not in (0, 32, 64, 128, 256):
+        raise ValueError("group must be 0, 32, 64, 128 or 256")
+    return -(-K // group) if group else 1
+
+
+def _q8_scale(name, t, device, rows, cols, group):
+    """Scales of a quantised matrix: (address, leading dimension)."""
+    import torch
+    if not group:
+        return _q8_tensor(name, t, device, (torch.float32,), (rows,))[0], 1
+    return _q8_tensor(name, t, device, (torch.float32,), (rows, _q8_groups(cols, group)))
+
+
+def _q8_rows(M, K, device):
+    """M x K integers in rows of whole 16-byte units, as linear_i8 reads them without a copy."""
+    import torch
+    return torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :K]
+
+
+def quantize_rows(x, group=0, stream=None):
+    """x (M,K), bf16 or fp32, as 8-bit integers times scales: (q, scale) with
+    scale = max(max |x| / 127, 2^-126) of each row (fp32 (M,), group 0) or of
+    each `group` columns of it (32, 64, 128 or 256; fp32 (M, ceil(K/group))), and
+    q (M,K) int8 = x / scale to the nearest, ties to even.  A row (group) with an
+    infinity or NaN has scale NaN and q 0.  linear_i8 takes (q, scale) of group 0
+    as its weight (one scale a channel) and as its input."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be (M, K)")
+    M, K = x.shape
+    groups = _q8_groups(K, group)
+    at, ldx = _q8_tensor("x", x, x.device, (torch.bfloat16, torch.float32), (M, K))
+    with _LossStream(x.device, stream, x) as st:
+        q = _q8_rows(M, K, x.device)
+        scale = torch.empty((M, groups) if group else (M,), dtype=torch.float32, device=x.device)
+        mkp_quantize_rows(M, K, at, ldx, MKP_F32 if x.dtype == torch.float32 else MKP_BF16, group, q,
+                          max(q.stride(0), K), scale, max(groups, 1), st)
+    return q, scale
+
+
+def dequantize_rows(q, scale, group=0, dtype=None, stream=None):
+    """The values that quantize_rows' (q, scale) stand for, in dtype bfloat16
+    (the default) or float32."""
+    import torch
+    dtype = dtype or torch.bfloat16
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("dtype must be bfloat16 or float32")
+    if q.dim() != 2:
+        raise ValueError("q must be (M, K)")
+    M, K = q.shape
+    _q8_groups(K, group)
+    at, ldq = _q8_tensor("q", q, q.device, (torch.int8,), (M, K))
+    sat, lds = _q8_scale("scale", scale, q.device, M, K, group)
+    with _LossStream(q.device, stream, q, scale) as st:
+        y = torch.empty((M, K), dtype=dtype, device=q.device)
+        mkp_dequantize_rows(M, K, at, ldq, sat, lds, group, y, K, MKP_F32 if dtype == torch.float32 else MKP_BF16, st)
+    return y
+
+
+# (by the extents, the input's type and the alignment of both operands)
+_linear_i8_bytes = functools.lru_cache(maxsize=1024)(mkp_linear_i8_workspace)
+_q8_backward_bytes = functools.lru_cache(maxsize=1024)(mkp_linear_q8_backward_workspace)
+
+
+def linear_i8(x, w, w_scale, bias=None, act=None, x_scale=None, dtype=None, out=None, stream=None):
+    """A linear layer in 8-bit integers: act(x . (w_scale w)^T + bias), w (N,K)
+    int8 and w_scale (N,) fp32 as quantize_rows makes them of the layer's weight.
+    x (M,K) bf16 or fp32 is quantised token by token within the call; x int8
+    comes with its x_scale (M,).  bias (N,) fp32 or None, act
+    None/"relu"/"gelu"/"gelu_tanh"/"silu".  Returns (or fills) out (M,N) in dtype
+    float32 (the default) or bfloat16, without a grad_fn."""
+    import torch
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError("x must be (M, K) and w (N, K)")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {[a for a in ACTIVATIONS if a]}")
+    M, K = x.shape
+    N = w.shape[0]
+    dev = x.device
+    xat, ldx = _q8_tensor("x", x, dev, (torch.bfloat16, torch.float32, torch.int8), (M, K))
+    wat, ldw = _q8_tensor("w", w, dev, (torch.int8,), (N, K))
+    sw = _q8_tensor("w_scale", w_scale, dev, (torch.float32,), (N,))[0]
+    if (x.dtype == torch.int8) != (x_scale is not None):
+        raise ValueError("x_scale comes with an int8 x, and only with one")
+    sx = 0 if x_scale is None else _q8_tensor("x_scale", x_scale, dev, (torch.float32,), (M,))[0]
+    b = 0 if bias is None else _q8_tensor("bias", bias, dev, (torch.float32,), (N,))[0]
+    if out is not None:
+        if dtype is not None and out.dtype != dtype:
+            raise TypeError("out is not of dtype")
+        yat, ldy = _q8_tensor("out", out, dev, (torch.float32, torch.bfloat16), (M, N))
+    elif dtype not in (None, torch.float32, torch.bfloat16):
+        raise TypeError("dtype must be float32 or bfloat16")
+    xt = MKP_I8 if x_scale is not None else MKP_F32 if x.dtype == torch.float32 else MKP_BF16
+    n = _linear_i8_bytes(M, N, K, xat & 15, ldx, xt, wat & 15, ldw)
+    with _LossStream(dev, stream, x, w, w_scale, bias, x_scale, out) as st:
+        if out is None:
+            out = torch.empty((M, N), dtype=dtype or torch.float32, device=dev)
+            yat, ldy = out.data_ptr(), N
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        mkp_linear_i8(M, N, K, xat, ldx, xt, sx, wat, ldw, sw, b, ACTIVATIONS[act], yat, ldy,
+                      MKP_F32 if out.dtype == torch.float32 else MKP_BF16, ws, n, st)
+    return out
+
+
+def linear_q8_backward(dy, x, x_scale, z=None, z_scale=None, z_group=0, act=None, need_dz=True, need_dw=True,
+                       need_dbias=True, grad_dtype=None, stream=None):
+    """Backward pass of y = act(z), z = x . w^T + bias, from dy (M,N), bf16 or
+    fp32, and what was kept in 8 bits: x (M,K) int8 with x_scale (M,)
+    (quantize_rows of the layer's input) and, unless act is None, z (M,N) int8
+    with z_scale (quantize_rows of its pre-activation, in groups of z_group
+    columns).  Returns (dz, dw, dbias): dz = dy act'(z) bf16 (dw's and dx's
+    operand; dx is gemm(dz, w)), dw = dz^T x in grad_dtype (bfloat16, the default,
+    or float32), dbias fp32; None for those not needed.  No grad_fn."""
+    import torch
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
+        raise ValueError("dy must be (M, N) and x (M, K)")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {[a for a in ACTIVATIONS if a]}")
+    if grad_dtype not in (None, torch.bfloat16, torch.float32):
+        raise TypeError("grad_dtype must be bfloat16 or float32")
+    M, N = dy.shape
+    K = x.shape[1]
+    dev = dy.device
+    dyat, lddy = _q8_tensor("dy", dy, dev, (torch.bfloat16, torch.float32), (M, N))
+    xat, ldx = _q8_tensor("x", x, dev, (torch.int8,), (M, K))
+    sx = _q8_tensor("x_scale", x_scale, dev, (torch.float32,), (M,))[0]
+    code = ACTIVATIONS[act]
+    zat = ldz = sz = ldzs = 0
+    if code != MKP_ACT_NONE:
+        if z is None or z_scale is None:
+            raise ValueError("an activation's slope needs z and z_scale")
+        _q8_groups(N, z_group)
+        zat, ldz = _q8_tensor("z", z, dev, (torch.int8,), (M, N))
+        sz, ldzs = _q8_scale("z_scale", z_scale, dev, M, N, z_group)
+    n = _q8_backward_bytes(M, N, K, bool(need_dw), bool(need_dbias))
+    with _LossStream(dev, stream, dy, x, x_scale, z, z_scale) as st:
+        dz = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if need_dz else None
+        dw = torch.empty((N, K), dtype=grad_dtype or torch.bfloat16, device=dev) if need_dw else None
+        dbias = torch.empty(N, dtype=torch.float32, device=dev) if need_dbias else None
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        mkp_linear_q8_backward(M, N, K, dyat, lddy, MKP_F32 if dy.dtype == torch.float32 else MKP_BF16, xat, ldx, sx, zat,
+                               ldz, sz, ldzs, z_group if code else 0, code, dz, N, dw, K,
+                               MKP_F32 if grad_dtype == torch.float32 else MKP_BF16, dbias, ws, n, st)
+    return dz, dw, dbias

@@ -24,8 +24,10 @@ UNITS = [
     ("kernels.hip", "kernels_p3.o", ["-DMKP_PART=3"]),
     ("kernels.hip", "kernels_p4.o", ["-DMKP_PART=4"]),
     ("loss.hip", "loss.o", []),
+    ("q8.hip", "q8.o", []),
     ("planner.cpp", "planner.o", []),
     ("loss_api.cpp", "loss_api.o", []),
+    ("q8_api.cpp", "q8_api.o", []),
     ("api.cpp", "api.o", []),
 ]
 SOURCES = sorted({u[0] for u in UNITS})
@@ -73,10 +75,10 @@ def parse_resource_usage(remarks: str) -> dict:
 
 
 def too_few_waves(usage: dict) -> list:
-    """The vocabulary losses' tile kernels whose registers leave a SIMD fewer
+    """The tile kernels of the fused products whose registers leave a SIMD fewer
     than two waves: their launches count two workgroups of the 128 x 128 tile
     (or the eight waves of a 256 x 256 one) on a CU."""
-    tiles = ("loss_forward_kernel", "loss_grad_kernel", "loss_products_kernel")
+    tiles = ("loss_forward_kernel", "loss_grad_kernel", "loss_products_kernel", "i8_tile_kernel", "q8_product_kernel")
     return sorted(k for k, u in usage.items() if any(t in k for t in tiles) and u.get("occupancy", 0) < 2)
 
 
@@ -112,16 +114,16 @@ def build_library(verbose: bool = False) -> str:
             u = usage[k]
             f.write(f"{k} vgpr={u.get('vgpr')} agpr={u.get('agpr')} scratch={u.get('scratch')} "
                     f"lds={u.get('lds')} occupancy={u.get('occupancy')}\n")
-    # a GEMM micro-kernel or a loss kernel's tile that spills to scratch has
+    # a GEMM micro-kernel or a fused product's tile that spills to scratch has
     # lost its register tiling; refuse to ship it
     tiles = ("gemm_tile_kernel", "gemm_dual_kernel", "loss_forward_kernel", "loss_grad_kernel",
-             "loss_products_kernel", "loss_stream_kernel")
+             "loss_products_kernel", "loss_stream_kernel", "i8_tile_kernel", "q8_product_kernel")
     spills = [k for k, u in usage.items() if any(t in k for t in tiles) and u.get("scratch", 0) > 0]
     if spills:
         raise RuntimeError("tile kernels use scratch memory: " + ", ".join(spills))
     alone = too_few_waves(usage)
     if alone:
-        raise RuntimeError("loss tiles counted as two workgroups per CU fit one: " + ", ".join(alone))
+        raise RuntimeError("tiles counted as two workgroups per CU fit one: " + ", ".join(alone))
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs, "-ldl"]
     if verbose:
@@ -136,7 +138,7 @@ FAST = os.path.join(HERE, "_mkpfast" + (sysconfig.get_config_var("EXT_SUFFIX") o
 
 
 def build_fast_binding(verbose: bool = False) -> str:
-    """The CPython marshalling module for the GEMM and loss entry points (host C,
+    """The CPython marshalling module for the GEMM, loss and 8-bit entry points (host C,
     linked against libmkp.so next to it)."""
     tmp = FAST + ".tmp"
     cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-Wall", "-I", sysconfig.get_paths()["include"],

@@ -1450,6 +1450,7 @@ int mkp_trace_dump(char* buf, size_t len) {
                                  : k == -1   ? "splitk_reduce"
                                  : k == -2   ? "zero_fill"
                                  : k == -3   ? "pack_rows"
+                                 : k <= kTraceQ8   ? q8_launch_name(kTraceQ8 - k)
                                  : k <= kTraceLoss ? loss_launch_name(kTraceLoss - k)
                                              : "transpose_b";
         if (i) o << ",";

@@ -1,4 +1,4 @@
-/* Argument marshalling for the GEMM and vocabulary-loss entry points of
+/* Argument marshalling for the GEMM, vocabulary-loss and 8-bit entry points of
  * libmkp.so, as a CPython extension: integers in (and floats, for the losses),
  * the C ABI's status code out.  It exists because a
  * ctypes call converts each of its 10-14 arguments through Python objects,
@@ -83,7 +83,7 @@ static PyObject* py_gemm_batched_bt(PyObject* self, PyObject* const* a, Py_ssize
     return call_batched(mkp_gemm_batched_bt, "gemm_batched_bt", a, n);
 }
 
-/* The vocabulary losses' arguments, by kind: i an integer, p an address, f a
+/* The vocabulary losses' and 8-bit calls' arguments, by kind: i an integer, p an address, f a
  * float, in the order of the C ABI. */
 typedef union {
     int64_t i;
@@ -141,6 +141,36 @@ static PyObject* py_linear_distill_backward(PyObject* self, PyObject* const* a, 
         v[26].i, v[27].p));
 }
 
+static PyObject* py_quantize_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    arg_t v[11];
+    if (get_args("iipiiipipip", a, n, v, "quantize_rows")) return NULL;
+    return PyLong_FromLong(
+        mkp_quantize_rows(v[0].i, v[1].i, v[2].p, v[3].i, (int)v[4].i, v[5].i, v[6].p, v[7].i, v[8].p, v[9].i, v[10].p));
+}
+static PyObject* py_dequantize_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    arg_t v[11];
+    if (get_args("iipipiipiip", a, n, v, "dequantize_rows")) return NULL;
+    return PyLong_FromLong(
+        mkp_dequantize_rows(v[0].i, v[1].i, v[2].p, v[3].i, v[4].p, v[5].i, v[6].i, v[7].p, v[8].i, (int)v[9].i, v[10].p));
+}
+static PyObject* py_linear_i8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    arg_t v[18];
+    if (get_args("iiipiippippipiipip", a, n, v, "linear_i8")) return NULL;
+    return PyLong_FromLong(mkp_linear_i8(v[0].i, v[1].i, v[2].i, v[3].p, v[4].i, (int)v[5].i, v[6].p, v[7].p, v[8].i, v[9].p,
+                                         v[10].p, (int)v[11].i, v[12].p, v[13].i, (int)v[14].i, v[15].p, v[16].i, v[17].p));
+}
+static PyObject* py_linear_q8_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    arg_t v[24];
+    if (get_args("iiipiipippipiiipipiippip", a, n, v, "linear_q8_backward")) return NULL;
+    return PyLong_FromLong(mkp_linear_q8_backward(
+        v[0].i, v[1].i, v[2].i, v[3].p, v[4].i, (int)v[5].i, v[6].p, v[7].i, v[8].p, v[9].p, v[10].i, v[11].p, v[12].i, v[13].i,
+        (int)v[14].i, v[15].p, v[16].i, v[17].p, v[18].i, (int)v[19].i, v[20].p, v[21].p, v[22].i, v[23].p));
+}
+
 static PyMethodDef methods[] = {
     {"gemm", (PyCFunction)(void (*)(void))py_gemm, METH_FASTCALL, "mkp_gemm"},
     {"gemm_bt", (PyCFunction)(void (*)(void))py_gemm_bt, METH_FASTCALL, "mkp_gemm_bt"},
@@ -152,6 +182,10 @@ static PyMethodDef methods[] = {
     {"linear_distill", (PyCFunction)(void (*)(void))py_linear_distill, METH_FASTCALL, "mkp_linear_distill"},
     {"linear_distill_backward", (PyCFunction)(void (*)(void))py_linear_distill_backward, METH_FASTCALL,
      "mkp_linear_distill_backward"},
+    {"quantize_rows", (PyCFunction)(void (*)(void))py_quantize_rows, METH_FASTCALL, "mkp_quantize_rows"},
+    {"dequantize_rows", (PyCFunction)(void (*)(void))py_dequantize_rows, METH_FASTCALL, "mkp_dequantize_rows"},
+    {"linear_i8", (PyCFunction)(void (*)(void))py_linear_i8, METH_FASTCALL, "mkp_linear_i8"},
+    {"linear_q8_backward", (PyCFunction)(void (*)(void))py_linear_q8_backward, METH_FASTCALL, "mkp_linear_q8_backward"},
     {NULL, NULL, 0, NULL},
 };
 

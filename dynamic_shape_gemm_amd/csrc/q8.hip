@@ -1,0 +1,768 @@
+// 8-bit matrices on CDNA4 (gfx950): quantisation by rows and back, a linear
+// layer in 8-bit integers, and the backward pass of a layer whose input and
+// pre-activation were kept in 8 bits.
+//
+// Row m (or a group of columns of it) is held as integers q = rne(x / s) of
+// -127 .. 127 and one binary32 scale s = max(max |x| / 127, 2^-126); where the
+// row holds an infinity or NaN, s is NaN and q is 0, so that every product with
+// it is NaN.
+#include "q8.h"
+
+#include "act.h"
+#include "tile.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace mkp {
+namespace {
+
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2a1 __attribute__((ext_vector_type(2), aligned(1)));
+typedef float f32x4a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+constexpr float kTiny = 1.17549435e-38f;   // 2^-126
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
+// (a vector's element by value: __builtin_bit_cast of one in place reads element 0)
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16);
+}
+
+// Eight consecutive values of a row as read: bf16 or binary32, zeros past `nvalid`.
+template <bool F32>
+struct Raw8;
+template <>
+struct Raw8<false> {
+    u32x4 w;
+    __device__ __forceinline__ void zero() { w = u32x4{0, 0, 0, 0}; }
+    __device__ __forceinline__ void load(const void* row, int64_t c, int nvalid, bool vec) {
+        const uint16_t* p = (const uint16_t*)row + c;
+        w = vec && nvalid >= 8 ? *(const u32x4*)p : load8_any(p, nvalid);
+    }
+    // The largest |x|, as the bits of a value of X's type: all infinities and
+    // NaN are above every finite one.
+    __device__ __forceinline__ uint32_t top() const {
+        u16x2 m = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+        return std::max((uint32_t)m[0], (uint32_t)m[1]);
+    }
+    static __device__ __forceinline__ float top_value(uint32_t t) { return __builtin_bit_cast(float, t << 16); }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = bf16_lo(w[i]);
+            v[2 * i + 1] = bf16_hi(w[i]);
+        }
+    }
+};
+template <>
+struct Raw8<true> {
+    f32x4 a, b;
+    __device__ __forceinline__ void zero() { a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+    __device__ __forceinline__ void load(const void* row, int64_t c, int nvalid, bool) {
+        const float* p = (const float*)row + c;
+        if (nvalid >= 8) {
+            a = *(const f32x4a4*)p;
+            b = *(const f32x4a4*)(p + 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = i < nvalid ? p[i] : 0.0f;
+                b[i] = i + 4 < nvalid ? p[i + 4] : 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m = std::max(m, abs_bits(a[i]));
+            m = std::max(m, abs_bits(b[i]));
+        }
+        return m;
+    }
+    static __device__ __forceinline__ float top_value(uint32_t t) { return __builtin_bit_cast(float, t); }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[i + 4] = b[i];
+        }
+    }
+};
+
+// A row's (group's) scale, and what its values are multiplied by.
+struct Scale8 {
+    float s, inv;
+    bool ok;
+    __device__ __forceinline__ explicit Scale8(float top) {
+        ok = top < INFINITY;
+        s = fmaxf(top / 127.0f, kTiny);
+        inv = 1.0f / s;
+        if (!ok) {
+            s = __builtin_nanf("");
+            inv = 0.0f;
+        }
+    }
+};
+
+// Eight values to integers, a byte each.  x * inv + 1.5 * 2^23 rounds to the
+// nearest integer n, whose low byte is the sum's; inv is 1 / s rounded, so n can
+// be the neighbour of the nearest when x / s is next to a half.  The rest r = x -
+// n s is exact (a multiple of half a unit of s below 2^24 of them), so where 2 |r|
+// reaches s -- rarely, and a branch for the whole wave -- n is put right: away
+// from r beyond s, and to the even neighbour at s.
+__device__ __forceinline__ u32x2 to_i8(const float (&v)[8], const Scale8& sc) {
+    constexpr float kMagic = 12582912.0f;
+    float t[8], most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        t[i] = fmaf(v[i], sc.inv, kMagic);
+        most = fmaxf(most, fabsf(fmaf(kMagic - t[i], sc.s, v[i])));
+    }
+    if (2.0f * most >= sc.s) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float n = t[i] - kMagic, r = fmaf(-n, sc.s, v[i]), r2 = 2.0f * fabsf(r);
+            const bool odd = (__builtin_bit_cast(uint32_t, t[i]) & 1) != 0;
+            if (r2 > sc.s || (r2 == sc.s && odd)) t[i] += copysignf(1.0f, r);
+        }
+    }
+    u32x2 out;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = __builtin_bit_cast(uint32_t, t[4 * h + i]);
+        out[h] = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u) | __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+        out[h] = sc.ok ? out[h] : 0u;
+    }
+    return out;
+}
+
+// Up to eight bytes to a row (any alignment).
+__device__ __forceinline__ void store_i8(int8_t* p, u32x2 w, int n, bool vec) {
+    if (n >= 8) {
+        if (vec) *(u32x2*)p = w;
+        else *(u32x2a1*)p = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
+    }
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    return std::max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true));
+}
+// The largest of the 4, 8, 16 or 32 lanes around this one, or of the wave.
+__device__ __forceinline__ uint32_t max4(uint32_t v) { return dpp_max<0x4E>(dpp_max<0xB1>(v)); }
+__device__ __forceinline__ uint32_t max16(uint32_t v) { return dpp_max<0x140>(dpp_max<0x141>(max4(v))); }
+__device__ __forceinline__ uint32_t max_wave(uint32_t v) {
+    v = max16(v);
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    return std::max(std::max(a, b), std::max(c, d));
+}
+
+// ---- a scale for each row ----------------------------------------------------
+
+// TPR threads hold a row, C chunks of eight values each, between its maximum and
+// its integers; a row of more (LOOP) is read twice.
+template <bool F32, int TPR, int C, bool LOOP>
+__global__ __launch_bounds__(256) void quantize_row_kernel(QuantArgs a) {
+    __shared__ uint32_t buf[4];
+    const int tid = threadIdx.x, at = tid % TPR;
+    const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + tid / TPR;
+    if (TPR < 256 && m >= a.M) return;   // (whole waves)
+    const char* row = (const char*)a.x + m * a.ldx * (F32 ? 4 : 2);
+    const bool vec = ((uintptr_t)row & 15) == 0;
+    Raw8<F32> raw[C];
+    uint32_t top = 0;
+    for (int c0 = 0; c0 < a.K; c0 += TPR * 8 * C) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = c0 + (i * TPR + at) * 8;
+            if (c < a.K) raw[i].load(row, c, a.K - c, vec);
+            else raw[i].zero();
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) top = std::max(top, raw[i].top());
+        if constexpr (!LOOP) break;
+    }
+    top = max_wave(top);
+    if constexpr (TPR == 256) {
+        if ((tid & 63) == 0) buf[tid >> 6] = top;
+        __syncthreads();
+        top = std::max(std::max(buf[0], buf[1]), std::max(buf[2], buf[3]));
+    }
+    const Scale8 sc(Raw8<F32>::top_value(top));
+    if (at == 0) a.s[m * a.lds] = sc.s;
+    int8_t* q = a.q + m * a.ldq;
+    const bool qvec = ((uintptr_t)q & 7) == 0;
+    for (int c0 = 0; c0 < a.K + a.pad; c0 += TPR * 8 * C) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = c0 + (i * TPR + at) * 8;
+            if constexpr (LOOP) {
+                if (c < a.K) raw[i].load(row, c, a.K - c, vec);
+                else raw[i].zero();
+            }
+            float v[8];
+            raw[i].values(v);
+            store_i8(q + c, to_i8(v, sc), a.K + a.pad - c, qvec);
+        }
+        if constexpr (!LOOP) break;
+    }
+}
+
+// ---- a scale for each group of columns ----------------------------------------
+
+// A workgroup's chunks of eight columns: `rows` rows of `cpr` chunks, row after
+// row; a thread takes every 256th of them.
+struct Walk {
+    int r, c, dr, dc, cpr;
+    __device__ __forceinline__ Walk(int cpr_) : cpr(cpr_) {
+        r = threadIdx.x / cpr;
+        c = threadIdx.x - r * cpr;
+        dr = 256 / cpr;
+        dc = 256 - dr * cpr;
+    }
+    __device__ __forceinline__ void next() {
+        r += dr;
+        c += dc;
+        if (c >= cpr) {
+            c -= cpr;
+            ++r;
+        }
+    }
+};
+
+// G lanes (4 .. 32) hold a group; a row's chunks are padded to whole groups.
+template <bool F32, int G>
+__global__ __launch_bounds__(256) void quantize_group_kernel(QuantArgs a, int rows, int cpr) {
+    constexpr int U = 4;
+    const int64_t m0 = (int64_t)blockIdx.x * rows;
+    const int rn = (int)std::min<int64_t>(rows, a.M - m0);
+    Walk w(cpr);
+    while (true) {
+        Raw8<F32> raw[U];
+        int r[U], c[U];
+        // (a thread that is past the end stays with its wave: the lanes of a group meet below)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            r[u] = w.r;
+            c[u] = w.c * 8;
+            w.next();
+            const char* row = (const char*)a.x + (m0 + r[u]) * a.ldx * (F32 ? 4 : 2);
+            if (r[u] < rn && c[u] < a.K) raw[u].load(row, c[u], a.K - c[u], ((uintptr_t)row & 15) == 0);
+            else raw[u].zero();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint32_t top = max4(raw[u].top());
+            if constexpr (G >= 8) top = dpp_max<0x141>(top);
+            if constexpr (G >= 16) top = dpp_max<0x140>(top);
+            if constexpr (G >= 32) top = std::max(top, (uint32_t)__shfl_xor((int)top, 16));
+            const Scale8 sc(Raw8<F32>::top_value(top));
+            float v[8];
+            raw[u].values(v);
+            const u32x2 q = to_i8(v, sc);
+            if (r[u] < rn) {
+                if (c[u] < a.K && c[u] % (G * 8) == 0) a.s[(m0 + r[u]) * a.lds + c[u] / (G * 8)] = sc.s;
+                int8_t* d = a.q + (m0 + r[u]) * a.ldq + c[u];
+                store_i8(d, q, a.K + a.pad - c[u], ((uintptr_t)d & 7) == 0);
+            }
+        }
+        if (__ballot(w.r < rn) == 0) break;
+    }
+}
+
+// ---- and back ------------------------------------------------------------------
+
+__device__ __forceinline__ u32x2 load_i8(const int8_t* p, int n) {
+    u32x2 w = {0, 0};
+    if (n >= 8) {
+        if (((uintptr_t)p & 7) == 0) w = *(const u32x2*)p;
+        else w = *(const u32x2a1*)p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) w[i >> 2] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
+    }
+    return w;
+}
+__device__ __forceinline__ float i8_at(u32x2 w, int i) { return (float)(int8_t)(w[i >> 2] >> (8 * (i & 3))); }
+
+// Up to eight values to a row of bf16 or binary32 (any alignment of its elements).
+template <bool F32>
+__device__ __forceinline__ void store_values(void* row, int64_t c, const float (&v)[8], int n) {
+    if constexpr (F32) {
+        float* p = (float*)row + c;
+        if (n >= 8) {
+            *(f32x4a4*)p = f32x4{v[0], v[1], v[2], v[3]};
+            *(f32x4a4*)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) p[i] = v[i];
+        }
+    } else {
+        uint16_t* p = (uint16_t*)row + c;
+        if (n >= 8 && ((uintptr_t)p & 15) == 0) {
+            *(u32x4*)p = u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) p[i] = f32_to_bf16(v[i]);
+        }
+    }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void dequantize_kernel(QuantArgs a, int rows, int cpr, int shift) {
+    constexpr int U = 4;
+    const int64_t m0 = (int64_t)blockIdx.x * rows;
+    const int rn = (int)std::min<int64_t>(rows, a.M - m0);
+    Walk w(cpr);
+    while (w.r < rn) {
+        u32x2 q[U];
+        float s[U];
+        int r[U], c[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            r[u] = w.r;
+            c[u] = w.c * 8;
+            w.next();
+            if (r[u] >= rn) continue;
+            q[u] = load_i8(a.q + (m0 + r[u]) * a.ldq + c[u], a.K - c[u]);
+            s[u] = a.s[(m0 + r[u]) * a.lds + (c[u] >> shift)];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r[u] >= rn) continue;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i8_at(q[u], i) * s[u];
+            store_values<F32>((char*)a.x + (m0 + r[u]) * a.ldx * (F32 ? 4 : 2), c[u], v, a.K - c[u]);
+        }
+    }
+}
+
+// ---- rows of any alignment into aligned ones -------------------------------------
+
+__global__ __launch_bounds__(256) void q8_pack_kernel(const int8_t* src, int64_t lds, int8_t* dst, int64_t ldd, int64_t rows,
+                                                      int cols) {
+    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (m >= rows) return;
+    const int8_t* s = src + m * lds;
+    int8_t* d = dst + m * ldd;
+    for (int c = (threadIdx.x & 63) * 8; c < ldd; c += 512) *(u32x2*)(d + c) = c < cols ? load_i8(s + c, cols - c) : u32x2{0, 0};
+}
+
+// ---- the product in 8-bit integers -------------------------------------------------
+
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
+
+template <int ACT, int N>
+__device__ __forceinline__ void act_run(f32x4* v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[i][r] = act_t<ACT>(v[i][r]);
+}
+// act of 4 N values.
+template <int N>
+__device__ __forceinline__ void act_run(int act, f32x4* v) {
+    switch (act) {
+        case ACT_RELU: return act_run<ACT_RELU, N>(v);
+        case ACT_GELU: return act_run<ACT_GELU, N>(v);
+        case ACT_GELU_TANH: return act_run<ACT_GELU_TANH, N>(v);
+        case ACT_SILU: return act_run<ACT_SILU, N>(v);
+    }
+}
+
+// One tile over one split's K steps (of 128 integers).  The sums are exact in 32
+// bits (K at most 131071); what is past K reads as zeros in both operands, or, in
+// the last 16 bytes, as zeros in A.
+template <class T>
+__device__ __forceinline__ void i8_tile(const I8Args& a, int m0, int n0, int split, lds_t* smem, int wave, int lane) {
+    const int kp = (a.K + 15) >> 4 << 3;   // 16-bit columns
+    const int all = (kp + 63) >> 6, per = (all + a.splits - 1) / a.splits;
+    const int s0 = std::min(split * per, all), steps = std::min(per, all - s0);
+    const int tail = s0 + steps == all ? kp & 63 : 0;
+    const int rows = (int)std::min<int64_t>(a.M - m0, T::BM), cols = a.N - n0;
+    Operand<T::HA, false, T::IA, T::NW> A;
+    Operand<T::HB, false, T::IB, T::NW> B;
+    A.init((const uint16_t*)(a.A + (int64_t)m0 * a.lda) + s0 * 64, a.lda >> 1, rows, steps, tail, wave, lane,
+           (const uint16_t*)kZeros);
+    B.init((const uint16_t*)(a.B + (int64_t)n0 * a.ldb) + s0 * 64, a.ldb >> 1, cols, steps, tail, wave, lane,
+           (const uint16_t*)kZeros);
+    Acc<T> acc;
+    main_loop<T>(A, B, steps, smem, wave, lane, acc);
+    const Place<T> at(wave, lane);
+    if (a.splits > 1) {
+        int* P = a.part + ((int64_t)split * a.M + m0) * a.ldp + n0;
+#pragma unroll
+        for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) {
+                const int row = at.row(ha, i);
+                if (row >= rows) continue;
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                    for (int j = 0; j < T::FN; ++j)
+                        if (n0 + at.col(hb, j) < a.ldp) *(i32x4*)(P + row * a.ldp + at.col(hb, j)) = acc[ha][hb][i][j];
+            }
+        return;
+    }
+    f32x4 sb[2][T::FN], bias[2][T::FN];
+#pragma unroll
+    for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int n = std::min(n0 + at.col(hb, j) + r, a.N - 1);
+                sb[hb][j][r] = a.sb[n];
+                bias[hb][j][r] = a.bias != nullptr ? a.bias[n] : 0.0f;
+            }
+    float* D = (float*)a.C + (int64_t)m0 * a.ldc + n0;
+    const bool vec = ((uintptr_t)D & 15) == 0 && a.ldc % 4 == 0;
+#pragma unroll
+    for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            const int row = at.row(ha, i);
+            const float sa = a.sa[m0 + std::min(row, rows - 1)];
+            f32x4 v[2][T::FN];
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[hb][j][r] = fmaf((float)acc[ha][hb][i][j][r] * sb[hb][j][r], sa, bias[hb][j][r]);
+            act_run<2 * T::FN>(a.act, &v[0][0]);
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                for (int j = 0; j < T::FN; ++j) {
+                    const int col = at.col(hb, j);
+                    const f32x4 y = v[hb][j];
+                    if (a.bf16) {
+                        *(u32x2 __attribute__((address_space(3)))*)(smem + row * staged_ld<T> + col * 2) =
+                            u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+                    } else if (row < rows) {
+                        float* d = D + row * a.ldc + col;
+                        if (vec && col + 4 <= cols) *(f32x4*)d = y;
+                        else
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (col + r < cols) d[r] = y[r];
+                    }
+                }
+            __builtin_amdgcn_sched_barrier(0);   // (a row at a time: the accumulators fill the registers)
+        }
+    if (a.bf16)
+        store_staged<T>((uint16_t*)a.C + n0, a.ldc, rows, cols, smem, wave, lane, [&](int r) { return (int64_t)m0 + r; });
+}
+
+template <class T>
+constexpr int tile_lds() {
+    return std::max(T::LDS, T::BM * staged_ld<T>);
+}
+
+template <class T>
+__global__ __launch_bounds__(T::NT, 2) void i8_tile_kernel(I8Args a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char raw[tile_lds<T>()];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int tm, tn, split;
+    if (!map_tile(blockIdx.x, (int)((a.M + T::BM - 1) / T::BM), (a.N + T::BN - 1) / T::BN, tm, tn, split, a.splits)) return;
+    i8_tile<T>(a, tm * T::BM, tn * T::BN, split, (lds_t*)raw, wave, lane);
+}
+
+// Four columns a thread: the partial sums, joined exactly, and the epilogue.
+__global__ __launch_bounds__(256) void i8_finish_kernel(I8Args a) {
+    const int quads = (a.N + 3) >> 2;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = i / quads;
+    const int n = (int)(i - m * quads) * 4;
+    if (m >= a.M) return;
+    const int* p = a.part + m * a.ldp + n;
+    i32x4 t = {0, 0, 0, 0};
+    constexpr int U = 8;
+    for (int s0 = 0; s0 < a.splits; s0 += U) {
+        i32x4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = s0 + u < a.splits ? *(const i32x4*)(p + (s0 + u) * a.M * a.ldp) : i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < U; ++u) t += x[u];
+    }
+    const float sa = a.sa[m];
+    f32x4 v;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int c = std::min(n + r, a.N - 1);
+        v[r] = fmaf((float)t[r] * a.sb[c], sa, a.bias != nullptr ? a.bias[c] : 0.0f);
+    }
+    act_run<1>(a.act, &v);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        if (n + r >= a.N) break;
+        if (a.bf16) ((uint16_t*)a.C)[m * a.ldc + n + r] = f32_to_bf16(v[r]);
+        else ((float*)a.C)[m * a.ldc + n + r] = v[r];
+    }
+}
+
+// ---- backward -----------------------------------------------------------------------
+
+// dz = dy act'(z), what is made of it, and the input's integers in bf16.
+// Workgroups of the first kind take kQ8SumRows rows of 512 columns, a wave every
+// fourth row; of the second 4 rows of the input.
+template <bool F32>
+__global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first, int cols, int zshift) {
+    __shared__ float red[4][512];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if ((int)blockIdx.x >= first) {
+        const int64_t m = (int64_t)(blockIdx.x - first) * 4 + wave;
+        if (m >= a.M) return;
+        const int8_t* x = a.x + m * a.ldx;
+        uint16_t* d = a.xb + m * a.Kp;
+        for (int k = lane * 8; k < a.Kp; k += 512) {
+            const u32x2 w = load_i8(x + k, a.K - k);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i8_at(w, i);
+            store_values<false>(d, k, v, 8);
+        }
+        return;
+    }
+    const int rb = blockIdx.x / cols, n = (blockIdx.x - rb * cols) * 512 + lane * 8;
+    const int left = a.N - n;
+    const int64_t m0 = (int64_t)rb * kQ8SumRows;
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    constexpr int U = 4;
+    if (n < a.Np) {
+        for (int r0 = wave; r0 < kQ8SumRows; r0 += 4 * U) {
+            Raw8<F32> dy[U];
+            u32x2 z[U];
+            float zs[U], xs[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t m = m0 + r0 + 4 * u;
+                dy[u].zero();
+                z[u] = u32x2{0, 0};
+                zs[u] = 0.0f;
+                xs[u] = 0.0f;
+                if (m >= a.M) continue;
+                const char* row = (const char*)a.dy + m * a.lddy * (F32 ? 4 : 2);
+                dy[u].load(row, n, left, ((uintptr_t)row & 15) == 0);
+                if (a.act != ACT_NONE) {
+                    z[u] = load_i8(a.z + m * a.ldz + n, left);
+                    zs[u] = a.zs[m * a.ldzs + (n >> zshift)];
+                }
+                xs[u] = a.xs != nullptr ? a.xs[m] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t m = m0 + r0 + 4 * u;
+                float g[8];
+                dy[u].values(g);
+                if (a.act != ACT_NONE && m < a.M) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) g[i] *= act_slope(a.act, i8_at(z[u], i) * zs[u]);
+                }
+                if (m < a.M) {
+                    if (a.dz != nullptr) store_values<false>(a.dz + m * a.lddz, n, g, left);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[i] += g[i];
+                }
+                if (a.a != nullptr) {   // (rows from M on: zeros)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) g[i] = m < a.M ? g[i] * xs[u] : 0.0f;
+                    store_values<false>(a.a + m * a.Np, n, g, 8);
+                }
+            }
+        }
+    }
+    if (a.dbias == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[wave][lane * 8 + i] = sum[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 512; i += 256) {
+        const int c = (blockIdx.x - rb * cols) * 512 + i;
+        if (c < a.Np) a.dbp[(int64_t)rb * a.Np + c] = (red[0][i] + red[1][i]) + (red[2][i] + red[3][i]);
+    }
+}
+
+// A tile of dW = a^T . xb over one split of the rows.
+template <class T>
+__global__ __launch_bounds__(T::NT, 2) void q8_product_kernel(Q8GradArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char raw[tile_lds<T>()];
+    lds_t* smem = (lds_t*)raw;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int tm, tn, split;
+    if (!map_tile(blockIdx.x, (a.N + T::BM - 1) / T::BM, (a.K + T::BN - 1) / T::BN, tm, tn, split, a.splits)) return;
+    const int n0 = tm * T::BM, k0 = tn * T::BN;
+    const int all = a.Mr >> 6, per = (all + a.splits - 1) / a.splits;
+    const int s0 = std::min(split * per, all), steps = std::min(per, all - s0);
+    Operand<T::HA, true, T::IA, T::NW> A;
+    Operand<T::HB, true, T::IB, T::NW> B;
+    A.init(a.a + (int64_t)s0 * 64 * a.Np + n0, a.Np, a.Np - n0, steps, 0, wave, lane);
+    B.init(a.xb + (int64_t)s0 * 64 * a.Kp + k0, a.Kp, a.Kp - k0, steps, s0 + steps == all ? (int)(a.M & 63) : 0, wave, lane);
+    Acc<T> acc;
+    main_loop<T>(A, B, steps, smem, wave, lane, acc);
+    if (a.splits == 1) {
+        store_tile<T>(acc, 1.0f, a.dw, a.dw_f32, a.lddw, k0, a.N - n0, a.K - k0, smem, wave, lane,
+                      [&](int r) { return (int64_t)n0 + r; });
+        return;
+    }
+    const Place<T> at(wave, lane);
+    float* P = a.part + ((int64_t)split * a.N + n0) * a.Kp + k0;
+#pragma unroll
+    for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            if (n0 + at.row(ha, i) >= a.N) continue;
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                for (int j = 0; j < T::FN; ++j)
+                    if (k0 + at.col(hb, j) < a.Kp)
+                        *(f32x4*)(P + (int64_t)at.row(ha, i) * a.Kp + at.col(hb, j)) = acc[ha][hb][i][j];
+        }
+}
+
+// dW from its partials, eight columns a thread; then dbias from its column sums.
+__global__ __launch_bounds__(256) void q8_finish_kernel(Q8GradArgs a, int first) {
+    if ((int)blockIdx.x >= first) {
+        const int n = (blockIdx.x - first) * 256 + threadIdx.x;
+        if (n >= a.N) return;
+        const int parts = (int)((a.M + kQ8SumRows - 1) / kQ8SumRows);
+        constexpr int U = 8;
+        float t = 0.0f;
+        for (int i0 = 0; i0 < parts; i0 += U) {
+            float x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = i0 + u < parts ? a.dbp[(int64_t)(i0 + u) * a.Np + n] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) t += x[u];
+        }
+        a.dbias[n] = t;
+        return;
+    }
+    const int cpr = a.Kp >> 3;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = i / cpr;
+    const int k = (int)(i - n * cpr) * 8;
+    if (n >= a.N) return;
+    const float* p = a.part + n * a.Kp + k;
+    const int64_t sp = (int64_t)a.N * a.Kp;
+    f32x4 lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
+    constexpr int U = 4;
+    for (int s0 = 0; s0 < a.splits; s0 += U) {
+        f32x4 x[U], y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool on = s0 + u < a.splits;
+            x[u] = on ? *(const f32x4*)(p + (s0 + u) * sp) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            y[u] = on ? *(const f32x4*)(p + (s0 + u) * sp + 4) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            lo += x[u];
+            hi += y[u];
+        }
+    }
+    const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    if (a.dw_f32) store_values<true>((float*)a.dw + n * a.lddw, k, v, a.K - k);
+    else store_values<false>((uint16_t*)a.dw + n * a.lddw, k, v, a.K - k);
+}
+
+using I256 = LTile<2, 4, 4, 2, false, false, MulI8>;
+using I128 = LTile<2, 2, 2, 2, false, false, MulI8>;
+using G256 = LTile<2, 4, 4, 2, true, true>;
+using G128 = LTile<2, 2, 2, 2, true, true>;
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int log2i(int v) { return 31 - __builtin_clz((unsigned)v); }
+
+// Rows of a workgroup that walks chunks: about 1024 of them.
+int walk_rows(int64_t M, int cpr) { return (int)std::max<int64_t>(1, std::min<int64_t>(M, 1024 / cpr)); }
+
+template <bool F32>
+hipError_t quantize(const QuantArgs& a, hipStream_t st) {
+    if (a.group == 0) {
+        const int K = a.K + a.pad;
+        const dim3 waves((unsigned)up(a.M, 4)), wgs((unsigned)a.M), b(256);
+        if (K <= 512) return launch_kernel(quantize_row_kernel<F32, 64, 1, false>, waves, b, st, a);
+        if (K <= 1024) return launch_kernel(quantize_row_kernel<F32, 64, 2, false>, waves, b, st, a);
+        if (K <= 2048) return launch_kernel(quantize_row_kernel<F32, 256, 1, false>, wgs, b, st, a);
+        if (K <= 4096) return launch_kernel(quantize_row_kernel<F32, 256, 2, false>, wgs, b, st, a);
+        if (K <= 8192) return launch_kernel(quantize_row_kernel<F32, 256, 4, false>, wgs, b, st, a);
+        if (K <= 16384) return launch_kernel(quantize_row_kernel<F32, 256, 8, false>, wgs, b, st, a);
+        return launch_kernel(quantize_row_kernel<F32, 256, 4, true>, wgs, b, st, a);
+    }
+    const int cpr = (int)up(a.K, a.group) * (a.group / 8), rows = walk_rows(a.M, cpr);
+    const dim3 grid((unsigned)up(a.M, rows)), b(256);
+    switch (a.group) {
+        case 32: return launch_kernel(quantize_group_kernel<F32, 4>, grid, b, st, a, rows, cpr);
+        case 64: return launch_kernel(quantize_group_kernel<F32, 8>, grid, b, st, a, rows, cpr);
+        case 128: return launch_kernel(quantize_group_kernel<F32, 16>, grid, b, st, a, rows, cpr);
+        default: return launch_kernel(quantize_group_kernel<F32, 32>, grid, b, st, a, rows, cpr);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_quantize(const QuantArgs& a, hipStream_t st) { return a.f32 ? quantize<true>(a, st) : quantize<false>(a, st); }
+
+hipError_t launch_dequantize(const QuantArgs& a, hipStream_t st) {
+    const int cpr = (int)up(a.K, 8), rows = walk_rows(a.M, cpr), shift = a.group == 0 ? 31 : log2i(a.group);
+    const dim3 grid((unsigned)up(a.M, rows));
+    return a.f32 ? launch_kernel(dequantize_kernel<true>, grid, dim3(256), st, a, rows, cpr, shift)
+                 : launch_kernel(dequantize_kernel<false>, grid, dim3(256), st, a, rows, cpr, shift);
+}
+
+hipError_t launch_q8_pack(const int8_t* src, int64_t lds, int8_t* dst, int64_t ldd, int64_t rows, int cols, hipStream_t st) {
+    return launch_kernel(q8_pack_kernel, dim3((unsigned)up(rows, 4)), dim3(256), st, src, lds, dst, ldd, rows, cols);
+}
+
+hipError_t launch_i8_product(const I8Args& a, hipStream_t st) {
+    const dim3 grid((unsigned)(up(a.M, a.tile) * up(a.N, a.tile) * a.splits));
+    return a.tile == 256 ? launch_kernel(i8_tile_kernel<I256>, grid, dim3(I256::NT), st, a)
+                         : launch_kernel(i8_tile_kernel<I128>, grid, dim3(I128::NT), st, a);
+}
+
+hipError_t launch_i8_finish(const I8Args& a, hipStream_t st) {
+    return launch_kernel(i8_finish_kernel, dim3((unsigned)up(a.M * up(a.N, 4), 256)), dim3(256), st, a);
+}
+
+hipError_t launch_q8_slopes(const Q8GradArgs& a, hipStream_t st) {
+    const int cols = (int)up(a.Np, 512), shift = a.zgroup == 0 ? 31 : log2i(a.zgroup);
+    const int64_t rows = a.a != nullptr ? a.Mr : a.M;
+    const int64_t first = up(rows, kQ8SumRows) * cols, second = a.xb != nullptr ? up(a.M, 4) : 0;
+    const dim3 grid((unsigned)(first + second));
+    return a.dy_f32 ? launch_kernel(q8_slopes_kernel<true>, grid, dim3(256), st, a, (int)first, cols, shift)
+                    : launch_kernel(q8_slopes_kernel<false>, grid, dim3(256), st, a, (int)first, cols, shift);
+}
+
+hipError_t launch_q8_product(const Q8GradArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)(up(a.N, a.tile) * up(a.K, a.tile) * a.splits));
+    return a.tile == 256 ? launch_kernel(q8_product_kernel<G256>, grid, dim3(G256::NT), st, a)
+                         : launch_kernel(q8_product_kernel<G128>, grid, dim3(G128::NT), st, a);
+}
+
+hipError_t launch_q8_finish(const Q8GradArgs& a, hipStream_t st) {
+    const int64_t first = a.dw != nullptr && a.splits > 1 ? up((int64_t)a.N * (a.Kp >> 3), 256) : 0;
+    const int64_t second = a.dbias != nullptr ? up(a.N, 256) : 0;
+    return launch_kernel(q8_finish_kernel, dim3((unsigned)(first + second)), dim3(256), st, a, (int)first);
+}
+
+}  // namespace mkp

@@ -1,0 +1,373 @@
+// C-ABI of the 8-bit matrices: argument checks, the workspaces' layouts and the
+// order of the launches.  Nothing here allocates device memory or waits: the
+// caller gives the workspace, so calls can be captured into a graph, and two
+// graphs (or streams) with a workspace each never meet.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <string>
+
+#include "../../include/mkp.h"
+#include "internal.h"
+#include "kernels.h"
+#include "q8.h"
+
+namespace mkp {
+
+const char* q8_launch_name(int i) {
+    static const char* const names[QL_COUNT] = {"q8_quantize", "q8_dequantize", "q8_pack",    "i8_product",
+                                                "i8_finish",   "q8_slopes",     "q8_product", "q8_finish"};
+    return i >= 0 && i < QL_COUNT ? names[i] : "q8";
+}
+
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool real_type(int t) { return t == MKP_BF16 || t == MKP_F32; }
+double size_of(int t) { return t == MKP_F32 ? 4.0 : t == MKP_I8 ? 1.0 : 2.0; }
+
+constexpr int64_t kMaxRows = (int64_t(1) << 24) - 1;   // a workgroup of 256 threads a row, counted in 32 bits
+constexpr int64_t kMaxCols = int64_t(1) << 22;         // and leading dimensions: a tile's rows stay within 32-bit offsets
+constexpr int64_t kMaxDepth = 131071;                  // 128^2 times this is below 2^31
+
+int check_extents(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0) return report(MKP_ERR_INVALID_ARG, "negative dimension");
+    if (M > kMaxRows || N > kMaxCols || K > kMaxCols)
+        return report(MKP_ERR_UNSUPPORTED, "more than 2^24 - 1 rows or 2^22 columns");
+    return MKP_OK;
+}
+int check_ld(int64_t ld, int64_t cols, const char* name) {
+    if (ld < cols) return report(MKP_ERR_INVALID_ARG, std::string(name) + " is less than a row");
+    if (ld > 4 * kMaxCols) return report(MKP_ERR_UNSUPPORTED, std::string(name) + " exceeds 2^24");
+    return MKP_OK;
+}
+int check_group(int64_t group) {
+    if (group == 0 || group == 32 || group == 64 || group == 128 || group == kQ8MaxGroup) return MKP_OK;
+    return report(MKP_ERR_INVALID_ARG, "group must be 0, 32, 64, 128 or 256");
+}
+int64_t groups_of(int64_t K, int64_t group) { return group == 0 ? 1 : ceil_div(K, group); }
+
+#define MKP_TRY(call)               \
+    do {                            \
+        const int rc_ = (call);     \
+        if (rc_ != MKP_OK) return rc_; \
+    } while (0)
+
+int go(hipStream_t st, int what, double flops, double bytes, const std::function<hipError_t()>& fn) {
+    const hipError_t e = traced_launch(st, kTraceQ8 - what, flops, bytes, fn);
+    if (e == hipSuccess) return MKP_OK;
+    return report(MKP_ERR_HIP, std::string(q8_launch_name(what)) + " launch: " + hipGetErrorString(e));
+}
+
+int check_workspace(const void* ws, int64_t have, size_t need) {
+    if (need == 0 || (ws && have >= 0 && (size_t)have >= need && aligned16(ws))) return MKP_OK;
+    return report(MKP_ERR_INVALID_ARG, "workspace of " + std::to_string(need) + " bytes, 16-byte aligned, needed");
+}
+
+// ---- quantisation ----------------------------------------------------------
+
+int convert(bool back, int64_t M, int64_t K, void* X, int64_t ldx, int type, int64_t group, int8_t* Q, int64_t ldq, float* S,
+            int64_t lds, void* stream) {
+    MKP_TRY(check_extents(M, 0, K));
+    MKP_TRY(check_group(group));
+    if (!real_type(type)) return report(MKP_ERR_INVALID_ARG, "type must be MKP_BF16 or MKP_F32");
+    MKP_TRY(check_ld(ldx, K, "ldx"));
+    MKP_TRY(check_ld(ldq, K, "ldq"));
+    MKP_TRY(check_ld(lds, groups_of(K, group), "lds"));
+    if (M == 0 || K == 0) return MKP_OK;
+    if (!X || !Q || !S) return report(MKP_ERR_INVALID_ARG, "X, Q or S is NULL");
+    begin_call();
+    const QuantArgs a{M, (int)K, X, ldx, type == MKP_F32, (int)group, Q, ldq, S, lds, 0};
+    const double m = (double)M, k = (double)K;
+    const double bytes = (size_of(type) + 1.0) * m * k + 4.0 * m * (double)groups_of(K, group);
+    const hipStream_t st = (hipStream_t)stream;
+    return back ? go(st, QL_DEQUANTIZE, m * k, bytes, [&] { return launch_dequantize(a, st); })
+                : go(st, QL_QUANTIZE, 3.0 * m * k, bytes, [&] { return launch_quantize(a, st); });
+}
+
+// ---- linear layer ------------------------------------------------------------
+
+struct LinearLayout {
+    int tile = 256, splits = 1;
+    bool quantise = false, pack_a = false, pack_b = false;
+    int64_t Ka = 0, Kb = 0, ldp = 0;   // bytes of a packed row, a row of partial sums
+    size_t a = 0, s = 0, b = 0, part = 0, bytes = 0;
+};
+
+LinearLayout linear_layout(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, int x_type, const void* W,
+                           int64_t ldw) {
+    LinearLayout l;
+    l.quantise = x_type != MKP_I8;
+    l.pack_a = !l.quantise && (!aligned16(X) || ldx % 16 != 0 || K % 16 != 0);
+    l.pack_b = !aligned16(W) || ldw % 16 != 0;
+    l.Ka = round_up(K, 16);
+    l.Kb = round_up(K, 16);
+    l.tile = ceil_div(M, 256) * ceil_div(N, 256) >= 192 ? 256 : 128;
+    const int64_t slots = l.tile == 256 ? 256 : 512, tiles = ceil_div(M, l.tile) * ceil_div(N, l.tile), steps = ceil_div(K, 128);
+    const int64_t want = std::max<int64_t>(1, std::min(slots / std::max<int64_t>(tiles, 1), steps / 2));
+    l.splits = (int)ceil_div(steps, std::max<int64_t>(1, ceil_div(steps, want)));
+    l.splits = std::max(l.splits, 1);
+    l.ldp = round_up(N, 4);
+    size_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t here = at;
+        at += (size_t)round_up(bytes, 256);
+        return here;
+    };
+    if (l.quantise || l.pack_a) l.a = take(M * l.Ka);
+    if (l.quantise) l.s = take(4 * M);
+    if (l.pack_b) l.b = take(N * l.Kb);
+    if (l.splits > 1) l.part = take(4 * M * l.ldp * l.splits);
+    l.bytes = at;
+    return l;
+}
+
+int check_linear(int64_t M, int64_t N, int64_t K, int64_t ldx, int x_type, int64_t ldw) {
+    MKP_TRY(check_extents(M, N, K));
+    if (K > kMaxDepth) return report(MKP_ERR_UNSUPPORTED, "K exceeds 131071: a sum need not fit 32 bits");
+    if (x_type != MKP_I8 && !real_type(x_type)) return report(MKP_ERR_INVALID_ARG, "x_type must be MKP_BF16, MKP_F32 or MKP_I8");
+    MKP_TRY(check_ld(ldx, K, "ldx"));
+    MKP_TRY(check_ld(ldw, K, "ldw"));
+    return MKP_OK;
+}
+
+int linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, int x_type, const float* x_scale, const int8_t* W,
+           int64_t ldw, const float* w_scale, const float* bias, int act, void* Y, int64_t ldy, int y_type, void* workspace,
+           int64_t workspace_bytes, void* stream) {
+    MKP_TRY(check_linear(M, N, K, ldx, x_type, ldw));
+    MKP_TRY(check_ld(ldy, N, "ldy"));
+    if (!real_type(y_type)) return report(MKP_ERR_INVALID_ARG, "y_type must be MKP_BF16 or MKP_F32");
+    if (act < 0 || act >= ACT_COUNT) return report(MKP_ERR_INVALID_ARG, "unknown activation");
+    if (M == 0 || N == 0) return MKP_OK;
+    if (!Y || !w_scale || (x_type == MKP_I8 && !x_scale)) return report(MKP_ERR_INVALID_ARG, "Y, w_scale or x_scale is NULL");
+    if (K > 0 && (!X || !W)) return report(MKP_ERR_INVALID_ARG, "X or W is NULL");
+    const LinearLayout l = linear_layout(M, N, K, X, ldx, x_type, W, ldw);
+    MKP_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
+    const int64_t tiles = ceil_div(M, l.tile) * ceil_div(N, l.tile) * l.splits;
+    if (tiles > UINT32_MAX / 512 || (l.splits > 1 && M * ceil_div(N, 4) > (int64_t)UINT32_MAX - 255) ||
+        (l.pack_b && N > kMaxRows))
+        return report(MKP_ERR_UNSUPPORTED, "grid too large");
+    begin_call();
+    const hipStream_t st = (hipStream_t)stream;
+    char* ws = (char*)workspace;
+    const double m = (double)M, n = (double)N, k = (double)K;
+    I8Args a{};
+    a.M = M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.A = (const int8_t*)X;
+    a.lda = ldx;
+    a.sa = x_scale;
+    a.B = W;
+    a.ldb = ldw;
+    a.sb = w_scale;
+    a.bias = bias;
+    a.act = act;
+    a.C = Y;
+    a.ldc = ldy;
+    a.bf16 = y_type == MKP_BF16;
+    a.tile = l.tile;
+    a.splits = l.splits;
+    a.part = (int*)(ws + l.part);
+    a.ldp = l.ldp;
+    if (l.quantise) {
+        const QuantArgs q{M, (int)K, (void*)X, ldx, x_type == MKP_F32, 0, (int8_t*)(ws + l.a), l.Ka, (float*)(ws + l.s), 1,
+                          (int)(l.Ka - K)};
+        MKP_TRY(go(st, QL_QUANTIZE, 3.0 * m * k, (size_of(x_type) + 1.0) * m * k, [&] { return launch_quantize(q, st); }));
+        a.sa = q.s;
+    } else if (l.pack_a) {
+        MKP_TRY(go(st, QL_PACK, 0.0, 2.0 * m * k,
+                   [&] { return launch_q8_pack((const int8_t*)X, ldx, (int8_t*)(ws + l.a), l.Ka, M, (int)K, st); }));
+    }
+    if (l.quantise || l.pack_a) {
+        a.A = (const int8_t*)(ws + l.a);
+        a.lda = l.Ka;
+    }
+    if (l.pack_b) {
+        MKP_TRY(go(st, QL_PACK, 0.0, 2.0 * n * k,
+                   [&] { return launch_q8_pack(W, ldw, (int8_t*)(ws + l.b), l.Kb, N, (int)K, st); }));
+        a.B = (const int8_t*)(ws + l.b);
+        a.ldb = l.Kb;
+    }
+    const double out = size_of(y_type) * m * n, parts = 4.0 * m * n * (double)l.splits;
+    MKP_TRY(go(st, QL_I8_PRODUCT, 2.0 * m * n * k, (m + n) * k + (l.splits > 1 ? parts : out),
+               [&] { return launch_i8_product(a, st); }));
+    if (l.splits == 1) return MKP_OK;
+    return go(st, QL_I8_FINISH, 0.0, parts + out, [&] { return launch_i8_finish(a, st); });
+}
+
+// ---- backward ------------------------------------------------------------------
+
+struct GradLayout {
+    int tile = 256, splits = 1;
+    int64_t Mr = 0, Np = 0, Kp = 0;
+    size_t a = 0, xb = 0, part = 0, dbp = 0, bytes = 0;
+};
+
+GradLayout grad_layout(int64_t M, int64_t N, int64_t K, bool dw, bool dbias) {
+    GradLayout l;
+    l.Mr = round_up(M, 64);
+    l.Np = round_up(N, 8);
+    l.Kp = round_up(K, 8);
+    l.tile = ceil_div(N, 256) * ceil_div(K, 256) >= 128 ? 256 : 128;
+    const int64_t slots = l.tile == 256 ? 256 : 512, tiles = ceil_div(N, l.tile) * ceil_div(K, l.tile), steps = l.Mr / 64;
+    const int64_t want = std::max<int64_t>(1, std::min(slots / std::max<int64_t>(tiles, 1), steps / 4));
+    l.splits = (int)std::max<int64_t>(1, ceil_div(steps, std::max<int64_t>(1, ceil_div(steps, want))));
+    size_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t here = at;
+        at += (size_t)round_up(bytes, 256);
+        return here;
+    };
+    if (dw) {
+        l.a = take(2 * l.Mr * l.Np);
+        l.xb = take(2 * M * l.Kp);
+        if (l.splits > 1) l.part = take(4 * N * l.Kp * l.splits);
+    }
+    if (dbias) l.dbp = take(4 * ceil_div(l.Mr, kQ8SumRows) * l.Np);
+    l.bytes = at;
+    return l;
+}
+
+int backward(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, int dy_type, const int8_t* X, int64_t ldx,
+             const float* x_scale, const int8_t* Z, int64_t ldz, const float* z_scale, int64_t ldzs, int64_t z_group, int act,
+             void* dZ, int64_t lddz, void* dW, int64_t lddw, int dw_type, float* dbias, void* workspace,
+             int64_t workspace_bytes, void* stream) {
+    MKP_TRY(check_extents(M, N, K));
+    if (!real_type(dy_type)) return report(MKP_ERR_INVALID_ARG, "dy_type must be MKP_BF16 or MKP_F32");
+    if (act < 0 || act >= ACT_COUNT) return report(MKP_ERR_INVALID_ARG, "unknown activation");
+    MKP_TRY(check_ld(lddy, N, "lddy"));
+    const bool sloped = act != ACT_NONE;
+    if (sloped) {
+        MKP_TRY(check_group(z_group));
+        MKP_TRY(check_ld(ldz, N, "ldz"));
+        MKP_TRY(check_ld(ldzs, groups_of(N, z_group), "ldzs"));
+    }
+    if (dZ) MKP_TRY(check_ld(lddz, N, "lddz"));
+    if (dW) {
+        if (!real_type(dw_type)) return report(MKP_ERR_INVALID_ARG, "dw_type must be MKP_BF16 or MKP_F32");
+        MKP_TRY(check_ld(ldx, K, "ldx"));
+        MKP_TRY(check_ld(lddw, K, "lddw"));
+    }
+    if (N == 0) return MKP_OK;
+    if (K == 0) dW = nullptr;
+    if (!dZ && !dW && !dbias) return MKP_OK;
+    if (M > 0 && (!dY || (sloped && (!Z || !z_scale)))) return report(MKP_ERR_INVALID_ARG, "dY, Z or z_scale is NULL");
+    if (M > 0 && dW && (!X || !x_scale)) return report(MKP_ERR_INVALID_ARG, "X or x_scale is NULL");
+    const GradLayout l = grad_layout(M, N, K, dW != nullptr, dbias != nullptr);
+    MKP_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
+    const int64_t slopes = ceil_div(l.Mr, kQ8SumRows) * ceil_div(l.Np, 512) + ceil_div(M, 4);
+    const int64_t tiles = dW ? ceil_div(N, l.tile) * ceil_div(K, l.tile) * l.splits : 0;
+    const int64_t joined = dW && l.splits > 1 ? N * (l.Kp / 8) : 0;
+    if (std::max(slopes * 256, std::max(tiles * 512, joined + N + 1024)) > (int64_t)UINT32_MAX)
+        return report(MKP_ERR_UNSUPPORTED, "grid too large");
+    if (M == 0 && !dW && !dbias) return MKP_OK;
+    begin_call();
+    const hipStream_t st = (hipStream_t)stream;
+    char* ws = (char*)workspace;
+    Q8GradArgs a{};
+    a.M = M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.dy = dY;
+    a.lddy = lddy;
+    a.dy_f32 = dy_type == MKP_F32;
+    a.act = act;
+    a.z = Z;
+    a.ldz = ldz;
+    a.zs = z_scale;
+    a.ldzs = ldzs;
+    a.zgroup = sloped ? (int)z_group : 0;
+    a.x = X;
+    a.ldx = ldx;
+    a.xs = x_scale;
+    a.dz = (uint16_t*)dZ;
+    a.lddz = lddz;
+    a.dw = dW;
+    a.lddw = lddw;
+    a.dw_f32 = dw_type == MKP_F32;
+    a.dbias = dbias;
+    a.a = dW ? (uint16_t*)(ws + l.a) : nullptr;
+    a.xb = dW ? (uint16_t*)(ws + l.xb) : nullptr;
+    a.part = (float*)(ws + l.part);
+    a.dbp = (float*)(ws + l.dbp);
+    a.Mr = (int)l.Mr;
+    a.Np = (int)l.Np;
+    a.Kp = (int)l.Kp;
+    a.tile = l.tile;
+    a.splits = l.splits;
+    const double m = (double)M, n = (double)N, k = (double)K, wb = size_of(dw_type);
+    if (M > 0)
+        MKP_TRY(go(st, QL_SLOPES, 4.0 * m * n,
+                   (size_of(dy_type) + (sloped ? 1.0 : 0.0) + (dZ ? 2.0 : 0.0) + (dW ? 2.0 : 0.0)) * m * n + (dW ? 3.0 * m * k : 0.0),
+                   [&] { return launch_q8_slopes(a, st); }));
+    const double parts = 4.0 * n * k * (double)l.splits;
+    if (dW)
+        MKP_TRY(go(st, QL_Q8_PRODUCT, 2.0 * m * n * k, 2.0 * m * (n + k) + (l.splits > 1 ? parts : wb * n * k),
+                   [&] { return launch_q8_product(a, st); }));
+    if (!dbias && !(dW && l.splits > 1)) return MKP_OK;
+    return go(st, QL_Q8_FINISH, 0.0,
+              (dW && l.splits > 1 ? parts + wb * n * k : 0.0) + (dbias ? 4.0 * n * (double)ceil_div(M, kQ8SumRows) : 0.0),
+              [&] { return launch_q8_finish(a, st); });
+}
+
+}  // namespace
+}  // namespace mkp
+
+using namespace mkp;
+
+extern "C" {
+
+int mkp_quantize_rows(int64_t M, int64_t K, const void* X, int64_t ldx, int x_type, int64_t group, int8_t* Q, int64_t ldq,
+                      float* S, int64_t lds, void* stream) {
+    return guarded([&] { return convert(false, M, K, (void*)X, ldx, x_type, group, Q, ldq, S, lds, stream); });
+}
+
+int mkp_dequantize_rows(int64_t M, int64_t K, const int8_t* Q, int64_t ldq, const float* S, int64_t lds, int64_t group, void* Y,
+                        int64_t ldy, int y_type, void* stream) {
+    return guarded([&] { return convert(true, M, K, Y, ldy, y_type, group, (int8_t*)Q, ldq, (float*)S, lds, stream); });
+}
+
+int mkp_linear_i8_workspace(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, int x_type, const int8_t* W,
+                            int64_t ldw, int64_t* bytes) {
+    return guarded([&] {
+        if (!bytes) return report(MKP_ERR_INVALID_ARG, "bytes is NULL");
+        MKP_TRY(check_linear(M, N, K, ldx, x_type, ldw));
+        *bytes = (int64_t)linear_layout(M, N, K, X, ldx, x_type, W, ldw).bytes;
+        return (int)MKP_OK;
+    });
+}
+
+int mkp_linear_i8(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, int x_type, const float* x_scale, const int8_t* W,
+                  int64_t ldw, const float* w_scale, const float* bias, int act, void* Y, int64_t ldy, int y_type,
+                  void* workspace, int64_t workspace_bytes, void* stream) {
+    return guarded([&] {
+        return linear(M, N, K, X, ldx, x_type, x_scale, W, ldw, w_scale, bias, act, Y, ldy, y_type, workspace, workspace_bytes,
+                      stream);
+    });
+}
+
+int mkp_linear_q8_backward_workspace(int64_t M, int64_t N, int64_t K, int need_dw, int need_dbias, int64_t* bytes) {
+    return guarded([&] {
+        if (!bytes) return report(MKP_ERR_INVALID_ARG, "bytes is NULL");
+        MKP_TRY(check_extents(M, N, K));
+        *bytes = (int64_t)grad_layout(M, N, K, need_dw != 0 && K > 0, need_dbias != 0).bytes;
+        return (int)MKP_OK;
+    });
+}
+
+int mkp_linear_q8_backward(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, int dy_type, const int8_t* X,
+                           int64_t ldx, const float* x_scale, const int8_t* Z, int64_t ldz, const float* z_scale, int64_t ldzs,
+                           int64_t z_group, int act, void* dZ, int64_t lddz, void* dW, int64_t lddw, int dw_type, float* dbias,
+                           void* workspace, int64_t workspace_bytes, void* stream) {
+    return guarded([&] {
+        return backward(M, N, K, dY, lddy, dy_type, X, ldx, x_scale, Z, ldz, z_scale, ldzs, z_group, act, dZ, lddz, dW, lddw,
+                        dw_type, dbias, workspace, workspace_bytes, stream);
+    });
+}
+
+}  // extern "C"

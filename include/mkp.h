@@ -67,10 +67,11 @@ enum {
     MKP_ACT_SILU = 4          /* x * sigmoid(x) */
 };
 
-/* element types of the vocabulary losses' gradients */
+/* element types of the vocabulary losses' gradients and of the 8-bit calls' operands */
 enum {
     MKP_BF16 = 0,
-    MKP_F32 = 1
+    MKP_F32 = 1,
+    MKP_I8 = 2                /* 8-bit integers with binary32 scales (mkp_linear_i8's input) */
 };
 
 /* flags of mkp_plan_describe (align_flags) and mkp_plan_with_table (flags) */
@@ -334,6 +335,80 @@ int mkp_linear_loss_workspace(int64_t M, int64_t V, int64_t K, int64_t k,
                               const void *W, int64_t ldw, int backward, int64_t *bytes);
 
 /*
+ * 8-bit matrices: row m of an M x K matrix is held as integers of -127 .. 127
+ * and binary32 scales s, one for the row (group 0) or one for each `group`
+ * (32, 64, 128 or 256) columns of it, the last group maybe shorter:
+ *   s = max(max |x| / 127, 2^-126),   q = x / s to the nearest, ties to even
+ * -- of exactly these numbers: a quotient next to a half goes where it belongs.
+ * Where the row (group) holds an infinity or NaN, s is NaN and q is 0, so
+ * that everything made of it is NaN.
+ *
+ * mkp_quantize_rows: X (x_type MKP_BF16 or MKP_F32) to integers Q and scales S
+ * (row m, group j at S[m * lds + j]; lds >= the groups of a row, 1 for group
+ * 0).  Bytes of Q between K and ldq are not written.  K == 0: nothing is.
+ * mkp_dequantize_rows: Y := q s, rounded once more for MKP_BF16.
+ * X, Q, S and Y may have any alignment of their elements; rows of X and Y that
+ * are 16-byte aligned and of Q that are 8-byte aligned are faster.
+ */
+int mkp_quantize_rows(int64_t M, int64_t K, const void *X, int64_t ldx, int x_type, int64_t group,
+                      int8_t *Q, int64_t ldq, float *S, int64_t lds, void *stream);
+int mkp_dequantize_rows(int64_t M, int64_t K, const int8_t *Q, int64_t ldq, const float *S, int64_t lds, int64_t group,
+                        void *Y, int64_t ldy, int y_type, void *stream);
+
+/*
+ * A linear layer in 8-bit integers, scales for each token and channel:
+ *   Y[m][n] := act(x_scale[m] * w_scale[n] * sum_k x[m][k] w[n][k] + bias[n])
+ * W: N x K integers (the layout of mkp_gemm_bt), w_scale: N scales, as
+ * mkp_quantize_rows makes them of a bf16 weight with group 0 (any values serve,
+ * -128 too).  x_type MKP_I8: X holds M x K integers and x_scale their M scales.
+ * MKP_BF16 or MKP_F32: X's rows are brought into that form within the call,
+ * exactly as mkp_quantize_rows would with group 0, and x_scale is not read.
+ * bias: N binary32 values or NULL; act: one of MKP_ACT_*; y_type MKP_BF16 or
+ * MKP_F32.  The sums are exact (integers of 32 bits, K at most 131071); they are
+ * scaled, biased and activated in binary32.  K == 0: Y := act(bias).
+ *
+ * Any alignment of X, W and Y serves.  W whose rows are not 16-byte aligned
+ * (address and ldw), or an X of MKP_I8 whose rows are not or whose K is not a
+ * multiple of 16, costs a padded copy per call.
+ */
+int mkp_linear_i8(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, int x_type, const float *x_scale,
+                  const int8_t *W, int64_t ldw, const float *w_scale, const float *bias, int act,
+                  void *Y, int64_t ldy, int y_type, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Backward pass of a linear layer y = act(z), z = x W^T + bias whose input x
+ * (M x K) and pre-activation z (M x N) were kept in 8 bits (mkp_quantize_rows):
+ *   dZ := dY * act'(z),   dW := dZ^T . x,   dbias := sum_m dZ[m]
+ * (the gradient by x is mkp_gemm's product of dZ with W).  dY: M x N, MKP_BF16
+ * or MKP_F32.  X with one scale a row (group 0); Z with scales z_scale (row m,
+ * group j at z_scale[m * ldzs + j]) for groups of z_group columns, not read
+ * for MKP_ACT_NONE.  act' of MKP_ACT_RELU is 0 at 0.  dZ: bf16; dW: N x K,
+ * dw_type MKP_BF16 or MKP_F32; dbias: N binary32 values; any of the three may be
+ * NULL and is then not computed (without dW, X and x_scale are not read).  They
+ * are overwritten; M == 0 makes dW and dbias 0.
+ *
+ * dZ is computed in binary32 and dbias summed so.  For dW, dZ times its row's
+ * x_scale is rounded to bf16 once (relative 2^-8 at most), the integers of x are exact in
+ * bf16, and products are summed in binary32: with MKP_F32 too, dW is as exact as
+ * that.
+ */
+int mkp_linear_q8_backward(int64_t M, int64_t N, int64_t K, const void *dY, int64_t lddy, int dy_type,
+                           const int8_t *X, int64_t ldx, const float *x_scale,
+                           const int8_t *Z, int64_t ldz, const float *z_scale, int64_t ldzs, int64_t z_group, int act,
+                           void *dZ, int64_t lddz, void *dW, int64_t lddw, int dw_type, float *dbias,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace these calls need (0: none; else 16-byte aligned, its
+ * contents of no meaning between calls).  As with the vocabulary losses, the
+ * calls allocate nothing and never wait, so they can be captured into a HIP
+ * graph; calls that may run at the same time need a workspace each, and the
+ * same call gives the same bits.  X, W and leading dimensions as in the call
+ * (only their alignment counts).  Pure host code. */
+int mkp_linear_i8_workspace(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, int x_type,
+                            const int8_t *W, int64_t ldw, int64_t *bytes);
+int mkp_linear_q8_backward_workspace(int64_t M, int64_t N, int64_t K, int need_dw, int need_dbias, int64_t *bytes);
+
+/*
  * Describe the plan the polymerizer picks for a shape, without launching.
  * align_flags: bit0 = A rows 16-byte aligned, bit1 = B rows, bit2 = C rows
  * (pass 7 for aligned operands); MKP_PLAN_B_NK plans for mkp_gemm_bt.
@@ -460,7 +535,7 @@ int mkp_stats(char *buf, size_t len);
 /* Launch trace (option "trace" = 1): every kernel launch (micro-kernels,
  * "<a>+<b>" for both regions in one launch of a kernel pair,
  * "splitk_reduce", "zero_fill", "pack_rows", "transpose_b", the vocabulary
- * losses' "loss_...") is bracketed by
+ * losses' "loss_...", the 8-bit calls' "q8_..." and "i8_...") is bracketed by
  * HIP events on its stream.  Waits for the recorded launches, writes a JSON
  * list [{"kernel","call","us","flops","bytes"}...] ("call": sequence number
  * of the GEMM call that made the launch; algorithmic work per launch:

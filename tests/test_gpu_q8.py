@@ -1,0 +1,555 @@
+"""GPU parity of the 8-bit matrices (quantize_rows, dequantize_rows, linear_i8,
+linear_q8_backward) with the 64-bit oracle on the same inputs.  Integers, scales
+and what they are read back as have to be equal; tolerances of the others are
+oracle.q8's, followed through the formulas element by element."""
+import math
+
+import pytest
+import torch
+
+from oracle import q8 as oracle
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, F64, I8 = torch.bfloat16, torch.float32, torch.float64, torch.int8
+ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def mkp(gpu):
+    import dynamic_shape_gemm_amd as m
+    return m
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def placed(v, pad=0, shift=0):
+    """v in rows of v.shape[1] + pad elements that start `shift` elements into
+    their buffer, with NaN (integers: 77) around them."""
+    M, K = v.shape
+    fill = NAN if v.is_floating_point() else 77
+    buf = torch.full((M * (K + pad) + shift + 64,), fill, device="cuda", dtype=v.dtype)
+    out = buf[shift:shift + M * (K + pad)].view(M, K + pad)[:, :K]
+    out.copy_(v)
+    return out
+
+
+def features(g, M, K, t=BF):
+    x = torch.randn(M, K, generator=g, device="cuda") * torch.exp(torch.randn(K, generator=g, device="cuda"))
+    return x.to(t)
+
+
+def same(got, want, what):
+    assert got.dtype == want.dtype and got.shape == want.shape, what
+    ok = (got == want) | (torch.isnan(got) & torch.isnan(want)) if got.is_floating_point() else got == want
+    assert ok.all(), f"{what}: {int((~ok).sum())} of {ok.numel()} differ, first at {int((~ok).reshape(-1).nonzero()[0])}"
+
+
+def within(got, ref, tol, what):
+    got = got.to(F64)
+    assert got.shape == ref.shape, what
+    equal = (got == ref) | (torch.isnan(got) & torch.isnan(ref))
+    err = torch.where(equal, torch.zeros_like(ref), (got - ref).abs())
+    bad = ~(equal | (err <= tol))
+    if bad.any():
+        i = int(torch.nan_to_num(err / tol, nan=math.inf).argmax())
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} off; worst at {i}: {got.reshape(-1)[i].item()} for "
+                             f"{ref.reshape(-1)[i].item()}, {err.reshape(-1)[i].item():.3e} > {tol.reshape(-1)[i].item():.3e}")
+
+
+# ---- quantisation ------------------------------------------------------------
+
+def check_store(mkp, x, group, what):
+    print(f"[case] {what} {tuple(x.shape)} {x.dtype} group={group}", flush=True)
+    q, s = mkp.quantize_rows(x, group=group)
+    wq, ws = oracle.quantize(x, group)
+    same(s, ws, what + " scale")
+    same(q, wq, what + " integers")
+    for t in (BF, F32):
+        y = mkp.dequantize_rows(q, s, group=group, dtype=t)
+        # (one product in binary32, rounded once more for bf16)
+        same(y, oracle.values(q, s, group).to(F32).to(t), what + " values")
+    return q, s
+
+
+@pytest.mark.parametrize("group", [0, 32, 64, 128, 256])
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,K", [(1, 1), (1, 4096), (3, 31), (5, 512), (2, 513), (7, 1024), (4, 1030), (9, 2048), (3, 2100),
+                                 (2, 4097), (3, 8192), (2, 8200), (2, 16384), (2, 16400), (1, 40000), (301, 257), (1000, 8)])
+def test_store(mkp, M, K, t, group):
+    check_store(mkp, features(gen(M + K), M, K, t), group, "store")
+
+
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("pad,shift", [(0, 1), (1, 0), (3, 5), (8, 0), (7, 8)])
+def test_store_strides(mkp, pad, shift, t, group):
+    for M, K in ((5, 100), (3, 2051), (2, 5000)):
+        x = placed(features(gen(K), M, K, t), pad, shift)
+        q, s = check_store(mkp, x, group, "strides")
+        # integers and scales in places of any alignment, their surroundings left alone
+        wide = torch.full((M, K + 9), 77, dtype=I8, device="cuda")
+        G = 1 if group == 0 else -(-K // group)
+        sw = torch.full((M, G + 2), NAN, device="cuda")
+        mkp.mkp_quantize_rows(M, K, x.data_ptr(), x.stride(0), mkp.MKP_F32 if t == F32 else mkp.MKP_BF16, group,
+                              wide.data_ptr() + 5, K + 9, sw.data_ptr() + 4, G + 2)
+        same(wide.view(-1)[5:].unfold(0, K, K + 9)[:M].contiguous() if M == 1 else
+             torch.as_strided(wide, (M, K), (K + 9, 1), 5), q, "strided integers")
+        keep = torch.as_strided(wide, (M - 1, 9), (K + 9, 1), 5 + K)
+        assert (keep == 77).all() and (wide.view(-1)[:5] == 77).all()
+        same(torch.as_strided(sw, (M, G), (G + 2, 1), 1).reshape(s.shape), s, "strided scales")
+        out = torch.full((M, K + 3), NAN, dtype=t, device="cuda")
+        mkp.mkp_dequantize_rows(M, K, wide.data_ptr() + 5, K + 9, sw.data_ptr() + 4, G + 2, group, out.data_ptr(), K + 3,
+                                mkp.MKP_F32 if t == F32 else mkp.MKP_BF16)
+        same(out[:, :K], mkp.dequantize_rows(q, s, group=group, dtype=t), "strided values")
+        assert torch.isnan(out[:, K:]).all()
+
+
+@pytest.mark.parametrize("group", [0, 32])
+def test_quotients_next_to_a_half(mkp, group):
+    """Scales of powers of two make ties; values one unit beside a half of a
+    scale that has all 24 digits, on either side, must not be taken for ties."""
+    K = 1024
+    x = (torch.arange(K, device="cuda", dtype=F32) * 0.5 - 255.75).clamp(-127, 127).repeat(3, 1)
+    x[:, ::32] = 127.0
+    x[1] *= 2.0 ** -20
+    x[2] *= 2.0 ** 90
+    check_store(mkp, x, group, "ties")
+    check_store(mkp, x.to(BF), group, "ties")
+    for k, top in enumerate((1.0, 1.7182817, 3.3333333e-5, 6.1e30)):
+        s = (torch.tensor(top, dtype=F64) / 127.0).to(F32).to(F64)
+        half = ((torch.arange(K, device="cuda", dtype=F64) % 126) + 0.5) * s.cuda()
+        for step in (-2, -1, 0, 1, 2):
+            v = (half.to(F32).view(torch.int32) + step).view(F32)
+            v[::32] = top
+            check_store(mkp, v[None].repeat(2, 1), group, f"beside halves {k} {step}")
+
+
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+def test_extremes(mkp, t, group):
+    big = torch.finfo(t).max
+    x = features(gen(5), 12, 700, t)
+    x[0, 3], x[1, 650], x[2, 699], x[3] = NAN, math.inf, -math.inf, NAN
+    x[4] = 0
+    x[5] = (x[5].float() * 1e-38).to(t)
+    x[6] = (x[6].float() * 1e-42).to(t)
+    x[7, 100], x[8, 100] = big, -big
+    x[9, :] = 2.0 ** -126 * 63
+    x[10, :] = -0.0
+    q, s = check_store(mkp, x, group, "extremes")
+    bad = torch.isnan(s if group else s[:, None])
+    assert bad[:4].any(1).all() and bad[3].all() and not bad[4:].any()
+
+
+def test_past_4_gib(mkp):
+    """Offsets that pass 32 bits: rows far into a wide array, two of them looked at."""
+    M, K = 70000, 65600
+    x = torch.empty((M, K), dtype=BF, device="cuda")
+    x[:] = 1.0
+    x[-1] = features(gen(1), 1, K)[0]
+    x[40000] = features(gen(2), 1, K)[0]
+    for group in (0, 128):
+        q, s = mkp.quantize_rows(x, group=group)
+        y = mkp.dequantize_rows(q, s, group=group)
+        for m in (0, 40000, M - 1):
+            wq, ws = oracle.quantize(x[m:m + 1], group)
+            same(q[m:m + 1], wq, "far integers")
+            same(s[m:m + 1], ws, "far scales")
+            same(y[m:m + 1], oracle.values(wq, ws, group).to(F32).to(BF), "far values")
+        del q, s, y
+
+
+# ---- linear layer --------------------------------------------------------------
+
+def layer(g, M, N, K, t=BF, bias=True):
+    w, ws = oracle.quantize(torch.randn(N, K, generator=g, device="cuda") / math.sqrt(max(K, 1)))
+    b = 0.5 * torch.randn(N, generator=g, device="cuda") if bias else None
+    return features(g, M, K, t), w, ws, b
+
+
+def check_linear(mkp, x, w, ws, b, act="none", t=F32, xs=None, what="linear", out=None):
+    print(f"[case] {what} x={tuple(x.shape)} {x.dtype} w={tuple(w.shape)} act={act} out={t}", flush=True)
+    y = mkp.linear_i8(x, w, ws, b, act=act, x_scale=xs, dtype=t, out=out)
+    q, s = (x, xs) if xs is not None else oracle.quantize(x)
+    ref, tol = oracle.linear(q, s, w, ws, b, act, t)
+    within(y, ref, tol, what)
+    return y
+
+
+SIZES = [(1, 1, 1), (1, 2, 16), (2, 5, 130), (1, 300, 4096), (3, 64, 127), (16, 200, 128), (17, 129, 272), (33, 1000, 640),
+         (64, 31, 1024), (65, 257, 2048), (100, 1024, 12544), (128, 128, 512), (129, 130, 1030), (200, 700, 768),
+         (257, 513, 96), (300, 2304, 768), (512, 300, 4000)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_linear(mkp, M, N, K):
+    x, w, ws, b = layer(gen(M + N), M, N, K)
+    check_linear(mkp, x, w, ws, b)
+    check_linear(mkp, x.float() * 1.001, w, ws, None, "gelu", BF)
+    q, s = oracle.quantize(x)
+    check_linear(mkp, placed(q, (-K) % 16), w, ws, b, "silu", BF, s)
+
+
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 8, 9, 15, 16, 17, 24, 31, 32, 33, 48, 63, 64, 65, 96, 127, 128, 129, 255, 256, 257])
+@pytest.mark.parametrize("N,K", [(40, 256), (4096, 1024), (1000, 4112), (20000, 192)])
+def test_few_tokens(mkp, M, N, K):
+    """Every number of tokens where another form may be taken, on both sides."""
+    x, w, ws, b = layer(gen(M), M, N, K)
+    check_linear(mkp, x, w, ws, b, "relu", F32)
+    q, s = oracle.quantize(x)
+    check_linear(mkp, placed(q, (-K) % 16), w, ws, None, "none", BF, s)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M", [1, 20, 150, 4100])
+def test_linear_activations(mkp, act, t, M):
+    x, w, ws, b = layer(gen(7), M, 520, 200)
+    check_linear(mkp, x, w, ws, 4.0 * b, act, t)
+
+
+@pytest.mark.parametrize("M,N,K", [(1025, 4000, 256), (4096, 4096, 384), (3000, 6000, 130)])
+def test_large_tiles(mkp, M, N, K):
+    x, w, ws, b = layer(gen(M), M, N, K)
+    check_linear(mkp, x, w, ws, b, "gelu_tanh", BF)
+    check_linear(mkp, x, w, ws, b, "none", F32)
+
+
+@pytest.mark.parametrize("M", [1, 12, 40, 300])
+@pytest.mark.parametrize("pad_x,pad_w,shift", [(0, 0, 1), (1, 3, 0), (16, 16, 0), (5, 0, 16), (0, 7, 3)])
+def test_linear_strides(mkp, M, pad_x, pad_w, shift):
+    """Operands and outputs of any alignment; the output's surroundings stay."""
+    N, K = 333, 208
+    x, w, ws, b = layer(gen(M), M, N, K)
+    q, s = oracle.quantize(x)
+    w2 = placed(w, pad_w, shift)
+    for pad_y in (0, 3, 8):
+        for t in (BF, F32):
+            out = torch.full((M, N + pad_y + 8), NAN, dtype=t, device="cuda")
+            check_linear(mkp, placed(x, pad_x, shift), w2, ws, b, "gelu", t, out=out[:, pad_y:N + pad_y])
+            assert torch.isnan(out[:, :pad_y]).all() and torch.isnan(out[:, N + pad_y:]).all()
+            out.fill_(NAN)
+            check_linear(mkp, placed(q, pad_x, shift), w2, ws, b, "none", t, s, out=out[:, pad_y:N + pad_y])
+            assert torch.isnan(out[:, :pad_y]).all() and torch.isnan(out[:, N + pad_y:]).all()
+
+
+@pytest.mark.parametrize("M", [1, 8, 40, 300, 4200])
+def test_largest_sums(mkp, M):
+    """-128 and 127 everywhere, at the most features whose sums fit 32 bits; what
+    lies behind a row's end reaches nothing."""
+    for K in (131071, 131056, 1000):
+        N = 20 if M < 1000 else 4000
+        if M * K > 1 << 27:
+            K = 4095
+        x = torch.full((M, K), -128, dtype=I8, device="cuda")
+        w = torch.full((N, K), -128, dtype=I8, device="cuda")
+        w[1::2] = 127
+        one = torch.ones(max(M, N), device="cuda")
+        check_linear(mkp, placed(x, 5), placed(w, (-K) % 16), one[:N] * 2.0 ** -20, None, "none", F32, one[:M], "largest sums")
+
+
+def test_empty_sums(mkp):
+    b = torch.randn(9, device="cuda")
+    for t in (F32, BF):
+        y = mkp.linear_i8(torch.empty((5, 0), dtype=BF, device="cuda"), torch.empty((9, 0), dtype=I8, device="cuda"),
+                          torch.ones(9, device="cuda"), b, act="relu", dtype=t)
+        same(y, b.clamp(min=0).to(t).repeat(5, 1), "no features")
+    assert mkp.linear_i8(torch.empty((0, 16), dtype=BF, device="cuda"), torch.ones((3, 16), dtype=I8, device="cuda"),
+                         torch.ones(3, device="cuda")).shape == (0, 3)
+    assert mkp.linear_i8(torch.ones((4, 16), dtype=BF, device="cuda"), torch.ones((0, 16), dtype=I8, device="cuda"),
+                         torch.ones(0, device="cuda")).shape == (4, 0)
+
+
+@pytest.mark.parametrize("M", [3, 60, 400])
+def test_rows_that_are_not_finite(mkp, M):
+    """NaN and infinities in a token reach its own outputs only, all of them."""
+    x, w, ws, b = layer(gen(M), M, 100, 300)
+    x[0, 5], x[M // 2, 299], x[M - 1, 0] = NAN, math.inf, -math.inf
+    y = check_linear(mkp, x, w, ws, b, "gelu", F32)
+    bad = torch.isnan(y)
+    assert bad[[0, M // 2, M - 1]].all() and int(bad.sum()) == 300
+    x[:] = 0
+    y = mkp.linear_i8(x, w, ws, b)
+    same(y, b.repeat(M, 1), "tokens of zeros")
+
+
+def test_far_weights(mkp):
+    """Offsets that pass 32 bits in the weight and in the output."""
+    N, K = 300000, 16400
+    w = torch.randint(-127, 128, (1, K), device="cuda", dtype=torch.int32).to(I8).repeat(N, 1)
+    w[N - 1] = 3
+    ws = torch.full((N,), 0.01, device="cuda")
+    for M in (2, 40):
+        x = features(gen(M), M, K)
+        q, s = oracle.quantize(x)
+        y = mkp.linear_i8(x, w, ws)
+        for sl in (slice(0, 70), slice(N // 2, N // 2 + 70), slice(N - 70, N)):
+            ref, tol = oracle.linear(q, s, w[sl], ws[sl], None, "none", F32)
+            within(y[:, sl], ref, tol, "far weights")
+    del w, y
+    M, N, K = 70000, 20000, 64
+    x, w, ws, _ = layer(gen(3), M, N, K)
+    y = mkp.linear_i8(x, w, ws)
+    for sl in (slice(0, 33), slice(M - 33, M)):
+        q, s = oracle.quantize(x[sl])
+        ref, tol = oracle.linear(q, s, w, ws, None, "none", F32)
+        within(y[sl], ref, tol, "far rows")
+
+
+# ---- backward --------------------------------------------------------------------
+
+def kept(g, M, N, K, group, t=BF):
+    x, xs = oracle.quantize(features(g, M, K))
+    z, zs = oracle.quantize(2.0 * torch.randn(M, N, generator=g, device="cuda"), group)
+    return torch.randn(M, N, generator=g, device="cuda").to(t), x, xs, z, zs
+
+
+def check_backward(mkp, dy, x, xs, z, zs, group, act, t=BF, what="backward", **need):
+    print(f"[case] {what} dy={tuple(dy.shape)} {dy.dtype} x={tuple(x.shape)} group={group} act={act} {t} {need}", flush=True)
+    dz, dw, db = mkp.linear_q8_backward(dy, x, xs, z, zs, z_group=group, act=act, grad_dtype=t, **need)
+    ref = oracle.backward(dy, x, xs, z, zs, group, act, t)
+    for name, got in (("dz", dz), ("dw", dw), ("dbias", db)):
+        assert (got is None) == (need.get("need_" + name) is False)
+        if got is not None:
+            within(got, *ref[name], what + " " + name)
+    return dz, dw, db
+
+
+BACK = [(1, 1, 1), (2, 8, 16), (31, 33, 40), (32, 7, 130), (33, 64, 64), (63, 256, 9), (64, 128, 128), (65, 130, 258),
+        (200, 300, 500), (333, 768, 768), (1000, 100, 36), (2049, 40, 300), (130, 2304, 768)]
+
+
+@pytest.mark.parametrize("M,N,K", BACK)
+def test_backward(mkp, M, N, K):
+    a = kept(gen(M + N), M, N, K, 64)
+    check_backward(mkp, *a, 64, "gelu")
+    check_backward(mkp, *a, 64, "silu", F32)
+    check_backward(mkp, *a[:3], None, None, 0, "none")
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("group", [0, 32, 64, 128, 256])
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+def test_backward_activations(mkp, act, group, t):
+    check_backward(mkp, *kept(gen(3), 70, 300, 48, group, t), group, act)
+
+
+@pytest.mark.parametrize("M,N,K", [(100, 4096, 2048), (700, 2900, 3000)])
+def test_backward_large_tiles(mkp, M, N, K):
+    a = kept(gen(M), M, N, K, 128)
+    check_backward(mkp, *a, 128, "silu")
+    check_backward(mkp, *a, 128, "gelu_tanh", F32)
+
+
+def test_backward_of_what_is_needed(mkp):
+    a = kept(gen(9), 150, 200, 96, 0, F32)
+    every = check_backward(mkp, *a, 0, "gelu")
+    for need in (dict(need_dw=False), dict(need_dz=False), dict(need_dbias=False), dict(need_dw=False, need_dbias=False),
+                 dict(need_dz=False, need_dbias=False), dict(need_dz=False, need_dw=False)):
+        got = check_backward(mkp, *a, 0, "gelu", **need)
+        for g, e in zip(got, every):
+            assert g is None or torch.equal(g, e)
+    assert mkp.linear_q8_backward(*a[:3], need_dz=False, need_dw=False, need_dbias=False) == (None, None, None)
+
+
+@pytest.mark.parametrize("pad,shift", [(0, 1), (1, 0), (3, 5), (16, 16)])
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+def test_backward_strides(mkp, pad, shift, t):
+    dy, x, xs, z, zs = kept(gen(1), 77, 203, 101, 32, t)
+    ref = check_backward(mkp, dy, x, xs, z, zs, 32, "silu")
+    wide = torch.full((77, zs.shape[1] + 3), NAN, device="cuda")
+    wide[:, 1:-2] = zs
+    got = check_backward(mkp, placed(dy, pad, shift), placed(x, pad, shift), xs, placed(z, pad, shift), wide[:, 1:-2], 32, "silu")
+    assert all(torch.equal(p, q) for p, q in zip(ref, got))
+    # outputs inside wider arrays
+    M, N, K = 77, 203, 101
+    n = mkp.mkp_linear_q8_backward_workspace(M, N, K, True, True)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for gt, code in ((BF, mkp.MKP_BF16), (F32, mkp.MKP_F32)):
+        dz = torch.full((M, N + 5), NAN, dtype=BF, device="cuda")
+        dw = torch.full((N, K + pad + 2), NAN, dtype=gt, device="cuda")
+        db = torch.full((N + 8,), NAN, device="cuda")
+        mkp.mkp_linear_q8_backward(M, N, K, dy, N, mkp.MKP_F32 if t == F32 else mkp.MKP_BF16, x, x.stride(0), xs, z,
+                                   z.stride(0), zs, zs.stride(0), 32, mkp.MKP_ACT_SILU, dz, N + 5, dw, K + pad + 2, code, db, ws, n)
+        want = oracle.backward(dy, x, xs, z, zs, 32, "silu", gt)
+        within(dz[:, :N], *want["dz"], "dz in a wider array")
+        within(dw[:, :K], *want["dw"], "dw in a wider array")
+        within(db[:N], *want["dbias"], "dbias")
+        assert torch.isnan(dz[:, N:]).all() and torch.isnan(dw[:, K:]).all() and torch.isnan(db[N:]).all()
+
+
+def test_backward_of_no_tokens(mkp):
+    e = lambda *s, t=F32: torch.empty(s, dtype=t, device="cuda")  # noqa: E731
+    dz, dw, db = mkp.linear_q8_backward(e(0, 24, t=BF), e(0, 40, t=I8), e(0), e(0, 24, t=I8), e(0), act="gelu")
+    assert dz.shape == (0, 24) and (dw == 0).all() and dw.shape == (24, 40) and (db == 0).all()
+    dz, dw, db = mkp.linear_q8_backward(torch.ones(3, 24, device="cuda"), e(3, 0, t=I8), torch.ones(3, device="cuda"))
+    assert dw.shape == (24, 0) and (db == 3).all() and (dz == 1).all()
+
+
+def test_rows_of_nan_scale(mkp):
+    """A token whose input could not be kept makes every weight gradient NaN; one
+    whose pre-activation could not, those of its own channels."""
+    dy, x, xs, z, zs = kept(gen(4), 90, 64, 48, 32)
+    bad = zs.clone()
+    bad[7, 1] = NAN
+    dz, dw, db = mkp.linear_q8_backward(dy, x, xs, z, bad, z_group=32, act="gelu")
+    assert torch.isnan(dz[7, 32:]).all() and int(torch.isnan(dz).sum()) == 32
+    assert torch.isnan(dw[32:]).all() and not torch.isnan(dw[:32]).any() and int(torch.isnan(db).sum()) == 32
+    xs[5] = NAN
+    _, dw, db = mkp.linear_q8_backward(dy, x, xs, z, zs, z_group=32, act="gelu")
+    assert torch.isnan(dw).all() and not torch.isnan(db).any()
+
+
+# ---- together ----------------------------------------------------------------------
+
+def test_serving_run(mkp):
+    """Two layers on one quantised input, then two in a row, as a decoder's block
+    runs them: for a prompt and for single tokens, the same numbers."""
+    g = gen(11)
+    x = features(g, 70, 512)
+    (w1, s1), (w2, s2), (w3, s3) = (mkp.quantize_rows(torch.randn(n, k, generator=g, device="cuda").to(BF) / math.sqrt(k))
+                                    for n, k in ((1100, 512), (1100, 512), (512, 1100)))
+    q, qs = mkp.quantize_rows(x)
+    gate = check_linear(mkp, q, w1, s1, None, "silu", F32, qs, "gate")
+    up = check_linear(mkp, q, w2, s2, None, "none", F32, qs, "up")
+    same(mkp.linear_i8(x, w2, s2), up, "quantised within the call or before it")
+    h = gate * up
+    y = check_linear(mkp, h, w3, s3, None, "none", BF, what="down")
+    for m in (0, 33, 69):   # a token at a time
+        one = x[m:m + 1]
+        hm = mkp.linear_i8(one, w1, s1, act="silu") * mkp.linear_i8(one, w2, s2)
+        same(mkp.linear_i8(hm, w3, s3, dtype=BF), y[m:m + 1], "a single token")
+
+
+def test_training_run(mkp):
+    """A layer's forward pass through the library, its input and pre-activation
+    kept in 8 bits, and its whole backward pass, against autograd in 64 bits on
+    the kept values."""
+    g = gen(12)
+    M, N, K = 260, 384, 200
+    x = features(g, M, K)
+    w = (torch.randn(N, K, generator=g, device="cuda") / math.sqrt(K)).to(BF)
+    b = torch.randn(N, generator=g, device="cuda")
+    z = mkp.linear(x, w, b)
+    xq, xs = mkp.quantize_rows(x)
+    zq, zs = mkp.quantize_rows(z, group=64)
+    dy = torch.randn(M, N, generator=g, device="cuda")
+    dz, dw, db = check_backward(mkp, dy, xq, xs, zq, zs, 64, "gelu", what="training")
+    dx = mkp.gemm(dz, w)
+    leaf = [t.to(F64).requires_grad_() for t in (oracle.values(xq, xs), w, b)]
+    kept_z = oracle.values(zq, zs, 64)
+    zz = leaf[0] @ leaf[1].t() + leaf[2]
+    out = oracle.act("gelu", zz + (kept_z - zz).detach())
+    out.backward(dy.to(F64))
+    ref = oracle.backward(dy, xq, xs, zq, zs, 64, "gelu", BF)
+    within(dw, leaf[1].grad, ref["dw"][1], "dw by autograd")
+    within(db, leaf[2].grad, ref["dbias"][1], "dbias by autograd")
+    terms = ref["dz"][0].abs() @ w.to(F64).abs()
+    within(dx, leaf[0].grad, (2.0 ** -8 + 2 * N * 2.0 ** -24) * 1.02 * terms + ref["dz"][1] @ w.to(F64).abs(), "dx by autograd")
+
+
+def calls(mkp, M=60, N=300, K=320):
+    """One call of each operator on inputs of its own: (name, inputs, call)."""
+    x, w, ws, b = layer(gen(M), M, N, K)
+    q, s = mkp.quantize_rows(x, group=64)
+    back = kept(gen(M + 1), M, N, K, 64)
+    return [("quantize", [x], lambda x, **o: mkp.quantize_rows(x, group=64, **o)),
+            ("dequantize", [q, s], lambda q, s, **o: (mkp.dequantize_rows(q, s, group=64, **o),)),
+            ("linear", [x, w, ws, b], lambda x, w, ws, b, **o: (mkp.linear_i8(x, w, ws, b, act="gelu", **o),)),
+            ("backward", list(back), lambda *a, **o: mkp.linear_q8_backward(*a, z_group=64, act="silu", **o))]
+
+
+def test_streams(mkp):
+    """From torch's current stream and from the stream argument, two at once,
+    inputs dropped as soon as the call returns."""
+    for M in (4, 60, 700):
+        for name, inputs, call in calls(mkp, M):
+            ref = [t.clone() for t in call(*inputs)]
+            torch.cuda.synchronize()
+            streams = [torch.cuda.Stream() for _ in range(2)]
+            for rep in range(3):
+                got = []
+                for st in streams:
+                    mine = [t.clone() for t in inputs]
+                    st.wait_stream(torch.cuda.current_stream())
+                    if rep == 0:
+                        with torch.cuda.stream(st):
+                            got.append(call(*mine))
+                            for t in mine:
+                                t.record_stream(st)
+                    else:
+                        got.append(call(*mine, stream=st if rep == 1 else st.cuda_stream))
+                    shapes = [(t.shape, t.dtype) for t in mine]
+                    del mine
+                    junk = [torch.full(sh, 99, device="cuda", dtype=dt) for sh, dt in shapes]
+                torch.cuda.synchronize()
+                for outs in got:
+                    for o, r in zip(outs, ref):
+                        same(o, r, f"{name} on a stream")
+                del junk
+
+
+@pytest.mark.parametrize("M", [1, 30, 300])
+def test_captured_into_graphs(mkp, M):
+    """Two graphs with a workspace each, replayed with new inputs and eager calls
+    between, bit for bit as eager calls."""
+    for name, inputs, call in calls(mkp, M):
+        call(*inputs)
+        torch.cuda.synchronize()
+        graphs = []
+        for k in range(2):
+            mine = [t.clone() for t in inputs]
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                outs = call(*mine)
+            graphs.append((graph, mine, outs))
+        for rep in range(4):
+            for k, (graph, mine, outs) in enumerate(graphs):
+                for t in mine:
+                    t.copy_(t.flip(0).clone())
+                graph.replay()
+                want = call(*mine)
+                torch.cuda.synchronize()
+                for o, r in zip(outs, want):
+                    same(o, r, f"{name} replay {rep} of graph {k}")
+
+
+def test_same_bits_again(mkp):
+    for M in (1, 33, 1500):
+        for name, inputs, call in calls(mkp, M, 520, 1111):
+            first = [t.clone() for t in call(*inputs)]
+            for _ in range(3):
+                for o, r in zip(call(*inputs), first):
+                    same(o, r, f"{name} again")
+
+
+def test_guarded_workspace(mkp):
+    """Every call inside a workspace of exactly the reported bytes, whatever it
+    held before."""
+    for M, N, K in ((1, 40, 1000), (20, 300, 4096), (100, 1024, 1500), (300, 260, 96), (2000, 3000, 144)):
+        x, w, ws, b = layer(gen(M), M, N, K)
+        for xx, xt in ((x, mkp.MKP_BF16), (placed(oracle.quantize(x)[0], 1), mkp.MKP_I8)):
+            sx = torch.rand(M, device="cuda")
+            for ww in (placed(w, (-K) % 16), placed(w, 1)):
+                n = mkp.mkp_linear_i8_workspace(M, N, K, xx, xx.stride(0), xt, ww, ww.stride(0))
+                buf = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+                y = torch.empty((M, N), device="cuda")
+                mkp.mkp_linear_i8(M, N, K, xx, xx.stride(0), xt, sx, ww, ww.stride(0), ws, b, 0, y, N, mkp.MKP_F32,
+                                  buf.data_ptr() + 256, n)
+                assert (buf[:256] == 0xA5).all() and (buf[256 + n:] == 0xA5).all()
+                q, s = (xx, sx) if xt == mkp.MKP_I8 else oracle.quantize(x)
+                within(y, *oracle.linear(q, s, w, ws, b, "none", F32), "guarded")
+        dy, x, xs, z, zs = kept(gen(M), M, N, K, 0)
+        n = mkp.mkp_linear_q8_backward_workspace(M, N, K, True, True)
+        buf = torch.full((n + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+        dw, db = torch.empty((N, K), device="cuda"), torch.empty(N, device="cuda")
+        mkp.mkp_linear_q8_backward(M, N, K, dy, N, mkp.MKP_BF16, x, x.stride(0), xs, z, z.stride(0), zs, 1, 0, mkp.MKP_ACT_RELU,
+                                   None, 0, dw, K, mkp.MKP_F32, db, buf.data_ptr() + 256, n)
+        assert (buf[:256] == 0xFF).all() and (buf[256 + n:] == 0xFF).all()
+        ref = oracle.backward(dy, x, xs, z, zs, 0, "relu", F32)
+        within(dw, *ref["dw"], "guarded dw")
+        within(db, *ref["dbias"], "guarded dbias")
