@@ -797,18 +797,39 @@ def linear_distill_backward(x, w, ids, teacher, lse, dloss, bias=None, temperatu
     return dx, dw, dbias
 
 
-def _q8_tensor(name, t, device, dtypes, shape):
-    """One operand of an 8-bit call: (address, leading dimension)."""
+# The current device and stream as numbers (what torch.cuda's functions wrap; a
+# Stream object costs 1.8 us, as long as the rest of a small call's checks)
+def _current(device):
+    """(whether `device` is the current one, its current stream's handle)"""
+    try:
+        return torch._C._cuda_getDevice() == device, torch._C._cuda_getCurrentRawStream(device)
+    except AttributeError:
+        return torch.cuda.current_device() == device, torch.cuda.current_stream(device).cuda_stream
+
+
+def _q8_on(stream, inputs, call):
+    """call(stream handle) on the stream an 8-bit call runs on (see _LossStream)."""
+    device = inputs[0].device
+    if stream is None:
+        here, st = _current(device.index)
+        if here:
+            return call(st)
+    with _LossStream(device, stream, *inputs) as st:
+        return call(st)
+
+
+def _q8_tensor(name, t, gpu, dtypes, shape):
+    """One operand of an 8-bit call on GPU number `gpu`: (address, leading dimension)."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d).split('.')[-1] for d in dtypes)}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on the same GPU as the other operands")
-    cols = shape[-1]
-    if cols > 1 and t.stride(-1) != 1:
+    if gpu < 0 or t.get_device() != gpu:
+        raise ValueError(f"{name} must be on the operands' GPU")
+    strides, cols = t.stride(), shape[-1]
+    if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    return t.data_ptr(), t.stride(0) if len(shape) == 2 and shape[0] > 1 else cols
+    return t.data_ptr(), strides[0] if len(shape) == 2 and shape[0] > 1 else cols
 
 
 def _q8_groups(K, group):
@@ -817,18 +838,18 @@ def _q8_groups(K, group):
     return -(-K // group) if group else 1
 
 
-def _q8_scale(name, t, device, rows, cols, group):
+def _q8_scale(name, t, gpu, rows, cols, group):
     """Scales of a quantised matrix: (address, leading dimension)."""
-    import torch
     if not group:
-        return _q8_tensor(name, t, device, (torch.float32,), (rows,))[0], 1
-    return _q8_tensor(name, t, device, (torch.float32,), (rows, _q8_groups(cols, group)))
+        return _q8_tensor(name, t, gpu, _F32, (rows,))[0], 1
+    return _q8_tensor(name, t, gpu, _F32, (rows, _q8_groups(cols, group)))
 
 
-def _q8_rows(M, K, device):
-    """M x K integers in rows of whole 16-byte units, as linear_i8 reads them without a copy."""
-    import torch
-    return torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :K]
+try:
+    _I8, _F32, _REAL = (torch.int8,), (torch.float32,), (torch.bfloat16, torch.float32)
+    _CODES = {torch.bfloat16: MKP_BF16, torch.float32: MKP_F32, torch.int8: MKP_I8}
+except NameError:
+    pass
 
 
 def quantize_rows(x, group=0, stream=None):
@@ -837,43 +858,57 @@ def quantize_rows(x, group=0, stream=None):
     each `group` columns of it (32, 64, 128 or 256; fp32 (M, ceil(K/group))), and
     q (M,K) int8 = x / scale to the nearest, ties to even.  A row (group) with an
     infinity or NaN has scale NaN and q 0.  linear_i8 takes (q, scale) of group 0
-    as its weight (one scale a channel) and as its input."""
-    import torch
+    as its weight (one scale a channel) and as its input.  q's rows take whole
+    16-byte units, as linear_i8 reads them without a copy."""
     if x.dim() != 2:
         raise ValueError("x must be (M, K)")
     M, K = x.shape
     groups = _q8_groups(K, group)
-    at, ldx = _q8_tensor("x", x, x.device, (torch.bfloat16, torch.float32), (M, K))
-    with _LossStream(x.device, stream, x) as st:
-        q = _q8_rows(M, K, x.device)
+    at, ldx = _q8_tensor("x", x, x.get_device(), _REAL, (M, K))
+    ldq = (K + 15) // 16 * 16
+
+    def call(st):
+        q = torch.empty((M, ldq), dtype=torch.int8, device=x.device)
         scale = torch.empty((M, groups) if group else (M,), dtype=torch.float32, device=x.device)
-        mkp_quantize_rows(M, K, at, ldx, MKP_F32 if x.dtype == torch.float32 else MKP_BF16, group, q,
-                          max(q.stride(0), K), scale, max(groups, 1), st)
-    return q, scale
+        _check(_f_quantize_rows(M, K, at, ldx, _CODES[x.dtype], group, q.data_ptr(), ldq, scale.data_ptr(), groups or 1, st))
+        return (q if ldq == K else q[:, :K]), scale
+
+    return _q8_on(stream, (x,), call)
 
 
 def dequantize_rows(q, scale, group=0, dtype=None, stream=None):
     """The values that quantize_rows' (q, scale) stand for, in dtype bfloat16
     (the default) or float32."""
-    import torch
     dtype = dtype or torch.bfloat16
-    if dtype not in (torch.bfloat16, torch.float32):
+    if dtype not in _REAL:
         raise TypeError("dtype must be bfloat16 or float32")
     if q.dim() != 2:
         raise ValueError("q must be (M, K)")
     M, K = q.shape
+    gpu = q.get_device()
     _q8_groups(K, group)
-    at, ldq = _q8_tensor("q", q, q.device, (torch.int8,), (M, K))
-    sat, lds = _q8_scale("scale", scale, q.device, M, K, group)
-    with _LossStream(q.device, stream, q, scale) as st:
+    at, ldq = _q8_tensor("q", q, gpu, _I8, (M, K))
+    sat, lds = _q8_scale("scale", scale, gpu, M, K, group)
+
+    def call(st):
         y = torch.empty((M, K), dtype=dtype, device=q.device)
-        mkp_dequantize_rows(M, K, at, ldq, sat, lds, group, y, K, MKP_F32 if dtype == torch.float32 else MKP_BF16, st)
-    return y
+        _check(_f_dequantize_rows(M, K, at, ldq, sat, lds or 1, group, y.data_ptr(), K, _CODES[dtype], st))
+        return y
+
+    return _q8_on(stream, (q, scale), call)
 
 
 # (by the extents, the input's type and the alignment of both operands)
 _linear_i8_bytes = functools.lru_cache(maxsize=1024)(mkp_linear_i8_workspace)
 _q8_backward_bytes = functools.lru_cache(maxsize=1024)(mkp_linear_q8_backward_workspace)
+
+
+def _q8_workspace(n, device):
+    """(tensor or None, address)"""
+    if n == 0:
+        return None, 0
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr()
 
 
 def linear_i8(x, w, w_scale, bias=None, act=None, x_scale=None, dtype=None, out=None, stream=None):
@@ -883,37 +918,38 @@ def linear_i8(x, w, w_scale, bias=None, act=None, x_scale=None, dtype=None, out=
     comes with its x_scale (M,).  bias (N,) fp32 or None, act
     None/"relu"/"gelu"/"gelu_tanh"/"silu".  Returns (or fills) out (M,N) in dtype
     float32 (the default) or bfloat16, without a grad_fn."""
-    import torch
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
         raise ValueError("x must be (M, K) and w (N, K)")
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {[a for a in ACTIVATIONS if a]}")
     M, K = x.shape
     N = w.shape[0]
-    dev = x.device
-    xat, ldx = _q8_tensor("x", x, dev, (torch.bfloat16, torch.float32, torch.int8), (M, K))
-    wat, ldw = _q8_tensor("w", w, dev, (torch.int8,), (N, K))
-    sw = _q8_tensor("w_scale", w_scale, dev, (torch.float32,), (N,))[0]
-    if (x.dtype == torch.int8) != (x_scale is not None):
-        raise ValueError("x_scale comes with an int8 x, and only with one")
-    sx = 0 if x_scale is None else _q8_tensor("x_scale", x_scale, dev, (torch.float32,), (M,))[0]
-    b = 0 if bias is None else _q8_tensor("bias", bias, dev, (torch.float32,), (N,))[0]
+    gpu = x.get_device()
+    xat, ldx = _q8_tensor("x", x, gpu, _REAL if x_scale is None else _I8, (M, K))
+    wat, ldw = _q8_tensor("w", w, gpu, _I8, (N, K))
+    sw = _q8_tensor("w_scale", w_scale, gpu, _F32, (N,))[0]
+    sx = 0 if x_scale is None else _q8_tensor("x_scale", x_scale, gpu, _F32, (M,))[0]
+    b = 0 if bias is None else _q8_tensor("bias", bias, gpu, _F32, (N,))[0]
     if out is not None:
         if dtype is not None and out.dtype != dtype:
             raise TypeError("out is not of dtype")
-        yat, ldy = _q8_tensor("out", out, dev, (torch.float32, torch.bfloat16), (M, N))
-    elif dtype not in (None, torch.float32, torch.bfloat16):
-        raise TypeError("dtype must be float32 or bfloat16")
-    xt = MKP_I8 if x_scale is not None else MKP_F32 if x.dtype == torch.float32 else MKP_BF16
+        dtype = out.dtype
+        yat, ldy = _q8_tensor("out", out, gpu, _REAL, (M, N))
+    else:
+        yat, ldy, dtype = 0, N, dtype or torch.float32
+        if dtype not in _REAL:
+            raise TypeError("dtype must be float32 or bfloat16")
+    xt = _CODES[x.dtype]
     n = _linear_i8_bytes(M, N, K, xat & 15, ldx, xt, wat & 15, ldw)
-    with _LossStream(dev, stream, x, w, w_scale, bias, x_scale, out) as st:
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype or torch.float32, device=dev)
-            yat, ldy = out.data_ptr(), N
-        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        mkp_linear_i8(M, N, K, xat, ldx, xt, sx, wat, ldw, sw, b, ACTIVATIONS[act], yat, ldy,
-                      MKP_F32 if out.dtype == torch.float32 else MKP_BF16, ws, n, st)
-    return out
+
+    def call(st):
+        y = torch.empty((M, N), dtype=dtype, device=x.device) if out is None else out
+        ws, at = _q8_workspace(n, x.device)
+        _check(_f_linear_i8(M, N, K, xat, ldx, xt, sx, wat, ldw, sw, b, ACTIVATIONS[act], yat or y.data_ptr(), ldy,
+                            _CODES[dtype], at, n, st))
+        return y
+
+    return _q8_on(stream, (x, w, w_scale, bias, x_scale, out), call)
 
 
 def linear_q8_backward(dy, x, x_scale, z=None, z_scale=None, z_group=0, act=None, need_dz=True, need_dw=True,
@@ -925,34 +961,38 @@ def linear_q8_backward(dy, x, x_scale, z=None, z_scale=None, z_group=0, act=None
     columns).  Returns (dz, dw, dbias): dz = dy act'(z) bf16 (dw's and dx's
     operand; dx is gemm(dz, w)), dw = dz^T x in grad_dtype (bfloat16, the default,
     or float32), dbias fp32; None for those not needed.  No grad_fn."""
-    import torch
     if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
         raise ValueError("dy must be (M, N) and x (M, K)")
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {[a for a in ACTIVATIONS if a]}")
-    if grad_dtype not in (None, torch.bfloat16, torch.float32):
+    grad_dtype = grad_dtype or torch.bfloat16
+    if grad_dtype not in _REAL:
         raise TypeError("grad_dtype must be bfloat16 or float32")
     M, N = dy.shape
     K = x.shape[1]
-    dev = dy.device
-    dyat, lddy = _q8_tensor("dy", dy, dev, (torch.bfloat16, torch.float32), (M, N))
-    xat, ldx = _q8_tensor("x", x, dev, (torch.int8,), (M, K))
-    sx = _q8_tensor("x_scale", x_scale, dev, (torch.float32,), (M,))[0]
+    gpu = dy.get_device()
+    dyat, lddy = _q8_tensor("dy", dy, gpu, _REAL, (M, N))
+    xat, ldx = _q8_tensor("x", x, gpu, _I8, (M, K))
+    sx = _q8_tensor("x_scale", x_scale, gpu, _F32, (M,))[0]
     code = ACTIVATIONS[act]
     zat = ldz = sz = ldzs = 0
     if code != MKP_ACT_NONE:
         if z is None or z_scale is None:
             raise ValueError("an activation's slope needs z and z_scale")
         _q8_groups(N, z_group)
-        zat, ldz = _q8_tensor("z", z, dev, (torch.int8,), (M, N))
-        sz, ldzs = _q8_scale("z_scale", z_scale, dev, M, N, z_group)
+        zat, ldz = _q8_tensor("z", z, gpu, _I8, (M, N))
+        sz, ldzs = _q8_scale("z_scale", z_scale, gpu, M, N, z_group)
     n = _q8_backward_bytes(M, N, K, bool(need_dw), bool(need_dbias))
-    with _LossStream(dev, stream, dy, x, x_scale, z, z_scale) as st:
+
+    def call(st):
+        dev = dy.device
         dz = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if need_dz else None
-        dw = torch.empty((N, K), dtype=grad_dtype or torch.bfloat16, device=dev) if need_dw else None
+        dw = torch.empty((N, K), dtype=grad_dtype, device=dev) if need_dw else None
         dbias = torch.empty(N, dtype=torch.float32, device=dev) if need_dbias else None
-        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        mkp_linear_q8_backward(M, N, K, dyat, lddy, MKP_F32 if dy.dtype == torch.float32 else MKP_BF16, xat, ldx, sx, zat,
-                               ldz, sz, ldzs, z_group if code else 0, code, dz, N, dw, K,
-                               MKP_F32 if grad_dtype == torch.float32 else MKP_BF16, dbias, ws, n, st)
-    return dz, dw, dbias
+        ws, at = _q8_workspace(n, dev)
+        _check(_f_linear_q8_backward(M, N, K, dyat, lddy, _CODES[dy.dtype], xat, ldx, sx, zat, ldz, sz, ldzs or 1,
+                                     z_group if code else 0, code, _addr(dz), N, _addr(dw), K, _CODES[grad_dtype],
+                                     _addr(dbias), at, n, st))
+        return dz, dw, dbias
+
+    return _q8_on(stream, (dy, x, x_scale, z, z_scale), call)

@@ -8,6 +8,8 @@
 
 namespace mkp {
 
+constexpr int kI8StreamRows = 32;   // most tokens of the product for few
+constexpr int kI8StreamUnits = 64;  // runs of 512 features that it quantises by itself
 constexpr int kQ8MaxGroup = 256;   // columns of one scale, if not the whole row
 
 // A matrix <-> its 8-bit form.
@@ -40,6 +42,9 @@ struct I8Args {
     void* C;
     int64_t ldc;
     bool bf16;             // C holds bf16 instead of binary32
+    bool quantise;         // few tokens: x is X itself (lda its leading dimension), quantised by the product
+    const void* x;
+    bool x_f32;
     int tile;              // rows and columns of a tile: 256 or 128
     int splits;            // of K; more than one: partial sums, joined by another launch
     int* part;             // [splits][M][ldp]
@@ -85,6 +90,7 @@ hipError_t launch_dequantize(const QuantArgs& a, hipStream_t st);
 hipError_t launch_q8_pack(const int8_t* src, int64_t lds, int8_t* dst, int64_t ldd, int64_t rows, int cols,
                           hipStream_t st);
 hipError_t launch_i8_product(const I8Args& a, hipStream_t st);
+hipError_t launch_i8_stream(const I8Args& a, hipStream_t st);     // at most kI8StreamRows tokens, rows of any alignment
 hipError_t launch_i8_finish(const I8Args& a, hipStream_t st);     // C from its partial sums
 hipError_t launch_q8_slopes(const Q8GradArgs& a, hipStream_t st);  // dz, a, xb, dbp
 hipError_t launch_q8_product(const Q8GradArgs& a, hipStream_t st); // dW, or its partials

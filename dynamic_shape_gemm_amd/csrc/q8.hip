@@ -19,7 +19,20 @@ namespace {
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2a1 __attribute__((ext_vector_type(2), aligned(1)));
+// (memory of any alignment of its elements is read and written by whole vectors:
+// the same instructions as for aligned ones)
+typedef uint32_t u32x4a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4a1 __attribute__((ext_vector_type(4), aligned(1)));
 typedef float f32x4a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+
+// Device memory's own address space: what is chosen between two pointers is
+// otherwise read by instructions that wait for LDS too.
+template <class V>
+__device__ __forceinline__ V load_global(const void* p) {
+    return *(const V __attribute__((address_space(1)))*)p;
+}
 
 constexpr float kTiny = 1.17549435e-38f;   // 2^-126
 
@@ -38,9 +51,11 @@ template <>
 struct Raw8<false> {
     u32x4 w;
     __device__ __forceinline__ void zero() { w = u32x4{0, 0, 0, 0}; }
-    __device__ __forceinline__ void load(const void* row, int64_t c, int nvalid, bool vec) {
+    __device__ __forceinline__ void read(const void* p) { w = load_global<u32x4a2>(p); }
+    __device__ __forceinline__ void load(const void* row, int64_t c, int nvalid) {
         const uint16_t* p = (const uint16_t*)row + c;
-        w = vec && nvalid >= 8 ? *(const u32x4*)p : load8_any(p, nvalid);
+        if (nvalid >= 8) read(p);
+        else w = load8_elems(p, nvalid);
     }
     // The largest |x|, as the bits of a value of X's type: all infinities and
     // NaN are above every finite one.
@@ -63,11 +78,14 @@ template <>
 struct Raw8<true> {
     f32x4 a, b;
     __device__ __forceinline__ void zero() { a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
-    __device__ __forceinline__ void load(const void* row, int64_t c, int nvalid, bool) {
+    __device__ __forceinline__ void read(const void* p) {
+        a = load_global<f32x4a4>(p);
+        b = load_global<f32x4a4>((const float*)p + 4);
+    }
+    __device__ __forceinline__ void load(const void* row, int64_t c, int nvalid) {
         const float* p = (const float*)row + c;
         if (nvalid >= 8) {
-            a = *(const f32x4a4*)p;
-            b = *(const f32x4a4*)(p + 4);
+            read(p);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -145,10 +163,9 @@ __device__ __forceinline__ u32x2 to_i8(const float (&v)[8], const Scale8& sc) {
 }
 
 // Up to eight bytes to a row (any alignment).
-__device__ __forceinline__ void store_i8(int8_t* p, u32x2 w, int n, bool vec) {
+__device__ __forceinline__ void store_i8(int8_t* p, u32x2 w, int n) {
     if (n >= 8) {
-        if (vec) *(u32x2*)p = w;
-        else *(u32x2a1*)p = w;
+        *(u32x2a1*)p = w;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -181,14 +198,13 @@ __global__ __launch_bounds__(256) void quantize_row_kernel(QuantArgs a) {
     const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + tid / TPR;
     if (TPR < 256 && m >= a.M) return;   // (whole waves)
     const char* row = (const char*)a.x + m * a.ldx * (F32 ? 4 : 2);
-    const bool vec = ((uintptr_t)row & 15) == 0;
     Raw8<F32> raw[C];
     uint32_t top = 0;
     for (int c0 = 0; c0 < a.K; c0 += TPR * 8 * C) {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int c = c0 + (i * TPR + at) * 8;
-            if (c < a.K) raw[i].load(row, c, a.K - c, vec);
+            if (c < a.K) raw[i].load(row, c, a.K - c);
             else raw[i].zero();
         }
 #pragma unroll
@@ -204,18 +220,17 @@ __global__ __launch_bounds__(256) void quantize_row_kernel(QuantArgs a) {
     const Scale8 sc(Raw8<F32>::top_value(top));
     if (at == 0) a.s[m * a.lds] = sc.s;
     int8_t* q = a.q + m * a.ldq;
-    const bool qvec = ((uintptr_t)q & 7) == 0;
     for (int c0 = 0; c0 < a.K + a.pad; c0 += TPR * 8 * C) {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int c = c0 + (i * TPR + at) * 8;
             if constexpr (LOOP) {
-                if (c < a.K) raw[i].load(row, c, a.K - c, vec);
+                if (c < a.K) raw[i].load(row, c, a.K - c);
                 else raw[i].zero();
             }
             float v[8];
             raw[i].values(v);
-            store_i8(q + c, to_i8(v, sc), a.K + a.pad - c, qvec);
+            store_i8(q + c, to_i8(v, sc), a.K + a.pad - c);
         }
         if constexpr (!LOOP) break;
     }
@@ -260,7 +275,7 @@ __global__ __launch_bounds__(256) void quantize_group_kernel(QuantArgs a, int ro
             c[u] = w.c * 8;
             w.next();
             const char* row = (const char*)a.x + (m0 + r[u]) * a.ldx * (F32 ? 4 : 2);
-            if (r[u] < rn && c[u] < a.K) raw[u].load(row, c[u], a.K - c[u], ((uintptr_t)row & 15) == 0);
+            if (r[u] < rn && c[u] < a.K) raw[u].load(row, c[u], a.K - c[u]);
             else raw[u].zero();
         }
 #pragma unroll
@@ -275,8 +290,7 @@ __global__ __launch_bounds__(256) void quantize_group_kernel(QuantArgs a, int ro
             const u32x2 q = to_i8(v, sc);
             if (r[u] < rn) {
                 if (c[u] < a.K && c[u] % (G * 8) == 0) a.s[(m0 + r[u]) * a.lds + c[u] / (G * 8)] = sc.s;
-                int8_t* d = a.q + (m0 + r[u]) * a.ldq + c[u];
-                store_i8(d, q, a.K + a.pad - c[u], ((uintptr_t)d & 7) == 0);
+                store_i8(a.q + (m0 + r[u]) * a.ldq + c[u], q, a.K + a.pad - c[u]);
             }
         }
         if (__ballot(w.r < rn) == 0) break;
@@ -288,8 +302,7 @@ __global__ __launch_bounds__(256) void quantize_group_kernel(QuantArgs a, int ro
 __device__ __forceinline__ u32x2 load_i8(const int8_t* p, int n) {
     u32x2 w = {0, 0};
     if (n >= 8) {
-        if (((uintptr_t)p & 7) == 0) w = *(const u32x2*)p;
-        else w = *(const u32x2a1*)p;
+        w = *(const u32x2a1*)p;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -314,8 +327,8 @@ __device__ __forceinline__ void store_values(void* row, int64_t c, const float (
         }
     } else {
         uint16_t* p = (uint16_t*)row + c;
-        if (n >= 8 && ((uintptr_t)p & 15) == 0) {
-            *(u32x4*)p = u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+        if (n >= 8) {
+            *(u32x4a2*)p = u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -366,8 +379,6 @@ __global__ __launch_bounds__(256) void q8_pack_kernel(const int8_t* src, int64_t
 }
 
 // ---- the product in 8-bit integers -------------------------------------------------
-
-__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
 template <int ACT, int N>
 __device__ __forceinline__ void act_run(f32x4* v) {
@@ -521,6 +532,160 @@ __global__ __launch_bounds__(256) void i8_finish_kernel(I8Args a) {
     }
 }
 
+// ---- few tokens ------------------------------------------------------------------------
+
+// Up to sixteen bytes of a row (any alignment), zeros from `n` on.
+__device__ __forceinline__ u32x4 load16(const int8_t* p, int n) {
+    if (n >= 16) return *(const u32x4a1*)p;
+    const u32x2 lo = load_i8(p, n), hi = load_i8(p + 8, n - 8);
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+
+// At most 16 FM tokens: the weight streams past them, through registers.  A
+// workgroup takes a run of output channels, in NF fragments of 16, and its eight
+// waves a part of the features each (64 at a step), so every byte of W is read
+// once, by one lane, D steps ahead of its use; the waves' sums meet in LDS.
+//
+// UNITS > 0: X is bf16 or binary32 and quantised here, by every workgroup for
+// itself, into LDS, while the weight's first loads are on their way.  A wave
+// holds up to UNITS runs of 512 features in registers between their row's
+// maximum and their integers.
+template <int FM, int NF, int UNITS, bool F32>
+__global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
+    constexpr int NW = 8, D = 8;
+    // [M][K to 64, and 16]: at most 8 UNITS runs of 512
+    __shared__ __attribute__((aligned(16))) unsigned char xq[UNITS > 0 ? 4096 * UNITS + 256 * FM : 16];
+    __shared__ i32x4 red[NW][NF * FM][64];
+    __shared__ uint32_t tops[16 * FM];
+    __shared__ float sx[16 * FM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, s16 = lane & 15, M = (int)a.M;
+    const int n0 = blockIdx.x * cols, left = std::min(cols, a.N - n0);
+    const int steps = a.K >> 6, tail = a.K & 63;   // (a last step that is not full is one wave's, at the end)
+    const int s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
+    const int xld = (a.K + 63) / 64 * 64 + 16;
+
+    // X's own loads come first: they are waited for first
+    const int parts = std::max((a.K + 511) >> 9, 1), units = M * parts;
+    Raw8<F32> raw[UNITS > 0 ? UNITS : 1];
+    if constexpr (UNITS > 0) {
+        if (tid < 16 * FM) tops[tid] = 0;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            // (without branches: a load behind one is waited for with all that follow it)
+            const int unit = wave + u * NW, m = unit / parts, c = (unit - m * parts) * 512 + lane * 8;
+            const char* p = (const char*)a.x + (m * a.lda + c) * (F32 ? 4 : 2);
+            raw[u].read(unit < units && c + 8 <= a.K ? p : (const char*)kZeros);
+            if ((a.K & 7) != 0 && unit < units && c < a.K && c + 8 > a.K) raw[u].load(p, 0, a.K - c);
+        }
+    }
+    const int8_t* wp[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) wp[f] = a.B + (int64_t)(n0 + std::min(f * 16 + s16, left - 1)) * a.ldb + g * 16;
+    const int8_t* xp[FM];
+#pragma unroll
+    for (int m = 0; m < FM; ++m) xp[m] = UNITS > 0 ? nullptr : a.A + std::min(m * 16 + s16, M - 1) * a.lda + g * 16;
+    u32x4 wb[D][NF], xb[UNITS > 0 ? 1 : D][FM];
+    auto load = [&](int i, int s) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) wb[i][f] = load_global<u32x4a1>(steps > 0 ? wp[f] + s * 64 : (const int8_t*)kZeros);
+        if constexpr (UNITS == 0) {
+#pragma unroll
+            for (int m = 0; m < FM; ++m) xb[i][m] = load_global<u32x4a1>(steps > 0 ? xp[m] + s * 64 : (const int8_t*)kZeros);
+        }
+    };
+    const int last = std::max(s1 - 1, 0);   // (a wave without a step reads one of another's, unused)
+#pragma unroll
+    for (int i = 0; i < D; ++i) load(i, std::min(s0 + i, last));
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (UNITS > 0) {
+        uint32_t top[UNITS];
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) top[u] = max_wave(raw[u].top());
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u)
+            if (lane == 0 && wave + u * NW < units) atomicMax(&tops[(wave + u * NW) / parts], top[u]);
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int unit = wave + u * NW, m = unit / parts, part = unit - m * parts, c = part * 512 + lane * 8;
+            if (unit >= units) break;
+            const Scale8 sc(Raw8<F32>::top_value(tops[m]));
+            if (part == 0 && lane == 0) sx[m] = sc.s;
+            float v[8];
+            raw[u].values(v);
+            if (c < xld - 16) *(u32x2*)(xq + m * xld + c) = to_i8(v, sc);
+        }
+        __syncthreads();
+    }
+    i32x4 acc[NF][FM];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int m = 0; m < FM; ++m) acc[f][m] = i32x4{0, 0, 0, 0};
+    auto multiply = [&](int i, int s) {
+#pragma unroll
+        for (int m = 0; m < FM; ++m) {
+            u32x4 x;
+            if constexpr (UNITS > 0) x = *(const u32x4*)(xq + std::min(m * 16 + s16, M - 1) * xld + s * 64 + g * 16);
+            else x = xb[i][m];
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                acc[f][m] = MulI8::mul(__builtin_bit_cast(bf16x8, wb[i][f]), __builtin_bit_cast(bf16x8, x), acc[f][m]);
+        }
+    };
+    int s = s0;
+    for (; s + D < s1; s += D) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) {
+            multiply(i, s + i);
+            load(i, std::min(s + D + i, last));
+            __builtin_amdgcn_sched_barrier(0);   // (kept in this order: the compiler puts the loads last)
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < D; ++i)
+        if (s + i < s1) multiply(i, s + i);
+    if (tail > 0 && wave == NW - 1) {
+        const int n = tail - g * 16;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) wb[0][f] = load16(wp[f] + steps * 64, n);
+        if constexpr (UNITS == 0) {
+#pragma unroll
+            for (int m = 0; m < FM; ++m) xb[0][m] = load16(xp[m] + steps * 64, n);
+        }
+        multiply(0, steps);
+    }
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int m = 0; m < FM; ++m) red[wave][f * FM + m][lane] = acc[f][m];
+    __syncthreads();
+    for (int e = wave; e < NF * FM; e += NW) {
+        const int f = e / FM, m = (e - f * FM) * 16 + s16, c = f * 16 + g * 4;
+        i32x4 t = red[0][e][lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) t += red[w][e][lane];
+        if (m >= M || c >= left) continue;
+        const float sa = UNITS > 0 ? sx[m] : a.sa[m];
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int n = n0 + std::min(c + r, left - 1);
+            v[r] = fmaf((float)t[r] * a.sb[n], sa, a.bias != nullptr ? a.bias[n] : 0.0f);
+        }
+        act_run<1>(a.act, &v);
+        const int64_t at = m * a.ldc + n0 + c;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (c + r >= left) break;
+            if (a.bf16) ((uint16_t*)a.C)[at + r] = f32_to_bf16(v[r]);
+            else ((float*)a.C)[at + r] = v[r];
+        }
+    }
+}
+
 // ---- backward -----------------------------------------------------------------------
 
 // dz = dy act'(z), what is made of it, and the input's integers in bf16.
@@ -563,7 +728,7 @@ __global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first,
                 xs[u] = 0.0f;
                 if (m >= a.M) continue;
                 const char* row = (const char*)a.dy + m * a.lddy * (F32 ? 4 : 2);
-                dy[u].load(row, n, left, ((uintptr_t)row & 15) == 0);
+                dy[u].load(row, n, left);
                 if (a.act != ACT_NONE) {
                     z[u] = load_i8(a.z + m * a.ldz + n, left);
                     zs[u] = a.zs[m * a.ldzs + (n >> zshift)];
@@ -690,6 +855,9 @@ using I128 = LTile<2, 2, 2, 2, false, false, MulI8>;
 using G256 = LTile<2, 4, 4, 2, true, true>;
 using G128 = LTile<2, 2, 2, 2, true, true>;
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int log2i(int v) { return 31 - __builtin_clz((unsigned)v); }
 
@@ -738,6 +906,33 @@ hipError_t launch_i8_product(const I8Args& a, hipStream_t st) {
     const dim3 grid((unsigned)(up(a.M, a.tile) * up(a.N, a.tile) * a.splits));
     return a.tile == 256 ? launch_kernel(i8_tile_kernel<I256>, grid, dim3(I256::NT), st, a)
                          : launch_kernel(i8_tile_kernel<I128>, grid, dim3(I128::NT), st, a);
+}
+
+hipError_t launch_i8_stream(const I8Args& a, hipStream_t st) {
+    // every CU a run of channels, at most 64 of them at a time
+    const int passes = (int)up(a.N, 256 * 64), cols = (int)up(a.N, 256 * passes);
+    const dim3 grid((unsigned)up(a.N, cols)), b(512);
+    const int units = a.quantise ? (int)std::max<int64_t>(1, up(a.M * up(a.K, 512), 8)) : 0;
+    auto go = [&](auto fm, auto nf, auto un, auto f32) {
+        return launch_kernel(i8_stream_kernel<decltype(fm)::value, decltype(nf)::value, decltype(un)::value,
+                                                  decltype(f32)::value>, grid, b, st, a, cols);
+    };
+    auto by_units = [&](auto fm, auto nf) {
+        if (units == 0) return go(fm, nf, Int<0>{}, Int<0>{});
+        if constexpr (decltype(fm)::value == 1) {
+            if (a.x_f32) return units <= 1 ? go(fm, nf, Int<1>{}, Int<1>{}) : units <= 4 ? go(fm, nf, Int<4>{}, Int<1>{})
+                                                                                        : go(fm, nf, Int<8>{}, Int<1>{});
+            return units <= 1 ? go(fm, nf, Int<1>{}, Int<0>{}) : units <= 4 ? go(fm, nf, Int<4>{}, Int<0>{})
+                                                                            : go(fm, nf, Int<8>{}, Int<0>{});
+        } else {
+            return a.x_f32 ? go(fm, nf, Int<8>{}, Int<1>{}) : go(fm, nf, Int<8>{}, Int<0>{});
+        }
+    };
+    auto by_cols = [&](auto fm) {
+        return cols <= 16 ? by_units(fm, Int<1>{}) : cols <= 32 ? by_units(fm, Int<2>{})
+               : cols <= 48 ? by_units(fm, Int<3>{}) : by_units(fm, Int<4>{});
+    };
+    return a.M <= 16 ? by_cols(Int<1>{}) : by_cols(Int<2>{});
 }
 
 hipError_t launch_i8_finish(const I8Args& a, hipStream_t st) {

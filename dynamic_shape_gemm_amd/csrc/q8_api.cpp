@@ -93,7 +93,7 @@ int convert(bool back, int64_t M, int64_t K, void* X, int64_t ldx, int type, int
 
 struct LinearLayout {
     int tile = 256, splits = 1;
-    bool quantise = false, pack_a = false, pack_b = false;
+    bool stream = false, quantise = false, pack_a = false, pack_b = false;
     int64_t Ka = 0, Kb = 0, ldp = 0;   // bytes of a packed row, a row of partial sums
     size_t a = 0, s = 0, b = 0, part = 0, bytes = 0;
 };
@@ -101,6 +101,16 @@ struct LinearLayout {
 LinearLayout linear_layout(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, int x_type, const void* W,
                            int64_t ldw) {
     LinearLayout l;
+    l.stream = M <= kI8StreamRows;
+    if (l.stream) {   // (rows of any alignment; few enough features are quantised by the product)
+        l.quantise = x_type != MKP_I8 && M * ceil_div(K, 512) > kI8StreamUnits;
+        l.Ka = round_up(K, 16);
+        if (l.quantise) {
+            l.s = (size_t)round_up(M * l.Ka, 256);
+            l.bytes = l.s + (size_t)(4 * M);
+        }
+        return l;
+    }
     l.quantise = x_type != MKP_I8;
     l.pack_a = !l.quantise && (!aligned16(X) || ldx % 16 != 0 || K % 16 != 0);
     l.pack_b = !aligned16(W) || ldw % 16 != 0;
@@ -147,7 +157,7 @@ int linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, int x_ty
     if (K > 0 && (!X || !W)) return report(MKP_ERR_INVALID_ARG, "X or W is NULL");
     const LinearLayout l = linear_layout(M, N, K, X, ldx, x_type, W, ldw);
     MKP_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
-    const int64_t tiles = ceil_div(M, l.tile) * ceil_div(N, l.tile) * l.splits;
+    const int64_t tiles = l.stream ? 0 : ceil_div(M, l.tile) * ceil_div(N, l.tile) * l.splits;
     if (tiles > UINT32_MAX / 512 || (l.splits > 1 && M * ceil_div(N, 4) > (int64_t)UINT32_MAX - 255) ||
         (l.pack_b && N > kMaxRows))
         return report(MKP_ERR_UNSUPPORTED, "grid too large");
@@ -193,9 +203,14 @@ int linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, int x_ty
         a.B = (const int8_t*)(ws + l.b);
         a.ldb = l.Kb;
     }
+    if (l.stream && !l.quantise && x_type != MKP_I8) {
+        a.quantise = true;
+        a.x = X;
+        a.x_f32 = x_type == MKP_F32;
+    }
     const double out = size_of(y_type) * m * n, parts = 4.0 * m * n * (double)l.splits;
     MKP_TRY(go(st, QL_I8_PRODUCT, 2.0 * m * n * k, (m + n) * k + (l.splits > 1 ? parts : out),
-               [&] { return launch_i8_product(a, st); }));
+               [&] { return l.stream ? launch_i8_stream(a, st) : launch_i8_product(a, st); }));
     if (l.splits == 1) return MKP_OK;
     return go(st, QL_I8_FINISH, 0.0, parts + out, [&] { return launch_i8_finish(a, st); });
 }

@@ -254,10 +254,13 @@ def test_largest_sums(mkp, M):
 
 def test_empty_sums(mkp):
     b = torch.randn(9, device="cuda")
-    for t in (F32, BF):
-        y = mkp.linear_i8(torch.empty((5, 0), dtype=BF, device="cuda"), torch.empty((9, 0), dtype=I8, device="cuda"),
-                          torch.ones(9, device="cuda"), b, act="relu", dtype=t)
-        same(y, b.clamp(min=0).to(t).repeat(5, 1), "no features")
+    for M in (5, 40):
+        for xs in (None, torch.ones(M, device="cuda")):
+            for t in (F32, BF):
+                y = mkp.linear_i8(torch.empty((M, 0), dtype=BF if xs is None else I8, device="cuda"),
+                                  torch.empty((9, 0), dtype=I8, device="cuda"), torch.ones(9, device="cuda"), b, act="relu",
+                                  x_scale=xs, dtype=t)
+                same(y, b.clamp(min=0).to(t).repeat(M, 1), "no features")
     assert mkp.linear_i8(torch.empty((0, 16), dtype=BF, device="cuda"), torch.ones((3, 16), dtype=I8, device="cuda"),
                          torch.ones(3, device="cuda")).shape == (0, 3)
     assert mkp.linear_i8(torch.ones((4, 16), dtype=BF, device="cuda"), torch.ones((0, 16), dtype=I8, device="cuda"),
