@@ -58,33 +58,32 @@ __device__ __forceinline__ float act_apply(int act, float v) {
 //   gelu       Phi(z) + z phi(z)
 //   relu       1 above 0, else 0 (at 0 too)
 // Absolute errors below 3e-7: Phi's 0.75e-7, else roundings of values of at most 1.2.
-__device__ __forceinline__ float act_slope(int act, float z) {
-    switch (act) {
-        case ACT_RELU: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
-        case ACT_GELU: {
-            const float a = fabsf(z) * 0.70710678118654752f;
-            const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * a);
-            float poly = 1.061405429f;
-            poly = fmaf(poly, t, -1.453152027f);
-            poly = fmaf(poly, t, 1.421413741f);
-            poly = fmaf(poly, t, -0.284496736f);
-            poly = fmaf(poly, t, 0.254829592f);
-            const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * a * a);
-            const float q = poly * t * e;
-            return fmaf(z * 0.39894228040143268f, e, 0.5f * (z < 0.0f ? q : 2.0f - q));
-        }
-        case ACT_GELU_TANH: {
-            const float c = 2.0f * 0.79788456080286536f, z2 = z * z;
-            const float p = sigmoid_fast(c * (z + 0.044715f * z2 * z));
-            const float w = p * (1.0f - p);
-            return w > 0.0f ? fmaf(z * w, c * fmaf(3.0f * 0.044715f, z2, 1.0f), p) : p;
-        }
-        case ACT_SILU: {
-            const float p = sigmoid_fast(z);
-            return p * fmaf(z, 1.0f - p, 1.0f);
-        }
-        default: return 1.0f;
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+    if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
+    if constexpr (ACT == ACT_GELU) {
+        const float a = fabsf(z) * 0.70710678118654752f;
+        const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * a);
+        float poly = 1.061405429f;
+        poly = fmaf(poly, t, -1.453152027f);
+        poly = fmaf(poly, t, 1.421413741f);
+        poly = fmaf(poly, t, -0.284496736f);
+        poly = fmaf(poly, t, 0.254829592f);
+        const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * a * a);
+        const float q = poly * t * e;
+        return fmaf(z * 0.39894228040143268f, e, 0.5f * (z < 0.0f ? q : 2.0f - q));
     }
+    if constexpr (ACT == ACT_GELU_TANH) {
+        const float c = 2.0f * 0.79788456080286536f, z2 = z * z;
+        const float p = sigmoid_fast(c * (z + 0.044715f * z2 * z));
+        const float w = p * (1.0f - p);
+        return w > 0.0f ? fmaf(z * w, c * fmaf(3.0f * 0.044715f, z2, 1.0f), p) : p;
+    }
+    if constexpr (ACT == ACT_SILU) {
+        const float p = sigmoid_fast(z);
+        return p * fmaf(z, 1.0f - p, 1.0f);
+    }
+    return 1.0f;
 }
 
 }  // namespace

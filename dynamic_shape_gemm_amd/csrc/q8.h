@@ -45,7 +45,7 @@ struct I8Args {
     bool quantise;         // few tokens: x is X itself (lda its leading dimension), quantised by the product
     const void* x;
     bool x_f32;
-    int tile;              // rows and columns of a tile: 256 or 128
+    int tile;              // rows and columns of a tile: 256, 128 or 64
     int splits;            // of K; more than one: partial sums, joined by another launch
     int* part;             // [splits][M][ldp]
     int64_t ldp;
@@ -77,11 +77,11 @@ struct Q8GradArgs {
     uint16_t* a;           // dz times its row's scale in bf16, Mr x Np (rows past M zero)
     uint16_t* xb;          // x's integers in bf16, M x Kp
     float* part;           // dW's partials [splits][N][Kp] (several splits)
-    float* dbp;            // column sums of dz over kQ8SumRows rows each, [Mr / kQ8SumRows][Np]
+    float* dbp;            // column sums of dz over sum_rows rows each, [M / sum_rows][Np]
     int Mr, Np, Kp;
+    int sum_rows;          // a multiple of 16
     int tile, splits;
 };
-constexpr int kQ8SumRows = 32;
 
 // Launches; each returns the launch's status.
 hipError_t launch_quantize(const QuantArgs& a, hipStream_t st);

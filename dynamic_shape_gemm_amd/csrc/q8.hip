@@ -401,8 +401,29 @@ __device__ __forceinline__ void act_run(int act, f32x4* v) {
 // One tile over one split's K steps (of 128 integers).  The sums are exact in 32
 // bits (K at most 131071); what is past K reads as zeros in both operands, or, in
 // the last 16 bytes, as zeros in A.
+// A tile's bf16 values, staged in LDS, to rows of any alignment.
 template <class T>
-__device__ __forceinline__ void i8_tile(const I8Args& a, int m0, int n0, int split, lds_t* smem, int wave, int lane) {
+__device__ __forceinline__ void store_rows16(uint16_t* D, int64_t ld, int rows, int cols, const lds_t* smem, int tid) {
+    __syncthreads();
+    constexpr int CPR = T::BN / 8;
+    for (int q = tid; q < T::BM * CPR; q += T::NT) {
+        const int r = q / CPR, c = (q % CPR) * 8;
+        if (r >= rows || c >= cols) continue;
+        const u32x4 w = *(const u32x4 __attribute__((address_space(3)))*)(smem + r * staged_ld<T> + c * 2);
+        uint16_t* d = D + r * ld + c;
+        if (c + 8 <= cols) *(u32x4a2*)d = w;
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < cols) d[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+}
+
+template <class T>
+constexpr int staged_ld32 = T::BN * 4 + 16;
+template <class T, int ACT>
+__device__ __forceinline__ void i8_tile(const I8Args& a, int m0, int n0, int split, lds_t* smem, float* edge, int wave,
+                                        int lane) {
     const int kp = (a.K + 15) >> 4 << 3;   // 16-bit columns
     const int all = (kp + 63) >> 6, per = (all + a.splits - 1) / a.splits;
     const int s0 = std::min(split * per, all), steps = std::min(per, all - s0);
@@ -414,6 +435,17 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, int m0, int n0, int spl
            (const uint16_t*)kZeros);
     B.init((const uint16_t*)(a.B + (int64_t)n0 * a.ldb) + s0 * 64, a.ldb >> 1, cols, steps, tail, wave, lane,
            (const uint16_t*)kZeros);
+    // The epilogue's operands are read ahead of the product, into LDS: read after
+    // it, row by row, they cost a 128 x 128 tile 4 us of 8.5 (109 x 887 x 144).
+    const int tid = wave * 64 + lane;
+    if (a.splits == 1) {
+        for (int i = tid; i < T::BN; i += T::NT) {
+            const int n = n0 + std::min(i, cols - 1);
+            edge[i] = a.sb[n];
+            edge[T::BN + i] = a.bias != nullptr ? a.bias[n] : 0.0f;
+        }
+        for (int i = tid; i < T::BM; i += T::NT) edge[2 * T::BN + i] = a.sa[m0 + std::min(i, rows - 1)];
+    }
     Acc<T> acc;
     main_loop<T>(A, B, steps, smem, wave, lane, acc);
     const Place<T> at(wave, lane);
@@ -433,70 +465,110 @@ __device__ __forceinline__ void i8_tile(const I8Args& a, int m0, int n0, int spl
             }
         return;
     }
+    // One row of fragments (registers: a row at a time), to LDS.  Both types go
+    // through it, binary32 half the tile's rows at a time, and leave by one loop in
+    // whole row segments: stores beside each fragment's arithmetic are code that is
+    // jumped over, and fetched, for every fragment (bf16, 109 x 887 x 144 on 128 x
+    // 128 tiles: 8.0 us so, 6.6 now).
     f32x4 sb[2][T::FN], bias[2][T::FN];
+    auto columns = [&] {
+        asm volatile("" ::: "memory");   // (by each type's branch for itself: nothing of a row is worked out ahead of both)
 #pragma unroll
-    for (int hb = 0; hb < 2; ++hb)
+        for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-        for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int n = std::min(n0 + at.col(hb, j) + r, a.N - 1);
-                sb[hb][j][r] = a.sb[n];
-                bias[hb][j][r] = a.bias != nullptr ? a.bias[n] : 0.0f;
+            for (int j = 0; j < T::FN; ++j) {
+                sb[hb][j] = *(const f32x4*)(edge + at.col(hb, j));
+                bias[hb][j] = *(const f32x4*)(edge + T::BN + at.col(hb, j));
             }
-    float* D = (float*)a.C + (int64_t)m0 * a.ldc + n0;
-    const bool vec = ((uintptr_t)D & 15) == 0 && a.ldc % 4 == 0;
+    };
+    auto row_to = [&](int ha, int i, auto&& put) {
+        const float sa = edge[2 * T::BN + at.row(ha, i)];
+        f32x4 v[2][T::FN];
 #pragma unroll
-    for (int ha = 0; ha < 2; ++ha)
+        for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-        for (int i = 0; i < T::FM; ++i) {
-            const int row = at.row(ha, i);
-            const float sa = a.sa[m0 + std::min(row, rows - 1)];
-            f32x4 v[2][T::FN];
+            for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-            for (int hb = 0; hb < 2; ++hb)
+                for (int r = 0; r < 4; ++r)
+                    v[hb][j][r] = fmaf((float)acc[ha][hb][i][j][r] * sb[hb][j][r], sa, bias[hb][j][r]);
+        act_run<ACT, 2 * T::FN>(&v[0][0]);
 #pragma unroll
-                for (int j = 0; j < T::FN; ++j)
+        for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[hb][j][r] = fmaf((float)acc[ha][hb][i][j][r] * sb[hb][j][r], sa, bias[hb][j][r]);
-            act_run<2 * T::FN>(a.act, &v[0][0]);
+            for (int j = 0; j < T::FN; ++j) put(at.row(ha, i), at.col(hb, j), v[hb][j]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (a.bf16) {
+        columns();
 #pragma unroll
-            for (int hb = 0; hb < 2; ++hb)
+        for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
-                for (int j = 0; j < T::FN; ++j) {
-                    const int col = at.col(hb, j);
-                    const f32x4 y = v[hb][j];
-                    if (a.bf16) {
-                        *(u32x2 __attribute__((address_space(3)))*)(smem + row * staged_ld<T> + col * 2) =
-                            u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-                    } else if (row < rows) {
-                        float* d = D + row * a.ldc + col;
-                        if (vec && col + 4 <= cols) *(f32x4*)d = y;
-                        else
+            for (int i = 0; i < T::FM; ++i)
+                row_to(ha, i, [&](int row, int col, f32x4 y) {
+                    *(u32x2 __attribute__((address_space(3)))*)(smem + row * staged_ld<T> + col * 2) =
+                        u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+                });
+        store_rows16<T>((uint16_t*)a.C + (int64_t)m0 * a.ldc + n0, a.ldc, rows, cols, smem, tid);
+        return;
+    }
+    columns();
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (col + r < cols) d[r] = y[r];
-                    }
-                }
-            __builtin_amdgcn_sched_barrier(0);   // (a row at a time: the accumulators fill the registers)
+    for (int ha = 0; ha < 2; ++ha) {
+        if (ha) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+            row_to(ha, i, [&](int row, int col, f32x4 y) {
+                *(f32x4 __attribute__((address_space(3)))*)(smem + (row - ha * T::HA) * staged_ld32<T> + col * 4) = y;
+            });
+        __syncthreads();
+        float* D = (float*)a.C + (int64_t)(m0 + ha * T::HA) * a.ldc + n0;
+        constexpr int CPR = T::BN / 4;
+        for (int q = tid; q < T::HA * CPR; q += T::NT) {
+            const int r = q / CPR, c = (q % CPR) * 4;
+            if (r >= rows - ha * T::HA || c >= cols) continue;
+            const f32x4 y = *(const f32x4 __attribute__((address_space(3)))*)(smem + r * staged_ld32<T> + c * 4);
+            float* d = D + r * a.ldc + c;
+            if (c + 4 <= cols) *(f32x4a4*)d = y;
+            else
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < cols) d[e] = y[e];
         }
-    if (a.bf16)
-        store_staged<T>((uint16_t*)a.C + n0, a.ldc, rows, cols, smem, wave, lane, [&](int r) { return (int64_t)m0 + r; });
+    }
 }
 
 template <class T>
 constexpr int tile_lds() {
     return std::max(T::LDS, T::BM * staged_ld<T>);
 }
-
 template <class T>
+constexpr int i8_lds() {
+    return std::max(tile_lds<T>(), T::HA * staged_ld32<T>);
+}
+
+// H: T, or the tile of half its rows that a last round of unsplit tiles is cut
+// into.  An instance for each activation: a switch between them inside an epilogue
+// costs its jumps' instruction fetches, 4 us of 9 for the smallest products on
+// 128 x 128 tiles.
+template <class T, class H, int ACT>
 __global__ __launch_bounds__(T::NT, 2) void i8_tile_kernel(I8Args a) {
-    __shared__ __attribute__((aligned(1024))) unsigned char raw[tile_lds<T>()];
+    __shared__ __attribute__((aligned(1024))) unsigned char raw[std::max(i8_lds<T>(), i8_lds<H>())];
+    __shared__ __attribute__((aligned(16))) float edge[T::BM + 2 * T::BN];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rows = (int)((a.M + T::BM - 1) / T::BM), cols = (a.N + T::BN - 1) / T::BN;
     int tm, tn, split;
-    if (!map_tile(blockIdx.x, (int)((a.M + T::BM - 1) / T::BM), (a.N + T::BN - 1) / T::BN, tm, tn, split, a.splits)) return;
-    i8_tile<T>(a, tm * T::BM, tn * T::BN, split, (lds_t*)raw, wave, lane);
+    if constexpr (T::BM > H::BM) {
+        if (a.splits == 1) {
+            int half;
+            if (!map_rounds(blockIdx.x, rows, cols, 256, true, tm, tn, half)) return;
+            if (half < 0) i8_tile<T, ACT>(a, tm * T::BM, tn * T::BN, 0, (lds_t*)raw, edge, wave, lane);
+            else if (tm * T::BM + half * H::BM < a.M)
+                i8_tile<H, ACT>(a, tm * T::BM + half * H::BM, tn * T::BN, 0, (lds_t*)raw, edge, wave, lane);
+            return;
+        }
+    }
+    if (!map_tile(blockIdx.x, rows, cols, tm, tn, split, a.splits)) return;
+    i8_tile<T, ACT>(a, tm * T::BM, tn * T::BN, split, (lds_t*)raw, edge, wave, lane);
 }
 
 // Four columns a thread: the partial sums, joined exactly, and the epilogue.
@@ -689,9 +761,9 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
 // ---- backward -----------------------------------------------------------------------
 
 // dz = dy act'(z), what is made of it, and the input's integers in bf16.
-// Workgroups of the first kind take kQ8SumRows rows of 512 columns, a wave every
+// Workgroups of the first kind take sum_rows rows of 512 columns, a wave every
 // fourth row; of the second 4 rows of the input.
-template <bool F32>
+template <bool F32, int ACT>
 __global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first, int cols, int zshift) {
     __shared__ float red[4][512];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -711,11 +783,11 @@ __global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first,
     }
     const int rb = blockIdx.x / cols, n = (blockIdx.x - rb * cols) * 512 + lane * 8;
     const int left = a.N - n;
-    const int64_t m0 = (int64_t)rb * kQ8SumRows;
+    const int64_t m0 = (int64_t)rb * a.sum_rows;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     constexpr int U = 4;
     if (n < a.Np) {
-        for (int r0 = wave; r0 < kQ8SumRows; r0 += 4 * U) {
+        for (int r0 = wave; r0 < a.sum_rows; r0 += 4 * U) {
             Raw8<F32> dy[U];
             u32x2 z[U];
             float zs[U], xs[U];
@@ -729,7 +801,7 @@ __global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first,
                 if (m >= a.M) continue;
                 const char* row = (const char*)a.dy + m * a.lddy * (F32 ? 4 : 2);
                 dy[u].load(row, n, left);
-                if (a.act != ACT_NONE) {
+                if constexpr (ACT != ACT_NONE) {
                     z[u] = load_i8(a.z + m * a.ldz + n, left);
                     zs[u] = a.zs[m * a.ldzs + (n >> zshift)];
                 }
@@ -740,16 +812,16 @@ __global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first,
                 const int64_t m = m0 + r0 + 4 * u;
                 float g[8];
                 dy[u].values(g);
-                if (a.act != ACT_NONE && m < a.M) {
+                if constexpr (ACT != ACT_NONE) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) g[i] *= act_slope(a.act, i8_at(z[u], i) * zs[u]);
+                    for (int i = 0; i < 8; ++i) g[i] *= act_slope<ACT>(i8_at(z[u], i) * zs[u]);
                 }
                 if (m < a.M) {
                     if (a.dz != nullptr) store_values<false>(a.dz + m * a.lddz, n, g, left);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) sum[i] += g[i];
                 }
-                if (a.a != nullptr) {   // (rows from M on: zeros)
+                if (a.a != nullptr && m < a.Mr) {   // (rows from M on: zeros)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) g[i] = m < a.M ? g[i] * xs[u] : 0.0f;
                     store_values<false>(a.a + m * a.Np, n, g, 8);
@@ -805,22 +877,27 @@ __global__ __launch_bounds__(T::NT, 2) void q8_product_kernel(Q8GradArgs a) {
         }
 }
 
-// dW from its partials, eight columns a thread; then dbias from its column sums.
+// dW from its partials, eight columns a thread; then dbias from its column sums,
+// 32 columns a workgroup, every eighth sum a thread.
 __global__ __launch_bounds__(256) void q8_finish_kernel(Q8GradArgs a, int first) {
+    __shared__ float red[8][32];
     if ((int)blockIdx.x >= first) {
-        const int n = (blockIdx.x - first) * 256 + threadIdx.x;
-        if (n >= a.N) return;
-        const int parts = (int)((a.M + kQ8SumRows - 1) / kQ8SumRows);
+        const int c = threadIdx.x & 31, grp = threadIdx.x >> 5, n = (blockIdx.x - first) * 32 + c;
+        const int parts = (int)((a.M + a.sum_rows - 1) / a.sum_rows);
         constexpr int U = 8;
         float t = 0.0f;
-        for (int i0 = 0; i0 < parts; i0 += U) {
+        for (int i0 = grp; i0 < parts; i0 += 8 * U) {
             float x[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) x[u] = i0 + u < parts ? a.dbp[(int64_t)(i0 + u) * a.Np + n] : 0.0f;
+            for (int u = 0; u < U; ++u)
+                x[u] = i0 + 8 * u < parts && n < a.N ? a.dbp[(int64_t)(i0 + 8 * u) * a.Np + n] : 0.0f;
 #pragma unroll
             for (int u = 0; u < U; ++u) t += x[u];
         }
-        a.dbias[n] = t;
+        red[grp][c] = t;
+        __syncthreads();
+        if (grp == 0 && n < a.N)
+            a.dbias[n] = ((red[0][c] + red[1][c]) + (red[2][c] + red[3][c])) + ((red[4][c] + red[5][c]) + (red[6][c] + red[7][c]));
         return;
     }
     const int cpr = a.Kp >> 3;
@@ -851,6 +928,8 @@ __global__ __launch_bounds__(256) void q8_finish_kernel(Q8GradArgs a, int first)
 }
 
 using I256 = LTile<2, 4, 4, 2, false, false, MulI8>;
+using I256Half = LTile<2, 4, 2, 2, false, false, MulI8>;
+using I64 = LTile<2, 2, 1, 1, false, false, MulI8>;
 using I128 = LTile<2, 2, 2, 2, false, false, MulI8>;
 using G256 = LTile<2, 4, 4, 2, true, true>;
 using G128 = LTile<2, 2, 2, 2, true, true>;
@@ -859,6 +938,16 @@ template <int N>
 using Int = std::integral_constant<int, N>;
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+template <class F>
+hipError_t by_act(int act, F&& f) {
+    switch (act) {
+        case ACT_RELU: return f(Int<ACT_RELU>{});
+        case ACT_GELU: return f(Int<ACT_GELU>{});
+        case ACT_GELU_TANH: return f(Int<ACT_GELU_TANH>{});
+        case ACT_SILU: return f(Int<ACT_SILU>{});
+        default: return f(Int<ACT_NONE>{});
+    }
+}
 int log2i(int v) { return 31 - __builtin_clz((unsigned)v); }
 
 // Rows of a workgroup that walks chunks: about 1024 of them.
@@ -903,9 +992,16 @@ hipError_t launch_q8_pack(const int8_t* src, int64_t lds, int8_t* dst, int64_t l
 }
 
 hipError_t launch_i8_product(const I8Args& a, hipStream_t st) {
-    const dim3 grid((unsigned)(up(a.M, a.tile) * up(a.N, a.tile) * a.splits));
-    return a.tile == 256 ? launch_kernel(i8_tile_kernel<I256>, grid, dim3(I256::NT), st, a)
-                         : launch_kernel(i8_tile_kernel<I128>, grid, dim3(I128::NT), st, a);
+    // (halved tiles of a last round: at most 128 workgroups more)
+    const dim3 grid((unsigned)(up(a.M, a.tile) * up(a.N, a.tile) * a.splits + (a.tile == 256 && a.splits == 1 ? 128 : 0)));
+    return by_act(a.splits > 1 ? ACT_NONE : a.act, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        switch (a.tile) {
+            case 256: return launch_kernel(i8_tile_kernel<I256, I256Half, ACT>, grid, dim3(I256::NT), st, a);
+            case 128: return launch_kernel(i8_tile_kernel<I128, I128, ACT>, grid, dim3(I128::NT), st, a);
+            default: return launch_kernel(i8_tile_kernel<I64, I64, ACT>, grid, dim3(I64::NT), st, a);
+        }
+    });
 }
 
 hipError_t launch_i8_stream(const I8Args& a, hipStream_t st) {
@@ -942,10 +1038,13 @@ hipError_t launch_i8_finish(const I8Args& a, hipStream_t st) {
 hipError_t launch_q8_slopes(const Q8GradArgs& a, hipStream_t st) {
     const int cols = (int)up(a.Np, 512), shift = a.zgroup == 0 ? 31 : log2i(a.zgroup);
     const int64_t rows = a.a != nullptr ? a.Mr : a.M;
-    const int64_t first = up(rows, kQ8SumRows) * cols, second = a.xb != nullptr ? up(a.M, 4) : 0;
+    const int64_t first = up(rows, a.sum_rows) * cols, second = a.xb != nullptr ? up(a.M, 4) : 0;
     const dim3 grid((unsigned)(first + second));
-    return a.dy_f32 ? launch_kernel(q8_slopes_kernel<true>, grid, dim3(256), st, a, (int)first, cols, shift)
-                    : launch_kernel(q8_slopes_kernel<false>, grid, dim3(256), st, a, (int)first, cols, shift);
+    return by_act(a.act, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        return a.dy_f32 ? launch_kernel(q8_slopes_kernel<true, ACT>, grid, dim3(256), st, a, (int)first, cols, shift)
+                        : launch_kernel(q8_slopes_kernel<false, ACT>, grid, dim3(256), st, a, (int)first, cols, shift);
+    });
 }
 
 hipError_t launch_q8_product(const Q8GradArgs& a, hipStream_t st) {
@@ -956,7 +1055,7 @@ hipError_t launch_q8_product(const Q8GradArgs& a, hipStream_t st) {
 
 hipError_t launch_q8_finish(const Q8GradArgs& a, hipStream_t st) {
     const int64_t first = a.dw != nullptr && a.splits > 1 ? up((int64_t)a.N * (a.Kp >> 3), 256) : 0;
-    const int64_t second = a.dbias != nullptr ? up(a.N, 256) : 0;
+    const int64_t second = a.dbias != nullptr ? up(a.N, 32) : 0;
     return launch_kernel(q8_finish_kernel, dim3((unsigned)(first + second)), dim3(256), st, a, (int)first);
 }
 
