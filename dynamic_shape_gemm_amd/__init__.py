@@ -868,8 +868,8 @@ def quantize_rows(x, group=0, stream=None):
     ldq = (K + 15) // 16 * 16
 
     def call(st):
-        q = torch.empty((M, ldq), dtype=torch.int8, device=x.device)
-        scale = torch.empty((M, groups) if group else (M,), dtype=torch.float32, device=x.device)
+        q = x.new_empty((M, ldq), dtype=torch.int8)
+        scale = x.new_empty((M, groups) if group else (M,), dtype=torch.float32)
         _check(_f_quantize_rows(M, K, at, ldx, _CODES[x.dtype], group, q.data_ptr(), ldq, scale.data_ptr(), groups or 1, st))
         return (q if ldq == K else q[:, :K]), scale
 
@@ -891,7 +891,7 @@ def dequantize_rows(q, scale, group=0, dtype=None, stream=None):
     sat, lds = _q8_scale("scale", scale, gpu, M, K, group)
 
     def call(st):
-        y = torch.empty((M, K), dtype=dtype, device=q.device)
+        y = q.new_empty((M, K), dtype=dtype)
         _check(_f_dequantize_rows(M, K, at, ldq, sat, lds or 1, group, y.data_ptr(), K, _CODES[dtype], st))
         return y
 
@@ -903,11 +903,11 @@ _linear_i8_bytes = functools.lru_cache(maxsize=1024)(mkp_linear_i8_workspace)
 _q8_backward_bytes = functools.lru_cache(maxsize=1024)(mkp_linear_q8_backward_workspace)
 
 
-def _q8_workspace(n, device):
-    """(tensor or None, address)"""
+def _q8_workspace(n, like):
+    """(tensor on `like`'s GPU or None, address)"""
     if n == 0:
         return None, 0
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws = like.new_empty(n, dtype=torch.uint8)
     return ws, ws.data_ptr()
 
 
@@ -943,8 +943,8 @@ def linear_i8(x, w, w_scale, bias=None, act=None, x_scale=None, dtype=None, out=
     n = _linear_i8_bytes(M, N, K, xat & 15, ldx, xt, wat & 15, ldw)
 
     def call(st):
-        y = torch.empty((M, N), dtype=dtype, device=x.device) if out is None else out
-        ws, at = _q8_workspace(n, x.device)
+        y = x.new_empty((M, N), dtype=dtype) if out is None else out
+        ws, at = _q8_workspace(n, x)
         _check(_f_linear_i8(M, N, K, xat, ldx, xt, sx, wat, ldw, sw, b, ACTIVATIONS[act], yat or y.data_ptr(), ldy,
                             _CODES[dtype], at, n, st))
         return y
@@ -985,11 +985,10 @@ def linear_q8_backward(dy, x, x_scale, z=None, z_scale=None, z_group=0, act=None
     n = _q8_backward_bytes(M, N, K, bool(need_dw), bool(need_dbias))
 
     def call(st):
-        dev = dy.device
-        dz = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if need_dz else None
-        dw = torch.empty((N, K), dtype=grad_dtype, device=dev) if need_dw else None
-        dbias = torch.empty(N, dtype=torch.float32, device=dev) if need_dbias else None
-        ws, at = _q8_workspace(n, dev)
+        dz = dy.new_empty((M, N), dtype=torch.bfloat16) if need_dz else None
+        dw = dy.new_empty((N, K), dtype=grad_dtype) if need_dw else None
+        dbias = dy.new_empty(N, dtype=torch.float32) if need_dbias else None
+        ws, at = _q8_workspace(n, dy)
         _check(_f_linear_q8_backward(M, N, K, dyat, lddy, _CODES[dy.dtype], xat, ldx, sx, zat, ldz, sz, ldzs or 1,
                                      z_group if code else 0, code, _addr(dz), N, _addr(dw), K, _CODES[grad_dtype],
                                      _addr(dbias), at, n, st))

@@ -118,9 +118,13 @@ struct Scale8 {
     float s, inv;
     bool ok;
     __device__ __forceinline__ explicit Scale8(float top) {
+        // top / 127 rounded to nearest, from the rounded reciprocal of 127 and the exact
+        // rest (Markstein); below 2^-126 the result does not count
         ok = top < INFINITY;
-        s = fmaxf(top / 127.0f, kTiny);
-        inv = 1.0f / s;
+        constexpr float r = 1.0f / 127.0f;
+        const float q = top * r;
+        s = fmaxf(fmaf(fmaf(-127.0f, q, top), r, q), kTiny);
+        inv = __builtin_amdgcn_rcpf(s);
         if (!ok) {
             s = __builtin_nanf("");
             inv = 0.0f;
@@ -129,7 +133,7 @@ struct Scale8 {
 };
 
 // Eight values to integers, a byte each.  x * inv + 1.5 * 2^23 rounds to the
-// nearest integer n, whose low byte is the sum's; inv is 1 / s rounded, so n can
+// nearest integer n, whose low byte is the sum's; inv is 1 / s to a unit, so n can
 // be the neighbour of the nearest when x / s is next to a half.  The rest r = x -
 // n s is exact (a multiple of half a unit of s below 2^24 of them), so where 2 |r|
 // reaches s -- rarely, and a branch for the whole wave -- n is put right: away
@@ -258,39 +262,56 @@ struct Walk {
     }
 };
 
-// G lanes (4 .. 32) hold a group; a row's chunks are padded to whole groups.
+// G lanes (2 .. 16) hold a group, sixteen columns each; a row's chunks are padded to
+// whole groups.  Bound by the bytes and, half as much, by some 10 instructions an
+// element (8192 x 11008 bf16 in groups of 128: TODO us, TODO TB/s; eight columns a
+// lane, with a scale's divisions for each eight, took 70).
 template <bool F32, int G>
 __global__ __launch_bounds__(256) void quantize_group_kernel(QuantArgs a, int rows, int cpr) {
-    constexpr int U = 4;
+    constexpr int U = 2;
     const int64_t m0 = (int64_t)blockIdx.x * rows;
     const int rn = (int)std::min<int64_t>(rows, a.M - m0);
     Walk w(cpr);
     while (true) {
-        Raw8<F32> raw[U];
+        Raw8<F32> raw[U][2];
         int r[U], c[U];
         // (a thread that is past the end stays with its wave: the lanes of a group meet below)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             r[u] = w.r;
-            c[u] = w.c * 8;
+            c[u] = w.c * 16;
             w.next();
             const char* row = (const char*)a.x + (m0 + r[u]) * a.ldx * (F32 ? 4 : 2);
-            if (r[u] < rn && c[u] < a.K) raw[u].load(row, c[u], a.K - c[u]);
-            else raw[u].zero();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = c[u] + 8 * h;
+                if (r[u] < rn && k < a.K) raw[u][h].load(row, k, a.K - k);
+                else raw[u][h].zero();
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            uint32_t top = max4(raw[u].top());
+            uint32_t top = dpp_max<0xB1>(std::max(raw[u][0].top(), raw[u][1].top()));
+            if constexpr (G >= 4) top = dpp_max<0x4E>(top);
             if constexpr (G >= 8) top = dpp_max<0x141>(top);
             if constexpr (G >= 16) top = dpp_max<0x140>(top);
-            if constexpr (G >= 32) top = std::max(top, (uint32_t)__shfl_xor((int)top, 16));
             const Scale8 sc(Raw8<F32>::top_value(top));
-            float v[8];
-            raw[u].values(v);
-            const u32x2 q = to_i8(v, sc);
-            if (r[u] < rn) {
-                if (c[u] < a.K && c[u] % (G * 8) == 0) a.s[(m0 + r[u]) * a.lds + c[u] / (G * 8)] = sc.s;
-                store_i8(a.q + (m0 + r[u]) * a.ldq + c[u], q, a.K + a.pad - c[u]);
+            u32x2 q[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v[8];
+                raw[u][h].values(v);
+                q[h] = to_i8(v, sc);
+            }
+            const int n = a.K + a.pad - c[u];
+            if (r[u] >= rn || n <= 0) continue;
+            if (c[u] % (G * 16) == 0 && c[u] < a.K) a.s[(m0 + r[u]) * a.lds + c[u] / (G * 16)] = sc.s;
+            int8_t* d = a.q + (m0 + r[u]) * a.ldq + c[u];
+            if (n >= 16) {
+                *(u32x4a1*)d = u32x4{q[0][0], q[0][1], q[1][0], q[1][1]};
+            } else {
+                store_i8(d, q[0], n);
+                store_i8(d + 8, q[1], n - 8);
             }
         }
         if (__ballot(w.r < rn) == 0) break;
@@ -571,6 +592,21 @@ __global__ __launch_bounds__(T::NT, 2) void i8_tile_kernel(I8Args a) {
     i8_tile<T, ACT>(a, tm * T::BM, tn * T::BN, split, (lds_t*)raw, edge, wave, lane);
 }
 
+// Up to four consecutive values of C.
+__device__ __forceinline__ void store4(const I8Args& a, int64_t at, f32x4 v, int n) {
+    if (n >= 4) {
+        if (a.bf16) *(u32x2a1*)((uint16_t*)a.C + at) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        else *(f32x4a4*)((float*)a.C + at) = v;
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < 3; ++r) {
+        if (r >= n) break;
+        if (a.bf16) ((uint16_t*)a.C)[at + r] = f32_to_bf16(v[r]);
+        else ((float*)a.C)[at + r] = v[r];
+    }
+}
+
 // Four columns a thread: the partial sums, joined exactly, and the epilogue.
 __global__ __launch_bounds__(256) void i8_finish_kernel(I8Args a) {
     const int quads = (a.N + 3) >> 2;
@@ -579,6 +615,14 @@ __global__ __launch_bounds__(256) void i8_finish_kernel(I8Args a) {
     const int n = (int)(i - m * quads) * 4;
     if (m >= a.M) return;
     const int* p = a.part + m * a.ldp + n;
+    const float sa = a.sa[m];
+    f32x4 sb, bias;   // (read with the sums, not after them)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int c = std::min(n + r, a.N - 1);
+        sb[r] = a.sb[c];
+        bias[r] = a.bias != nullptr ? a.bias[c] : 0.0f;
+    }
     i32x4 t = {0, 0, 0, 0};
     constexpr int U = 8;
     for (int s0 = 0; s0 < a.splits; s0 += U) {
@@ -588,20 +632,11 @@ __global__ __launch_bounds__(256) void i8_finish_kernel(I8Args a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) t += x[u];
     }
-    const float sa = a.sa[m];
     f32x4 v;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int c = std::min(n + r, a.N - 1);
-        v[r] = fmaf((float)t[r] * a.sb[c], sa, a.bias != nullptr ? a.bias[c] : 0.0f);
-    }
+    for (int r = 0; r < 4; ++r) v[r] = fmaf((float)t[r] * sb[r], sa, bias[r]);
     act_run<1>(a.act, &v);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        if (n + r >= a.N) break;
-        if (a.bf16) ((uint16_t*)a.C)[m * a.ldc + n + r] = f32_to_bf16(v[r]);
-        else ((float*)a.C)[m * a.ldc + n + r] = v[r];
-    }
+    store4(a, m * a.ldc + n, v, a.N - n);
 }
 
 // ---- few tokens ------------------------------------------------------------------------
@@ -666,6 +701,18 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
             for (int m = 0; m < FM; ++m) xb[i][m] = load_global<u32x4a1>(steps > 0 ? xp[m] + s * 64 : (const int8_t*)kZeros);
         }
     };
+    // (and the epilogue's operands: a fragment a wave, NF FM of them)
+    static_assert(NF * FM <= NW, "a fragment a wave");
+    const int ef = wave / FM, em = (wave - ef * FM) * 16 + s16, ec = ef * 16 + g * 4;
+    f32x4 sb, bias = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int n = n0 + std::min(ec + r, left - 1);
+        sb[r] = a.sb[n];
+        if (a.bias != nullptr) bias[r] = a.bias[n];
+    }
+    float sa = 0.0f;
+    if constexpr (UNITS == 0) sa = a.sa[std::min(em, M - 1)];
     const int last = std::max(s1 - 1, 0);   // (a wave without a step reads one of another's, unused)
 #pragma unroll
     for (int i = 0; i < D; ++i) load(i, std::min(s0 + i, last));
@@ -734,28 +781,16 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
 #pragma unroll
         for (int m = 0; m < FM; ++m) red[wave][f * FM + m][lane] = acc[f][m];
     __syncthreads();
-    for (int e = wave; e < NF * FM; e += NW) {
-        const int f = e / FM, m = (e - f * FM) * 16 + s16, c = f * 16 + g * 4;
-        i32x4 t = red[0][e][lane];
+    if (wave >= NF * FM || em >= M || ec >= left) return;
+    i32x4 t = red[0][wave][lane];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) t += red[w][e][lane];
-        if (m >= M || c >= left) continue;
-        const float sa = UNITS > 0 ? sx[m] : a.sa[m];
-        f32x4 v;
+    for (int w = 1; w < NW; ++w) t += red[w][wave][lane];
+    if constexpr (UNITS > 0) sa = sx[em];
+    f32x4 v;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int n = n0 + std::min(c + r, left - 1);
-            v[r] = fmaf((float)t[r] * a.sb[n], sa, a.bias != nullptr ? a.bias[n] : 0.0f);
-        }
-        act_run<1>(a.act, &v);
-        const int64_t at = m * a.ldc + n0 + c;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if (c + r >= left) break;
-            if (a.bf16) ((uint16_t*)a.C)[at + r] = f32_to_bf16(v[r]);
-            else ((float*)a.C)[at + r] = v[r];
-        }
-    }
+    for (int r = 0; r < 4; ++r) v[r] = fmaf((float)t[r] * sb[r], sa, bias[r]);
+    act_run<1>(a.act, &v);
+    store4(a, (int64_t)em * a.ldc + n0 + ec, v, left - ec);
 }
 
 // ---- backward -----------------------------------------------------------------------
@@ -856,12 +891,28 @@ __global__ __launch_bounds__(T::NT, 2) void q8_product_kernel(Q8GradArgs a) {
     B.init(a.xb + (int64_t)s0 * 64 * a.Kp + k0, a.Kp, a.Kp - k0, steps, s0 + steps == all ? (int)(a.M & 63) : 0, wave, lane);
     Acc<T> acc;
     main_loop<T>(A, B, steps, smem, wave, lane, acc);
+    const Place<T> at(wave, lane);
+    if (a.splits == 1 && !a.dw_f32) {
+#pragma unroll
+        for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                    for (int j = 0; j < T::FN; ++j) {
+                        const f32x4 v = acc[ha][hb][i][j];
+                        *(u32x2 __attribute__((address_space(3)))*)(smem + at.row(ha, i) * staged_ld<T> + at.col(hb, j) * 2) =
+                            u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                    }
+        store_rows16<T>((uint16_t*)a.dw + (int64_t)n0 * a.lddw + k0, a.lddw, a.N - n0, a.K - k0, smem, wave * 64 + lane);
+        return;
+    }
     if (a.splits == 1) {
-        store_tile<T>(acc, 1.0f, a.dw, a.dw_f32, a.lddw, k0, a.N - n0, a.K - k0, smem, wave, lane,
+        store_tile<T>(acc, 1.0f, a.dw, true, a.lddw, k0, a.N - n0, a.K - k0, smem, wave, lane,
                       [&](int r) { return (int64_t)n0 + r; });
         return;
     }
-    const Place<T> at(wave, lane);
     float* P = a.part + ((int64_t)split * a.N + n0) * a.Kp + k0;
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha)
@@ -950,8 +1001,13 @@ hipError_t by_act(int act, F&& f) {
 }
 int log2i(int v) { return 31 - __builtin_clz((unsigned)v); }
 
-// Rows of a workgroup that walks chunks: about 1024 of them.
-int walk_rows(int64_t M, int cpr) { return (int)std::max<int64_t>(1, std::min<int64_t>(M, 1024 / cpr)); }
+// Rows of a workgroup that walks chunks: about 1024 of them, fewer (to 256) until
+// there are two workgroups a CU (509 x 770 binary32 in groups of 64: 6.1 us with
+// 1024, TODO so).
+int walk_rows(int64_t M, int cpr) {
+    const int64_t chunks = std::min<int64_t>(1024, std::max<int64_t>(256, M * cpr / 512));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(M, chunks / cpr));
+}
 
 template <bool F32>
 hipError_t quantize(const QuantArgs& a, hipStream_t st) {
@@ -966,13 +1022,13 @@ hipError_t quantize(const QuantArgs& a, hipStream_t st) {
         if (K <= 16384) return launch_kernel(quantize_row_kernel<F32, 256, 8, false>, wgs, b, st, a);
         return launch_kernel(quantize_row_kernel<F32, 256, 4, true>, wgs, b, st, a);
     }
-    const int cpr = (int)up(a.K, a.group) * (a.group / 8), rows = walk_rows(a.M, cpr);
+    const int cpr = (int)up(a.K, a.group) * (a.group / 16), rows = walk_rows(a.M, cpr);
     const dim3 grid((unsigned)up(a.M, rows)), b(256);
     switch (a.group) {
-        case 32: return launch_kernel(quantize_group_kernel<F32, 4>, grid, b, st, a, rows, cpr);
-        case 64: return launch_kernel(quantize_group_kernel<F32, 8>, grid, b, st, a, rows, cpr);
-        case 128: return launch_kernel(quantize_group_kernel<F32, 16>, grid, b, st, a, rows, cpr);
-        default: return launch_kernel(quantize_group_kernel<F32, 32>, grid, b, st, a, rows, cpr);
+        case 32: return launch_kernel(quantize_group_kernel<F32, 2>, grid, b, st, a, rows, cpr);
+        case 64: return launch_kernel(quantize_group_kernel<F32, 4>, grid, b, st, a, rows, cpr);
+        case 128: return launch_kernel(quantize_group_kernel<F32, 8>, grid, b, st, a, rows, cpr);
+        default: return launch_kernel(quantize_group_kernel<F32, 16>, grid, b, st, a, rows, cpr);
     }
 }
 

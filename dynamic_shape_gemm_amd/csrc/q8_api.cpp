@@ -98,44 +98,55 @@ struct LinearLayout {
     size_t a = 0, s = 0, b = 0, part = 0, bytes = 0;
 };
 
-// The product's time in us on tiles of one size, K in `splits` parts.  `fit`
+// What a product takes, in us, on tiles of one size: a launch's start, a
+// workgroup's ends and one of its steps (128 bytes of an operand's row); `fit`
 // workgroups share a CU, and what a CU does in a step takes as long however many
-// of them it is divided over; the busiest CU's steps and ends count.
-double product_us(int64_t M, int64_t N, int64_t steps, int tile, int64_t splits) {
-    struct Tile {
-        double start, end, step;   // of a launch; of a workgroup; of 128 features of one
-        int64_t fit;
-    };
-    const Tile t = tile == 256 ? Tile{0.0, 10.4, 0.88, 1} : tile == 128 ? Tile{0.3, 5.7, 0.51, 2} : Tile{2.5, 2.1, 0.24, 4};
-    const int64_t per = ceil_div(steps, splits), busiest = ceil_div(ceil_div(M, tile) * ceil_div(N, tile) * splits, 256);
-    double us = t.start + (double)per * t.step * (double)busiest + t.end * (double)ceil_div(busiest, t.fit);
-    if (splits > 1)   // and the partial sums' launch, with what a launch costs its caller
-        us += 3.0 + std::max(4.0, 2.1 + 1e-6 * (double)(M * N) * (0.71 + 0.59 * (double)splits));
-    return us;
-}
+// of them it is divided over, so the busiest CU's steps and ends count.
+struct TileCost {
+    int tile;
+    double start, end, step;
+    unsigned fit;   // a power of two
+};
 
-// The tile and the parts of K that cost least.  Fitted to 3060 measurements of 200
-// extents (33 to 8192 x 128 to 12544 x 128 to 12544): the choice is 1.2 % behind the
-// fastest in the mean, 20 % at most.  One tile for all: 256 loses 9.3 us to 64's 4.1
-// at 109 x 887 x 144, 64 loses 563 to 256's 300 at 8192 x 11008 x 4096.  No splits:
-// 105 x 1024 x 12544 takes 36 us on the 64 tile, in eight parts 8.3 + 4.0.
-void choose_tile(int64_t M, int64_t N, int64_t K, int& tile, int& splits) {
-    const int64_t steps = std::max<int64_t>(1, ceil_div(K, 128));
+// The tile, and the parts of the sum, that cost least; `joined` is what several
+// parts cost on top.
+template <size_t n, class F>
+void choose_tile(const TileCost (&tiles)[n], int64_t rows, int64_t cols, int64_t depth, int& tile, int& splits, F&& joined) {
+    const uint32_t steps = (uint32_t)std::max<int64_t>(depth, 1);
     double best = INFINITY;
-    for (const int t : {256, 128, 64}) {
-        if (ceil_div(M, t) * ceil_div(N, t) > (int64_t(1) << 22) && t < 256) break;   // (what a launch can count)
-        for (const int64_t want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
-            if (want > steps) break;
-            const int64_t s = ceil_div(steps, ceil_div(steps, want));
-            const double us = product_us(M, N, steps, t, s);
+    for (const TileCost& t : tiles) {
+        const int64_t count = ceil_div(rows, t.tile) * ceil_div(cols, t.tile);
+        if (t.tile < 256 && count > (int64_t(1) << 22)) break;   // (launch limits)
+        for (const uint32_t want : {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 20, 24, 28, 32}) {
+            if (want > steps || (want > 1 && count * want > 8 * 256)) break;
+            const uint32_t per = (steps + want - 1) / want, s = (steps + per - 1) / per;
+            const int64_t busiest = (count * s + 255) >> 8;
+            const double us = t.start + (double)per * t.step * (double)busiest + t.end * (double)((busiest + (int64_t)t.fit - 1) / (int64_t)t.fit) +
+                              (s > 1 ? joined((double)s) : 0.0);
             if (us < best) {
                 best = us;
-                tile = t;
+                tile = t.tile;
                 splits = (int)s;
             }
         }
     }
 }
+
+// linear_i8's.  Fitted to measurements of 200 extents (33 to 8192 x 128 to 12544 x 128
+// to 12544): the choice is 0.7 % behind the fastest in the mean, 15 % at most.  One tile for all: 256 loses 9.3 us to 64's 4.1 at 109 x 887 x 144, 64 loses
+// 563 to 256's 300 at 8192 x 11008 x 4096.  No splits: 105 x 1024 x 12544 takes 36
+// us on the 64 tile, in eight parts 8.3 + 4.0.  (3 us of host time for the launch
+// that joins the parts.)
+constexpr TileCost kI8Tiles[] = {{256, 0.0, 10.3, 1.34, 1}, {128, 1.3, 4.4, 0.52, 2}, {64, 1.4, 1.8, 0.24, 4}};
+double i8_joined(double mn, double splits) { return 3.0 + std::max(2.9, 0.5 + 1e-6 * mn * (1.0 + 0.82 * splits)); }
+
+// linear_q8_backward's dW.  Fitted to measurements of 100 extents (32 to 8192 x 128 to
+// 12544 x 128 to 12544): 0.8 % behind the fastest in the mean, 15 % at most.
+// One tile for all: 256 loses 14.3 us to 128's 7.4 at 333 x 768 x 768, 128 loses 869
+// to 583 at 8192 x 11008 x 4096.  No splits: 8192 x 768 x 768 takes 66 us on the 128
+// tile, in six parts 17.4 + 4.0.
+constexpr TileCost kGradTiles[] = {{256, 0.1, 10.4, 1.18, 1}, {128, 3.1, 5.0, 0.44, 2}};
+double grad_joined(double nk, double splits) { return std::max(3.1, 4.4 + 1e-6 * nk * (0.65 + 0.51 * splits)); }
 
 LinearLayout linear_layout(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, int x_type, const void* W,
                            int64_t ldw) {
@@ -155,7 +166,7 @@ LinearLayout linear_layout(int64_t M, int64_t N, int64_t K, const void* X, int64
     l.pack_b = !aligned16(W) || ldw % 16 != 0;
     l.Ka = round_up(K, 16);
     l.Kb = round_up(K, 16);
-    choose_tile(M, N, K, l.tile, l.splits);
+    choose_tile(kI8Tiles, M, N, ceil_div(K, 128), l.tile, l.splits, [&](double s) { return i8_joined((double)(M * N), s); });
     l.ldp = round_up(N, 4);
     size_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -263,10 +274,9 @@ GradLayout grad_layout(int64_t M, int64_t N, int64_t K, bool dw, bool dbias) {
     l.Mr = round_up(M, 64);
     l.Np = round_up(N, 8);
     l.Kp = round_up(K, 8);
-    l.tile = ceil_div(N, 256) * ceil_div(K, 256) >= 128 ? 256 : 128;
-    const int64_t slots = l.tile == 256 ? 256 : 512, tiles = ceil_div(N, l.tile) * ceil_div(K, l.tile), steps = l.Mr / 64;
-    const int64_t want = std::max<int64_t>(1, std::min(slots / std::max<int64_t>(tiles, 1), steps / 4));
-    l.splits = (int)std::max<int64_t>(1, ceil_div(steps, std::max<int64_t>(1, ceil_div(steps, want))));
+    // (dW's bits are the same whatever else is asked for: the launch that joins its
+    // parts, there for dbias anyway, counts as half of one)
+    choose_tile(kGradTiles, N, K, l.Mr / 64, l.tile, l.splits, [&](double s) { return grad_joined((double)(N * K), s); });
     size_t at = 0;
     auto take = [&](int64_t bytes) {
         const size_t here = at;
