@@ -142,6 +142,12 @@ try:
     from . import _mkpfast as _fast
 except ImportError:
     _fast = None
+# The 8-bit helpers' common case in C++ against torch; the helpers' own Python
+# where it is absent, and for everything it leaves to them.
+try:
+    from . import _mkptorch as _direct
+except ImportError:
+    _direct = None
 _f_gemm = _fast.gemm if _fast else _lib.mkp_gemm
 _f_gemm_bt = _fast.gemm_bt if _fast else _lib.mkp_gemm_bt
 _f_gemm_batched = _fast.gemm_batched if _fast else _lib.mkp_gemm_batched
@@ -860,6 +866,10 @@ def quantize_rows(x, group=0, stream=None):
     infinity or NaN has scale NaN and q 0.  linear_i8 takes (q, scale) of group 0
     as its weight (one scale a channel) and as its input.  q's rows take whole
     16-byte units, as linear_i8 reads them without a copy."""
+    if stream is None and _direct is not None:
+        out = _direct.quantize_rows(x, group)
+        if out is not None:
+            return out
     if x.dim() != 2:
         raise ValueError("x must be (M, K)")
     M, K = x.shape
@@ -882,6 +892,10 @@ def dequantize_rows(q, scale, group=0, dtype=None, stream=None):
     dtype = dtype or torch.bfloat16
     if dtype not in _REAL:
         raise TypeError("dtype must be bfloat16 or float32")
+    if stream is None and _direct is not None:
+        y = _direct.dequantize_rows(q, scale, group, _CODES[dtype])
+        if y is not None:
+            return y
     if q.dim() != 2:
         raise ValueError("q must be (M, K)")
     M, K = q.shape
@@ -918,6 +932,11 @@ def linear_i8(x, w, w_scale, bias=None, act=None, x_scale=None, dtype=None, out=
     comes with its x_scale (M,).  bias (N,) fp32 or None, act
     None/"relu"/"gelu"/"gelu_tanh"/"silu".  Returns (or fills) out (M,N) in dtype
     float32 (the default) or bfloat16, without a grad_fn."""
+    if stream is None and out is None and _direct is not None:
+        y = _direct.linear_i8(x, w, w_scale, bias, ACTIVATIONS.get(act, -1), x_scale,
+                              MKP_F32 if dtype is None else _CODES.get(dtype, -1))
+        if y is not None:
+            return y
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
         raise ValueError("x must be (M, K) and w (N, K)")
     if act not in ACTIVATIONS:
@@ -961,6 +980,12 @@ def linear_q8_backward(dy, x, x_scale, z=None, z_scale=None, z_group=0, act=None
     columns).  Returns (dz, dw, dbias): dz = dy act'(z) bf16 (dw's and dx's
     operand; dx is gemm(dz, w)), dw = dz^T x in grad_dtype (bfloat16, the default,
     or float32), dbias fp32; None for those not needed.  No grad_fn."""
+    if stream is None and _direct is not None:
+        out = _direct.linear_q8_backward(dy, x, x_scale, z, z_scale, z_group, ACTIVATIONS.get(act, -1), bool(need_dz),
+                                         bool(need_dw), bool(need_dbias),
+                                         MKP_BF16 if grad_dtype is None else _CODES.get(grad_dtype, -1))
+        if out is not None:
+            return out
     if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
         raise ValueError("dy must be (M, N) and x (M, K)")
     if act not in ACTIVATIONS:

@@ -95,6 +95,7 @@ def build_library(verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         jobs.append((src, obj, cmd, subprocess.Popen(cmd, stderr=subprocess.PIPE, text=True)))
+    torch_job = start_torch_binding(obj_dir, verbose)
     usage, objs, failed = {}, [], None
     for src, obj, cmd, proc in jobs:
         _, err = proc.communicate()
@@ -107,6 +108,8 @@ def build_library(verbose: bool = False) -> str:
         if proc.returncode != 0 and failed is None:
             failed = subprocess.CalledProcessError(proc.returncode, cmd)
         objs.append(obj)
+    if torch_job is not None:
+        torch_job.wait()
     if failed is not None:
         raise failed
     with open(RESOURCE_REPORT, "w") as f:
@@ -131,6 +134,7 @@ def build_library(verbose: bool = False) -> str:
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
     build_fast_binding(verbose)
+    link_torch_binding(obj_dir, torch_job, verbose)
     return LIB
 
 
@@ -149,6 +153,51 @@ def build_fast_binding(verbose: bool = False) -> str:
     subprocess.run(cmd, check=True)
     os.replace(tmp, FAST)
     return FAST
+
+
+DIRECT = os.path.join(HERE, "_mkptorch" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
+def torch_dir():
+    """Where the installed torch lies, or None."""
+    import importlib.util
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+
+
+def start_torch_binding(obj_dir: str, verbose: bool = False):
+    """Starts compiling the C++ form of the 8-bit helpers (host code against
+    torch's headers); None without torch."""
+    where = torch_dir()
+    if where is None:
+        return None
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           "-isystem", os.path.join(where, "include"), "-isystem", os.path.join(where, "include/torch/csrc/api/include"),
+           "-isystem", os.path.join(rocm, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(ROOT, "include"), "-c", os.path.join(CSRC, "mkptorch.cpp"),
+           "-o", os.path.join(obj_dir, "mkptorch.o")]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.Popen(cmd)
+
+
+def link_torch_binding(obj_dir: str, job, verbose: bool = False) -> None:
+    """Links it against libmkp.so next to it; torch's libraries are the ones that
+    the process has loaded by then."""
+    if job is None:
+        if os.path.exists(DIRECT):
+            os.remove(DIRECT)   # (built against a torch that is gone)
+        return
+    if job.returncode != 0:
+        raise subprocess.CalledProcessError(job.returncode, job.args)
+    tmp = DIRECT + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-fPIC", os.path.join(obj_dir, "mkptorch.o"), "-o", tmp, "-L", HERE, "-lmkp",
+           "-L", os.path.join(torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, DIRECT)
 
 
 if __name__ == "__main__":

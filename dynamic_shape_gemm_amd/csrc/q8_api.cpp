@@ -148,6 +148,25 @@ double i8_joined(double mn, double splits) { return 3.0 + std::max(2.9, 0.5 + 1e
 constexpr TileCost kGradTiles[] = {{256, 0.1, 10.4, 1.18, 1}, {128, 3.1, 5.0, 0.44, 2}};
 double grad_joined(double nk, double splits) { return std::max(3.1, 4.4 + 1e-6 * nk * (0.65 + 0.51 * splits)); }
 
+// choose() fills in tile and splits; a thread keeps its last choices by extents (the
+// call and its workspace's size ask for the same one, a model's layers for a few).
+template <int which, class F>
+void remembered(int64_t M, int64_t N, int64_t K, int& tile, int& splits, F&& choose) {
+    struct Entry {
+        int64_t M, N, K;
+        int tile, splits;
+    };
+    thread_local Entry table[64] = {};   // (tile 0: empty)
+    Entry& e = table[((uint64_t)M * 0x9E3779B97F4A7C15u ^ (uint64_t)N * 0xC2B2AE3D27D4EB4Fu ^ (uint64_t)K * 0x165667B19E3779F9u) >> 58];
+    if (e.tile == 0 || e.M != M || e.N != N || e.K != K) {
+        choose();
+        e = Entry{M, N, K, tile, splits};
+        return;
+    }
+    tile = e.tile;
+    splits = e.splits;
+}
+
 LinearLayout linear_layout(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, int x_type, const void* W,
                            int64_t ldw) {
     LinearLayout l;
@@ -166,7 +185,9 @@ LinearLayout linear_layout(int64_t M, int64_t N, int64_t K, const void* X, int64
     l.pack_b = !aligned16(W) || ldw % 16 != 0;
     l.Ka = round_up(K, 16);
     l.Kb = round_up(K, 16);
-    choose_tile(kI8Tiles, M, N, ceil_div(K, 128), l.tile, l.splits, [&](double s) { return i8_joined((double)(M * N), s); });
+    remembered<0>(M, N, K, l.tile, l.splits, [&] {
+        choose_tile(kI8Tiles, M, N, ceil_div(K, 128), l.tile, l.splits, [&](double s) { return i8_joined((double)(M * N), s); });
+    });
     l.ldp = round_up(N, 4);
     size_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -276,7 +297,9 @@ GradLayout grad_layout(int64_t M, int64_t N, int64_t K, bool dw, bool dbias) {
     l.Kp = round_up(K, 8);
     // (dW's bits are the same whatever else is asked for: the launch that joins its
     // parts, there for dbias anyway, counts as half of one)
-    choose_tile(kGradTiles, N, K, l.Mr / 64, l.tile, l.splits, [&](double s) { return grad_joined((double)(N * K), s); });
+    remembered<1>(M, N, K, l.tile, l.splits, [&] {
+        choose_tile(kGradTiles, N, K, l.Mr / 64, l.tile, l.splits, [&](double s) { return grad_joined((double)(N * K), s); });
+    });
     size_t at = 0;
     auto take = [&](int64_t bytes) {
         const size_t here = at;

@@ -556,3 +556,38 @@ def test_guarded_workspace(mkp):
         ref = oracle.backward(dy, x, xs, z, zs, 0, "relu", F32)
         within(dw, *ref["dw"], "guarded dw")
         within(db, *ref["dbias"], "guarded dbias")
+
+
+def test_helpers_own_way(mkp, monkeypatch):
+    """The helpers without their C++ form: the same bits, and the same refusals."""
+    with_it = [(name, [t.clone() for t in call(*inputs)]) for M in (1, 30, 300) for name, inputs, call in calls(mkp, M)]
+    assert mkp._direct is not None
+    x, w, ws, b = layer(gen(1), 4, 10, 64)
+    q, s = mkp.quantize_rows(x)
+    refused = [(TypeError, lambda: mkp.quantize_rows(x.half())), (ValueError, lambda: mkp.quantize_rows(x, group=48)),
+               (ValueError, lambda: mkp.quantize_rows(x.t())), (ValueError, lambda: mkp.quantize_rows(x.cpu())),
+               (ValueError, lambda: mkp.quantize_rows(x[0])), (mkp.MkpError, lambda: mkp.quantize_rows(x[:1].expand(4, 64))),
+               (TypeError, lambda: mkp.dequantize_rows(q, s, dtype=torch.int8)), (ValueError, lambda: mkp.dequantize_rows(q, s[:3])),
+               (ValueError, lambda: mkp.dequantize_rows(q, s, group=32)), (ValueError, lambda: mkp.linear_i8(x, w, ws[:9])),
+               (ValueError, lambda: mkp.linear_i8(x, w.cpu(), ws)), (TypeError, lambda: mkp.linear_i8(x, w, ws, b.double())),
+               (ValueError, lambda: mkp.linear_i8(x, w, ws, act="abs")), (TypeError, lambda: mkp.linear_i8(x, w, ws, x_scale=s)),
+               (TypeError, lambda: mkp.linear_i8(q, w, ws)), (TypeError, lambda: mkp.linear_i8(x, w, ws, dtype=torch.float16)),
+               (ValueError, lambda: mkp.linear_q8_backward(x, q, s, act="relu")),
+               (ValueError, lambda: mkp.linear_q8_backward(x, q, s, q, s, z_group=32, act="relu")),
+               (TypeError, lambda: mkp.linear_q8_backward(x, x, s)), (ValueError, lambda: mkp.linear_q8_backward(x, q[:3], s)),
+               (TypeError, lambda: mkp.linear_q8_backward(x, q, s, grad_dtype=torch.float16))]
+
+    def refuse():
+        for i, (kind, call) in enumerate(refused):
+            with pytest.raises(kind):
+                call()
+                raise AssertionError(f"call {i} was not refused")
+
+    refuse()
+    monkeypatch.setattr(mkp, "_direct", None)
+    refuse()
+    again = [(name, call(*inputs)) for M in (1, 30, 300) for name, inputs, call in calls(mkp, M)]
+    for (name, first), (_, second) in zip(with_it, again):
+        for o, r in zip(second, first):
+            same(o, r, name)
+            assert o.stride() == r.stride()
