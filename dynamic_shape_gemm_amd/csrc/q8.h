@@ -93,7 +93,7 @@ hipError_t launch_i8_product(const I8Args& a, hipStream_t st);
 hipError_t launch_i8_stream(const I8Args& a, hipStream_t st);     // at most kI8StreamRows tokens, rows of any alignment
 hipError_t launch_i8_finish(const I8Args& a, hipStream_t st);     // C from its partial sums
 hipError_t launch_q8_slopes(const Q8GradArgs& a, hipStream_t st);  // dz, a, xb, dbp
-hipError_t launch_q8_product(const Q8GradArgs& a, hipStream_t st); // dW, or its partials
-hipError_t launch_q8_finish(const Q8GradArgs& a, hipStream_t st);  // dW and dbias from their partials
+hipError_t launch_q8_product(const Q8GradArgs& a, hipStream_t st); // dW and dbias (one split), or dW's partials
+hipError_t launch_q8_finish(const Q8GradArgs& a, hipStream_t st);  // dW from its partials, and dbias
 
 }  // namespace mkp

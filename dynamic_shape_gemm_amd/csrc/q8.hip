@@ -874,14 +874,46 @@ __global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first,
     }
 }
 
-// A tile of dW = a^T . xb over one split of the rows.
+// dbias of 32 columns from its column sums, every NT / 32-th sum a thread, in a fixed
+// order whatever NT is: eight interleaved series of sums, then those.
+template <int NT>
+__device__ __forceinline__ void q8_dbias(const Q8GradArgs& a, int n0, float* red) {
+    const int c = threadIdx.x & 31, grp = threadIdx.x >> 5, n = n0 + c;
+    const int parts = (int)((a.M + a.sum_rows - 1) / a.sum_rows);
+    if (grp < 8) {
+        constexpr int U = 8;
+        float t = 0.0f;
+        for (int i0 = grp; i0 < parts; i0 += 8 * U) {
+            float x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                x[u] = i0 + 8 * u < parts && n < a.N ? a.dbp[(int64_t)(i0 + 8 * u) * a.Np + n] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) t += x[u];
+        }
+        red[grp * 32 + c] = t;
+    }
+    __syncthreads();
+    if (grp == 0 && n < a.N)
+        a.dbias[n] = ((red[c] + red[32 + c]) + (red[64 + c] + red[96 + c])) +
+                     ((red[128 + c] + red[160 + c]) + (red[192 + c] + red[224 + c]));
+}
+
+// A tile of dW = a^T . xb over one split of the rows.  The workgroups past the tiles
+// make dbias, which spares small calls a launch (unsplit ones: else the launch that
+// joins the partials does).
 template <class T>
 __global__ __launch_bounds__(T::NT, 2) void q8_product_kernel(Q8GradArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char raw[tile_lds<T>()];
     lds_t* smem = (lds_t*)raw;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int tm, tn, split;
-    if (!map_tile(blockIdx.x, (a.N + T::BM - 1) / T::BM, (a.K + T::BN - 1) / T::BN, tm, tn, split, a.splits)) return;
+    const int rows = (a.N + T::BM - 1) / T::BM, cols = (a.K + T::BN - 1) / T::BN;
+    if ((int)blockIdx.x >= rows * cols * a.splits) {
+        q8_dbias<T::NT>(a, (blockIdx.x - rows * cols * a.splits) * 32, (float*)raw);
+        return;
+    }
+    if (!map_tile(blockIdx.x, rows, cols, tm, tn, split, a.splits)) return;
     const int n0 = tm * T::BM, k0 = tn * T::BN;
     const int all = a.Mr >> 6, per = (all + a.splits - 1) / a.splits;
     const int s0 = std::min(split * per, all), steps = std::min(per, all - s0);
@@ -928,27 +960,11 @@ __global__ __launch_bounds__(T::NT, 2) void q8_product_kernel(Q8GradArgs a) {
         }
 }
 
-// dW from its partials, eight columns a thread; then dbias from its column sums,
-// 32 columns a workgroup, every eighth sum a thread.
+// dW from its partials, eight columns a thread; then dbias.
 __global__ __launch_bounds__(256) void q8_finish_kernel(Q8GradArgs a, int first) {
-    __shared__ float red[8][32];
+    __shared__ float red[256];
     if ((int)blockIdx.x >= first) {
-        const int c = threadIdx.x & 31, grp = threadIdx.x >> 5, n = (blockIdx.x - first) * 32 + c;
-        const int parts = (int)((a.M + a.sum_rows - 1) / a.sum_rows);
-        constexpr int U = 8;
-        float t = 0.0f;
-        for (int i0 = grp; i0 < parts; i0 += 8 * U) {
-            float x[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                x[u] = i0 + 8 * u < parts && n < a.N ? a.dbp[(int64_t)(i0 + 8 * u) * a.Np + n] : 0.0f;
-#pragma unroll
-            for (int u = 0; u < U; ++u) t += x[u];
-        }
-        red[grp][c] = t;
-        __syncthreads();
-        if (grp == 0 && n < a.N)
-            a.dbias[n] = ((red[0][c] + red[1][c]) + (red[2][c] + red[3][c])) + ((red[4][c] + red[5][c]) + (red[6][c] + red[7][c]));
+        q8_dbias<256>(a, (blockIdx.x - first) * 32, red);
         return;
     }
     const int cpr = a.Kp >> 3;
@@ -1104,7 +1120,7 @@ hipError_t launch_q8_slopes(const Q8GradArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_q8_product(const Q8GradArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)(up(a.N, a.tile) * up(a.K, a.tile) * a.splits));
+    const dim3 grid((unsigned)(up(a.N, a.tile) * up(a.K, a.tile) * a.splits + (a.dbias != nullptr && a.splits == 1 ? up(a.N, 32) : 0)));
     return a.tile == 256 ? launch_kernel(q8_product_kernel<G256>, grid, dim3(G256::NT), st, a)
                          : launch_kernel(q8_product_kernel<G128>, grid, dim3(G128::NT), st, a);
 }

@@ -348,7 +348,7 @@ int backward(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, int 
     const int64_t slopes = ceil_div(l.Mr, l.sum_rows) * ceil_div(l.Np, 512) + ceil_div(M, 4);
     const int64_t tiles = dW ? ceil_div(N, l.tile) * ceil_div(K, l.tile) * l.splits : 0;
     const int64_t joined = dW && l.splits > 1 ? N * (l.Kp / 8) : 0;
-    if (std::max(slopes * 256, std::max(tiles * 512, joined + 8 * N + 1024)) > (int64_t)UINT32_MAX)
+    if (std::max(slopes * 256, std::max(tiles * 512 + 16 * N + 1024, joined + 8 * N + 1024)) > (int64_t)UINT32_MAX)
         return report(MKP_ERR_UNSUPPORTED, "grid too large");
     if (M == 0 && !dW && !dbias) return MKP_OK;
     begin_call();
@@ -391,13 +391,13 @@ int backward(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, int 
         MKP_TRY(go(st, QL_SLOPES, 4.0 * m * n,
                    (size_of(dy_type) + (sloped ? 1.0 : 0.0) + (dZ ? 2.0 : 0.0) + (dW ? 2.0 : 0.0)) * m * n + (dW ? 3.0 * m * k : 0.0),
                    [&] { return launch_q8_slopes(a, st); }));
-    const double parts = 4.0 * n * k * (double)l.splits;
+    const double parts = 4.0 * n * k * (double)l.splits, sums = dbias ? 4.0 * n * (double)ceil_div(M, l.sum_rows) : 0.0;
     if (dW)
-        MKP_TRY(go(st, QL_Q8_PRODUCT, 2.0 * m * n * k, 2.0 * m * (n + k) + (l.splits > 1 ? parts : wb * n * k),
+        MKP_TRY(go(st, QL_Q8_PRODUCT, 2.0 * m * n * k, 2.0 * m * (n + k) + (l.splits > 1 ? parts : wb * n * k + sums),
                    [&] { return launch_q8_product(a, st); }));
-    if (!dbias && !(dW && l.splits > 1)) return MKP_OK;
+    if (dW ? l.splits == 1 : !dbias) return MKP_OK;
     return go(st, QL_Q8_FINISH, 0.0,
-              (dW && l.splits > 1 ? parts + wb * n * k : 0.0) + (dbias ? 4.0 * n * (double)ceil_div(M, l.sum_rows) : 0.0),
+              (dW ? parts + wb * n * k : 0.0) + sums,
               [&] { return launch_q8_finish(a, st); });
 }
 
