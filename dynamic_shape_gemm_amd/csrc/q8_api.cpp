@@ -99,13 +99,14 @@ struct LinearLayout {
 };
 
 // What a product takes, in us, on tiles of one size: a launch's start, a
-// workgroup's ends and one of its steps (128 bytes of an operand's row); `fit`
-// workgroups share a CU, and what a CU does in a step takes as long however many
-// of them it is divided over, so the busiest CU's steps and ends count.
+// workgroup's ends, and one of its steps (128 bytes of an operand's row) where n
+// workgroups share a CU: n `step`, at least `alone`; `fit` of them do.  The busiest
+// CU counts.  (The constants are those whose choices lose least, not each one a time
+// of its own.)
 struct TileCost {
     int tile;
-    double start, end, step;
-    unsigned fit;   // a power of two
+    double start, end, step, alone;
+    int64_t fit;
 };
 
 // The tile, and the parts of the sum, that cost least; `joined` is what several
@@ -120,9 +121,10 @@ void choose_tile(const TileCost (&tiles)[n], int64_t rows, int64_t cols, int64_t
         for (const uint32_t want : {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 20, 24, 28, 32}) {
             if (want > steps || (want > 1 && count * want > 8 * 256)) break;
             const uint32_t per = (steps + want - 1) / want, s = (steps + per - 1) / per;
-            const int64_t busiest = (count * s + 255) >> 8;
-            const double us = t.start + (double)per * t.step * (double)busiest + t.end * (double)((busiest + (int64_t)t.fit - 1) / (int64_t)t.fit) +
-                              (s > 1 ? joined((double)s) : 0.0);
+            const int64_t busiest = (count * s + 255) >> 8, full = busiest / t.fit, rest = busiest - full * t.fit;
+            const double step = (double)full * std::max(t.alone, (double)t.fit * t.step) +
+                                (rest > 0 ? std::max(t.alone, (double)rest * t.step) : 0.0);
+            const double us = t.start + (double)per * step + t.end * (double)(full + (rest > 0)) + (s > 1 ? joined((double)s) : 0.0);
             if (us < best) {
                 best = us;
                 tile = t.tile;
@@ -133,20 +135,26 @@ void choose_tile(const TileCost (&tiles)[n], int64_t rows, int64_t cols, int64_t
 }
 
 // linear_i8's.  Fitted to measurements of 200 extents (33 to 8192 x 128 to 12544 x 128
-// to 12544): the choice is 0.7 % behind the fastest in the mean, 15 % at most.  One tile for all: 256 loses 9.3 us to 64's 4.1 at 109 x 887 x 144, 64 loses
-// 563 to 256's 300 at 8192 x 11008 x 4096.  No splits: 105 x 1024 x 12544 takes 36
-// us on the 64 tile, in eight parts 8.3 + 4.0.  (3 us of host time for the launch
-// that joins the parts.)
-constexpr TileCost kI8Tiles[] = {{256, 0.0, 10.3, 1.34, 1}, {128, 1.3, 4.4, 0.52, 2}, {64, 1.4, 1.8, 0.24, 4}};
-double i8_joined(double mn, double splits) { return 3.0 + std::max(2.9, 0.5 + 1e-6 * mn * (1.0 + 0.82 * splits)); }
+// to 12544): the choice is 0.6 % behind the fastest in the mean, 14 % at most.  One
+// tile for all: 256 loses 7.5 us to 64's 4.1 at 109 x 887 x 144, 64 loses 563 to
+// 256's 300 at 8192 x 11008 x 4096.  No splits: 105 x 1024 x 12544 takes 36 us on the
+// 64 tile, in eight parts 8.3 + 4.0.  (Parts are written and read, and joined by a
+// launch that costs the caller 3 us.)
+constexpr TileCost kI8Tiles[] = {
+    {256, 0.1, 7.4, 1.2, 1.2, 1}, {128, 2.3, 4.0, 0.5, 0.5, 2}, {64, 1.9, 1.5, 0.28, 0.29, 4}};
+double i8_joined(double mn, double splits) {
+    return 0.8e-6 * mn * splits + 3.0 + std::max(4.0, 2.1 + 1e-6 * mn * (0.71 + 0.59 * splits));
+}
 
 // linear_q8_backward's dW.  Fitted to measurements of 100 extents (32 to 8192 x 128 to
-// 12544 x 128 to 12544): 0.8 % behind the fastest in the mean, 15 % at most.
-// One tile for all: 256 loses 14.3 us to 128's 7.4 at 333 x 768 x 768, 128 loses 869
-// to 583 at 8192 x 11008 x 4096.  No splits: 8192 x 768 x 768 takes 66 us on the 128
-// tile, in six parts 17.4 + 4.0.
-constexpr TileCost kGradTiles[] = {{256, 0.1, 10.4, 1.18, 1}, {128, 3.1, 5.0, 0.44, 2}};
-double grad_joined(double nk, double splits) { return std::max(3.1, 4.4 + 1e-6 * nk * (0.65 + 0.51 * splits)); }
+// 12544 x 128 to 12544): 0.7 % behind the fastest in the mean, 15 % at most.  One tile
+// for all: 256 loses 14.3 us to 128's 7.4 at 333 x 768 x 768, 128 loses 869 to 583 at
+// 8192 x 11008 x 4096.  No splits: 8192 x 768 x 768 takes 71 us on the 128 tile, in six
+// parts 17.4 + 4.0.
+constexpr TileCost kGradTiles[] = {{256, 0.9, 11.0, 0.65, 0.65, 1}, {128, 2.6, 4.9, 0.335, 0.43, 2}};
+double grad_joined(double nk, double splits) {
+    return 0.8e-6 * nk * splits + std::max(4.1, 1e-6 * nk * (0.28 + 0.67 * splits));
+}
 
 // choose() fills in tile and splits; a thread keeps its last choices by extents (the
 // call and its workspace's size ask for the same one, a model's layers for a few).
