@@ -120,7 +120,7 @@ def build_library(verbose: bool = False) -> str:
     # a GEMM micro-kernel or a fused product's tile that spills to scratch has
     # lost its register tiling; refuse to ship it
     tiles = ("gemm_tile_kernel", "gemm_dual_kernel", "loss_forward_kernel", "loss_grad_kernel",
-             "loss_products_kernel", "loss_stream_kernel", "i8_tile_kernel", "q8_product_kernel")
+             "loss_products_kernel", "loss_stream_kernel", "i8_tile_kernel", "i8_stream_kernel", "q8_product_kernel")
     spills = [k for k, u in usage.items() if any(t in k for t in tiles) and u.get("scratch", 0) > 0]
     if spills:
         raise RuntimeError("tile kernels use scratch memory: " + ", ".join(spills))

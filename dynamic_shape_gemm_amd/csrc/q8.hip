@@ -34,6 +34,11 @@ __device__ __forceinline__ V load_global(const void* p) {
     return *(const V __attribute__((address_space(1)))*)p;
 }
 
+template <class V>
+__device__ __forceinline__ V load_once(const void* p) {
+    return __builtin_nontemporal_load((const V __attribute__((address_space(1)))*)p);
+}
+
 constexpr float kTiny = 1.17549435e-38f;   // 2^-126
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
@@ -648,10 +653,32 @@ __device__ __forceinline__ u32x4 load16(const int8_t* p, int n) {
     return u32x4{lo[0], lo[1], hi[0], hi[1]};
 }
 
+// a (rows 0-7 in lanes of low s, and their second 64 bytes in those of high s) and b
+// (rows 8-15 likewise) into rows 0-15 of the first and of the second 64 bytes.
+__device__ __forceinline__ void exchange(u32x4 a, u32x4 b, u32x4 (&out)[2]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int x = (int)a[i], y = (int)b[i];
+        out[0][i] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, 0x128, 0xf, 0xc, false);   // (lanes rotated by 8 of 16)
+        out[1][i] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, 0x128, 0xf, 0x3, false);
+    }
+}
+
 // At most 16 FM tokens: the weight streams past them, through registers.  A
 // workgroup takes a run of output channels, in NF fragments of 16, and its eight
-// waves a part of the features each (64 at a step), so every byte of W is read
+// waves a part of the features each (128 at a step), so every byte of W is read
 // once, by one lane, D steps ahead of its use; the waves' sums meet in LDS.
+//
+// A load takes whole lines, 128 bytes of each of eight rows: lane 16 g + s row s % 8,
+// bytes 16 (g + 4 (s / 8)).  Two of them, of a fragment's first and last eight rows,
+// make the two multiplications' operands (row s, bytes 16 g and 64 + 16 g) by
+// exchanging halves of every 16 lanes.  (As the multiplication wants them, 64 bytes of
+// each of 16 rows a load: 32 x 4096 x 11008 21.8 us, 17.0 so; 24 x 11008 x 4096 14.7,
+// 12.9.)  W's loads are marked as read once: nothing of it stays in the caches for
+// the next layers' (cold, 1 x 32000 x 4096 29.6 us without, 25.9 so, 5.1 TB/s; 1 x 11008
+// x 4096 11.8, 10.5, 4.3 TB/s of a launch that takes 2.5 by itself; a weight that the
+// last-level cache still holds: 9.7, 9.5).  Two steps ahead: four took 31.6 and 12.3,
+// the requests in the other's way; one 9.2 us against 7.1 at 1 x 1024 x 12544.
 //
 // UNITS > 0: X is bf16 or binary32 and quantised here, by every workgroup for
 // itself, into LDS, while the weight's first loads are on their way.  A wave
@@ -659,8 +686,8 @@ __device__ __forceinline__ u32x4 load16(const int8_t* p, int n) {
 // maximum and their integers.
 template <int FM, int NF, int UNITS, bool F32>
 __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
-    constexpr int NW = 8, D = 8;
-    // [M][K to 64, and 16]: at most 8 UNITS runs of 512
+    constexpr int NW = 8, D = 2;
+    // [M][K to 128, and 16]: at most 8 UNITS runs of 512
     __shared__ __attribute__((aligned(16))) unsigned char xq[UNITS > 0 ? 4096 * UNITS + 256 * FM : 16];
     __shared__ i32x4 red[NW][NF * FM][64];
     __shared__ uint32_t tops[16 * FM];
@@ -668,9 +695,10 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, s16 = lane & 15, M = (int)a.M;
     const int n0 = blockIdx.x * cols, left = std::min(cols, a.N - n0);
-    const int steps = a.K >> 6, tail = a.K & 63;   // (a last step that is not full is one wave's, at the end)
+    const int steps = a.K >> 7, tail = a.K & 127;   // (a last step that is not full is one wave's, at the end)
     const int s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
-    const int xld = (a.K + 63) / 64 * 64 + 16;
+    const int xld = (a.K + 127) / 128 * 128 + 16;
+    const int r8 = s16 & 7, chunk = (g + 4 * (s16 >> 3)) * 16;
 
     // X's own loads come first: they are waited for first
     const int parts = std::max((a.K + 511) >> 9, 1), units = M * parts;
@@ -686,19 +714,18 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
             if ((a.K & 7) != 0 && unit < units && c < a.K && c + 8 > a.K) raw[u].load(p, 0, a.K - c);
         }
     }
-    const int8_t* wp[NF];
+    const int8_t *wp[2 * NF], *xp[2 * FM];
 #pragma unroll
-    for (int f = 0; f < NF; ++f) wp[f] = a.B + (int64_t)(n0 + std::min(f * 16 + s16, left - 1)) * a.ldb + g * 16;
-    const int8_t* xp[FM];
+    for (int f = 0; f < 2 * NF; ++f) wp[f] = a.B + (int64_t)(n0 + std::min(f * 8 + r8, left - 1)) * a.ldb + chunk;
 #pragma unroll
-    for (int m = 0; m < FM; ++m) xp[m] = UNITS > 0 ? nullptr : a.A + std::min(m * 16 + s16, M - 1) * a.lda + g * 16;
-    u32x4 wb[D][NF], xb[UNITS > 0 ? 1 : D][FM];
+    for (int m = 0; m < 2 * FM; ++m) xp[m] = UNITS > 0 ? nullptr : a.A + std::min(m * 8 + r8, M - 1) * a.lda + chunk;
+    u32x4 wb[D][2 * NF], xb[UNITS > 0 ? 1 : D][2 * FM];
     auto load = [&](int i, int s) {
 #pragma unroll
-        for (int f = 0; f < NF; ++f) wb[i][f] = load_global<u32x4a1>(steps > 0 ? wp[f] + s * 64 : (const int8_t*)kZeros);
+        for (int f = 0; f < 2 * NF; ++f) wb[i][f] = load_once<u32x4a1>(steps > 0 ? wp[f] + s * 128 : (const int8_t*)kZeros);
         if constexpr (UNITS == 0) {
 #pragma unroll
-            for (int m = 0; m < FM; ++m) xb[i][m] = load_global<u32x4a1>(steps > 0 ? xp[m] + s * 64 : (const int8_t*)kZeros);
+            for (int m = 0; m < 2 * FM; ++m) xb[i][m] = load_global<u32x4a1>(steps > 0 ? xp[m] + s * 128 : (const int8_t*)kZeros);
         }
     };
     // (and the epilogue's operands: a fragment a wave, NF FM of them)
@@ -744,14 +771,24 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
 #pragma unroll
         for (int m = 0; m < FM; ++m) acc[f][m] = i32x4{0, 0, 0, 0};
     auto multiply = [&](int i, int s) {
+        u32x4 w[NF][2];
+#pragma unroll
+        for (int f = 0; f < NF; ++f) exchange(wb[i][2 * f], wb[i][2 * f + 1], w[f]);
 #pragma unroll
         for (int m = 0; m < FM; ++m) {
-            u32x4 x;
-            if constexpr (UNITS > 0) x = *(const u32x4*)(xq + std::min(m * 16 + s16, M - 1) * xld + s * 64 + g * 16);
-            else x = xb[i][m];
+            u32x4 x[2];
+            if constexpr (UNITS > 0) {
+                const unsigned char* p = xq + std::min(m * 16 + s16, M - 1) * xld + s * 128 + g * 16;
+                x[0] = *(const u32x4*)p;
+                x[1] = *(const u32x4*)(p + 64);
+            } else {
+                exchange(xb[i][2 * m], xb[i][2 * m + 1], x);
+            }
 #pragma unroll
-            for (int f = 0; f < NF; ++f)
-                acc[f][m] = MulI8::mul(__builtin_bit_cast(bf16x8, wb[i][f]), __builtin_bit_cast(bf16x8, x), acc[f][m]);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+                    acc[f][m] = MulI8::mul(__builtin_bit_cast(bf16x8, w[f][h]), __builtin_bit_cast(bf16x8, x[h]), acc[f][m]);
         }
     };
     int s = s0;
@@ -767,12 +804,12 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
     for (int i = 0; i < D; ++i)
         if (s + i < s1) multiply(i, s + i);
     if (tail > 0 && wave == NW - 1) {
-        const int n = tail - g * 16;
+        const int n = tail - chunk;
 #pragma unroll
-        for (int f = 0; f < NF; ++f) wb[0][f] = load16(wp[f] + steps * 64, n);
+        for (int f = 0; f < 2 * NF; ++f) wb[0][f] = load16(wp[f] + steps * 128, n);
         if constexpr (UNITS == 0) {
 #pragma unroll
-            for (int m = 0; m < FM; ++m) xb[0][m] = load16(xp[m] + steps * 64, n);
+            for (int m = 0; m < 2 * FM; ++m) xb[0][m] = load16(xp[m] + steps * 128, n);
         }
         multiply(0, steps);
     }

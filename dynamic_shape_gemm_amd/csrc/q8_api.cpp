@@ -377,7 +377,7 @@ int backward(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, int 
     a.zgroup = sloped ? (int)z_group : 0;
     a.x = X;
     a.ldx = ldx;
-    a.xs = x_scale;
+    a.xs = dW ? x_scale : nullptr;
     a.dz = (uint16_t*)dZ;
     a.lddz = lddz;
     a.dw = dW;
