@@ -124,7 +124,7 @@ struct Scale8 {
     bool ok;
     __device__ __forceinline__ explicit Scale8(float top) {
         // top / 127 rounded to nearest, from the rounded reciprocal of 127 and the exact
-        // rest (Markstein); below 2^-126 the result does not count
+        // rest (Markstein; right for every mantissa); below 2^-126 it does not count
         ok = top < INFINITY;
         constexpr float r = 1.0f / 127.0f;
         const float q = top * r;
@@ -199,7 +199,9 @@ __device__ __forceinline__ uint32_t max_wave(uint32_t v) {
 // ---- a scale for each row ----------------------------------------------------
 
 // TPR threads hold a row, C chunks of eight values each, between its maximum and
-// its integers; a row of more (LOOP) is read twice.
+// its integers, so X is read once; a row of more (LOOP) is read twice.  A wave a row
+// up to 1024 columns (no barrier), a workgroup above.  Bound by the bytes (8192 x 4096
+// bf16: 22 us, 4.5 TB/s), one row by latencies (1 x 4096: 4.0 us, a launch's 2.5 in it).
 template <bool F32, int TPR, int C, bool LOOP>
 __global__ __launch_bounds__(256) void quantize_row_kernel(QuantArgs a) {
     __shared__ uint32_t buf[4];
@@ -269,8 +271,8 @@ struct Walk {
 
 // G lanes (2 .. 16) hold a group, sixteen columns each; a row's chunks are padded to
 // whole groups.  Bound by the bytes and, half as much, by some 10 instructions an
-// element (8192 x 11008 bf16 in groups of 128: TODO us, TODO TB/s; eight columns a
-// lane, with a scale's divisions for each eight, took 70).
+// element (8192 x 11008 bf16 in groups of 128: 60 us, 4.5 TB/s; eight columns a lane,
+// with a scale's two divisions for each eight, took 70).
 template <bool F32, int G>
 __global__ __launch_bounds__(256) void quantize_group_kernel(QuantArgs a, int rows, int cpr) {
     constexpr int U = 2;
@@ -363,6 +365,8 @@ __device__ __forceinline__ void store_values(void* row, int64_t c, const float (
     }
 }
 
+// y = q s, eight columns a thread, four chunks read before the first is used.  Bound
+// by the bytes (8192 x 11008 to bf16: 43 us, 6.3 TB/s).
 template <bool F32>
 __global__ __launch_bounds__(256) void dequantize_kernel(QuantArgs a, int rows, int cpr, int shift) {
     constexpr int U = 4;
@@ -395,6 +399,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(QuantArgs a, int rows, 
 
 // ---- rows of any alignment into aligned ones -------------------------------------
 
+// A wave a row.
 __global__ __launch_bounds__(256) void q8_pack_kernel(const int8_t* src, int64_t lds, int8_t* dst, int64_t ldd, int64_t rows,
                                                       int cols) {
     const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -424,7 +429,11 @@ __device__ __forceinline__ void act_run(int act, f32x4* v) {
     }
 }
 
-// One tile over one split's K steps (of 128 integers).  The sums are exact in 32
+// One tile over one split's K steps (of 128 integers).  256 x 256 tiles, one a CU: 1.4
+// us a step, as long as of bf16 for twice the work, so the LDS (196 KB read and
+// 64 KB written a step) and the loads bound it, not the MFMAs (48-60 % busy); 4096 x
+// 4096 x 4096 57 us, 2420 TOPS.  64 x 64 tiles, four a CU, for latency: 509 x 2304 x
+// 768 6.2 us, where 128 x 128 take 8.1 and 256 x 256 10.2.  The sums are exact in 32
 // bits (K at most 131071); what is past K reads as zeros in both operands, or, in
 // the last 16 bytes, as zeros in A.
 // A tile's bf16 values, staged in LDS, to rows of any alignment.
@@ -612,7 +621,9 @@ __device__ __forceinline__ void store4(const I8Args& a, int64_t at, f32x4 v, int
     }
 }
 
-// Four columns a thread: the partial sums, joined exactly, and the epilogue.
+// Four columns a thread: the partial sums, joined exactly, and the epilogue.  Bound by
+// latency where it is used most (105 x 1024 in eight parts: 3.9 us), by the parts'
+// bytes else (2048 x 4096 in two: 17 us, 4.9 TB/s).
 __global__ __launch_bounds__(256) void i8_finish_kernel(I8Args a) {
     const int quads = (a.N + 3) >> 2;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -834,7 +845,11 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
 
 // dz = dy act'(z), what is made of it, and the input's integers in bf16.
 // Workgroups of the first kind take sum_rows rows of 512 columns, a wave every
-// fourth row; of the second 4 rows of the input.
+// fourth row; of the second 4 rows of the input.  The product's operand dz x_scale is
+// rounded here, once, from binary32 (made from the bf16 dz in the product it would be
+// rounded twice), and x's integers become bf16 here, exactly, so that the product's
+// loop does nothing but multiply.  Bound by the bytes: 8192 x 11008 with 8192 x 4096
+// of x, 730 MB, 120 us, 6.1 TB/s.
 template <bool F32, int ACT>
 __global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first, int cols, int zshift) {
     __shared__ float red[4][512];
@@ -936,7 +951,11 @@ __device__ __forceinline__ void q8_dbias(const Q8GradArgs& a, int n0, float* red
                      ((red[128 + c] + red[160 + c]) + (red[192 + c] + red[224 + c]));
 }
 
-// A tile of dW = a^T . xb over one split of the rows.  The workgroups past the tiles
+// A tile of dW = a^T . xb over one split of the rows (64 a step), both operands read
+// across their rows.  256 x 256 tiles, one a CU, come at 1.43 us a step, 1500 TFLOP/s in
+// full rounds (8192 x 11008 x 4096, two rounds and 0.69: 570 us, 1300); 128 x 128 tiles,
+// two a CU, where the result is small (8192 x 2304 x 768 in four parts: 33 us).  The
+// workgroups past the tiles
 // make dbias, which spares small calls a launch (unsplit ones: else the launch that
 // joins the partials does).
 template <class T>
@@ -1056,7 +1075,7 @@ int log2i(int v) { return 31 - __builtin_clz((unsigned)v); }
 
 // Rows of a workgroup that walks chunks: about 1024 of them, fewer (to 256) until
 // there are two workgroups a CU (509 x 770 binary32 in groups of 64: 6.1 us with
-// 1024, TODO so).
+// 1024, 4.1 so).
 int walk_rows(int64_t M, int cpr) {
     const int64_t chunks = std::min<int64_t>(1024, std::max<int64_t>(256, M * cpr / 512));
     return (int)std::max<int64_t>(1, std::min<int64_t>(M, chunks / cpr));
