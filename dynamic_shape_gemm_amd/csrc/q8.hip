@@ -28,15 +28,17 @@ typedef float f32x4a4 __attribute__((ext_vector_type(4), aligned(4)));
 __device__ __attribute__((aligned(16))) const uint32_t kZeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 
 // Device memory's own address space: what is chosen between two pointers is
-// otherwise read by instructions that wait for LDS too.
-template <class V>
+// otherwise read by instructions that wait for LDS too.  ALIGN: p's alignment.
+template <class V, int ALIGN>
 __device__ __forceinline__ V load_global(const void* p) {
-    return *(const V __attribute__((address_space(1)))*)p;
+    typedef V U __attribute__((aligned(ALIGN)));
+    return *(const U __attribute__((address_space(1)))*)p;
 }
 
-template <class V>
+template <class V, int ALIGN>
 __device__ __forceinline__ V load_once(const void* p) {
-    return __builtin_nontemporal_load((const V __attribute__((address_space(1)))*)p);
+    typedef V U __attribute__((aligned(ALIGN)));
+    return __builtin_nontemporal_load((const U __attribute__((address_space(1)))*)p);
 }
 
 constexpr float kTiny = 1.17549435e-38f;   // 2^-126
@@ -56,7 +58,7 @@ template <>
 struct Raw8<false> {
     u32x4 w;
     __device__ __forceinline__ void zero() { w = u32x4{0, 0, 0, 0}; }
-    __device__ __forceinline__ void read(const void* p) { w = load_global<u32x4a2>(p); }
+    __device__ __forceinline__ void read(const void* p) { w = load_global<u32x4, 2>(p); }
     __device__ __forceinline__ void load(const void* row, int64_t c, int nvalid) {
         const uint16_t* p = (const uint16_t*)row + c;
         if (nvalid >= 8) read(p);
@@ -84,8 +86,8 @@ struct Raw8<true> {
     f32x4 a, b;
     __device__ __forceinline__ void zero() { a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
     __device__ __forceinline__ void read(const void* p) {
-        a = load_global<f32x4a4>(p);
-        b = load_global<f32x4a4>((const float*)p + 4);
+        a = load_global<f32x4, 4>(p);
+        b = load_global<f32x4, 4>((const float*)p + 4);
     }
     __device__ __forceinline__ void load(const void* row, int64_t c, int nvalid) {
         const float* p = (const float*)row + c;
@@ -340,14 +342,23 @@ __device__ __forceinline__ u32x2 load_i8(const int8_t* p, int n) {
 }
 __device__ __forceinline__ float i8_at(u32x2 w, int i) { return (float)(int8_t)(w[i >> 2] >> (8 * (i & 3))); }
 
+// ONCE: past the caches (streaming stores).
+template <class V, int ALIGN, bool ONCE>
+__device__ __forceinline__ void store_vec(void* p, V v) {
+    typedef V U __attribute__((aligned(ALIGN)));
+    typedef U __attribute__((address_space(1))) * at;
+    if constexpr (ONCE) __builtin_nontemporal_store(v, (at)p);
+    else *(at)p = v;
+}
+
 // Up to eight values to a row of bf16 or binary32 (any alignment of its elements).
-template <bool F32>
+template <bool F32, bool ONCE = false>
 __device__ __forceinline__ void store_values(void* row, int64_t c, const float (&v)[8], int n) {
     if constexpr (F32) {
         float* p = (float*)row + c;
         if (n >= 8) {
-            *(f32x4a4*)p = f32x4{v[0], v[1], v[2], v[3]};
-            *(f32x4a4*)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            store_vec<f32x4, 4, ONCE>(p, f32x4{v[0], v[1], v[2], v[3]});
+            store_vec<f32x4, 4, ONCE>(p + 4, f32x4{v[4], v[5], v[6], v[7]});
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -356,7 +367,8 @@ __device__ __forceinline__ void store_values(void* row, int64_t c, const float (
     } else {
         uint16_t* p = (uint16_t*)row + c;
         if (n >= 8) {
-            *(u32x4a2*)p = u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+            store_vec<u32x4, 2, ONCE>(
+                p, u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])});
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -366,8 +378,11 @@ __device__ __forceinline__ void store_values(void* row, int64_t c, const float (
 }
 
 // y = q s, eight columns a thread, four chunks read before the first is used.  Bound
-// by the bytes (8192 x 11008 to bf16: 43 us, 6.3 TB/s).
-template <bool F32>
+// by the bytes (8192 x 11008 to bf16: 41.5 us, 6.5 TB/s).  ONCE: an output that would
+// take much of the last-level cache is written past it (quantised, read back and
+// added to, us, into the cache / past it: 90 MB of bf16 82 / 81, 135 MB 129 / 120, 180
+// MB 180 / 159; 67 MB 57 / 58).
+template <bool F32, bool ONCE>
 __global__ __launch_bounds__(256) void dequantize_kernel(QuantArgs a, int rows, int cpr, int shift) {
     constexpr int U = 4;
     const int64_t m0 = (int64_t)blockIdx.x * rows;
@@ -392,7 +407,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(QuantArgs a, int rows, 
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = i8_at(q[u], i) * s[u];
-            store_values<F32>((char*)a.x + (m0 + r[u]) * a.ldx * (F32 ? 4 : 2), c[u], v, a.K - c[u]);
+            store_values<F32, ONCE>((char*)a.x + (m0 + r[u]) * a.ldx * (F32 ? 4 : 2), c[u], v, a.K - c[u]);
         }
     }
 }
@@ -430,9 +445,10 @@ __device__ __forceinline__ void act_run(int act, f32x4* v) {
 }
 
 // One tile over one split's K steps (of 128 integers).  256 x 256 tiles, one a CU: 1.4
-// us a step, as long as of bf16 for twice the work, so the LDS (196 KB read and
-// 64 KB written a step) and the loads bound it, not the MFMAs (48-60 % busy); 4096 x
-// 4096 x 4096 57 us, 2420 TOPS.  64 x 64 tiles, four a CU, for latency: 509 x 2304 x
+// us a step, as long as of bf16 for twice the work.  MFMAs take 64-68 % of that time
+// (48-60 % of the launch's, whose ends are not hidden with one tile a CU), LDS 21-25 %,
+// the rest are the waves' waits for each other and for a step's loads; 4096 x 4096 x
+// 4096 57 us, 2420 TOPS.  64 x 64 tiles, four a CU, for latency: 509 x 2304 x
 // 768 6.2 us, where 128 x 128 take 8.1 and 256 x 256 10.2.  The sums are exact in 32
 // bits (K at most 131071); what is past K reads as zeros in both operands, or, in
 // the last 16 bytes, as zeros in A.
@@ -733,10 +749,10 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
     u32x4 wb[D][2 * NF], xb[UNITS > 0 ? 1 : D][2 * FM];
     auto load = [&](int i, int s) {
 #pragma unroll
-        for (int f = 0; f < 2 * NF; ++f) wb[i][f] = load_once<u32x4a1>(steps > 0 ? wp[f] + s * 128 : (const int8_t*)kZeros);
+        for (int f = 0; f < 2 * NF; ++f) wb[i][f] = load_once<u32x4, 1>(steps > 0 ? wp[f] + s * 128 : (const int8_t*)kZeros);
         if constexpr (UNITS == 0) {
 #pragma unroll
-            for (int m = 0; m < 2 * FM; ++m) xb[i][m] = load_global<u32x4a1>(steps > 0 ? xp[m] + s * 128 : (const int8_t*)kZeros);
+            for (int m = 0; m < 2 * FM; ++m) xb[i][m] = load_global<u32x4, 1>(steps > 0 ? xp[m] + s * 128 : (const int8_t*)kZeros);
         }
     };
     // (and the epilogue's operands: a fragment a wave, NF FM of them)
@@ -1060,6 +1076,8 @@ using G128 = LTile<2, 2, 2, 2, true, true>;
 template <int N>
 using Int = std::integral_constant<int, N>;
 
+constexpr int64_t kOnceBytes = int64_t(100) << 20;
+
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 template <class F>
 hipError_t by_act(int act, F&& f) {
@@ -1111,8 +1129,13 @@ hipError_t launch_quantize(const QuantArgs& a, hipStream_t st) { return a.f32 ? 
 hipError_t launch_dequantize(const QuantArgs& a, hipStream_t st) {
     const int cpr = (int)up(a.K, 8), rows = walk_rows(a.M, cpr), shift = a.group == 0 ? 31 : log2i(a.group);
     const dim3 grid((unsigned)up(a.M, rows));
-    return a.f32 ? launch_kernel(dequantize_kernel<true>, grid, dim3(256), st, a, rows, cpr, shift)
-                 : launch_kernel(dequantize_kernel<false>, grid, dim3(256), st, a, rows, cpr, shift);
+    const bool once = a.M * a.K * (a.f32 ? 4 : 2) >= kOnceBytes;
+    auto go = [&](auto f32) {
+        constexpr bool F32 = decltype(f32)::value != 0;
+        return once ? launch_kernel(dequantize_kernel<F32, true>, grid, dim3(256), st, a, rows, cpr, shift)
+                    : launch_kernel(dequantize_kernel<F32, false>, grid, dim3(256), st, a, rows, cpr, shift);
+    };
+    return a.f32 ? go(Int<1>{}) : go(Int<0>{});
 }
 
 hipError_t launch_q8_pack(const int8_t* src, int64_t lds, int8_t* dst, int64_t ldd, int64_t rows, int cols, hipStream_t st) {

@@ -591,3 +591,22 @@ def test_helpers_own_way(mkp, monkeypatch):
         for o, r in zip(second, first):
             same(o, r, name)
             assert o.stride() == r.stride()
+
+
+def test_outputs_beyond_the_caches(mkp):
+    """Outputs larger than the caches, with odd rows: binary32 and bf16."""
+    M, K = 5003, 12007
+    x = features(gen(1), M, K)
+    for group in (0, 256):
+        q, s = mkp.quantize_rows(x, group=group)
+        for t in (BF, F32):
+            y = mkp.dequantize_rows(q, s, group=group, dtype=t)
+            for m in (slice(0, 40), slice(M // 2, M // 2 + 40), slice(M - 40, M)):
+                same(y[m], oracle.values(q[m], s[m], group).to(F32).to(t), "values past the caches")
+    M, N, K = 12001, 12003, 96
+    x, w, ws, b = layer(gen(2), M, N, K)
+    for t in (BF, F32):
+        y = mkp.linear_i8(x, w, ws, b, act="relu", dtype=t)
+        for m in (slice(0, 300), slice(M - 300, M)):
+            q, s = oracle.quantize(x[m])
+            within(y[m], *oracle.linear(q, s, w, ws, b, "relu", t), "a layer past the caches")
