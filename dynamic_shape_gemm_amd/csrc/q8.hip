@@ -273,7 +273,7 @@ struct Walk {
 
 // G lanes (2 .. 16) hold a group, sixteen columns each; a row's chunks are padded to
 // whole groups.  Bound by the bytes and, half as much, by some 10 instructions an
-// element (8192 x 11008 bf16 in groups of 128: 60 us, 4.5 TB/s; eight columns a lane,
+// element (8192 x 11008 bf16 in groups of 128: 47 us, 5.7 TB/s; eight columns a lane,
 // with a scale's two divisions for each eight, took 70).
 template <bool F32, int G>
 __global__ __launch_bounds__(256) void quantize_group_kernel(QuantArgs a, int rows, int cpr) {
@@ -971,9 +971,8 @@ __device__ __forceinline__ void q8_dbias(const Q8GradArgs& a, int n0, float* red
 // across their rows.  256 x 256 tiles, one a CU, come at 1.43 us a step, 1500 TFLOP/s in
 // full rounds (8192 x 11008 x 4096, two rounds and 0.69: 570 us, 1300); 128 x 128 tiles,
 // two a CU, where the result is small (8192 x 2304 x 768 in four parts: 33 us).  The
-// workgroups past the tiles
-// make dbias, which spares small calls a launch (unsplit ones: else the launch that
-// joins the partials does).
+// workgroups past the tiles make dbias, which spares small calls a launch (unsplit
+// ones: else the launch that joins the partials does).
 template <class T>
 __global__ __launch_bounds__(T::NT, 2) void q8_product_kernel(Q8GradArgs a) {
     __shared__ __attribute__((aligned(1024))) unsigned char raw[tile_lds<T>()];

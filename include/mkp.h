@@ -349,6 +349,7 @@ int mkp_linear_loss_workspace(int64_t M, int64_t V, int64_t K, int64_t k,
  * mkp_dequantize_rows: Y := q s, rounded once more for MKP_BF16.
  * X, Q, S and Y may have any alignment of their elements; rows of X and Y that
  * are 16-byte aligned and of Q that are 8-byte aligned are faster.
+ * Here and in the calls below no output may overlap an operand or another output.
  */
 int mkp_quantize_rows(int64_t M, int64_t K, const void *X, int64_t ldx, int x_type, int64_t group,
                       int8_t *Q, int64_t ldq, float *S, int64_t lds, void *stream);
@@ -365,7 +366,8 @@ int mkp_dequantize_rows(int64_t M, int64_t K, const int8_t *Q, int64_t ldq, cons
  * exactly as mkp_quantize_rows would with group 0, and x_scale is not read.
  * bias: N binary32 values or NULL; act: one of MKP_ACT_*; y_type MKP_BF16 or
  * MKP_F32.  The sums are exact (integers of 32 bits, K at most 131071); they are
- * scaled, biased and activated in binary32.  K == 0: Y := act(bias).
+ * scaled (by w_scale first), biased and activated in binary32.  K == 0:
+ * Y := act(bias).
  *
  * Any alignment of X, W and Y serves.  W whose rows are not 16-byte aligned
  * (address and ldw), or an X of MKP_I8 whose rows are not or whose K is not a
