@@ -9,6 +9,7 @@
 namespace mkp {
 
 constexpr int kI8StreamRows = 32;   // most tokens of the product for few
+constexpr int kI8StreamInput = 131072;   // and, where tiles take W as it is, most integers of X
 constexpr int kI8StreamUnits = 64;  // runs of 512 features that it quantises by itself
 constexpr int kQ8MaxGroup = 256;   // columns of one scale, if not the whole row
 

@@ -178,8 +178,15 @@ void remembered(int64_t M, int64_t N, int64_t K, int& tile, int& splits, F&& cho
 LinearLayout linear_layout(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, int x_type, const void* W,
                            int64_t ldw) {
     LinearLayout l;
-    l.stream = M <= kI8StreamRows;
-    if (l.stream) {   // (rows of any alignment; few enough features are quantised by the product)
+    l.pack_b = !aligned16(W) || ldw % 16 != 0;
+    // Every workgroup of the product for few tokens reads the whole of X, which takes
+    // it 3 us per 100 KB: past 128 KB tiles, with parts of K, are faster (us a call, X in
+    // 8 bits, few tokens / tiles: 32 x 1024 x 4096 7.2 / 7.9, x 12544 16.2 / 9.3; 8 x 1024 x
+    // 12544 8.6 / 8.6, x 32768 17.8 / 12.3; of 880 extents to 32 x 8192 x 32768 the choice is
+    // 1 % behind the faster in the mean) unless all of W were to be copied for them.
+    l.stream = M <= kI8StreamRows && (M * K <= kI8StreamInput || l.pack_b);
+    if (l.stream) {
+        l.pack_b = false;   // (rows of any alignment; few enough features are quantised by the product)
         l.quantise = x_type != MKP_I8 && M * ceil_div(K, 512) > kI8StreamUnits;
         l.Ka = round_up(K, 16);
         if (l.quantise) {
@@ -190,7 +197,6 @@ LinearLayout linear_layout(int64_t M, int64_t N, int64_t K, const void* X, int64
     }
     l.quantise = x_type != MKP_I8;
     l.pack_a = !l.quantise && (!aligned16(X) || ldx % 16 != 0 || K % 16 != 0);
-    l.pack_b = !aligned16(W) || ldw % 16 != 0;
     l.Ka = round_up(K, 16);
     l.Kb = round_up(K, 16);
     remembered<0>(M, N, K, l.tile, l.splits, [&] {

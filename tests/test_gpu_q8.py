@@ -204,6 +204,18 @@ def test_few_tokens(mkp, M, N, K):
     check_linear(mkp, placed(q, (-K) % 16), w, ws, None, "none", BF, s)
 
 
+@pytest.mark.parametrize("M,N,K", [(32, 200, 4096), (32, 200, 4097), (31, 1024, 12544), (9, 130, 20011), (4, 600, 32768),
+                                   (4, 600, 32770), (2, 33, 131071), (1, 1000, 131071)])
+def test_few_tokens_of_many_features(mkp, M, N, K):
+    """On both sides of where tiles are taken; the same bits wherever W lies."""
+    x, w, ws, b = layer(gen(M + K), M, N, K)
+    q, s = oracle.quantize(x)
+    aligned = placed(w, (-K) % 16)
+    for xs, a in ((None, x), (s, q), (s, placed(q, (-K) % 16))):
+        y = check_linear(mkp, a, aligned, ws, b, "silu", BF, xs)
+        same(check_linear(mkp, a, placed(w, 1, 3), ws, b, "silu", BF, xs), y, "an unaligned weight")
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("M", [1, 20, 150, 4100])
