@@ -201,46 +201,56 @@ __device__ __forceinline__ uint32_t max_wave(uint32_t v) {
 // ---- a scale for each row ----------------------------------------------------
 
 // TPR threads hold a row, C chunks of eight values each, between its maximum and
-// its integers, so X is read once; a row of more (LOOP) is read twice.  A wave a row
-// up to 1024 columns (no barrier), a workgroup above.  Bound by the bytes (8192 x 4096
-// bf16: 22 us, 4.5 TB/s), one row by latencies (1 x 4096: 4.0 us, a launch's 2.5 in it).
+// its integers, so X is read once; a row of more than 65536 (LOOP) is read twice.  A
+// wave a row up to 1024 columns (no barrier), a workgroup above, of 1024 threads from
+// 8192 columns on (bf16, 256 threads of eight or, LOOP, four chunks / 1024: 105 x 12544
+// 6.0 / 4.1 us, 4096 x 12544 27.5 / 28.8, 32 x 30000 11.5 / 5.1, 2048 x 30000 50.8 /
+// 32.2; below, 4096 x 8192, 16.9 / 19.0).  Bound by the bytes (8192 x 4096 bf16: 16 us in
+// a row of calls, 6.2 TB/s), one row by latencies (1 x 4096: 4.0 us, a launch's 2.5 in it).
 template <bool F32, int TPR, int C, bool LOOP>
-__global__ __launch_bounds__(256) void quantize_row_kernel(QuantArgs a) {
-    __shared__ uint32_t buf[4];
+__global__ __launch_bounds__(std::max(TPR, 256)) void quantize_row_kernel(QuantArgs a) {
+    constexpr int NT = std::max(TPR, 256), NW = TPR / 64;
+    __shared__ uint32_t buf[16];
     const int tid = threadIdx.x, at = tid % TPR;
-    const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + tid / TPR;
+    const int64_t m = (int64_t)blockIdx.x * (NT / TPR) + tid / TPR;
     if (TPR < 256 && m >= a.M) return;   // (whole waves)
     const char* row = (const char*)a.x + m * a.ldx * (F32 ? 4 : 2);
     Raw8<F32> raw[C];
-    uint32_t top = 0;
-    for (int c0 = 0; c0 < a.K; c0 += TPR * 8 * C) {
+    auto load = [&](int c0) {   // (without branches: a load behind one is waited for before the next)
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int c = c0 + (i * TPR + at) * 8;
-            if (c < a.K) raw[i].load(row, c, a.K - c);
-            else raw[i].zero();
+            raw[i].read(c + 8 <= a.K ? row + (int64_t)c * (F32 ? 4 : 2) : (const char*)kZeros);
         }
+        if ((a.K & 7) != 0)
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int c = c0 + (i * TPR + at) * 8;
+                if (c < a.K && c + 8 > a.K) raw[i].load(row, c, a.K - c);
+            }
+    };
+    uint32_t top = 0;
+    for (int c0 = 0; c0 < a.K; c0 += TPR * 8 * C) {
+        load(c0);
 #pragma unroll
         for (int i = 0; i < C; ++i) top = std::max(top, raw[i].top());
         if constexpr (!LOOP) break;
     }
     top = max_wave(top);
-    if constexpr (TPR == 256) {
+    if constexpr (NW > 1) {
         if ((tid & 63) == 0) buf[tid >> 6] = top;
         __syncthreads();
-        top = std::max(std::max(buf[0], buf[1]), std::max(buf[2], buf[3]));
+#pragma unroll
+        for (int w = 0; w < NW; ++w) top = std::max(top, buf[w]);
     }
     const Scale8 sc(Raw8<F32>::top_value(top));
     if (at == 0) a.s[m * a.lds] = sc.s;
     int8_t* q = a.q + m * a.ldq;
     for (int c0 = 0; c0 < a.K + a.pad; c0 += TPR * 8 * C) {
+        if constexpr (LOOP) load(c0);
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int c = c0 + (i * TPR + at) * 8;
-            if constexpr (LOOP) {
-                if (c < a.K) raw[i].load(row, c, a.K - c);
-                else raw[i].zero();
-            }
             float v[8];
             raw[i].values(v);
             store_i8(q + c, to_i8(v, sc), a.K + a.pad - c);
@@ -1102,14 +1112,16 @@ template <bool F32>
 hipError_t quantize(const QuantArgs& a, hipStream_t st) {
     if (a.group == 0) {
         const int K = a.K + a.pad;
-        const dim3 waves((unsigned)up(a.M, 4)), wgs((unsigned)a.M), b(256);
+        const dim3 waves((unsigned)up(a.M, 4)), wgs((unsigned)a.M), b(256), wide(1024);
         if (K <= 512) return launch_kernel(quantize_row_kernel<F32, 64, 1, false>, waves, b, st, a);
         if (K <= 1024) return launch_kernel(quantize_row_kernel<F32, 64, 2, false>, waves, b, st, a);
         if (K <= 2048) return launch_kernel(quantize_row_kernel<F32, 256, 1, false>, wgs, b, st, a);
         if (K <= 4096) return launch_kernel(quantize_row_kernel<F32, 256, 2, false>, wgs, b, st, a);
         if (K <= 8192) return launch_kernel(quantize_row_kernel<F32, 256, 4, false>, wgs, b, st, a);
-        if (K <= 16384) return launch_kernel(quantize_row_kernel<F32, 256, 8, false>, wgs, b, st, a);
-        return launch_kernel(quantize_row_kernel<F32, 256, 4, true>, wgs, b, st, a);
+        if (K <= 16384) return launch_kernel(quantize_row_kernel<F32, 1024, 2, false>, wgs, wide, st, a);
+        if (K <= 32768) return launch_kernel(quantize_row_kernel<F32, 1024, 4, false>, wgs, wide, st, a);
+        if (K <= 65536) return launch_kernel(quantize_row_kernel<F32, 1024, 8, false>, wgs, wide, st, a);
+        return launch_kernel(quantize_row_kernel<F32, 1024, 4, true>, wgs, wide, st, a);
     }
     const int cpr = (int)up(a.K, a.group) * (a.group / 16), rows = walk_rows(a.M, cpr);
     const dim3 grid((unsigned)up(a.M, rows)), b(256);

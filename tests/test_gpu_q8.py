@@ -78,7 +78,8 @@ def check_store(mkp, x, group, what):
 @pytest.mark.parametrize("group", [0, 32, 64, 128, 256])
 @pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("M,K", [(1, 1), (1, 4096), (3, 31), (5, 512), (2, 513), (7, 1024), (4, 1030), (9, 2048), (3, 2100),
-                                 (2, 4097), (3, 8192), (2, 8200), (2, 16384), (2, 16400), (1, 40000), (301, 257), (1000, 8)])
+                                 (2, 4097), (3, 8192), (2, 8200), (2, 16384), (2, 16400), (1, 40000), (301, 257), (1000, 8),
+                                 (3, 32767), (2, 32772), (2, 65536), (3, 65543), (2, 70001)])
 def test_store(mkp, M, K, t, group):
     check_store(mkp, features(gen(M + K), M, K, t), group, "store")
 
