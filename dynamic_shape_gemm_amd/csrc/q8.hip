@@ -875,22 +875,42 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
 // rounded here, once, from binary32 (made from the bf16 dz in the product it would be
 // rounded twice), and x's integers become bf16 here, exactly, so that the product's
 // loop does nothing but multiply.  Bound by the bytes: 8192 x 11008 with 8192 x 4096
-// of x, 730 MB, 120 us, 6.1 TB/s.
+// of x, 730 MB, 118 us, 6.2 TB/s.  (Loads behind branches: 120; 8192 x 2304 with
+// 8192 x 768, binary32 dy, 33.4 us against 29.8; 333 x 768 with 333 x 12544 14.5, one load
+// of x ahead, against 10.4.)
 template <bool F32, int ACT>
 __global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first, int cols, int zshift) {
     __shared__ float red[4][512];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const char* const zeros = (const char*)kZeros;
     if ((int)blockIdx.x >= first) {
         const int64_t m = (int64_t)(blockIdx.x - first) * 4 + wave;
         if (m >= a.M) return;
         const int8_t* x = a.x + m * a.ldx;
         uint16_t* d = a.xb + m * a.Kp;
-        for (int k = lane * 8; k < a.Kp; k += 512) {
-            const u32x2 w = load_i8(x + k, a.K - k);
-            float v[8];
+        constexpr int U = 4;
+        for (int k0 = lane * 8; k0 < a.Kp; k0 += 512 * U) {
+            u32x2 w[U];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i8_at(w, i);
-            store_values<false>(d, k, v, 8);
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + 512 * u;
+                w[u] = load_global<u32x2, 1>(k + 8 <= a.K ? (const char*)x + k : zeros);
+            }
+            if ((a.K & 7) != 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int k = k0 + 512 * u;
+                    if (k < a.K && k + 8 > a.K) w[u] = load_i8(x + k, a.K - k);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + 512 * u;
+                if (k >= a.Kp) break;
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = i8_at(w[u], i);
+                store_values<false>(d, k, v, 8);
+            }
         }
         return;
     }
@@ -905,21 +925,24 @@ __global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first,
             u32x2 z[U];
             float zs[U], xs[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < U; ++u) {   // (without branches: see quantize_row_kernel)
                 const int64_t m = m0 + r0 + 4 * u;
-                dy[u].zero();
-                z[u] = u32x2{0, 0};
-                zs[u] = 0.0f;
-                xs[u] = 0.0f;
-                if (m >= a.M) continue;
-                const char* row = (const char*)a.dy + m * a.lddy * (F32 ? 4 : 2);
-                dy[u].load(row, n, left);
+                const bool on = m < a.M, whole = on && left >= 8;
+                dy[u].read(whole ? (const char*)a.dy + (m * a.lddy + n) * (F32 ? 4 : 2) : zeros);
                 if constexpr (ACT != ACT_NONE) {
-                    z[u] = load_i8(a.z + m * a.ldz + n, left);
-                    zs[u] = a.zs[m * a.ldzs + (n >> zshift)];
+                    z[u] = load_global<u32x2, 1>(whole ? (const char*)a.z + m * a.ldz + n : zeros);
+                    zs[u] = load_global<float, 4>(on ? (const char*)(a.zs + m * a.ldzs + (n >> zshift)) : zeros);
                 }
-                xs[u] = a.xs != nullptr ? a.xs[m] : 0.0f;
+                xs[u] = load_global<float, 4>(on && a.xs != nullptr ? (const char*)(a.xs + m) : zeros);
             }
+            if ((a.N & 7) != 0 && left < 8)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t m = m0 + r0 + 4 * u;
+                    if (m >= a.M) continue;
+                    dy[u].load((const char*)a.dy + m * a.lddy * (F32 ? 4 : 2), n, left);
+                    if constexpr (ACT != ACT_NONE) z[u] = load_i8(a.z + m * a.ldz + n, left);
+                }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t m = m0 + r0 + 4 * u;
