@@ -436,12 +436,18 @@ __global__ __launch_bounds__(256) void q8_pack_kernel(const int8_t* src, int64_t
 
 // ---- the product in 8-bit integers -------------------------------------------------
 
+// (a row or channel of scale NaN stays NaN; the GEMM's rectifier makes it 0)
+template <int ACT>
+__device__ __forceinline__ float act_keep(float v) {
+    if constexpr (ACT == ACT_RELU) return v <= 0.0f ? 0.0f : v;
+    return act_t<ACT>(v);
+}
 template <int ACT, int N>
 __device__ __forceinline__ void act_run(f32x4* v) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[i][r] = act_t<ACT>(v[i][r]);
+        for (int r = 0; r < 4; ++r) v[i][r] = act_keep<ACT>(v[i][r]);
 }
 // act of 4 N values.
 template <int N>

@@ -623,3 +623,26 @@ def test_outputs_beyond_the_caches(mkp):
         for m in (slice(0, 300), slice(M - 300, M)):
             q, s = oracle.quantize(x[m])
             within(y[m], *oracle.linear(q, s, w, ws, b, "relu", t), "a layer past the caches")
+
+
+# tokens of linear_i8's forms: (M, N, K) of the streaming product with X quantised by it,
+# by a launch before it, tiles of each size, and tiles with parts of K
+FORMS = [(3, 100, 300), (30, 100, 4096), (60, 100, 300), (400, 300, 300), (4100, 4000, 130), (100, 64, 4096)]
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_not_finite_through_activations(mkp, M, N, K, t, act):
+    """A token or a channel of scale NaN is NaN after every activation, and
+    nothing else is."""
+    x, w, ws, b = layer(gen(M + K), M, N, K)
+    x[0, 5], x[M // 2, K - 1], x[M - 1, 0] = NAN, math.inf, -math.inf
+    ws[[2, N - 1]] = NAN
+    want = torch.zeros((M, N), dtype=torch.bool, device="cuda")
+    want[[0, M // 2, M - 1]] = True
+    want[:, [2, N - 1]] = True
+    q, s = oracle.quantize(x)
+    for xx, xs in ((x, None), (placed(q, (-K) % 16), s)):
+        y = check_linear(mkp, xx, w, ws, b, act, t, xs, "not finite")
+        assert torch.equal(torch.isnan(y), want)
