@@ -1199,7 +1199,8 @@ hipError_t launch_i8_stream(const I8Args& a, hipStream_t st) {
     // every CU a run of channels, at most 64 of them at a time
     const int passes = (int)up(a.N, 256 * 64), cols = (int)up(a.N, 256 * passes);
     const dim3 grid((unsigned)up(a.N, cols)), b(512);
-    const int units = a.quantise ? (int)std::max<int64_t>(1, up(a.M * up(a.K, 512), 8)) : 0;
+    // (a row without features takes a run too: its scale is made there)
+    const int units = a.quantise ? (int)up(a.M * std::max<int64_t>(up(a.K, 512), 1), 8) : 0;
     auto go = [&](auto fm, auto nf, auto un, auto f32) {
         return launch_kernel(i8_stream_kernel<decltype(fm)::value, decltype(nf)::value, decltype(un)::value,
                                                   decltype(f32)::value>, grid, b, st, a, cols);

@@ -646,3 +646,18 @@ def test_not_finite_through_activations(mkp, M, N, K, t, act):
     for xx, xs in ((x, None), (placed(q, (-K) % 16), s)):
         y = check_linear(mkp, xx, w, ws, b, act, t, xs, "not finite")
         assert torch.equal(torch.isnan(y), want)
+
+
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+def test_empty_sums_of_every_few_tokens(mkp, t):
+    """No features: act(bias) for every number of tokens, whatever a kernel before
+    left in its workgroups' memory (here NaN, in the outputs that its tiles stage)."""
+    N = 5000
+    b = torch.randn(N, device="cuda")
+    one = torch.ones(4096, device="cuda")
+    bad = torch.full((4096, 64), NAN, device="cuda", dtype=t)
+    w = torch.ones((4096, 64), dtype=I8, device="cuda")
+    for M in range(1, 34):
+        assert torch.isnan(mkp.linear_i8(bad, w, one, dtype=BF)).all()
+        y = mkp.linear_i8(bad[:M, :0], torch.empty((N, 0), dtype=I8, device="cuda"), torch.ones(N, device="cuda"), b)
+        same(y, b.repeat(M, 1), f"{M} tokens of no features")
