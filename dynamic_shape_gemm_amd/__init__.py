@@ -879,6 +879,8 @@ def quantize_rows(x, group=0, stream=None):
 
     def call(st):
         q = x.new_empty((M, ldq), dtype=torch.int8)
+        if K == 0 and not group:   # (the library writes nothing of rows without columns)
+            return q, x.new_full((M,), 2.0 ** -126, dtype=torch.float32)
         scale = x.new_empty((M, groups) if group else (M,), dtype=torch.float32)
         _check(_f_quantize_rows(M, K, at, ldx, _CODES[x.dtype], group, q.data_ptr(), ldq, scale.data_ptr(), groups or 1, st))
         return (q if ldq == K else q[:, :K]), scale

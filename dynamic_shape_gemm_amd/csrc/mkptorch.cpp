@@ -94,7 +94,7 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int gpu = current_gpu(t, 2);
     if (gpu < 0 || !real_code(*t, code)) Py_RETURN_NONE;
     const int64_t M = t->size(0), K = t->size(1), groups = group ? (K + group - 1) / group : 1, ldq = (K + 15) / 16 * 16;
-    if (!view(t, gpu, t->scalar_type(), M, K, x)) Py_RETURN_NONE;
+    if (K == 0 || !view(t, gpu, t->scalar_type(), M, K, x)) Py_RETURN_NONE;   // (no columns: the helper's own way)
     Tensor q = make(*t, {M, ldq}, at::kChar);
     Tensor s = group ? make(*t, {M, groups}, at::kFloat) : make(*t, {M}, at::kFloat);
     if (mkp_quantize_rows(M, K, x.p, x.ld, code, group, (int8_t*)q.data_ptr(), ldq, (float*)s.data_ptr(), groups > 0 ? groups : 1,

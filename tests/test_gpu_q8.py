@@ -661,3 +661,23 @@ def test_empty_sums_of_every_few_tokens(mkp, t):
         assert torch.isnan(mkp.linear_i8(bad, w, one, dtype=BF)).all()
         y = mkp.linear_i8(bad[:M, :0], torch.empty((N, 0), dtype=I8, device="cuda"), torch.ones(N, device="cuda"), b)
         same(y, b.repeat(M, 1), f"{M} tokens of no features")
+
+
+@pytest.mark.parametrize("own_way", [False, True])
+def test_rows_of_no_columns(mkp, own_way, monkeypatch):
+    """A scale for each row of no columns too, the least one; nothing to sum gives act(bias)."""
+    if own_way:
+        monkeypatch.setattr(mkp, "_direct", None)
+    b = torch.randn(9, device="cuda")
+    for M in (1, 12, 300):
+        for stream in (None, torch.cuda.Stream()):
+            del [torch.full((M,), NAN, device="cuda") for _ in range(4)][:]
+            q, s = mkp.quantize_rows(torch.empty((M, 0), dtype=BF, device="cuda"), stream=stream)
+            torch.cuda.synchronize()
+            assert q.shape == (M, 0) and q.dtype == I8
+            same(s, torch.full((M,), 2.0 ** -126, device="cuda"), "scales of no columns")
+            assert mkp.dequantize_rows(q, s).shape == (M, 0)
+            y = mkp.linear_i8(q, torch.empty((9, 0), dtype=I8, device="cuda"), torch.ones(9, device="cuda"), b, x_scale=s)
+            same(y, b.repeat(M, 1), "a layer of no features")
+        q, s = mkp.quantize_rows(torch.empty((M, 0), device="cuda"), group=64)
+        assert q.shape == (M, 0) and s.shape == (M, 0)
