@@ -908,7 +908,7 @@ def dequantize_rows(q, scale, group=0, dtype=None, stream=None):
 
     def call(st):
         y = q.new_empty((M, K), dtype=dtype)
-        _check(_f_dequantize_rows(M, K, at, ldq, sat, lds or 1, group, y.data_ptr(), K, _CODES[dtype], st))
+        _check(_f_dequantize_rows(M, K, at, ldq, sat, lds, group, y.data_ptr(), K, _CODES[dtype], st))
         return y
 
     return _q8_on(stream, (q, scale), call)
@@ -1016,7 +1016,7 @@ def linear_q8_backward(dy, x, x_scale, z=None, z_scale=None, z_group=0, act=None
         dw = dy.new_empty((N, K), dtype=grad_dtype) if need_dw else None
         dbias = dy.new_empty(N, dtype=torch.float32) if need_dbias else None
         ws, at = _q8_workspace(n, dy)
-        _check(_f_linear_q8_backward(M, N, K, dyat, lddy, _CODES[dy.dtype], xat, ldx, sx, zat, ldz, sz, ldzs or 1,
+        _check(_f_linear_q8_backward(M, N, K, dyat, lddy, _CODES[dy.dtype], xat, ldx, sx, zat, ldz, sz, ldzs,
                                      z_group if code else 0, code, _addr(dz), N, _addr(dw), K, _CODES[grad_dtype],
                                      _addr(dbias), at, n, st))
         return dz, dw, dbias

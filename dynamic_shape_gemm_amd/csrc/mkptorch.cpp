@@ -46,10 +46,7 @@ bool view(const Tensor* t, int gpu, at::ScalarType type, int64_t rows, int64_t c
 // A quantised matrix's scales: a vector (group 0), or a matrix of them.
 bool scales(const Tensor* t, int gpu, int64_t rows, int64_t cols, int64_t group, View& v) {
     if (group == 0) return view(t, gpu, at::kFloat, rows, -1, v);
-    const int64_t n = (cols + group - 1) / group;
-    if (!view(t, gpu, at::kFloat, rows, n, v)) return false;
-    if (v.ld < 1) v.ld = 1;
-    return true;
+    return view(t, gpu, at::kFloat, rows, (cols + group - 1) / group, v);
 }
 
 bool known_group(int64_t g) { return g == 0 || g == 32 || g == 64 || g == 128 || g == 256; }

@@ -681,3 +681,27 @@ def test_rows_of_no_columns(mkp, own_way, monkeypatch):
             same(y, b.repeat(M, 1), "a layer of no features")
         q, s = mkp.quantize_rows(torch.empty((M, 0), device="cuda"), group=64)
         assert q.shape == (M, 0) and s.shape == (M, 0)
+
+
+@pytest.mark.parametrize("own_way", [False, True])
+def test_scales_broadcast_over_rows_are_refused(mkp, own_way, monkeypatch):
+    """A scale with one place for all rows has a leading dimension of 0: the library says so
+    instead of reading past it."""
+    if own_way:
+        monkeypatch.setattr(mkp, "_direct", None)
+    dy, x, xs, z, zs = kept(gen(2), 40, 64, 48, 64)
+    one = torch.ones((1, 1), device="cuda")
+    for bad in (one.expand(40, 1), one[0].expand(40, 1)):
+        assert bad.stride(0) == 0
+        with pytest.raises(mkp.MkpError):
+            mkp.dequantize_rows(z, bad, group=64)
+        with pytest.raises(mkp.MkpError):
+            mkp.linear_q8_backward(dy, x, xs, z, bad, z_group=64, act="gelu")
+    for bad in (one[0].expand(40),):
+        with pytest.raises(ValueError):
+            mkp.dequantize_rows(z, bad)
+        with pytest.raises(ValueError):
+            mkp.linear_q8_backward(dy, x, bad, z, zs, z_group=64, act="gelu")
+    # (one row is all rows; without an activation z's scales are not looked at)
+    same(mkp.dequantize_rows(z[:1], one, group=64), z[:1].to(BF), "one row")
+    mkp.linear_q8_backward(dy, x, xs, z, one.expand(40, 1), z_group=64)
