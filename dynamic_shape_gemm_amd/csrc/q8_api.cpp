@@ -30,7 +30,7 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool real_type(int t) { return t == MKP_BF16 || t == MKP_F32; }
 double size_of(int t) { return t == MKP_F32 ? 4.0 : t == MKP_I8 ? 1.0 : 2.0; }
 
-constexpr int64_t kMaxRows = (int64_t(1) << 24) - 1;   // a workgroup of 256 threads a row, counted in 32 bits
+constexpr int64_t kMaxRows = (int64_t(1) << 24) - 1;   // at least 256 threads a row, counted in 32 bits
 constexpr int64_t kMaxCols = int64_t(1) << 22;         // and leading dimensions: a tile's rows stay within 32-bit offsets
 constexpr int64_t kMaxDepth = 131071;                  // 128^2 times this is below 2^31
 

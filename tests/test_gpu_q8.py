@@ -705,3 +705,33 @@ def test_scales_broadcast_over_rows_are_refused(mkp, own_way, monkeypatch):
     # (one row is all rows; without an activation z's scales are not looked at)
     same(mkp.dequantize_rows(z[:1], one, group=64), z[:1].to(BF), "one row")
     mkp.linear_q8_backward(dy, x, xs, z, one.expand(40, 1), z_group=64)
+
+
+@pytest.mark.parametrize("K,t", [(8200, BF), (8193, F32), (16400, BF)], ids=["bf16", "f32", "bf16_wide"])
+def test_more_long_rows_than_workgroups_of_1024(mkp, K, t):
+    """2^22 rows of more than 8192 columns: 2^32 threads, were a workgroup of 1024 a row's."""
+    M = 1 << 22
+    torch.cuda.empty_cache()
+    size = M * K * (2 if t == BF else 4) + M * (K + 32)
+    if torch.cuda.mem_get_info()[0] < size + (8 << 30):
+        pytest.skip(f"{size >> 30} GiB and some are not free")
+    x = torch.empty((M, K), dtype=t, device="cuda")
+    x.fill_(1.0)
+    rows = [0, 1, 12345, M // 2, M - 2, M - 1]
+    some = features(gen(K), len(rows), K, t)
+    for i, m in enumerate(rows):
+        x[m] = some[i]
+    wq, ws = oracle.quantize(some)
+    q, s = mkp.quantize_rows(x)
+    same(q[rows], wq, "integers")
+    same(s[rows], ws, "scales")
+    assert int((s == torch.tensor(1.0 / 127.0, dtype=F32, device="cuda")).sum()) == M - len(rows)
+    y = mkp.dequantize_rows(q[M - 2:], s[M - 2:])
+    same(y, oracle.values(wq[4:], ws[4:]).to(F32).to(BF), "values")
+    del q
+    torch.cuda.empty_cache()
+    w, sw = oracle.quantize(torch.randn(16, K, generator=gen(1), device="cuda"))
+    y = mkp.linear_i8(x, w, sw)
+    within(y[rows], *oracle.linear(wq, ws, w, sw, None, "none", F32), "a layer of as many tokens")
+    del x, y
+    torch.cuda.empty_cache()
