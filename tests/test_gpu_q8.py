@@ -735,3 +735,21 @@ def test_more_long_rows_than_workgroups_of_1024(mkp, K, t):
     within(y[rows], *oracle.linear(wq, ws, w, sw, None, "none", F32), "a layer of as many tokens")
     del x, y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_slopes_are_exact_to_their_bound(mkp, act):
+    """One token whose gradient is 1: dbias is the slope itself, in binary32.  Scales
+    of 0.01 to 0.98 bring |z| from 0.01 to 124, every place of each slope."""
+    z = (torch.arange(254, device="cuda", dtype=torch.int32) % 127 + 1).to(I8)
+    z[127:] *= -1
+    one = torch.ones((1, 254), device="cuda")
+    worst = 0.0
+    for i in range(200):
+        zs = torch.tensor([0.01 * 1.0233 ** i], device="cuda")
+        _, _, db = mkp.linear_q8_backward(one, torch.zeros((1, 16), dtype=I8, device="cuda"), one[0, :1], z[None], zs, act=act,
+                                          need_dz=False, need_dw=False)
+        ref = oracle.slope(act, oracle.values(z[None], zs))[0]
+        within(db, ref, torch.full_like(ref, oracle.SLOPE), f"slope of {act}, scale {i}")
+        worst = max(worst, float((db.double() - ref).abs().max()))
+    print(f"[slope] {act} {worst:.3e}", flush=True)
