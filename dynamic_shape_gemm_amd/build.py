@@ -165,11 +165,18 @@ def torch_dir():
     return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
 
 
+def torch_for_rocm(where: str) -> bool:
+    """Whether a torch brings what the binding is compiled and linked against
+    (one for the CPU alone does not: the helpers keep their Python form)."""
+    needs = ("include/c10/hip/HIPFunctions.h", "include/c10/hip/HIPStream.h", "lib/libc10_hip.so")
+    return all(os.path.exists(os.path.join(where, n)) for n in needs)
+
+
 def start_torch_binding(obj_dir: str, verbose: bool = False):
     """Starts compiling the C++ form of the 8-bit helpers (host code against
-    torch's headers); None without torch."""
+    torch's headers); None without a torch for ROCm."""
     where = torch_dir()
-    if where is None:
+    if where is None or not torch_for_rocm(where):
         return None
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
@@ -187,7 +194,7 @@ def link_torch_binding(obj_dir: str, job, verbose: bool = False) -> None:
     the process has loaded by then."""
     if job is None:
         if os.path.exists(DIRECT):
-            os.remove(DIRECT)   # (built against a torch that is gone)
+            os.remove(DIRECT)   # (built against another torch)
         return
     if job.returncode != 0:
         raise subprocess.CalledProcessError(job.returncode, job.args)
