@@ -753,3 +753,27 @@ def test_slopes_are_exact_to_their_bound(mkp, act):
         within(db, ref, torch.full_like(ref, oracle.SLOPE), f"slope of {act}, scale {i}")
         worst = max(worst, float((db.double() - ref).abs().max()))
     print(f"[slope] {act} {worst:.3e}", flush=True)
+
+
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("N,K", [(256, 256), (2304, 768), (333, 517), (1003, 2050), (4100, 3000)])
+@pytest.mark.parametrize("M", [65, 1000, 4097, 8191, 8192])
+def test_backward_in_whole_numbers(mkp, M, N, K, act):
+    """Gradients and inputs of small whole numbers, scales of powers of two: every
+    product and every sum, in any order, is exact in binary32 (at most 8192 * 3 * 7 =
+    2^17.4, in quarters), so a row that is left out, or taken twice, shows in each element."""
+    g = gen(M + N)
+
+    def whole(hi, *shape):
+        return torch.randint(-hi, hi + 1, shape, generator=g, device="cuda", dtype=torch.int32)
+
+    dy = whole(3, M, N)
+    x, z = whole(7, M, K).to(I8), whole(5, M, N).to(I8)
+    xs = torch.exp2(whole(1, M).to(F32) - 1)
+    dz = dy * (z > 0) if act == "relu" else dy
+    want = dz.to(F64).t() @ (x.to(F64) * xs.to(F64)[:, None])
+    for t, gt in ((BF, F32), (F32, BF)):
+        got = mkp.linear_q8_backward(dy.to(t), placed(x, (-K) % 8), xs, z, torch.ones(M, device="cuda"), act=act, grad_dtype=gt)
+        same(got[0], dz.to(BF), "dz")
+        same(got[1], want.to(F32).to(gt), "dw")
+        same(got[2], dz.sum(0, dtype=torch.int64).to(F32), "dbias")
