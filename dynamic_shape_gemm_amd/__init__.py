@@ -981,7 +981,8 @@ def linear_q8_backward(dy, x, x_scale, z=None, z_scale=None, z_group=0, act=None
     with z_scale (quantize_rows of its pre-activation, in groups of z_group
     columns).  Returns (dz, dw, dbias): dz = dy act'(z) bf16 (dw's and dx's
     operand; dx is gemm(dz, w)), dw = dz^T x in grad_dtype (bfloat16, the default,
-    or float32), dbias fp32; None for those not needed.  No grad_fn."""
+    or float32, whose terms are held to 2^-16 instead of 2^-8, in twice the time),
+    dbias fp32; None for those not needed.  No grad_fn."""
     if stream is None and _direct is not None:
         out = _direct.linear_q8_backward(dy, x, x_scale, z, z_scale, z_group, ACTIVATIONS.get(act, -1), bool(need_dz),
                                          bool(need_dw), bool(need_dbias),

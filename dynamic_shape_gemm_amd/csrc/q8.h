@@ -81,6 +81,7 @@ struct Q8GradArgs {
     float* dbp;            // column sums of dz over sum_rows rows each, [M / sum_rows][Np]
     int Mr, Np, Kp;
     int sum_rows;          // a multiple of 16
+    bool low;              // a binary32 dW's second pass: a is what bf16 left of dz x_scale, dW is added to
     int tile, splits;
 };
 

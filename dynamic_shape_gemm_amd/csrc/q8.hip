@@ -173,6 +173,12 @@ __device__ __forceinline__ u32x2 to_i8(const float (&v)[8], const Scale8& sc) {
     return out;
 }
 
+// What rounding v to bf16 leaves of it, exactly (of an infinity or NaN: nothing).
+__device__ __forceinline__ float bf16_rest(float v) {
+    const float hi = bf16_lo(f32_to_bf16(v));
+    return fabsf(hi) < INFINITY ? v - hi : 0.0f;
+}
+
 // Up to eight bytes to a row (any alignment).
 __device__ __forceinline__ void store_i8(int8_t* p, u32x2 w, int n) {
     if (n >= 8) {
@@ -880,7 +886,9 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
 // fourth row; of the second 4 rows of the input.  The product's operand dz x_scale is
 // rounded here, once, from binary32 (made from the bf16 dz in the product it would be
 // rounded twice), and x's integers become bf16 here, exactly, so that the product's
-// loop does nothing but multiply.  Bound by the bytes: 8192 x 11008 with 8192 x 4096
+// loop does nothing but multiply.  For a binary32 dW another pass makes that operand
+// of what the rounding left: dz x_scale in two bf16 parts, relative 2^-16 (8192 x 2304 x
+// 768, against 64 bits: 2.5e-6 of dW's norm in 138 us a call; one part 1.7e-3, 71 us).  Bound by the bytes: 8192 x 11008 with 8192 x 4096
 // of x, 730 MB, 118 us, 6.2 TB/s.  (Loads behind branches: 120; 8192 x 2304 with
 // 8192 x 768, binary32 dy, 33.4 us against 29.8; 333 x 768 with 333 x 12544 14.5, one load
 // of x ahead, against 10.4.)
@@ -966,6 +974,9 @@ __global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first,
                 if (a.a != nullptr && m < a.Mr) {   // (rows from M on: zeros)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) g[i] = m < a.M ? g[i] * xs[u] : 0.0f;
+                    if (a.low)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) g[i] = bf16_rest(g[i]);
                     store_values<false>(a.a + m * a.Np, n, g, 8);
                 }
             }
@@ -1004,6 +1015,16 @@ __device__ __forceinline__ void q8_dbias(const Q8GradArgs& a, int n0, float* red
     if (grp == 0 && n < a.N)
         a.dbias[n] = ((red[c] + red[32 + c]) + (red[64 + c] + red[96 + c])) +
                      ((red[128 + c] + red[160 + c]) + (red[192 + c] + red[224 + c]));
+}
+
+// Four values of a row of K, zeros past it.
+__device__ __forceinline__ f32x4 load4_f32(const float* row, int k, int K) {
+    if (k + 4 <= K) return *(const f32x4a4*)(row + k);
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+        if (k + r < K) v[r] = row[k + r];
+    return v;
 }
 
 // A tile of dW = a^T . xb over one split of the rows (64 a step), both operands read
@@ -1051,6 +1072,19 @@ __global__ __launch_bounds__(T::NT, 2) void q8_product_kernel(Q8GradArgs a) {
         return;
     }
     if (a.splits == 1) {
+        if (a.low)
+#pragma unroll
+            for (int ha = 0; ha < 2; ++ha)
+#pragma unroll
+                for (int i = 0; i < T::FM; ++i) {
+                    const int row = n0 + at.row(ha, i);
+                    if (row >= a.N) continue;
+                    const float* d = (const float*)a.dw + row * a.lddw;
+#pragma unroll
+                    for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                        for (int j = 0; j < T::FN; ++j) acc[ha][hb][i][j] += load4_f32(d, k0 + at.col(hb, j), a.K);
+                }
         store_tile<T>(acc, 1.0f, a.dw, true, a.lddw, k0, a.N - n0, a.K - k0, smem, wave, lane,
                       [&](int r) { return (int64_t)n0 + r; });
         return;
@@ -1070,7 +1104,7 @@ __global__ __launch_bounds__(T::NT, 2) void q8_product_kernel(Q8GradArgs a) {
         }
 }
 
-// dW from its partials, eight columns a thread; then dbias.
+// dW from its partials (and, in a second pass, from itself), eight columns a thread; then dbias.
 __global__ __launch_bounds__(256) void q8_finish_kernel(Q8GradArgs a, int first) {
     __shared__ float red[256];
     if ((int)blockIdx.x >= first) {
@@ -1098,6 +1132,11 @@ __global__ __launch_bounds__(256) void q8_finish_kernel(Q8GradArgs a, int first)
             lo += x[u];
             hi += y[u];
         }
+    }
+    if (a.low) {
+        const float* d = (const float*)a.dw + n * a.lddw;
+        lo += load4_f32(d, k, a.K);
+        hi += load4_f32(d, k + 4, a.K);
     }
     const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     if (a.dw_f32) store_values<true>((float*)a.dw + n * a.lddw, k, v, a.K - k);
@@ -1235,7 +1274,7 @@ hipError_t launch_i8_finish(const I8Args& a, hipStream_t st) {
 hipError_t launch_q8_slopes(const Q8GradArgs& a, hipStream_t st) {
     const int cols = (int)up(a.Np, 512), shift = a.zgroup == 0 ? 31 : log2i(a.zgroup);
     const int64_t rows = a.a != nullptr ? a.Mr : a.M;
-    const int64_t first = up(rows, a.sum_rows) * cols, second = a.xb != nullptr ? up(a.M, 4) : 0;
+    const int64_t first = up(rows, a.sum_rows) * cols, second = a.xb != nullptr && !a.low ? up(a.M, 4) : 0;
     const dim3 grid((unsigned)(first + second));
     return by_act(a.act, [&](auto act) {
         constexpr int ACT = decltype(act)::value;

@@ -401,18 +401,27 @@ int backward(int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy, int 
     a.tile = l.tile;
     a.splits = l.splits;
     const double m = (double)M, n = (double)N, k = (double)K, wb = size_of(dw_type);
-    if (M > 0)
-        MKP_TRY(go(st, QL_SLOPES, 4.0 * m * n,
-                   (size_of(dy_type) + (sloped ? 1.0 : 0.0) + (dZ ? 2.0 : 0.0) + (dW ? 2.0 : 0.0)) * m * n + (dW ? 3.0 * m * k : 0.0),
-                   [&] { return launch_q8_slopes(a, st); }));
-    const double parts = 4.0 * n * k * (double)l.splits, sums = dbias ? 4.0 * n * (double)ceil_div(M, l.sum_rows) : 0.0;
-    if (dW)
-        MKP_TRY(go(st, QL_Q8_PRODUCT, 2.0 * m * n * k, 2.0 * m * (n + k) + (l.splits > 1 ? parts : wb * n * k + sums),
-                   [&] { return launch_q8_product(a, st); }));
-    if (dW ? l.splits == 1 : !dbias) return MKP_OK;
-    return go(st, QL_Q8_FINISH, 0.0,
-              (dW ? parts + wb * n * k : 0.0) + sums,
-              [&] { return launch_q8_finish(a, st); });
+    auto pass = [&]() -> int {
+        if (M > 0)
+            MKP_TRY(go(st, QL_SLOPES, 4.0 * m * n,
+                       (size_of(dy_type) + (sloped ? 1.0 : 0.0) + (a.dz ? 2.0 : 0.0) + (dW ? 2.0 : 0.0)) * m * n +
+                           (dW && !a.low ? 3.0 * m * k : 0.0),
+                       [&] { return launch_q8_slopes(a, st); }));
+        const double parts = 4.0 * n * k * (double)l.splits, sums = a.dbias ? 4.0 * n * (double)ceil_div(M, l.sum_rows) : 0.0;
+        const double grad = (a.low ? 2.0 : 1.0) * wb * n * k;
+        if (dW)
+            MKP_TRY(go(st, QL_Q8_PRODUCT, 2.0 * m * n * k, 2.0 * m * (n + k) + (l.splits > 1 ? parts : grad + sums),
+                       [&] { return launch_q8_product(a, st); }));
+        if (dW ? l.splits == 1 : a.dbias == nullptr) return MKP_OK;
+        return go(st, QL_Q8_FINISH, 0.0, (dW ? parts + grad : 0.0) + sums, [&] { return launch_q8_finish(a, st); });
+    };
+    MKP_TRY(pass());
+    if (!dW || !a.dw_f32 || M == 0) return MKP_OK;
+    // A binary32 dW: what bf16 left of the operand, through the same workspace, added to it.
+    a.low = true;
+    a.dz = nullptr;
+    a.dbias = nullptr;
+    return pass();
 }
 
 }  // namespace

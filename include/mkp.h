@@ -390,9 +390,10 @@ int mkp_linear_i8(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, i
  * are overwritten; M == 0 makes dW and dbias 0.
  *
  * dZ is computed in binary32 and dbias summed so.  For dW, dZ times its row's
- * x_scale is rounded to bf16 once (relative 2^-8 at most), the integers of x are exact in
- * bf16, and products are summed in binary32: with MKP_F32 too, dW is as exact as
- * that.
+ * x_scale (made of the binary32 dZ) becomes an operand in bf16, the integers of x are
+ * exact in bf16, and products are summed in binary32.  With MKP_BF16 that operand is
+ * rounded once, relative 2^-8 at most, as is the result; with MKP_F32 it is held in two
+ * parts, relative 2^-16, whose products take one after the other, twice the time.
  */
 int mkp_linear_q8_backward(int64_t M, int64_t N, int64_t K, const void *dY, int64_t lddy, int dy_type,
                            const int8_t *X, int64_t ldx, const float *x_scale,

@@ -100,7 +100,9 @@ def backward(dy, x, xs, z, zs, group, name, dtype):
 
     dz: the slope's error times |dy|, one product, one rounding to bf16.
     dbias: M additions of binary32.  dw: dz's error, its product with the scale
-    and that one's rounding to bf16 in every term, then M additions."""
+    and that one's rounding to bf16 (for a binary32 dw: to the sum of two bf16
+    parts, the second within 2^-8 of what the first leaves) in every term, then M
+    additions (of each part)."""
     dy = dy.to(F64)
     M = dy.shape[0]
     dz, e = dy, torch.zeros_like(dy)
@@ -114,7 +116,8 @@ def backward(dy, x, xs, z, zs, group, name, dtype):
     out["dbias"] = (dz.sum(0), e.sum(0) * (1 + add) + add * dz.abs().sum(0))
     if x is not None:
         v = values(x, xs)
-        each = dz.abs() * (half + 4.0 * U) + e * (1 + half)
+        operand = half if dtype is torch.bfloat16 else half * half * (1 + 2 ** -7)
+        each = dz.abs() * (operand + 4.0 * U) + e * (1 + half)
         terms = dz.abs().t() @ v.abs()
         dw = dz.t() @ v
         tol = (each.t() @ v.abs()) * (1 + add) + 2.0 * add * terms + least * x.to(F64).abs().sum(0)

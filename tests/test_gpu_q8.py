@@ -777,3 +777,51 @@ def test_backward_in_whole_numbers(mkp, M, N, K, act):
         same(got[0], dz.to(BF), "dz")
         same(got[1], want.to(F32).to(gt), "dw")
         same(got[2], dz.sum(0, dtype=torch.int64).to(F32), "dbias")
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 40, 24), (333, 768, 768), (8192, 300, 130), (700, 2900, 3000)])
+def test_binary32_weight_gradients(mkp, M, N, K):
+    """Two passes over one workspace: as exact as their bound whatever else is asked for,
+    the same bits again, from a graph and from another stream."""
+    a = kept(gen(M + K), M, N, K, 64, F32)
+    first = check_backward(mkp, *a, 64, "silu", F32)
+    for need in (dict(need_dz=False), dict(need_dbias=False), dict(need_dz=False, need_dbias=False)):
+        same(check_backward(mkp, *a, 64, "silu", F32, **need)[1], first[1], "dw alone")
+
+    def call(**o):
+        return mkp.linear_q8_backward(*a, z_group=64, act="silu", grad_dtype=F32, **o)
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    on = call(stream=st)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call()
+    for rep in range(3):
+        for o in outs:
+            o.fill_(NAN)
+        graph.replay()
+        again = call()
+        torch.cuda.synchronize()
+        for name, f, *others in zip(("dz", "dw", "dbias"), first, on, outs, again):
+            for o in others:
+                same(o, f, name)
+
+
+@pytest.mark.parametrize("gt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,K", [(70, 48), (2900, 3000)])
+def test_gradients_that_are_not_finite(mkp, N, K, gt):
+    """An infinite gradient makes its channel's weight gradient infinite, of x's sign; a
+    NaN, NaN; other channels are what they were."""
+    M = 200
+    dy, x, xs, _, _ = kept(gen(N), M, N, K, 0, F32)
+    x[x == 0] = 1
+    ref = mkp.linear_q8_backward(dy, x, xs, grad_dtype=gt)[1]
+    dy[7, 3], dy[199, 20], dy[64, N - 1] = math.inf, -math.inf, NAN
+    dw = mkp.linear_q8_backward(dy, x, xs, grad_dtype=gt)[1]
+    same(dw[3], torch.where(x[7] > 0, math.inf, -math.inf).to(gt), "an infinity")
+    same(dw[20], torch.where(x[199] > 0, -math.inf, math.inf).to(gt), "a negative one")
+    assert torch.isnan(dw[N - 1]).all()
+    rest = [n for n in range(N) if n not in (3, 20, N - 1)]
+    same(dw[rest], ref[rest], "the others")
