@@ -32,10 +32,10 @@ struct QuantArgs {
 struct I8Args {
     int64_t M;
     int N, K;
-    const int8_t* A;       // rows 16-byte aligned
+    const int8_t* A;       // rows 16-byte aligned on tiles, of any alignment in the stream
     int64_t lda;
     const float* sa;       // M
-    const int8_t* B;       // rows 16-byte aligned
+    const int8_t* B;       // as A's
     int64_t ldb;
     const float* sb;       // N
     const float* bias;     // N or null

@@ -466,14 +466,6 @@ __device__ __forceinline__ void act_run(int act, f32x4* v) {
     }
 }
 
-// One tile over one split's K steps (of 128 integers).  256 x 256 tiles, one a CU: 1.4
-// us a step, as long as of bf16 for twice the work.  MFMAs take 64-68 % of that time
-// (48-60 % of the launch's, whose ends are not hidden with one tile a CU), LDS 21-25 %,
-// the rest are the waves' waits for each other and for a step's loads; 4096 x 4096 x
-// 4096 57 us, 2420 TOPS.  64 x 64 tiles, four a CU, for latency: 509 x 2304 x
-// 768 6.2 us, where 128 x 128 take 8.1 and 256 x 256 10.2.  The sums are exact in 32
-// bits (K at most 131071); what is past K reads as zeros in both operands, or, in
-// the last 16 bytes, as zeros in A.
 // A tile's bf16 values, staged in LDS, to rows of any alignment.
 template <class T>
 __device__ __forceinline__ void store_rows16(uint16_t* D, int64_t ld, int rows, int cols, const lds_t* smem, int tid) {
@@ -494,6 +486,14 @@ __device__ __forceinline__ void store_rows16(uint16_t* D, int64_t ld, int rows, 
 
 template <class T>
 constexpr int staged_ld32 = T::BN * 4 + 16;
+// One tile over one split's K steps (of 128 integers).  256 x 256 tiles, one a CU: 1.4
+// us a step, as long as of bf16 for twice the work.  MFMAs take 64-68 % of that time
+// (48-60 % of the launch's, whose ends are not hidden with one tile a CU), LDS 21-25 %,
+// the rest are the waves' waits for each other and for a step's loads; 4096 x 4096 x
+// 4096 57 us, 2420 TOPS.  64 x 64 tiles, four a CU, for latency: 509 x 2304 x
+// 768 6.2 us, where 128 x 128 take 8.1 and 256 x 256 10.2.  The sums are exact in 32
+// bits (K at most 131071); what is past K reads as zeros in both operands, or, in
+// the last 16 bytes, as zeros in A.
 template <class T, int ACT>
 __device__ __forceinline__ void i8_tile(const I8Args& a, int m0, int n0, int split, lds_t* smem, float* edge, int wave,
                                         int lane) {

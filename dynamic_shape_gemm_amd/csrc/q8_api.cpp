@@ -239,8 +239,7 @@ int linear(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, int x_ty
     const LinearLayout l = linear_layout(M, N, K, X, ldx, x_type, W, ldw);
     MKP_TRY(check_workspace(workspace, workspace_bytes, l.bytes));
     const int64_t tiles = l.stream ? 0 : ceil_div(M, l.tile) * ceil_div(N, l.tile) * l.splits;
-    if (tiles > UINT32_MAX / 512 || (l.splits > 1 && M * ceil_div(N, 4) > (int64_t)UINT32_MAX - 255) ||
-        (l.pack_b && N > kMaxRows))
+    if (tiles > UINT32_MAX / 512 || (l.splits > 1 && M * ceil_div(N, 4) > (int64_t)UINT32_MAX - 255))
         return report(MKP_ERR_UNSUPPORTED, "grid too large");
     begin_call();
     const hipStream_t st = (hipStream_t)stream;

@@ -369,9 +369,10 @@ int mkp_dequantize_rows(int64_t M, int64_t K, const int8_t *Q, int64_t ldq, cons
  * scaled (by w_scale first), biased and activated in binary32.  K == 0:
  * Y := act(bias).
  *
- * Any alignment of X, W and Y serves.  W whose rows are not 16-byte aligned
- * (address and ldw), or an X of MKP_I8 whose rows are not or whose K is not a
- * multiple of 16, costs a padded copy per call.
+ * Any alignment of X, W and Y serves.  From 33 tokens on (fewer, where X has more
+ * than 128 K elements and W's rows are aligned), W whose rows are not 16-byte
+ * aligned (address and ldw), or an X of MKP_I8 whose rows are not or whose K is not
+ * a multiple of 16, costs a padded copy per call.
  */
 int mkp_linear_i8(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, int x_type, const float *x_scale,
                   const int8_t *W, int64_t ldw, const float *w_scale, const float *bias, int act,
