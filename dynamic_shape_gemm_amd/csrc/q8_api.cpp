@@ -135,11 +135,11 @@ void choose_tile(const TileCost (&tiles)[n], int64_t rows, int64_t cols, int64_t
 }
 
 // linear_i8's.  Fitted to measurements of 200 extents (33 to 8192 x 128 to 12544 x 128
-// to 12544): the choice is 0.6 % behind the fastest in the mean, 14 % at most.  One
-// tile for all: 256 loses 7.5 us to 64's 4.1 at 109 x 887 x 144, 64 loses 563 to
-// 256's 300 at 8192 x 11008 x 4096.  No splits: 105 x 1024 x 12544 takes 36 us on the
-// 64 tile, in eight parts 8.3 + 4.0.  (Parts are written and read, and joined by a
-// launch that costs the caller 3 us.)
+// to 12544): the choice is 0.6 % behind the fastest in the mean, 14 % at most (of 200
+// others 1.2 % and 23 %).  One tile for all: 256 loses 7.5 us to 64's 4.1 at 109 x 887 x
+// 144, 64 loses 563 to 256's 300 at 8192 x 11008 x 4096.  No splits: 105 x 1024 x 12544
+// takes 36 us on the 64 tile, in eight parts 8.3 + 4.0.  (Parts are written and read, and
+// joined by a launch that costs the caller 3 us.)
 constexpr TileCost kI8Tiles[] = {
     {256, 0.1, 7.4, 1.2, 1.2, 1}, {128, 2.3, 4.0, 0.5, 0.5, 2}, {64, 1.9, 1.5, 0.28, 0.29, 4}};
 double i8_joined(double mn, double splits) {
@@ -147,10 +147,10 @@ double i8_joined(double mn, double splits) {
 }
 
 // linear_q8_backward's dW.  Fitted to measurements of 100 extents (32 to 8192 x 128 to
-// 12544 x 128 to 12544): 0.7 % behind the fastest in the mean, 15 % at most.  One tile
-// for all: 256 loses 14.3 us to 128's 7.4 at 333 x 768 x 768, 128 loses 869 to 583 at
-// 8192 x 11008 x 4096.  No splits: 8192 x 768 x 768 takes 71 us on the 128 tile, in six
-// parts 17.4 + 4.0.
+// 12544 x 128 to 12544): 0.7 % behind the fastest in the mean, 15 % at most (of 100
+// others 0 % and 12 %).  One tile for all: 256 loses 14.3 us to 128's 7.4 at 333 x 768 x
+// 768, 128 loses 869 to 583 at 8192 x 11008 x 4096.  No splits: 8192 x 768 x 768 takes 71
+// us on the 128 tile, in six parts 17.4 + 4.0.
 constexpr TileCost kGradTiles[] = {{256, 0.9, 11.0, 0.65, 0.65, 1}, {128, 2.6, 4.9, 0.335, 0.43, 2}};
 double grad_joined(double nk, double splits) {
     return 0.8e-6 * nk * splits + std::max(4.1, 1e-6 * nk * (0.28 + 0.67 * splits));
