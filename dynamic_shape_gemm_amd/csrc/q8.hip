@@ -888,10 +888,10 @@ __global__ __launch_bounds__(512) void i8_stream_kernel(I8Args a, int cols) {
 // rounded twice), and x's integers become bf16 here, exactly, so that the product's
 // loop does nothing but multiply.  For a binary32 dW another pass makes that operand
 // of what the rounding left: dz x_scale in two bf16 parts, relative 2^-16 (8192 x 2304 x
-// 768, against 64 bits: 2.5e-6 of dW's norm in 138 us a call; one part 1.7e-3, 71 us).  Bound by the bytes: 8192 x 11008 with 8192 x 4096
-// of x, 730 MB, 118 us, 6.2 TB/s.  (Loads behind branches: 120; 8192 x 2304 with
-// 8192 x 768, binary32 dy, 33.4 us against 29.8; 333 x 768 with 333 x 12544 14.5, one load
-// of x ahead, against 10.4.)
+// 768, against 64 bits: 2.5e-6 of dW's norm in 138 us a call; one part 1.7e-3, 71 us).
+// Bound by the bytes: 8192 x 11008 with 8192 x 4096 of x, 730 MB, 118 us, 6.2 TB/s.
+// (Loads behind branches: 120; 8192 x 2304 with 8192 x 768, binary32 dy, 33.4 us against
+// 29.8; 333 x 768 with 333 x 12544 14.5, one load of x ahead, against 10.4.)
 template <bool F32, int ACT>
 __global__ __launch_bounds__(256) void q8_slopes_kernel(Q8GradArgs a, int first, int cols, int zshift) {
     __shared__ float red[4][512];
